@@ -333,6 +333,212 @@ ks_status_t ks_pair_closure(ks_pattern_t f, ks_pattern_t g, ks_closure_t* out);
 ks_status_t ks_chain_describe(const ks_pattern_t* p, int n, int64_t batch, ks_dtype_t dt,
                               unsigned flags, char* buf, size_t len);
 
+/*
+ * Operators around the product, for serving and fine-tuning a layer of KS
+ * factors: low-rank adapters beside a frozen projection, a preference loss on
+ * token logits, and the optimizer step. The conventions above hold for all of
+ * them: device pointers of the caller, asynchronous on `stream`, argument
+ * errors found on the host before any HIP call, no allocation, no atomics and
+ * a fixed summation order.
+ */
+
+/* Element types of single tensors (the types that ks_dtype_t combines). */
+typedef enum ks_elem_t {
+    KS_ELEM_F32 = 0,
+    KS_ELEM_BF16 = 1
+} ks_elem_t;
+
+/*
+ * Low-rank adapters of many requests. Adapter g of `count` has
+ *   A[g]      rank x n_in,   row-major, the weights' type of the ks_dtype_t
+ *   B[g]      n_out x rank,  row-major, the same type
+ *   scale[g]  fp32
+ * with the adapters one after another. Row n of a batch belongs to adapter
+ * g = ids[n]; an id outside [0, count) means none, so such a row gets the
+ * shared projection alone. 1 <= rank <= KS_ADAPTER_MAX_RANK and
+ * 1 <= count <= KS_ADAPTER_MAX_COUNT; batch * rank and each tensor's element
+ * count have to stay below 2^31, else KS_ERR_INVALID.
+ */
+#define KS_ADAPTER_MAX_RANK 256
+#define KS_ADAPTER_MAX_COUNT 65535
+
+typedef struct ks_adapters_t {
+    const void* A;        /* device */
+    const void* B;        /* device */
+    const float* scale;   /* device */
+    int64_t n_in, n_out;
+    int32_t rank, count;
+} ks_adapters_t;
+
+/*
+ * ks_adapter_matmul: Y += H B^T with H = scale X A^T, each row with its own
+ * adapter:
+ *   H[n][r] = scale[g] sum_k X[n][k] A[g][r][k],  Y[n][o] += sum_r H[n][r] B[g][o][r]
+ *   ids    device int32, batch values.
+ *   X      device, batch x n_in, X's type of dt (as for ks_matmul).
+ *   Y      device fp32, batch x n_out; added to.
+ *   H      device fp32, batch x rank: fully overwritten, zeros for rows
+ *          without an adapter. ks_adapter_backward reads it.
+ * The intermediate H is fp32 in every case. Pointers need the alignment of
+ * their element; 16 bytes select wider loads. Y and H must not overlap any
+ * input or each other (KS_ERR_OVERLAP).
+ */
+ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const void* X, float* Y, float* H,
+                              int64_t batch, ks_dtype_t dt, hipStream_t stream);
+
+/*
+ * ks_adapter_backward: gradients of ks_adapter_matmul. With
+ * E[n][r] = scale[g] sum_o dY[n][o] B[g][o][r]:
+ *   dX[n][k]    += sum_r E[n][r] A[g][r][k]      (NULL: not computed)
+ *   dA[g][r][k]  = sum_{n of g} E[n][r] X[n][k]  fp32, count x rank x n_in
+ *   dB[g][o][r]  = sum_{n of g} dY[n][o] H[n][r] fp32, count x n_out x rank
+ *   dY     device fp32, batch x n_out.   X, H: as ks_adapter_matmul had and wrote them.
+ *   dX     device fp32, batch x n_in; added to (the projection's own dX).
+ *   dA, dB fully overwritten, zeros for adapters without rows; both NULL: not
+ *          computed (then X and H may be NULL).
+ *   ws     device workspace of ks_adapter_backward_workspace_size bytes, 16-byte
+ *          aligned.
+ * Partial sums over ranges of an adapter's rows are added in a fixed order.
+ * batch = 0 writes the zeros of dA and dB.
+ */
+ks_status_t ks_adapter_backward_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes);
+ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X,
+                                const float* H, float* dX, float* dA, float* dB, int64_t batch, ks_dtype_t dt,
+                                void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ks_chain_adapter_matmul: the chain of ks_chain_matmul (KS_CHAIN_AUTO) and
+ * the adapters beside it, Y = X (W_{n-1} ... W_0)^T + H B^T. Long batches run
+ * in ranges of rows, so that the adapters add to values of Y that the last
+ * cache still holds. Y is fully overwritten; ad->n_in and ad->n_out have to be
+ * the chain's (KS_ERR_CHAIN_MISMATCH). Workspace as for ks_chain_matmul, of
+ * the size that ks_chain_adapter_workspace_size gives.
+ */
+ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad, int64_t batch,
+                                            ks_dtype_t dt, size_t* bytes);
+ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
+                                    const int32_t* ids, const void* X, float* Y, float* H, int64_t batch,
+                                    ks_dtype_t dt, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ks_chain_adapter_backward: dX of the chain (dY W_{n-1} ... W_0, W frozen)
+ * plus the adapters', and dA and dB (both NULL: not computed).
+ */
+ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
+                                                     int64_t batch, ks_dtype_t dt, size_t* bytes);
+ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
+                                      const int32_t* ids, const float* dY, const void* X, const float* H, float* dX,
+                                      float* dA, float* dB, int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes,
+                                      hipStream_t stream);
+
+/*
+ * Token logits. x[s][t][v] of `sequences` x `tokens` x `vocab` values lies at
+ * data[s * seq_stride + t * row_stride + v] (strides in elements, row_stride
+ * >= vocab, seq_stride >= (tokens - 1) * row_stride + vocab), so a batch with
+ * its last position cut off needs no copy. labels[s * label_stride + t] is the
+ * token that position t should give; a negative label masks the position: its
+ * logits are not read (they may hold anything), its log probability is 0 and
+ * its gradient is 0. A label >= vocab gives NaN.
+ */
+typedef struct ks_logits_t {
+    const void* data;       /* device */
+    const int64_t* labels;  /* device */
+    int64_t seq_stride, row_stride, label_stride;
+    int64_t sequences, tokens, vocab;
+    int32_t elem;           /* a ks_elem_t value */
+    int32_t reserved;       /* must be zero */
+} ks_logits_t;
+
+/*
+ * ks_sequence_logp: tokens[s][t] = x[s][t][label] - log sum_v exp x[s][t][v]
+ * (0 where masked) and total[s] = sum_t tokens[s][t]; both device fp32,
+ * contiguous.
+ *   stats  device fp32, sequences x tokens x 2, or NULL: each row's maximum and
+ *          its sum of exp(x - maximum), which ks_preference_backward reads.
+ */
+ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, float* stats, hipStream_t stream);
+
+/*
+ * ks_preference_loss: the paired preference loss of a policy against a
+ * reference. Sequences 0 .. P-1 are the chosen answers, P .. 2P-1 the rejected
+ * ones (sequences must be even: KS_ERR_INVALID).
+ *   rewards[s] = beta sum_t (tokens[s][t] - ref[s][t]) over unmasked t
+ *   z_i = rewards[i] - rewards[P + i]
+ *   loss = 1/P sum_i (1 - smoothing) log(1 + exp(-z_i)) + smoothing log(1 + exp(z_i))
+ *   ref     device fp32, ref[s * ref_stride + t]: the reference's tokens of
+ *           ks_sequence_logp; not read where masked.
+ *   loss    device fp32, one value (0 if there is no pair).
+ *   rewards device fp32, 2P.   tokens device fp32, 2P x T.
+ *   grad    device fp32, 2P: d loss / d total[s], for ks_preference_backward.
+ *   stats   device fp32, 2P x T x 2: as ks_sequence_logp writes them.
+ *   dlogits NULL: the loss alone. Else the gradient of the loss, of x's element
+ *           type, at dlogits[s * d_seq_stride + t * d_row_stride + v]; it may
+ *           be x's own memory with x's strides. Long batches run in ranges of
+ *           pairs, so that the gradient finds a pair's logits in the last cache.
+ * beta > 0 and 0 <= smoothing <= 1, else KS_ERR_INVALID.
+ *
+ * ks_preference_backward: that gradient from stats and grad of an earlier
+ * call, times upstream[0] (device fp32; NULL means 1).
+ */
+ks_status_t ks_preference_loss(const ks_logits_t* x, const float* ref, int64_t ref_stride, float beta, float smoothing,
+                               float* loss, float* rewards, float* tokens, float* grad, float* stats, void* dlogits,
+                               int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream);
+ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, const float* grad, const float* upstream,
+                                   void* dlogits, int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream);
+
+/*
+ * One optimizer step over many tensors. For each element
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr weight_decay) p - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, p rounded to the nearest value of its type at the end.
+ * state_bits 32: m and v are fp32. state_bits 8: one byte each, and
+ * scales[2 j], scales[2 j + 1] hold the scales of m and of v of the values
+ * 256 j .. 256 j + 255 of the tensor:
+ *   m = scale k |k| / 127^2  (k signed),   v = scale k^4 / 255^4  (k unsigned)
+ * A value between two codes takes the upper one with the probability that
+ * keeps its mean, so that the slow average v still moves by less than a code a
+ * step; v > 0 never becomes code 0. The random number of value i of a tensor
+ * is a hash of options->seed and 256 * (blocks of the tensors before it) + i,
+ * so a step is a function of its arguments. A block with a value that is not
+ * finite gets a scale that is not finite.
+ * The tensors' memory must not overlap between tensors; within one tensor that
+ * is checked (KS_ERR_OVERLAP). n = 0 and tensors with n = 0 are no-ops.
+ */
+typedef struct ks_adamw_tensor_t {
+    void* p;          /* device */
+    const void* g;    /* device */
+    void* m;          /* device: fp32, or int8  */
+    void* v;          /* device: fp32, or uint8 */
+    float* scales;    /* device: 2 ceil(n / 256) values; unused for 32 bits */
+    int64_t n;        /* elements, below 2^31 */
+    int32_t p_elem, g_elem;  /* ks_elem_t values */
+} ks_adamw_tensor_t;
+
+typedef struct ks_adamw_options_t {
+    double lr, beta1, beta2, eps, weight_decay;
+    double max_norm;      /* > 0: gradients are scaled by min(1, max_norm / (norm + 1e-6)) */
+    int64_t step;         /* >= 1 */
+    uint32_t seed;
+    int32_t state_bits;   /* 8 or 32 */
+} ks_adamw_options_t;
+
+/*
+ * ks_grad_norm: norm[0] = sqrt(sum of g^2 over all tensors), device fp32.
+ * Only g, g_elem and n of the tensors are read. ws of
+ * ks_grad_norm_workspace_size bytes, 16-byte aligned.
+ * ks_adamw_step: the step; norm (device fp32) is read if max_norm > 0. If that
+ * norm is not finite the step changes nothing.
+ * ks_adamw_state_values: m_out[i] and v_out[i] (host arrays of device fp32
+ * pointers) get the values that tensor i's 8-bit states stand for.
+ */
+ks_status_t ks_grad_norm_workspace_size(const ks_adamw_tensor_t* t, int n, size_t* bytes);
+ks_status_t ks_grad_norm(const ks_adamw_tensor_t* t, int n, float* norm, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+ks_status_t ks_adamw_step(const ks_adamw_tensor_t* t, int n, const ks_adamw_options_t* options, const float* norm,
+                          hipStream_t stream);
+ks_status_t ks_adamw_state_values(const ks_adamw_tensor_t* t, int n, float* const* m_out, float* const* v_out,
+                                  hipStream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

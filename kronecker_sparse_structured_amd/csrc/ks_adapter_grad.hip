@@ -1,0 +1,482 @@
+// ks_adapter_grad.hip -- gradients of the adapters beside a shared projection.
+// With g = ids[n] and E[n] = scale[g] dY[n] B[g]:
+//   dX[n] += E[n] A[g],  dA[g] = sum_{n of g} E[n]^T X[n],  dB[g] = sum_{n of g} dY[n]^T H[n]
+//
+// What it cannot do without: dY and X read once, dX read and written once (the
+// projection's own dX is there already). E needs a whole row of dY and dB a
+// whole column, so a pass that reads dY once leaves partial sums of one of
+// them: workgroups take up to 256 rows x 256 columns and leave both, E over
+// column ranges and dB over row ranges, a few percent of dY's bytes each.
+//   1. sort    rows by adapter (stable), cut into blocks of rows that belong
+//              to one adapter each: the rest never meets a mixed block.
+//   2. grad_y  a pass over dY: partial E and dB.
+//   3. sum     the partial sums, in order.
+//   4. grad_x  a pass over X and dX: dX, partial dA.
+//   5. sum     dA.
+// No atomics; the order of every sum is fixed by ids alone.
+//
+// The products run on the fp32 matrix instruction (16 x 16 x 4), whose operands
+// hold one value a lane: E, dA and dB are sums over thousands of values and stay
+// in fp32 throughout. The order of the instruction's inner index is free as long
+// as both operands agree on it.
+
+#include <algorithm>
+
+#include "ks_device.h"
+#include "ks_train.h"
+
+namespace ks {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 256;    // most rows of a block
+constexpr int kColsY = 256;      // columns of dY a workgroup takes
+constexpr int kColsX = 128;      // columns of X a workgroup takes
+constexpr int kPitch = 65;       // LDS row of a 64-wide tile: odd, so that row and column reads of 16 + 16 j
+                                 // places fall into 64 different banks
+
+struct Slot {
+    int adapter, start, len, reserved;   // rows order[start .. start + len); len 0: empty
+};
+struct Segment {
+    int start, len;                      // an adapter's rows in the order
+};
+
+// Blocks of adapter g start at slot floor(start / block) + g: at most one slot
+// an adapter is left empty, and no slot is claimed twice.
+__device__ __forceinline__ int first_slot(Segment s, int g, int block) { return s.start / block + g; }
+
+// One workgroup an adapter: its rows' places in the order are the rows of
+// smaller adapters plus its own before them. Each wave counts a run of the
+// ids, 64 at a time.
+__global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batch, int count, int block, int* order,
+                                                    Segment* segs, Slot* slots, int n_slots) {
+    __shared__ int wave_own[16], wave_less[16];
+    const int g = blockIdx.x, tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+    const int per = ((batch + 15) / 16 + 63) / 64 * 64;
+    const int i0 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(wave) * per));
+    const int i1 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(i0) + per));
+    int own = 0, less = 0;
+#pragma unroll 8
+    for (int i = i0; i < i1; i += 64) {
+        const int id = i + lane < i1 ? ids[i + lane] : -1;
+        own += __popcll(__ballot(id == g));
+        less += __popcll(__ballot(id >= 0 && id < g));
+    }
+    if (lane == 0) {
+        wave_own[wave] = own;
+        wave_less[wave] = less;
+    }
+    __syncthreads();
+    int start = 0, total = 0, at = 0;
+    for (int w = 0; w < 16; ++w) {
+        start += wave_less[w];
+        at += w < wave ? wave_own[w] : 0;
+        total += wave_own[w];
+    }
+    at += start;
+    if (own) {
+        for (int i = i0; i < i1; i += 64) {
+            const bool mine = i + lane < i1 && ids[i + lane] == g;
+            const uint64_t all = __ballot(mine);
+            if (mine) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = i + lane;
+            at += __popcll(all);
+        }
+    }
+    const Segment seg = {start, total};
+    if (tid == 0) segs[g] = seg;
+    const int s0 = first_slot(seg, g, block);
+    const int s1 = g + 1 < count ? first_slot(Segment{start + total, 0}, g + 1, block) : n_slots;
+    for (int s = s0 + tid; s < s1; s += 1024) {
+        const int done = (s - s0) * block;
+        const int len = max(0, min(block, total - done));
+        slots[s] = Slot{g, start + done, len, 0};
+    }
+}
+
+// A value at row `row` of a matrix, 0 where the place is outside.
+template <typename T>
+__device__ __forceinline__ float value_at(const T* p, int64_t row, int64_t width, int col, bool inside) {
+    const float x = to_f32(p[inside ? row * width + col : 0]);
+    return inside ? x : 0.0f;
+}
+
+// Partial E and dB of one block of rows and 256 columns of dY. RT: tiles of 16
+// ranks; blockIdx.z: which group of 16 RT ranks.
+//
+// dY goes through LDS in tiles of 64 x 64, the next tile's loads in flight
+// while this one is multiplied. A wave takes 16 rows of the tile for E (inner
+// index: the columns) and 16 columns for dB (inner index: the rows); lane group
+// lg takes the inner values 16 lg + j, which the odd pitch spreads over all
+// banks for both.
+template <typename TW, int RT>
+__global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const TW* B, const float* H,
+                                                          const float* scale, const int* order, const Slot* slots,
+                                                          int64_t batch, int n_out, int rank, float* e_part,
+                                                          float* db_part) {
+    constexpr int kR = 16 * RT + 1;
+    __shared__ float tile[64 * kPitch];
+    __shared__ float bt[kColsY * kR];      // B[o][r], all columns of the workgroup
+    __shared__ float ht[64 * kR];          // H[n][r], the row tile's
+    __shared__ int row_of[kMaxRows];
+    const Slot s = slots[blockIdx.x];
+    if (s.len == 0) return;
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, li = lane % 16, lg = lane / 16;
+    const int r0 = blockIdx.z * 16 * RT, base = blockIdx.y * kColsY;
+    const TW* b = B + static_cast<int64_t>(s.adapter) * n_out * rank;
+    const bool wide = n_out % 4 == 0 && reinterpret_cast<uintptr_t>(dY) % 16 == 0;
+    const float factor = scale[s.adapter];
+    const int row_tiles = (s.len + 63) / 64, col_tiles = min(kColsY / 64, (n_out - base + 63) / 64);
+    for (int i = tid; i < kMaxRows; i += kThreads) row_of[i] = order[s.start + min(i, s.len - 1)];
+    for (int i = tid; i < kColsY * 16 * RT; i += kThreads) {
+        const int o = i / (16 * RT), r = i % (16 * RT);
+        bt[o * kR + r] = value_at(b, base + o, rank, r0 + r, base + o < n_out && r0 + r < rank);
+    }
+    __syncthreads();
+    // thread: rows tid / 16 + 16 q of a tile, four columns from 4 (tid % 16)
+    float next[4][4], hnext[4 * RT];
+    auto load = [&](int rt, int ct) {
+        const int o = base + ct * 64 + 4 * (tid % 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int at = rt * 64 + tid / 16 + 16 * q;
+            const float* src = dY + static_cast<int64_t>(row_of[at]) * n_out + o;
+            const int valid = at < s.len ? n_out - o : 0;
+            if (wide && valid >= 4) {
+                load4_f32(src, next[q]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) next[q][i] = i < valid ? src[i] : 0.0f;
+            }
+        }
+        if (ct == 0 && db_part) {
+#pragma unroll
+            for (int q = 0; q < 4 * RT; ++q) {
+                const int n = (q * kThreads + tid) / (16 * RT), r = (q * kThreads + tid) % (16 * RT);
+                const int at = rt * 64 + n;
+                hnext[q] = value_at(H, row_of[at], rank, r0 + r, at < s.len && r0 + r < rank);
+            }
+        }
+    };
+    f32x4 d[kColsY / 64][RT];
+#pragma unroll
+    for (int c = 0; c < kColsY / 64; ++c)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) d[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    load(0, 0);
+    for (int rt = 0; rt < row_tiles; ++rt) {
+        f32x4 e[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) e[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ct = 0; ct < kColsY / 64; ++ct) {
+            if (ct >= col_tiles) break;
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tile[(tid / 16 + 16 * q) * kPitch + 4 * (tid % 16) + i] = next[q][i];
+            if (ct == 0 && db_part) {
+#pragma unroll
+                for (int q = 0; q < 4 * RT; ++q)
+                    ht[(q * kThreads + tid) / (16 * RT) * kR + (q * kThreads + tid) % (16 * RT)] = hnext[q];
+            }
+            __syncthreads();
+            if (ct + 1 < col_tiles) load(rt, ct + 1);
+            else if (rt + 1 < row_tiles) load(rt + 1, 0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float x = tile[(16 * wave + li) * kPitch + 16 * lg + j];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    e[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, bt[(ct * 64 + 16 * lg + j) * kR + 16 * t + li], e[t],
+                                                                0, 0, 0);
+            }
+            if (db_part) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = tile[(16 * lg + j) * kPitch + 16 * wave + li];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, ht[(16 * lg + j) * kR + 16 * t + li], d[ct][t],
+                                                                        0, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = rt * 64 + 16 * wave + 4 * lg + i, r = r0 + 16 * t + li;
+                if (at < s.len && r < rank)
+                    e_part[(static_cast<int64_t>(blockIdx.y) * batch + s.start + at) * rank + r] = factor * e[t][i];
+            }
+    }
+    if (!db_part) return;
+#pragma unroll
+    for (int ct = 0; ct < kColsY / 64; ++ct)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = base + ct * 64 + 16 * wave + 4 * lg + i, r = r0 + 16 * t + li;
+                if (o < n_out && r < rank)
+                    db_part[(static_cast<int64_t>(blockIdx.x) * n_out + o) * rank + r] = d[ct][t][i];
+            }
+}
+
+// dX and partial dA of one block of rows and 128 columns of X. A value of X is
+// used once, so it goes straight to the lane that multiplies it.
+template <typename TX, typename TW, int RT>
+__global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW* A, const float* E, const int* order,
+                                                          const Slot* slots, int n_in, int rank, float* dX,
+                                                          float* da_part) {
+    __shared__ int row_of[kMaxRows];
+    const Slot s = slots[blockIdx.x];
+    if (s.len == 0) return;
+    constexpr int kTiles = kColsX / 64;
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, li = lane % 16, lg = lane / 16;
+    const TW* a = A + static_cast<int64_t>(s.adapter) * rank * n_in;
+    const bool wide = n_in % 4 == 0 && reinterpret_cast<uintptr_t>(dX) % 16 == 0;
+    const int row_tiles = (s.len + 63) / 64, base = blockIdx.y * kColsX;
+    for (int i = tid; i < kMaxRows; i += kThreads) row_of[i] = order[s.start + min(i, s.len - 1)];
+    __syncthreads();
+    for (int r0 = 0; r0 < rank; r0 += 16 * RT) {
+        // A[r][k] of the workgroup's columns, for dX
+        float av[kTiles][RT][4];
+#pragma unroll
+        for (int ct = 0; ct < kTiles; ++ct)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = r0 + 16 * t + 4 * lg + j, k = base + ct * 64 + 16 * wave + li;
+                    av[ct][t][j] = value_at(a, r, n_in, k, r < rank && k < n_in);
+                }
+        f32x4 d[kTiles][RT];
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) d[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int rt = 0; rt < row_tiles; ++rt) {
+            if (da_part) {
+                float en[RT][16];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int at = rt * 64 + 16 * lg + j, r = r0 + 16 * t + li;
+                        en[t][j] = value_at(E, s.start + at, rank, r, at < s.len && r < rank);
+                    }
+#pragma unroll
+                for (int ct = 0; ct < kTiles; ++ct) {
+                    const int k = base + ct * 64 + 16 * wave + li;
+                    float x[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int at = rt * 64 + 16 * lg + j;
+                        x[j] = value_at(X, row_of[at], n_in, k, at < s.len && k < n_in);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+                            d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(en[t][j], x[j], d[ct][t], 0, 0, 0);
+                }
+            }
+            if (dX) {
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const int at = rt * 64 + 16 * nt + li;
+                    float ev[RT][4];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = r0 + 16 * t + 4 * lg + j;
+                            ev[t][j] = value_at(E, s.start + at, rank, r, at < s.len && r < rank);
+                        }
+                    float* row = dX + static_cast<int64_t>(row_of[at]) * n_in;
+#pragma unroll
+                    for (int ct = 0; ct < kTiles; ++ct) {
+                        // lane: columns k .. k + 3 of its row
+                        const int k = base + ct * 64 + 16 * wave + 4 * lg;
+                        const int valid = at < s.len ? n_in - k : 0;
+                        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (wide && valid >= 4) {
+                            acc = *reinterpret_cast<const f32x4*>(row + k);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < valid) acc[i] = row[k + i];
+                        }
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(av[ct][t][j], ev[t][j], acc, 0, 0, 0);
+                        if (wide && valid >= 4) {
+                            *reinterpret_cast<f32x4*>(row + k) = acc;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < valid) row[k + i] = acc[i];
+                        }
+                    }
+                }
+            }
+        }
+        if (da_part) {
+#pragma unroll
+            for (int ct = 0; ct < kTiles; ++ct)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 16 * t + 4 * lg + i;
+                        const int k = base + ct * 64 + 16 * wave + li;
+                        if (r < rank && k < n_in)
+                            da_part[(static_cast<int64_t>(blockIdx.x) * rank + r) * n_in + k] = d[ct][t][i];
+                    }
+        }
+    }
+}
+
+// E[i] = sum over the column ranges; `parts` planes of `stride` values.
+__global__ __launch_bounds__(kThreads) void sum_planes_kernel(const float* part, int64_t n, int64_t stride, int parts,
+                                                              float* out) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        float sum = 0.0f;
+        for (int p = 0; p < parts; ++p) sum += part[p * stride + i];
+        out[i] = sum;
+    }
+}
+
+// Gradient of one adapter's weights (`size` values each): the sum over its
+// blocks of rows, zeros without any.
+__global__ __launch_bounds__(kThreads) void sum_slots_kernel(const float* part, const Segment* segs, int64_t size,
+                                                             int block, float* out) {
+    const int g = blockIdx.y;
+    const Segment seg = segs[g];
+    const int s0 = first_slot(seg, g, block), blocks = (seg.len + block - 1) / block;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < size;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        float sum = 0.0f;
+        for (int b = 0; b < blocks; ++b) sum += part[(s0 + b) * size + i];
+        out[g * size + i] = sum;
+    }
+}
+
+struct Layout {
+    size_t order, segs, slots, e, e_part, w_part, total;
+    int block, n_slots, splits;
+};
+
+// Rows of a block: as many as leave each pass about two workgroups a compute
+// unit of the card's 256 (fewer partial sums against more of the card busy).
+int block_rows(int n_in, int n_out, int64_t batch) {
+    int block = kMaxRows;
+    while (block > 64 && (batch / block * ((n_out + kColsY - 1) / kColsY) < 512 ||
+                          batch / block * ((n_in + kColsX - 1) / kColsX) < 256))
+        block /= 2;
+    return block;
+}
+
+Layout layout_of(int n_in, int n_out, int rank, int count, int64_t batch) {
+    Layout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    l.block = block_rows(n_in, n_out, batch);
+    l.n_slots = static_cast<int>(batch / l.block) + count;
+    l.splits = (n_out + kColsY - 1) / kColsY;
+    l.order = take(static_cast<size_t>(batch) * 4);
+    l.segs = take(static_cast<size_t>(count) * sizeof(Segment));
+    l.slots = take(static_cast<size_t>(l.n_slots) * sizeof(Slot));
+    l.e = take(static_cast<size_t>(batch) * rank * 4);
+    l.e_part = take(l.splits > 1 ? static_cast<size_t>(l.splits) * batch * rank * 4 : 0);
+    // dB's partial sums are added before dA's are written
+    l.w_part = take(static_cast<size_t>(l.n_slots) * rank * std::max(n_in, n_out) * 4);
+    l.total = at;
+    return l;
+}
+
+template <typename TX, typename TW, int RT>
+ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX, float* dA, float* dB,
+                char* ws) {
+    const Layout l = layout_of(c.n_in, c.n_out, c.rank, c.count, c.batch);
+    int* order = reinterpret_cast<int*>(ws + l.order);
+    Segment* segs = reinterpret_cast<Segment*>(ws + l.segs);
+    Slot* slots = reinterpret_cast<Slot*>(ws + l.slots);
+    float* E = reinterpret_cast<float*>(ws + l.e);
+    float* e_part = l.splits > 1 ? reinterpret_cast<float*>(ws + l.e_part) : E;
+    float* w_part = reinterpret_cast<float*>(ws + l.w_part);
+    const TW* A = static_cast<const TW*>(c.A);
+    const TW* B = static_cast<const TW*>(c.B);
+    ks_status_t st = launch_kernel(sort_kernel, dim3(static_cast<unsigned>(c.count)), dim3(1024), 0, c.stream, c.ids,
+                                   static_cast<int>(c.batch), c.count, l.block, order, segs, slots, l.n_slots);
+    if (st != KS_OK) return st;
+    auto blocks_for = [](int64_t n) {
+        return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 16384));
+    };
+    if (c.batch > 0) {
+        const dim3 gy(static_cast<unsigned>(l.n_slots), static_cast<unsigned>(l.splits),
+                      static_cast<unsigned>((c.rank + 16 * RT - 1) / (16 * RT)));
+        st = launch_kernel(grad_y_kernel<TW, RT>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
+                           c.batch, c.n_out, c.rank, e_part, dB ? w_part : static_cast<float*>(nullptr));
+        if (st != KS_OK) return st;
+        if (l.splits > 1) {
+            const int64_t n = c.batch * c.rank;
+            st = launch_kernel(sum_planes_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, c.stream, e_part, n, n,
+                               l.splits, E);
+            if (st != KS_OK) return st;
+        }
+    }
+    if (dB) {
+        const int64_t size = static_cast<int64_t>(c.n_out) * c.rank;
+        st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
+                           c.stream, w_part, segs, size, l.block, dB);
+        if (st != KS_OK) return st;
+    }
+    if (c.batch > 0) {
+        const dim3 gx(static_cast<unsigned>(l.n_slots), static_cast<unsigned>((c.n_in + kColsX - 1) / kColsX));
+        st = launch_kernel(grad_x_kernel<TX, TW, RT>, gx, dim3(kThreads), 0, c.stream, static_cast<const TX*>(X), A, E,
+                           order, slots, c.n_in, c.rank, dX, dA ? w_part : static_cast<float*>(nullptr));
+        if (st != KS_OK) return st;
+    }
+    if (dA) {
+        const int64_t size = static_cast<int64_t>(c.n_in) * c.rank;
+        st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
+                           c.stream, w_part, segs, size, l.block, dA);
+    }
+    return st;
+}
+
+template <typename TX, typename TW>
+ks_status_t run_rank(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX, float* dA,
+                     float* dB, char* ws) {
+    if (c.rank <= 16) return run<TX, TW, 1>(c, dY, X, H, dX, dA, dB, ws);
+    return run<TX, TW, 2>(c, dY, X, H, dX, dA, dB, ws);
+}
+
+}  // namespace
+
+size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch) {
+    return layout_of(n_in, n_out, rank, count, batch).total;
+}
+
+ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,
+                                float* dA, float* dB, void* ws) {
+    char* w = static_cast<char*>(ws);
+    if (c.xt == kBF16) return run_rank<bf16_t, bf16_t>(c, dY, X, H, dX, dA, dB, w);
+    if (c.wt == kBF16) return run_rank<float, bf16_t>(c, dY, X, H, dX, dA, dB, w);
+    return run_rank<float, float>(c, dY, X, H, dX, dA, dB, w);
+}
+
+}  // namespace ks

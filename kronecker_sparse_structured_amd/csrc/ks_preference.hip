@@ -1,0 +1,388 @@
+// ks_preference.hip -- log probabilities of labelled tokens, the paired
+// preference loss on them, and its gradient with respect to the logits.
+//
+//   l = x[label] - log sum_v exp x[v]          for each unmasked row
+//   R[s] = beta sum_t (l - ref),  z_i = R[i] - R[P + i]
+//   loss = mean (1-e) log(1 + exp(-z)) + e log(1 + exp(z))
+//   dx[v] = c[s] (1[v = label] - exp(x[v] - max) / sum)
+//
+// A row of logits is 8 KB to 200 KB and everything else is small, so the work
+// is one stream over the logits for l and a second one for dx: the gradient's
+// factor c[s] depends on every row of both sequences of a pair, so no row can
+// be finished in the first stream. The caller runs ranges of pairs whose
+// logits fit the last cache, so that the second stream does not come from HBM.
+//
+// One workgroup a row. The maximum and the sum of exponentials are kept
+// together in one pass: each lane keeps its own running pair (m, s), rescales
+// s when m grows, and the lanes' pairs are joined at the end. Rows start at
+// any element (an odd vocabulary in bf16 puts them at any even byte), so a
+// row's head up to the next 16-byte boundary and its tail go element-wise and
+// the rest in 16-byte loads.
+//
+// exp(x - m) is exp2((x - m) log2 e): the difference is taken first, so that a
+// maximum at the type's lowest value (a fully masked vocabulary) cannot
+// overflow. The logarithm and l are settled in double, once a row.
+
+#include <algorithm>
+
+#include "ks_device.h"
+#include "ks_train.h"
+
+namespace ks {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLowest = -3.402823466e38f;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));   // elements in 16 bytes
+
+template <typename T>
+__device__ __forceinline__ void widen(u32x4 w, float (&x)[kVec<T>]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            x[i] = __uint_as_float(w[i]);
+        } else {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    return x != x ? 0x7fc0u : r;
+}
+
+template <typename T>
+__device__ __forceinline__ T narrow(float x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else return static_cast<bf16_t>(bf16_bits(x));
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 pack(const float (&x)[kVec<T>]) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+        else w[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+    }
+    return w;
+}
+
+// Elements before the first 16-byte boundary at or after p, at most n.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int n) {
+    const int bytes = static_cast<int>((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16);
+    return min(n, bytes / static_cast<int>(sizeof(T)));
+}
+
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+struct Rows {
+    ks_logits_t x;
+    int64_t s0, half;   // block of sequences [s0, s0 + n) and, beside it, + half
+    int n;              // sequences in the first block
+};
+
+// The sequence and position of a row number of the launch.
+__device__ __forceinline__ void row_of(const Rows& r, int64_t row, int64_t* s, int64_t* t) {
+    const int64_t q = row / r.x.tokens;
+    *t = row - q * r.x.tokens;
+    *s = q < r.n ? r.s0 + q : r.s0 + r.half + (q - r.n);
+}
+
+// Joins (m2, s2) to (m, s).
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    s = s * exp_of(m - top) + s2 * exp_of(m2 - top);
+    m = top;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void token_logp_kernel(const Rows r, float* tokens, float* stats) {
+    __shared__ float wave_m[kWaves], wave_s[kWaves];
+    constexpr int E = kVec<T>;
+    int64_t s_, t_;
+    row_of(r, blockIdx.x, &s_, &t_);
+    const int64_t at = s_ * r.x.tokens + t_;
+    const int64_t label = r.x.labels[s_ * r.x.label_stride + t_];
+    if (label < 0) {
+        if (threadIdx.x == 0) {
+            tokens[at] = 0.0f;
+            if (stats) {
+                stats[2 * at] = 0.0f;
+                stats[2 * at + 1] = 1.0f;
+            }
+        }
+        return;
+    }
+    const T* row = static_cast<const T*>(r.x.data) + s_ * r.x.seq_stride + t_ * r.x.row_stride;
+    const int V = static_cast<int>(r.x.vocab);
+    const int head = head_of(row, V);
+    const int vecs = (V - head) / E;
+    const int tail = head + vecs * E;
+    const u32x4* body = reinterpret_cast<const u32x4*>(row + head);
+    // the maximum starts at the lowest finite value: a row of -inf then sums to
+    // 0 instead of computing inf - inf on the way
+    float m = kLowest, s = 0.0f;
+    const int tid = threadIdx.x;
+    if (tid < head) {
+        const float x = to_f32(row[tid]);
+        join(m, s, fmaxf(x, kLowest), exp_of(x - fmaxf(x, kLowest)));
+    }
+    if (tid < V - tail) {
+        const float x = to_f32(row[tail + tid]);
+        join(m, s, fmaxf(x, kLowest), exp_of(x - fmaxf(x, kLowest)));
+    }
+    constexpr int U = 4;    // vectors in flight a lane
+    int v = tid;
+    for (; v + (U - 1) * kThreads < vecs; v += U * kThreads) {
+        u32x4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = body[v + u * kThreads];
+        float x[U][E], top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            widen<T>(w[u], x[u]);
+#pragma unroll
+            for (int i = 0; i < E; ++i) top = fmaxf(top, x[u][i]);
+        }
+        s *= exp_of(m - top);
+        m = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float part = 0.0f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) part += exp_of(x[u][i] - m);
+            s += part;
+        }
+    }
+    for (; v < vecs; v += kThreads) {
+        float x[E], top = m;
+        widen<T>(body[v], x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) top = fmaxf(top, x[i]);
+        s *= exp_of(m - top);
+        m = top;
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) part += exp_of(x[i] - m);
+        s += part;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float m2 = __shfl_xor(m, d, 64), s2 = __shfl_xor(s, d, 64);
+        join(m, s, m2, s2);
+    }
+    if (tid % 64 == 0) {
+        wave_m[tid / 64] = m;
+        wave_s[tid / 64] = s;
+    }
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) join(m, s, wave_m[w], wave_s[w]);
+        const float x = label < r.x.vocab ? to_f32(row[label]) : __builtin_nanf("");
+        tokens[at] = static_cast<float>((static_cast<double>(x) - static_cast<double>(m)) -
+                                        log(static_cast<double>(s)));
+        if (stats) {
+            stats[2 * at] = m;
+            stats[2 * at + 1] = s;
+        }
+    }
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+
+// total[s] = sum_t tokens: one wave a sequence.
+__global__ __launch_bounds__(kThreads) void sequence_sum_kernel(const float* tokens, int64_t T, int64_t S, float* total) {
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / 64;
+    if (s >= S) return;
+    double x = 0.0;
+    for (int64_t t = threadIdx.x % 64; t < T; t += 64) x += static_cast<double>(tokens[s * T + t]);
+    x = wave_sum(x);
+    if (threadIdx.x % 64 == 0) total[s] = static_cast<float>(x);
+}
+
+__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+
+// Rewards and gradient factors of pairs [p0, p0 + n), a wave a pair; with the
+// last range the loss over all pairs, from the rewards. One workgroup: a few
+// thousand values beside megabytes of logits.
+__global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, int64_t p0, int64_t n, const float* tokens,
+                                                         const float* ref, int64_t ref_stride, float beta,
+                                                         float smoothing, float* loss, float* rewards, float* grad) {
+    __shared__ double sums[16];
+    const int64_t P = x.sequences / 2, T = x.tokens;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    for (int64_t p = p0 + wave; p < p0 + n; p += 16) {
+        double R[2];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const int64_t s = p + side * P;
+            double sum = 0.0;
+            for (int64_t t = lane; t < T; t += 64) {
+                if (x.labels[s * x.label_stride + t] >= 0)
+                    sum += static_cast<double>(tokens[s * T + t]) - static_cast<double>(ref[s * ref_stride + t]);
+            }
+            R[side] = static_cast<double>(beta) * wave_sum(sum);
+        }
+        if (lane == 0) {
+            const double z = R[0] - R[1], e = smoothing;
+            const double up = 1.0 / (1.0 + exp(-z)), un = 1.0 / (1.0 + exp(z));
+            const double c = static_cast<double>(beta) * (e * up - (1.0 - e) * un) / static_cast<double>(P);
+            rewards[p] = static_cast<float>(R[0]);
+            rewards[p + P] = static_cast<float>(R[1]);
+            grad[p] = static_cast<float>(c);
+            grad[p + P] = static_cast<float>(-c);
+        }
+    }
+    if (p0 + n < P) return;
+    __threadfence_block();
+    __syncthreads();
+    double sum = 0.0;
+    for (int64_t p = threadIdx.x; p < P; p += 1024) {
+        const double z = static_cast<double>(rewards[p]) - static_cast<double>(rewards[p + P]), e = smoothing;
+        sum += (1.0 - e) * softplus(-z) + e * softplus(z);
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < 16; ++w) total += sums[w];
+        *loss = P > 0 ? static_cast<float>(total / static_cast<double>(P)) : 0.0f;
+    }
+}
+
+// dx of one row. The output row may start at another place of a 16-byte
+// granule than the input row: then it goes element-wise.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logit_grad_kernel(const Rows r, const float* stats, const float* grad,
+                                                              const float* upstream, T* d, int64_t d_seq,
+                                                              int64_t d_row) {
+    constexpr int E = kVec<T>;
+    int64_t s_, t_;
+    row_of(r, blockIdx.x, &s_, &t_);
+    const int64_t at = s_ * r.x.tokens + t_;
+    const int64_t label = r.x.labels[s_ * r.x.label_stride + t_];
+    const T* row = static_cast<const T*>(r.x.data) + s_ * r.x.seq_stride + t_ * r.x.row_stride;
+    T* out = d + s_ * d_seq + t_ * d_row;
+    const int V = static_cast<int>(r.x.vocab);
+    const int head = head_of(out, V);
+    const int vecs = (V - head) / E;
+    const int tail = head + vecs * E;
+    u32x4* obody = reinterpret_cast<u32x4*>(out + head);
+    const int tid = threadIdx.x;
+    if (label < 0) {
+        if (tid < head) out[tid] = narrow<T>(0.0f);
+        if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
+        const u32x4 none = {0u, 0u, 0u, 0u};
+        for (int v = tid; v < vecs; v += kThreads) obody[v] = none;
+        return;
+    }
+    const float m = stats[2 * at];
+    float c = grad[s_];
+    if (upstream) c *= *upstream;
+    const float scale = -c / stats[2 * at + 1];
+    // a label outside the vocabulary has no place to go: the whole row says so
+    const float c_label = label < r.x.vocab ? c : __builtin_nanf("");
+    const int place = label < r.x.vocab ? static_cast<int>(label) : 0;
+    auto one = [&](int v) {
+        float y = scale * exp_of(to_f32(row[v]) - m);
+        if (v == place) y += c_label;
+        out[v] = narrow<T>(y);
+    };
+    if (tid < head) one(tid);
+    if (tid < V - tail) one(tail + tid);
+    if (head_of(row, V) != head) {
+        for (int v = head + tid; v < tail; v += kThreads) one(v);
+        return;
+    }
+    const u32x4* body = reinterpret_cast<const u32x4*>(row + head);
+    auto vec = [&](int v, u32x4 w) {
+        float x[E];
+        widen<T>(w, x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = scale * exp_of(x[i] - m);
+        const int in = place - head - v * E;
+        if (in >= 0 && in < E) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (i == in) x[i] += c_label;
+        }
+        obody[v] = pack<T>(x);
+    };
+    constexpr int U = 4;
+    int v = tid;
+    for (; v + (U - 1) * kThreads < vecs; v += U * kThreads) {
+        u32x4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = body[v + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < U; ++u) vec(v + u * kThreads, w[u]);
+    }
+    for (; v < vecs; v += kThreads) vec(v, body[v]);
+}
+
+Rows rows_of(const LogitsCall& c, int64_t s0, int64_t n, int64_t half) {
+    Rows r;
+    r.x = c.x;
+    r.s0 = s0;
+    r.n = static_cast<int>(n);
+    r.half = half;
+    return r;
+}
+
+}  // namespace
+
+ks_status_t launch_token_logp(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, float* tokens, float* stats) {
+    const int64_t rows = (half ? 2 * n : n) * c.x.tokens;
+    if (rows == 0) return KS_OK;
+    const Rows r = rows_of(c, s0, n, half);
+    const dim3 grid(static_cast<unsigned>(rows));
+    return c.x.elem == KS_ELEM_BF16
+               ? launch_kernel(token_logp_kernel<bf16_t>, grid, dim3(kThreads), 0, c.stream, r, tokens, stats)
+               : launch_kernel(token_logp_kernel<float>, grid, dim3(kThreads), 0, c.stream, r, tokens, stats);
+}
+
+ks_status_t launch_sequence_sum(const LogitsCall& c, const float* tokens, float* total) {
+    if (c.x.sequences == 0) return KS_OK;
+    return launch_kernel(sequence_sum_kernel, dim3(static_cast<unsigned>((c.x.sequences + kWaves - 1) / kWaves)),
+                         dim3(kThreads), 0, c.stream, tokens, c.x.tokens, c.x.sequences, total);
+}
+
+ks_status_t launch_pair_loss(const LogitsCall& c, int64_t p0, int64_t n, const float* tokens, const float* ref,
+                             int64_t ref_stride, float beta, float smoothing, float* loss, float* rewards,
+                             float* grad) {
+    return launch_kernel(pair_loss_kernel, dim3(1), dim3(1024), 0, c.stream, c.x, p0, n, tokens, ref, ref_stride, beta,
+                         smoothing, loss, rewards, grad);
+}
+
+ks_status_t launch_logit_grad(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, const float* stats,
+                              const float* grad, const float* upstream, void* d, int64_t d_seq, int64_t d_row) {
+    const int64_t rows = (half ? 2 * n : n) * c.x.tokens;
+    if (rows == 0) return KS_OK;
+    const Rows r = rows_of(c, s0, n, half);
+    const dim3 grid(static_cast<unsigned>(rows));
+    if (c.x.elem == KS_ELEM_BF16)
+        return launch_kernel(logit_grad_kernel<bf16_t>, grid, dim3(kThreads), 0, c.stream, r, stats, grad, upstream,
+                             static_cast<bf16_t*>(d), d_seq, d_row);
+    return launch_kernel(logit_grad_kernel<float>, grid, dim3(kThreads), 0, c.stream, r, stats, grad, upstream,
+                         static_cast<float*>(d), d_seq, d_row);
+}
+
+}  // namespace ks

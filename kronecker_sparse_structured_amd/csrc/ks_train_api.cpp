@@ -1,0 +1,612 @@
+// ks_train_api.cpp -- the C ABI of the operators around the product: adapters
+// beside a projection, the preference loss, the optimizer step. Validation is
+// pure host code and returns before any HIP call, as in ks_api.cpp; see
+// include/ks.h for the operations.
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "ks_train.h"
+
+namespace {
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+
+// The integer a C caller passed for an enum parameter (any int is allowed
+// there in C; loading it as the enum type would be undefined).
+template <typename E>
+int enum_value(const E* e) {
+    static_assert(sizeof(E) == sizeof(int), "C enums are int-sized");
+    int v;
+    std::memcpy(&v, e, sizeof v);
+    return v;
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Half-open byte ranges [p, p + pb) and [q, q + qb) intersect.
+bool overlap(const void* p, uint64_t pb, const void* q, uint64_t qb) {
+    if (!p || !q || pb == 0 || qb == 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + qb && b < a + pb;
+}
+
+struct Range {
+    const void* p;
+    uint64_t bytes;
+};
+
+// Whether range i of `written` meets a later one of it or one of `read`.
+bool any_overlap(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    for (const Range* w = written.begin(); w != written.end(); ++w) {
+        for (const Range* v = w + 1; v != written.end(); ++v)
+            if (overlap(w->p, w->bytes, v->p, v->bytes)) return true;
+        for (const Range& r : read)
+            if (overlap(w->p, w->bytes, r.p, r.bytes)) return true;
+    }
+    return false;
+}
+
+size_t round256(uint64_t bytes) { return static_cast<size_t>((bytes + 255) / 256 * 256); }
+
+ks_status_t current_cus(int* cus) {
+    static std::mutex mu;
+    static std::vector<int> cache;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return KS_ERR_HIP;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= static_cast<int>(cache.size())) cache.resize(dev + 1, 0);
+    if (cache[dev] == 0 &&
+        (hipDeviceGetAttribute(&cache[dev], hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cache[dev] <= 0)) {
+        cache[dev] = 0;
+        return KS_ERR_HIP;
+    }
+    *cus = cache[dev];
+    return KS_OK;
+}
+
+// ---------------------------------------------------------------- adapters
+
+ks_status_t adapter_types(int dt, int* xt, int* wt) {
+    switch (dt) {
+        case KS_DTYPE_F32: *xt = ks::kF32; *wt = ks::kF32; return KS_OK;
+        case KS_DTYPE_BF16: *xt = ks::kBF16; *wt = ks::kBF16; return KS_OK;
+        case KS_DTYPE_BF16W: *xt = ks::kF32; *wt = ks::kBF16; return KS_OK;
+        default: return KS_ERR_DTYPE;
+    }
+}
+
+ks_status_t check_adapters(const ks_adapters_t* ad, int64_t batch) {
+    if (!ad) return KS_ERR_NULL;
+    if (batch < 0 || batch >= kLimit) return KS_ERR_BATCH;
+    if (ad->rank < 1 || ad->rank > KS_ADAPTER_MAX_RANK || ad->count < 1 || ad->count > KS_ADAPTER_MAX_COUNT)
+        return KS_ERR_INVALID;
+    if (ad->n_in < 1 || ad->n_out < 1 || ad->n_in >= kLimit || ad->n_out >= kLimit) return KS_ERR_INVALID;
+    if (ad->rank * ad->n_in >= kLimit || ad->rank * ad->n_out >= kLimit) return KS_ERR_INVALID;
+    if (ad->count * ad->rank * ad->n_in >= kLimit || ad->count * ad->rank * ad->n_out >= kLimit) return KS_ERR_INVALID;
+    if (batch * ad->rank >= kLimit) return KS_ERR_INVALID;
+    return KS_OK;
+}
+
+uint64_t a_bytes(const ks_adapters_t* ad, int wt) {
+    return static_cast<uint64_t>(ad->count) * ad->rank * ad->n_in * ks::elem_bytes(wt);
+}
+uint64_t b_bytes(const ks_adapters_t* ad, int wt) {
+    return static_cast<uint64_t>(ad->count) * ad->rank * ad->n_out * ks::elem_bytes(wt);
+}
+
+ks::AdapterCall adapter_call(const ks_adapters_t* ad, const int32_t* ids, int xt, int wt, int64_t batch,
+                             hipStream_t stream, int cus) {
+    ks::AdapterCall c;
+    c.A = ad->A; c.B = ad->B; c.scale = ad->scale; c.ids = ids;
+    c.n_in = static_cast<int>(ad->n_in); c.n_out = static_cast<int>(ad->n_out);
+    c.rank = ad->rank; c.count = ad->count;
+    c.xt = xt; c.wt = wt; c.batch = batch; c.stream = stream; c.num_cus = cus;
+    return c;
+}
+
+// Pointers of the adapters and of a forward call (batch > 0).
+ks_status_t check_forward(const ks_adapters_t* ad, const int32_t* ids, const void* X, const float* Y, const float* H,
+                          int64_t batch, int xt, int wt) {
+    if (!ad->A || !ad->B || !ad->scale || !ids || !X || !Y) return KS_ERR_NULL;
+    if (!aligned(ad->A, ks::elem_bytes(wt)) || !aligned(ad->B, ks::elem_bytes(wt)) || !aligned(ad->scale, 4) ||
+        !aligned(ids, 4) || !aligned(X, ks::elem_bytes(xt)) || !aligned(Y, 4) || !aligned(H, 4))
+        return KS_ERR_ALIGN;
+    const uint64_t n = static_cast<uint64_t>(batch);
+    if (any_overlap({{Y, n * ad->n_out * 4}, {H, n * ad->rank * 4}},
+                    {{X, n * ad->n_in * ks::elem_bytes(xt)}, {ids, n * 4}, {ad->A, a_bytes(ad, wt)},
+                     {ad->B, b_bytes(ad, wt)}, {ad->scale, static_cast<uint64_t>(ad->count) * 4}}))
+        return KS_ERR_OVERLAP;
+    return KS_OK;
+}
+
+ks_status_t check_backward(const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X, const float* H,
+                           const float* dX, const float* dA, const float* dB, int64_t batch, int xt, int wt,
+                           const void* ws, size_t need) {
+    if (!dA != !dB) return KS_ERR_NULL;
+    const uint64_t n = static_cast<uint64_t>(batch);
+    if (batch > 0) {
+        if (!ad->A || !ad->B || !ad->scale || !ids || !dY) return KS_ERR_NULL;
+        if (dA && (!X || !H)) return KS_ERR_NULL;
+        if (!aligned(ad->A, ks::elem_bytes(wt)) || !aligned(ad->B, ks::elem_bytes(wt)) || !aligned(ad->scale, 4) ||
+            !aligned(ids, 4) || !aligned(dY, 4) || !aligned(X, ks::elem_bytes(xt)) || !aligned(H, 4))
+            return KS_ERR_ALIGN;
+    }
+    if (!aligned(dX, 4) || !aligned(dA, 4) || !aligned(dB, 4) || !aligned(ws, 16)) return KS_ERR_ALIGN;
+    if (any_overlap({{dX, n * ad->n_in * 4},
+                     {dA, static_cast<uint64_t>(ad->count) * ad->rank * ad->n_in * 4},
+                     {dB, static_cast<uint64_t>(ad->count) * ad->rank * ad->n_out * 4},
+                     {ws, need}},
+                    {{X, n * ad->n_in * ks::elem_bytes(xt)}, {H, n * ad->rank * 4}, {dY, n * ad->n_out * 4},
+                     {ids, n * 4}, {ad->A, a_bytes(ad, wt)}, {ad->B, b_bytes(ad, wt)},
+                     {ad->scale, static_cast<uint64_t>(ad->count) * 4}}))
+        return KS_ERR_OVERLAP;
+    return KS_OK;
+}
+
+// Rows of a range: Y's part of it stays in the 256 MB last cache (with X's and
+// the chain's intermediate beside it) until the adapters have added to it.
+constexpr int64_t kRangeBytes = int64_t(64) << 20;
+
+int64_t range_rows(int64_t n_out, int64_t batch) {
+    int64_t rows = std::max<int64_t>(1, kRangeBytes / (n_out * 4));
+    rows = std::max<int64_t>(256, rows / 256 * 256);
+    return std::min(rows, batch);
+}
+
+ks_status_t chain_widths(const ks_pattern_t* p, int n, const ks_adapters_t* ad) {
+    const int64_t in = static_cast<int64_t>(p[0].a) * p[0].c * p[0].d;
+    const int64_t out = static_cast<int64_t>(p[n - 1].a) * p[n - 1].b * p[n - 1].d;
+    return in == ad->n_in && out == ad->n_out ? KS_OK : KS_ERR_CHAIN_MISMATCH;
+}
+
+// The chain's gradient goes factor by factor: dY is fp32, so the products run
+// with the weights' type alone.
+ks_dtype_t grad_dtype(int wt) { return wt == ks::kBF16 ? KS_DTYPE_BF16W : KS_DTYPE_F32; }
+
+struct ChainGrad {
+    size_t factor_ws;      // transposed blocks of one factor
+    size_t buffer;         // one intermediate
+    int buffers;
+    size_t adapter_ws;
+    size_t total;
+};
+
+ks_status_t chain_grad(const ks_pattern_t* p, int n, const ks_adapters_t* ad, int64_t batch, int dt, ChainGrad* out) {
+    size_t bytes = 0;
+    // the chain's own checks of patterns, batch and type
+    ks_status_t st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(dt), KS_CHAIN_NO_FUSE, &bytes);
+    if (st != KS_OK) return st;
+    st = check_adapters(ad, batch);
+    if (st != KS_OK) return st;
+    st = chain_widths(p, n, ad);
+    if (st != KS_OK) return st;
+    int xt = 0, wt = 0;
+    st = adapter_types(dt, &xt, &wt);
+    if (st != KS_OK) return st;
+    uint64_t widest = 0;
+    out->factor_ws = 0;
+    for (int k = 0; k < n; ++k) {
+        st = ks_matmul_dx_workspace_size(p[k], grad_dtype(wt), &bytes);
+        if (st != KS_OK) return st;
+        out->factor_ws = std::max(out->factor_ws, bytes);
+        if (k > 0) widest = std::max<uint64_t>(widest, static_cast<uint64_t>(p[k].a) * p[k].c * p[k].d);
+    }
+    out->buffers = n <= 1 ? 0 : (n == 2 ? 1 : 2);
+    out->buffer = round256(widest * static_cast<uint64_t>(batch) * 4);
+    st = ks_adapter_backward_workspace_size(ad, batch, &out->adapter_ws);
+    if (st != KS_OK) return st;
+    // the adapters run after the chain, over the same memory
+    out->total = std::max(out->factor_ws + out->buffers * out->buffer, out->adapter_ws);
+    return KS_OK;
+}
+
+// ---------------------------------------------------------------- logits
+
+ks_status_t check_logits(const ks_logits_t* x) {
+    if (!x) return KS_ERR_NULL;
+    if (x->elem != KS_ELEM_F32 && x->elem != KS_ELEM_BF16) return KS_ERR_DTYPE;
+    if (x->reserved != 0) return KS_ERR_INVALID;
+    if (x->sequences < 0 || x->tokens < 0 || x->vocab < 1) return KS_ERR_INVALID;
+    if (x->sequences >= kLimit || x->tokens >= kLimit || x->vocab >= kLimit) return KS_ERR_INVALID;
+    if (x->sequences * x->tokens >= kLimit) return KS_ERR_INVALID;
+    if (x->row_stride < x->vocab || x->label_stride < x->tokens) return KS_ERR_INVALID;
+    if (x->row_stride >= kLimit || x->label_stride >= kLimit) return KS_ERR_INVALID;
+    if (x->tokens > 0 && x->seq_stride < (x->tokens - 1) * x->row_stride + x->vocab) return KS_ERR_INVALID;
+    if (x->seq_stride >= (int64_t(1) << 40)) return KS_ERR_INVALID;
+    if (x->sequences > 0 && x->tokens > 0) {
+        if (!x->data || !x->labels) return KS_ERR_NULL;
+        if (!aligned(x->data, x->elem == KS_ELEM_BF16 ? 2 : 4) || !aligned(x->labels, 8)) return KS_ERR_ALIGN;
+    }
+    return KS_OK;
+}
+
+uint64_t span_bytes(int64_t seqs, int64_t seq, int64_t tokens, int64_t row, int64_t width, int size) {
+    if (seqs == 0 || tokens == 0) return 0;
+    return (static_cast<uint64_t>(seqs - 1) * seq + static_cast<uint64_t>(tokens - 1) * row + width) * size;
+}
+
+uint64_t logit_bytes(const ks_logits_t* x) {
+    return span_bytes(x->sequences, x->seq_stride, x->tokens, x->row_stride, x->vocab,
+                      x->elem == KS_ELEM_BF16 ? 2 : 4);
+}
+uint64_t label_bytes(const ks_logits_t* x) {
+    return span_bytes(x->sequences, x->label_stride, 1, 0, x->tokens, 8);
+}
+
+ks_status_t check_dlogits(const ks_logits_t* x, const void* d, int64_t d_seq, int64_t d_row) {
+    if (d_row < x->vocab || d_row >= kLimit || d_seq >= (int64_t(1) << 40)) return KS_ERR_INVALID;
+    if (x->tokens > 0 && d_seq < (x->tokens - 1) * d_row + x->vocab) return KS_ERR_INVALID;
+    if (!aligned(d, x->elem == KS_ELEM_BF16 ? 2 : 4)) return KS_ERR_ALIGN;
+    return KS_OK;
+}
+
+uint64_t dlogit_bytes(const ks_logits_t* x, int64_t d_seq, int64_t d_row) {
+    return span_bytes(x->sequences, d_seq, x->tokens, d_row, x->vocab, x->elem == KS_ELEM_BF16 ? 2 : 4);
+}
+
+// Logits and their gradient may be the same memory with the same strides.
+bool in_place(const ks_logits_t* x, const void* d, int64_t d_seq, int64_t d_row) {
+    return d == x->data && d_row == x->row_stride && (x->sequences <= 1 || d_seq == x->seq_stride);
+}
+
+// Pairs of a range: both sequences' logits and their gradient's lines stay in
+// the 256 MB last cache between the two passes.
+constexpr int64_t kPairBytes = int64_t(96) << 20;
+
+// ---------------------------------------------------------------- optimizer
+
+ks_status_t check_tensors(const ks_adamw_tensor_t* t, int n) {
+    if (n < 0) return KS_ERR_INVALID;
+    if (n > 0 && !t) return KS_ERR_NULL;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].n < 0 || t[i].n >= kLimit) return KS_ERR_INVALID;
+        if (t[i].g_elem != KS_ELEM_F32 && t[i].g_elem != KS_ELEM_BF16) return KS_ERR_DTYPE;
+        total += t[i].n;
+    }
+    return total >= (int64_t(1) << 44) ? KS_ERR_INVALID : KS_OK;
+}
+
+int elem_size(int e) { return e == KS_ELEM_BF16 ? 2 : 4; }
+
+// State pointers of an 8- or 32-bit tensor; p and g as well if `step`.
+ks_status_t check_states(const ks_adamw_tensor_t& t, int bits, bool step) {
+    if (t.n == 0) return KS_OK;
+    if (step && (!t.p || !t.g)) return KS_ERR_NULL;
+    if (step && t.p_elem != KS_ELEM_F32 && t.p_elem != KS_ELEM_BF16) return KS_ERR_DTYPE;
+    if (!t.m || !t.v || (bits == 8 && !t.scales)) return KS_ERR_NULL;
+    const int size = bits == 8 ? 1 : 4;
+    if (!aligned(t.m, size) || !aligned(t.v, size) || (bits == 8 && !aligned(t.scales, 4))) return KS_ERR_ALIGN;
+    if (step && (!aligned(t.p, elem_size(t.p_elem)) || !aligned(t.g, elem_size(t.g_elem)))) return KS_ERR_ALIGN;
+    if (!step) return KS_OK;
+    const uint64_t n = static_cast<uint64_t>(t.n);
+    return any_overlap({{t.p, n * elem_size(t.p_elem)}, {t.m, n * size}, {t.v, n * size},
+                        {bits == 8 ? t.scales : nullptr, (n + 255) / 256 * 8}},
+                       {{t.g, n * elem_size(t.g_elem)}})
+               ? KS_ERR_OVERLAP
+               : KS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const void* X, float* Y, float* H,
+                              int64_t batch, ks_dtype_t dt, hipStream_t stream) {
+    ks_status_t st = check_adapters(ad, batch);
+    if (st != KS_OK) return st;
+    int xt = 0, wt = 0;
+    st = adapter_types(enum_value(&dt), &xt, &wt);
+    if (st != KS_OK) return st;
+    if (batch == 0) return KS_OK;
+    if (!H) return KS_ERR_NULL;
+    st = check_forward(ad, ids, X, Y, H, batch, xt, wt);
+    if (st != KS_OK) return st;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != KS_OK) return st;
+    const ks::AdapterCall c = adapter_call(ad, ids, xt, wt, batch, stream, cus);
+    if (ks::adapter_one_launch(batch)) return ks::launch_adapter_rows(c, X, Y, H);
+    st = ks::launch_adapter_down(c, X, H);
+    return st != KS_OK ? st : ks::launch_adapter_up(c, H, Y);
+}
+
+ks_status_t ks_adapter_backward_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    const ks_status_t st = check_adapters(ad, batch);
+    if (st != KS_OK) return st;
+    *bytes = ks::adapter_grad_workspace(static_cast<int>(ad->n_in), static_cast<int>(ad->n_out), ad->rank, ad->count,
+                                        batch);
+    return KS_OK;
+}
+
+ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X,
+                                const float* H, float* dX, float* dA, float* dB, int64_t batch, ks_dtype_t dt,
+                                void* ws, size_t ws_bytes, hipStream_t stream) {
+    size_t need = 0;
+    ks_status_t st = ks_adapter_backward_workspace_size(ad, batch, &need);
+    if (st != KS_OK) return st;
+    int xt = 0, wt = 0;
+    st = adapter_types(enum_value(&dt), &xt, &wt);
+    if (st != KS_OK) return st;
+    if (!dA && !dB && (batch == 0 || !dX)) return KS_OK;
+    if (!ws || ws_bytes < need) return KS_ERR_WORKSPACE;
+    st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, need);
+    if (st != KS_OK) return st;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != KS_OK) return st;
+    return ks::launch_adapter_grad(adapter_call(ad, ids, xt, wt, batch, stream, cus), dY, X, H, dX, dA, dB, ws);
+}
+
+ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad, int64_t batch,
+                                            ks_dtype_t dt, size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    size_t need = 0;
+    const int code = enum_value(&dt);
+    ks_status_t st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &need);
+    if (st != KS_OK) return st;
+    st = check_adapters(ad, batch);
+    if (st != KS_OK) return st;
+    st = chain_widths(p, n, ad);
+    if (st != KS_OK) return st;
+    const int64_t rows = range_rows(ad->n_out, batch);
+    st = ks_chain_workspace_size(p, n, rows, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &need);
+    if (st != KS_OK) return st;
+    // H, for callers that do not keep it
+    *bytes = round256(need) + (ks::adapter_one_launch(batch) ? 0 : round256(static_cast<uint64_t>(batch) * ad->rank * 4));
+    return KS_OK;
+}
+
+ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
+                                    const int32_t* ids, const void* X, float* Y, float* H, int64_t batch,
+                                    ks_dtype_t dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+    size_t need = 0;
+    const int code = enum_value(&dt);
+    ks_status_t st = ks_chain_adapter_workspace_size(p, n, ad, batch, static_cast<ks_dtype_t>(code), &need);
+    if (st != KS_OK) return st;
+    int xt = 0, wt = 0;
+    st = adapter_types(code, &xt, &wt);
+    if (st != KS_OK) return st;
+    if (batch == 0) return KS_OK;
+    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
+    st = check_forward(ad, ids, X, Y, H, batch, xt, wt);
+    if (st != KS_OK) return st;
+    if (need > 0 && any_overlap({{ws, need}},
+                                {{X, static_cast<uint64_t>(batch) * ad->n_in * ks::elem_bytes(xt)},
+                                 {Y, static_cast<uint64_t>(batch) * ad->n_out * 4},
+                                 {H, static_cast<uint64_t>(batch) * ad->rank * 4},
+                                 {ids, static_cast<uint64_t>(batch) * 4},
+                                 {ad->A, a_bytes(ad, wt)},
+                                 {ad->B, b_bytes(ad, wt)}}))
+        return KS_ERR_OVERLAP;
+    if (need > 0 && !aligned(ws, 16)) return KS_ERR_ALIGN;
+    const int64_t step = range_rows(ad->n_out, batch);
+    const bool one = ks::adapter_one_launch(batch);
+    size_t chain_ws = 0;
+    st = ks_chain_workspace_size(p, n, step, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
+    if (st != KS_OK) return st;
+    if (!one && !H) H = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(chain_ws));
+    int cus = 0;
+    for (int64_t r = 0; r < batch; r += step) {
+        const int64_t rows = std::min(step, batch - r);
+        const char* x = static_cast<const char*>(X) + r * ad->n_in * ks::elem_bytes(xt);
+        float* y = Y + r * ad->n_out;
+        // the chain's checks (weights, alignment, overlaps) come with its first range
+        st = ks_chain_matmul(p, n, W, x, y, rows, static_cast<ks_dtype_t>(code), ws, chain_ws, KS_CHAIN_AUTO, stream);
+        if (st != KS_OK) return st;
+        if (r == 0) {
+            st = current_cus(&cus);
+            if (st != KS_OK) return st;
+            // H for all rows at once, after the chain's checks: an argument
+            // error launches nothing
+            if (!one) st = ks::launch_adapter_down(adapter_call(ad, ids, xt, wt, batch, stream, cus), X, H);
+            if (st != KS_OK) return st;
+        }
+        const ks::AdapterCall c = adapter_call(ad, ids + r, xt, wt, rows, stream, cus);
+        st = one ? ks::launch_adapter_rows(c, x, y, H) : ks::launch_adapter_up(c, H + r * ad->rank, y);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
+ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
+                                                     int64_t batch, ks_dtype_t dt, size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    ChainGrad g;
+    const ks_status_t st = chain_grad(p, n, ad, batch, enum_value(&dt), &g);
+    if (st != KS_OK) return st;
+    *bytes = g.total;
+    return KS_OK;
+}
+
+ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
+                                      const int32_t* ids, const float* dY, const void* X, const float* H, float* dX,
+                                      float* dA, float* dB, int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes,
+                                      hipStream_t stream) {
+    ChainGrad g;
+    const int code = enum_value(&dt);
+    ks_status_t st = chain_grad(p, n, ad, batch, code, &g);
+    if (st != KS_OK) return st;
+    int xt = 0, wt = 0;
+    st = adapter_types(code, &xt, &wt);
+    if (st != KS_OK) return st;
+    if (batch > 0 && (!W || !dX)) return KS_ERR_NULL;
+    if (batch == 0 && !dA && !dB) return KS_OK;
+    if (!ws || ws_bytes < g.total) return KS_ERR_WORKSPACE;
+    st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, g.total);
+    if (st != KS_OK) return st;
+    char* base = static_cast<char*>(ws);
+    if (batch > 0) {
+        for (int k = 0; k < n; ++k) {
+            if (!W[k]) return KS_ERR_NULL;
+            const uint64_t bytes = static_cast<uint64_t>(p[k].a) * p[k].b * p[k].c * p[k].d * ks::elem_bytes(wt);
+            if (any_overlap({{dX, static_cast<uint64_t>(batch) * ad->n_in * 4}, {ws, g.total}}, {{W[k], bytes}}))
+                return KS_ERR_OVERLAP;
+        }
+        const float* cur = dY;
+        for (int k = n - 1; k >= 0; --k) {
+            float* out = k == 0 ? dX : reinterpret_cast<float*>(base + g.factor_ws + (k % 2) * (g.buffers - 1) * g.buffer);
+            st = ks_matmul_dx(p[k], W[k], cur, out, batch, grad_dtype(wt), base, g.factor_ws, stream);
+            if (st != KS_OK) return st;
+            cur = out;
+        }
+    }
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != KS_OK) return st;
+    return ks::launch_adapter_grad(adapter_call(ad, ids, xt, wt, batch, stream, cus), dY, X, H,
+                                   batch > 0 ? dX : nullptr, dA, dB, ws);
+}
+
+ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, float* stats, hipStream_t stream) {
+    const ks_status_t st = check_logits(x);
+    if (st != KS_OK) return st;
+    if (x->sequences == 0) return KS_OK;
+    const uint64_t rows = static_cast<uint64_t>(x->sequences) * x->tokens;
+    if (!total || (rows > 0 && !tokens)) return KS_ERR_NULL;
+    if (!aligned(tokens, 4) || !aligned(total, 4) || !aligned(stats, 4)) return KS_ERR_ALIGN;
+    if (any_overlap({{tokens, rows * 4}, {total, static_cast<uint64_t>(x->sequences) * 4}, {stats, rows * 8}},
+                    {{x->data, logit_bytes(x)}, {x->labels, label_bytes(x)}}))
+        return KS_ERR_OVERLAP;
+    const ks::LogitsCall c{*x, stream};
+    const ks_status_t run = ks::launch_token_logp(c, 0, x->sequences, 0, tokens, stats);
+    return run != KS_OK ? run : ks::launch_sequence_sum(c, tokens, total);
+}
+
+ks_status_t ks_preference_loss(const ks_logits_t* x, const float* ref, int64_t ref_stride, float beta, float smoothing,
+                               float* loss, float* rewards, float* tokens, float* grad, float* stats, void* dlogits,
+                               int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream) {
+    ks_status_t st = check_logits(x);
+    if (st != KS_OK) return st;
+    if (x->sequences % 2 != 0 || ref_stride < x->tokens || ref_stride >= kLimit) return KS_ERR_INVALID;
+    if (!(beta > 0.0f) || !std::isfinite(beta) || !(smoothing >= 0.0f) || !(smoothing <= 1.0f)) return KS_ERR_INVALID;
+    const uint64_t rows = static_cast<uint64_t>(x->sequences) * x->tokens;
+    if (!loss || (x->sequences > 0 && (!rewards || !grad)) || (rows > 0 && (!ref || !tokens || !stats)))
+        return KS_ERR_NULL;
+    if (!aligned(loss, 4) || !aligned(rewards, 4) || !aligned(grad, 4) || !aligned(ref, 4) || !aligned(tokens, 4) ||
+        !aligned(stats, 4))
+        return KS_ERR_ALIGN;
+    const uint64_t seqs = static_cast<uint64_t>(x->sequences) * 4;
+    uint64_t db = 0;
+    bool same = false;
+    if (dlogits) {
+        st = check_dlogits(x, dlogits, d_seq_stride, d_row_stride);
+        if (st != KS_OK) return st;
+        db = dlogit_bytes(x, d_seq_stride, d_row_stride);
+        same = in_place(x, dlogits, d_seq_stride, d_row_stride);
+    }
+    const Range logits{x->data, logit_bytes(x)};
+    const Range none{nullptr, 0};
+    if (any_overlap({{loss, 4}, {rewards, seqs}, {grad, seqs}, {tokens, rows * 4}, {stats, rows * 8}, {dlogits, db}},
+                    {same ? none : logits, {x->labels, label_bytes(x)},
+                     {ref, span_bytes(x->sequences, ref_stride, 1, 0, x->tokens, 4)}}) ||
+        any_overlap({{loss, 4}, {rewards, seqs}, {grad, seqs}, {tokens, rows * 4}, {stats, rows * 8}}, {logits}))
+        return KS_ERR_OVERLAP;
+    const ks::LogitsCall c{*x, stream};
+    const int64_t P = x->sequences / 2;
+    const int64_t pair = std::max<int64_t>(1, 2 * x->tokens * x->row_stride * (x->elem == KS_ELEM_BF16 ? 2 : 4));
+    const int64_t step = dlogits ? std::max<int64_t>(1, kPairBytes / pair) : std::max<int64_t>(1, P);
+    int64_t p = 0;
+    do {
+        const int64_t n = std::min(step, P - p);
+        st = ks::launch_token_logp(c, p, n, P, tokens, stats);
+        if (st == KS_OK) st = ks::launch_pair_loss(c, p, n, tokens, ref, ref_stride, beta, smoothing, loss, rewards, grad);
+        if (st == KS_OK && dlogits)
+            st = ks::launch_logit_grad(c, p, n, P, stats, grad, nullptr, dlogits, d_seq_stride, d_row_stride);
+        if (st != KS_OK) return st;
+        p += n;
+    } while (p < P);
+    return KS_OK;
+}
+
+ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, const float* grad, const float* upstream,
+                                   void* dlogits, int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream) {
+    ks_status_t st = check_logits(x);
+    if (st != KS_OK) return st;
+    const uint64_t rows = static_cast<uint64_t>(x->sequences) * x->tokens;
+    if (rows == 0) return KS_OK;
+    if (!stats || !grad || !dlogits) return KS_ERR_NULL;
+    if (!aligned(stats, 4) || !aligned(grad, 4) || !aligned(upstream, 4)) return KS_ERR_ALIGN;
+    st = check_dlogits(x, dlogits, d_seq_stride, d_row_stride);
+    if (st != KS_OK) return st;
+    const Range logits{x->data, logit_bytes(x)};
+    const Range none{nullptr, 0};
+    if (any_overlap({{dlogits, dlogit_bytes(x, d_seq_stride, d_row_stride)}},
+                    {in_place(x, dlogits, d_seq_stride, d_row_stride) ? none : logits, {x->labels, label_bytes(x)},
+                     {stats, rows * 8}, {grad, static_cast<uint64_t>(x->sequences) * 4}, {upstream, 4}}))
+        return KS_ERR_OVERLAP;
+    return ks::launch_logit_grad(ks::LogitsCall{*x, stream}, 0, x->sequences, 0, stats, grad, upstream, dlogits,
+                                 d_seq_stride, d_row_stride);
+}
+
+ks_status_t ks_grad_norm_workspace_size(const ks_adamw_tensor_t* t, int n, size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    const ks_status_t st = check_tensors(t, n);
+    if (st != KS_OK) return st;
+    *bytes = ks::grad_norm_workspace(t, n);
+    return KS_OK;
+}
+
+ks_status_t ks_grad_norm(const ks_adamw_tensor_t* t, int n, float* norm, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+    size_t need = 0;
+    const ks_status_t st = ks_grad_norm_workspace_size(t, n, &need);
+    if (st != KS_OK) return st;
+    if (!norm) return KS_ERR_NULL;
+    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
+    if (!aligned(norm, 4) || !aligned(ws, 16)) return KS_ERR_ALIGN;
+    if (any_overlap({{norm, 4}, {ws, need}}, {})) return KS_ERR_OVERLAP;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].n == 0) continue;
+        if (!t[i].g) return KS_ERR_NULL;
+        if (!aligned(t[i].g, elem_size(t[i].g_elem))) return KS_ERR_ALIGN;
+        if (any_overlap({{norm, 4}, {ws, need}}, {{t[i].g, static_cast<uint64_t>(t[i].n) * elem_size(t[i].g_elem)}}))
+            return KS_ERR_OVERLAP;
+    }
+    return ks::launch_grad_norm(t, n, norm, ws, stream);
+}
+
+ks_status_t ks_adamw_step(const ks_adamw_tensor_t* t, int n, const ks_adamw_options_t* o, const float* norm,
+                          hipStream_t stream) {
+    ks_status_t st = check_tensors(t, n);
+    if (st != KS_OK) return st;
+    if (!o) return KS_ERR_NULL;
+    if (o->state_bits != 8 && o->state_bits != 32) return KS_ERR_INVALID;
+    if (o->step < 1) return KS_ERR_INVALID;
+    if (!(o->beta1 >= 0.0 && o->beta1 < 1.0) || !(o->beta2 >= 0.0 && o->beta2 < 1.0)) return KS_ERR_INVALID;
+    if (!(o->eps >= 0.0) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
+        return KS_ERR_INVALID;
+    if (!(o->max_norm >= 0.0) || !std::isfinite(o->max_norm)) return KS_ERR_INVALID;
+    if (o->max_norm > 0.0 && !norm) return KS_ERR_NULL;
+    if (!aligned(norm, 4)) return KS_ERR_ALIGN;
+    for (int i = 0; i < n; ++i) {
+        st = check_states(t[i], o->state_bits, true);
+        if (st != KS_OK) return st;
+    }
+    return ks::launch_adamw(t, n, *o, norm, stream);
+}
+
+ks_status_t ks_adamw_state_values(const ks_adamw_tensor_t* t, int n, float* const* m_out, float* const* v_out,
+                                  hipStream_t stream) {
+    ks_status_t st = check_tensors(t, n);
+    if (st != KS_OK) return st;
+    if (n > 0 && (!m_out || !v_out)) return KS_ERR_NULL;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].n == 0) continue;
+        st = check_states(t[i], 8, false);
+        if (st != KS_OK) return st;
+        if (!m_out[i] || !v_out[i]) return KS_ERR_NULL;
+        if (!aligned(m_out[i], 4) || !aligned(v_out[i], 4)) return KS_ERR_ALIGN;
+        const uint64_t k = static_cast<uint64_t>(t[i].n);
+        if (any_overlap({{m_out[i], k * 4}, {v_out[i], k * 4}}, {{t[i].m, k}, {t[i].v, k}, {t[i].scales, (k + 255) / 256 * 8}}))
+            return KS_ERR_OVERLAP;
+    }
+    return ks::launch_adamw_values(t, n, m_out, v_out, stream);
+}
+
+}  // extern "C"

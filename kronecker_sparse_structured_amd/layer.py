@@ -1,7 +1,9 @@
 """KSLinear: a chain of KS factors as a PyTorch layer, forward and backward
 through libks (KS abstract page, taxoreview.com "dblp:303/4794", first
 paragraph: the layer built from KS factors; the gradients are the chain rule
-on Y = X W^T, see include/ks.h).
+on Y = X W^T, see include/ks.h). AdapterLinear: such a layer, frozen, with
+low-rank adapters of many requests beside it. preference_loss: the paired
+preference loss on token logits.
 
 Argument marshalling only: every product runs in the HIP library. With
 gradients enabled each factor is its own launch, so that the intermediates
@@ -106,15 +108,115 @@ def make_layer_class():
     return KSLinear
 
 
+def make_adapter_class():
+    import torch
+
+    class AdapterFunction(torch.autograd.Function):
+        """Y = X W^T + H B^T over an AdapterChain; gradients of X, A and B."""
+
+        @staticmethod
+        def forward(ctx, X, A, B, chain, ids):
+            Y, H = chain.matmul(X, ids, keep=True)
+            ctx.chain = chain
+            ctx.save_for_backward(X, H, ids)
+            return Y
+
+        @staticmethod
+        def backward(ctx, dY):
+            X, H, ids = ctx.saved_tensors
+            weights = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+            dX, dA, dB = ctx.chain.backward(dY.float().contiguous(), X, H, ids, weights=weights)
+            kind = ctx.chain.weight_dtype
+            return (dX.to(X.dtype) if ctx.needs_input_grad[0] else None,
+                    dA.to(kind) if ctx.needs_input_grad[1] else None,
+                    dB.to(kind) if ctx.needs_input_grad[2] else None, None, None)
+
+    class AdapterLinear(torch.nn.Module):
+        """A frozen KSLinear with `adapters` low-rank adapters beside it:
+        y = layer(x) + alpha / rank x A[g]^T B[g]^T, where ids gives the
+        adapter g of each row (any id outside [0, adapters): none, the layer
+        alone). A is drawn N(0, 1/n_in) and B starts at zero, so a new adapter
+        changes nothing. Input (..., n_in) with ids (...), int32; output
+        (..., n_out), fp32."""
+
+        def __init__(self, layer, adapters: int, rank: int, alpha: float = 16.0, seed: int = 0):
+            super().__init__()
+            self.layer = layer
+            for w in layer.weights:
+                w.requires_grad_(False)
+            w = layer.weights[0]
+            gen = torch.Generator(device="cpu").manual_seed(seed)
+            A = torch.randn((adapters, rank, layer.n_in), generator=gen) / math.sqrt(layer.n_in)
+            self.A = torch.nn.Parameter(A.to(device=w.device, dtype=w.dtype))
+            self.B = torch.nn.Parameter(torch.zeros((adapters, layer.n_out, rank), device=w.device, dtype=w.dtype))
+            self.register_buffer("scale", torch.full((adapters,), alpha / rank, dtype=torch.float32, device=w.device))
+
+        def forward(self, x, ids):
+            lead = x.shape[:-1]
+            x2 = x.reshape(-1, self.layer.n_in).contiguous()
+            ids2 = ids.reshape(-1).contiguous()
+            # the handle holds addresses, so it is made for the tensors of this call
+            chain = libks.AdapterChain([w.detach() for w in self.layer.weights], self.layer.patterns,
+                                       self.A.detach(), self.B.detach(), self.scale)
+            if torch.is_grad_enabled() and (x2.requires_grad or self.A.requires_grad or self.B.requires_grad):
+                y = AdapterFunction.apply(x2, self.A, self.B, chain, ids2)
+            else:
+                y = chain.matmul(x2, ids2)
+            return y.reshape(*lead, self.layer.n_out)
+
+    return AdapterLinear
+
+
+def make_preference_function():
+    import torch
+
+    class PreferenceFunction(torch.autograd.Function):
+        """The paired preference loss; its gradient goes to the logits."""
+
+        @staticmethod
+        def forward(ctx, logits, labels, ref, beta, smoothing):
+            loss, rewards, tokens, grad, stats = libks._preference_forward(logits, labels, ref, beta, smoothing, None,
+                                                                           None)
+            ctx.save_for_backward(logits, labels, stats, grad)
+            ctx.mark_non_differentiable(rewards, tokens)
+            return loss, rewards, tokens
+
+        @staticmethod
+        def backward(ctx, upstream, _rewards, _tokens):
+            logits, labels, stats, grad = ctx.saved_tensors
+            return libks._preference_backward(logits, labels, stats, grad, upstream.float().contiguous()), None, None, \
+                None, None
+
+    return PreferenceFunction
+
+
+_PREFERENCE = None
+
+
+def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0):
+    """(loss, rewards, tokens) as libks.preference_loss gives them, with the
+    loss differentiable in the logits. The gradient is computed in backward(),
+    from the logits: they must not be changed in place before it."""
+    global _PREFERENCE
+    if _PREFERENCE is None:
+        _PREFERENCE = make_preference_function()
+    return _PREFERENCE.apply(logits, labels, ref, beta, smoothing)
+
+
 _LAYER = None
+_ADAPTER = None
 
 
 def __getattr__(name):
-    """``layer.KSLinear`` builds the class on first use (torch is imported
-    lazily, as everywhere in this package)."""
-    global _LAYER
+    """``layer.KSLinear`` and ``layer.AdapterLinear`` build their class on
+    first use (torch is imported lazily, as everywhere in this package)."""
+    global _LAYER, _ADAPTER
     if name == "KSLinear":
         if _LAYER is None:
             _LAYER = make_layer_class()
         return _LAYER
+    if name == "AdapterLinear":
+        if _ADAPTER is None:
+            _ADAPTER = make_adapter_class()
+        return _ADAPTER
     raise AttributeError(name)

@@ -67,6 +67,34 @@ class ks_closure_t(ctypes.Structure):
                 ("uniform", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class ks_adapters_t(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_in", ctypes.c_int64), ("n_out", ctypes.c_int64),
+                ("rank", ctypes.c_int32), ("count", ctypes.c_int32)]
+
+
+class ks_logits_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("labels", ctypes.c_void_p),
+                ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("label_stride", ctypes.c_int64),
+                ("sequences", ctypes.c_int64), ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("elem", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ks_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("p_elem", ctypes.c_int32), ("g_elem", ctypes.c_int32)]
+
+
+class ks_adamw_options_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("state_bits", ctypes.c_int32)]
+
+
+# ks_elem_t
+ELEM_F32, ELEM_BF16 = 0, 1
+
 _lib = None
 
 
@@ -133,6 +161,28 @@ def load(path: str = LIB_PATH):
     lib.ks_matmul_dw.restype = i32
     lib.ks_matmul_dw_noalloc.argtypes = [ks_pattern_t, vp, vp, vp, i64, i32, vp]
     lib.ks_matmul_dw_noalloc.restype = i32
+    pp, pa, pl, pt = (ctypes.POINTER(t) for t in (ks_pattern_t, ks_adapters_t, ks_logits_t, ks_adamw_tensor_t))
+    f32, size, psize = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    for name, args in {
+        "ks_adapter_matmul": [pa, vp, vp, vp, vp, i64, i32, vp],
+        "ks_adapter_backward_workspace_size": [pa, i64, psize],
+        "ks_adapter_backward": [pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size, vp],
+        "ks_chain_adapter_workspace_size": [pp, i32, pa, i64, i32, psize],
+        "ks_chain_adapter_matmul": [pp, i32, ctypes.POINTER(vp), pa, vp, vp, vp, vp, i64, i32, vp, size, vp],
+        "ks_chain_adapter_backward_workspace_size": [pp, i32, pa, i64, i32, psize],
+        "ks_chain_adapter_backward": [pp, i32, ctypes.POINTER(vp), pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size,
+                                      vp],
+        "ks_sequence_logp": [pl, vp, vp, vp, vp],
+        "ks_preference_loss": [pl, vp, i64, f32, f32, vp, vp, vp, vp, vp, vp, i64, i64, vp],
+        "ks_preference_backward": [pl, vp, vp, vp, vp, i64, i64, vp],
+        "ks_grad_norm_workspace_size": [pt, i32, psize],
+        "ks_grad_norm": [pt, i32, vp, vp, size, vp],
+        "ks_adamw_step": [pt, i32, ctypes.POINTER(ks_adamw_options_t), vp, vp],
+        "ks_adamw_state_values": [pt, i32, ctypes.POINTER(vp), ctypes.POINTER(vp), vp],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = i32
     _lib = lib
     return lib
 
@@ -401,3 +451,364 @@ def matmul_dw(dY, X, pattern, out=None, stream=None):
     ks_matmul_dw((a, b, c, d), dY, X, out, batch, dt, ws, nbytes, stream)
     return out
 
+
+# ---------------------------------------------------------------- adapters
+
+class AdapterChain:
+    """A chain of KS factors with low-rank adapters of many requests beside it:
+    Y[n] = X[n] W^T + H[n] B[g]^T, H[n] = scale[g] X[n] A[g]^T, g = ids[n]
+    (no adapter for an id outside [0, G)).
+
+    The handle keeps its weights (no copies: later in-place changes of them are
+    seen) and their addresses, so that a call only marshals its rows. W_k has
+    shape (a, d, b, c); A (G, rank, n_in); B (G, n_out, rank); scale (G,) fp32;
+    W, A and B have one type, fp32 or bf16; X has that type, or is fp32."""
+
+    def __init__(self, Ws, patterns, A, B, scale):
+        import torch
+        self.patterns = [tuple(int(v) for v in p) for p in patterns]
+        if not self.patterns or len(Ws) != len(self.patterns):
+            raise ValueError("one weight tensor for each pattern, at least one")
+        for i, (w, p) in enumerate(zip(Ws, self.patterns)):
+            _check_tensor(w, "W[%d]" % i)
+            if w.numel() != p[0] * p[1] * p[2] * p[3]:
+                raise ValueError("W[%d] must hold a*b*c*d = %d values" % (i, p[0] * p[1] * p[2] * p[3]))
+        for t, name in ((A, "A"), (B, "B"), (scale, "scale")):
+            _check_tensor(t, name)
+        first, last = self.patterns[0], self.patterns[-1]
+        self.n_in, self.n_out = first[0] * first[2] * first[3], last[0] * last[1] * last[3]
+        if A.dim() != 3 or A.shape[2] != self.n_in:
+            raise ValueError("A must be (adapters, rank, %d)" % self.n_in)
+        self.count, self.rank = int(A.shape[0]), int(A.shape[1])
+        if tuple(B.shape) != (self.count, self.n_out, self.rank):
+            raise ValueError("B must be (%d, %d, %d)" % (self.count, self.n_out, self.rank))
+        if tuple(scale.shape) != (self.count,) or scale.dtype != torch.float32:
+            raise ValueError("scale must be (%d,) fp32" % self.count)
+        if any(t.dtype != A.dtype for t in (*Ws, B)):
+            raise TypeError("W, A and B must have one type")
+        self.device = A.device
+        if any(t.device != self.device for t in (*Ws, B, scale)):
+            raise ValueError("all weights must be on one device")
+        self.weight_dtype = A.dtype
+        self._codes = {torch.float32: dtype_code(torch.float32, A.dtype)}
+        if A.dtype == torch.bfloat16:
+            self._codes[torch.bfloat16] = DTYPE_BF16
+        self._keep = (list(Ws), A, B, scale)
+        self._n = len(self.patterns)
+        self._p = _patterns(self.patterns)
+        self._w = (ctypes.c_void_p * self._n)(*[w.data_ptr() for w in Ws])
+        self._ad = ks_adapters_t(A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.n_in, self.n_out, self.rank,
+                                 self.count)
+        self._lib = load()
+
+    def _rows(self, X, ids):
+        import torch
+        if X.dim() != 2 or X.shape[1] != self.n_in:
+            raise ValueError("X must be (batch, %d)" % self.n_in)
+        if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
+            raise ValueError("ids must be (batch,) int32")
+        if X.device != self.device or ids.device != self.device:
+            raise ValueError("X and ids must be on the weights' device")
+        if not X.is_contiguous() or not ids.is_contiguous():
+            raise ValueError("X and ids must be contiguous")
+        code = self._codes.get(X.dtype)
+        if code is None:
+            raise TypeError("X must be fp32 or of the weights' type, not %s" % X.dtype)
+        return X.shape[0], code
+
+    def matmul(self, X, ids, out=None, keep=False, stream=None):
+        """Y (batch, n_out) fp32; with keep=True (Y, H), H (batch, rank) fp32
+        for backward()."""
+        import torch
+        batch, code = self._rows(X, ids)
+        if out is None:
+            out = torch.empty((batch, self.n_out), dtype=torch.float32, device=self.device)
+        else:
+            _check_out(out, (batch, self.n_out), torch.float32, self.device, "out")
+        H = torch.empty((batch, self.rank), dtype=torch.float32, device=self.device) if keep else None
+        size = ctypes.c_size_t(0)
+        _raise(self._lib.ks_chain_adapter_workspace_size(self._p, self._n, self._ad, batch, code, size),
+               "ks_chain_adapter_workspace_size", True)
+        ws = torch.empty(size.value, dtype=torch.uint8, device=self.device) if size.value else None
+        _raise(self._lib.ks_chain_adapter_matmul(
+            self._p, self._n, self._w, self._ad, ids.data_ptr(), X.data_ptr(), out.data_ptr(), _ptr(H), batch, code,
+            _ptr(ws), size.value, _stream(stream, X)), "ks_chain_adapter_matmul", True)
+        return (out, H) if keep else out
+
+    def backward(self, dY, X, H, ids, weights=True, stream=None):
+        """(dX, dA, dB), all fp32; (dX, None, None) with weights=False. W is
+        frozen. dY (batch, n_out) fp32; X, H and ids as matmul() had and gave
+        them."""
+        import torch
+        batch, code = self._rows(X, ids)
+        _check_out(dY, (batch, self.n_out), torch.float32, self.device, "dY")
+        _check_out(H, (batch, self.rank), torch.float32, self.device, "H")
+        dX = torch.empty((batch, self.n_in), dtype=torch.float32, device=self.device)
+        dA = dB = None
+        if weights:
+            dA = torch.empty((self.count, self.rank, self.n_in), dtype=torch.float32, device=self.device)
+            dB = torch.empty((self.count, self.n_out, self.rank), dtype=torch.float32, device=self.device)
+        size = ctypes.c_size_t(0)
+        _raise(self._lib.ks_chain_adapter_backward_workspace_size(self._p, self._n, self._ad, batch, code, size),
+               "ks_chain_adapter_backward_workspace_size", True)
+        ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=self.device)
+        _raise(self._lib.ks_chain_adapter_backward(
+            self._p, self._n, self._w, self._ad, ids.data_ptr(), dY.data_ptr(), X.data_ptr(), H.data_ptr(),
+            dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws.data_ptr(), size.value, _stream(stream, dY)),
+            "ks_chain_adapter_backward", True)
+        return dX, dA, dB
+
+
+def _check_out(t, shape, dtype, device, name):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s %s on %s" % (name, tuple(shape), dtype, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _adapters(A, B, scale, n_in, n_out):
+    import torch
+    for t, name in ((A, "A"), (B, "B"), (scale, "scale")):
+        _check_tensor(t, name)
+    if A.dim() != 3 or B.dim() != 3 or tuple(B.shape) != (A.shape[0], n_out, A.shape[1]) or A.shape[2] != n_in:
+        raise ValueError("A must be (adapters, rank, %d) and B (adapters, %d, rank)" % (n_in, n_out))
+    if tuple(scale.shape) != (A.shape[0],) or scale.dtype != torch.float32:
+        raise ValueError("scale must be (%d,) fp32" % A.shape[0])
+    if A.dtype != B.dtype:
+        raise TypeError("A and B must have one type")
+    return ks_adapters_t(A.data_ptr(), B.data_ptr(), scale.data_ptr(), n_in, n_out, A.shape[1], A.shape[0])
+
+
+def adapter_matmul(X, A, B, scale, ids, out, keep=False, stream=None):
+    """out (batch, n_out) fp32 += H B^T for any projection's output; returns
+    out, or (out, H) with keep=True."""
+    import torch
+    for t, name in ((X, "X"), (ids, "ids"), (out, "out")):
+        _check_tensor(t, name)
+    if X.dim() != 2 or out.dim() != 2 or out.shape[0] != X.shape[0] or out.dtype != torch.float32:
+        raise ValueError("X must be (batch, n_in) and out (batch, n_out) fp32")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
+        raise ValueError("ids must be (batch,) int32")
+    ad = _adapters(A, B, scale, X.shape[1], out.shape[1])
+    H = torch.empty((X.shape[0], ad.rank), dtype=torch.float32, device=X.device)
+    _raise(load().ks_adapter_matmul(ad, _ptr(ids), _ptr(X), _ptr(out), _ptr(H), X.shape[0],
+                                    dtype_code(X.dtype, A.dtype), _stream(stream, X)), "ks_adapter_matmul", True)
+    return (out, H) if keep else out
+
+
+def adapter_backward(dY, X, H, A, B, scale, ids, dX=None, stream=None):
+    """(dA, dB) fp32 of adapter_matmul; dX (batch, n_in) fp32, if given, is
+    added to."""
+    import torch
+    for t, name in ((dY, "dY"), (X, "X"), (H, "H"), (ids, "ids")):
+        _check_tensor(t, name)
+    if X.dim() != 2 or dY.dim() != 2 or dY.shape[0] != X.shape[0] or dY.dtype != torch.float32:
+        raise ValueError("X must be (batch, n_in) and dY (batch, n_out) fp32")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
+        raise ValueError("ids must be (batch,) int32")
+    ad = _adapters(A, B, scale, X.shape[1], dY.shape[1])
+    _check_out(H, (X.shape[0], ad.rank), torch.float32, X.device, "H")
+    if dX is not None:
+        _check_out(dX, tuple(X.shape), torch.float32, X.device, "dX")
+    dA = torch.empty(tuple(A.shape), dtype=torch.float32, device=X.device)
+    dB = torch.empty(tuple(B.shape), dtype=torch.float32, device=X.device)
+    size = ctypes.c_size_t(0)
+    _raise(load().ks_adapter_backward_workspace_size(ad, X.shape[0], size), "ks_adapter_backward_workspace_size", True)
+    ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=X.device)
+    _raise(load().ks_adapter_backward(ad, _ptr(ids), _ptr(dY), _ptr(X), _ptr(H), _ptr(dX), _ptr(dA), _ptr(dB),
+                                      X.shape[0], dtype_code(X.dtype, A.dtype), _ptr(ws), size.value,
+                                      _stream(stream, X)), "ks_adapter_backward", True)
+    return dA, dB
+
+
+# ---------------------------------------------------------------- preference loss
+
+def _elem(dtype, name) -> int:
+    import torch
+    if dtype == torch.float32:
+        return ELEM_F32
+    if dtype == torch.bfloat16:
+        return ELEM_BF16
+    raise TypeError("%s must be fp32 or bf16, not %s" % (name, dtype))
+
+
+def _logits(x, labels) -> ks_logits_t:
+    import torch
+    if x.dim() != 3 or tuple(labels.shape) != tuple(x.shape[:2]):
+        raise ValueError("logits must be (sequences, tokens, vocab) and labels (sequences, tokens)")
+    if labels.dtype != torch.int64:
+        raise TypeError("labels must be int64")
+    if not x.is_cuda or labels.device != x.device:
+        raise ValueError("logits and labels must be device tensors on one device")
+    elem = _elem(x.dtype, "logits")
+    S, T, V = x.shape
+    if (V > 1 and x.stride(2) != 1) or (T > 1 and labels.stride(1) != 1):
+        raise ValueError("the last dimension of logits and labels must be contiguous")
+    # strides of dimensions with at most one entry say nothing
+    row = x.stride(1) if T > 1 else max(V, 1)
+    seq = x.stride(0) if S > 1 else max((T - 1) * row + V, 0)
+    lab = labels.stride(0) if S > 1 else T
+    return ks_logits_t(x.data_ptr(), labels.data_ptr(), seq, row, lab, S, T, V, elem, 0)
+
+
+def _seq_stride(t, name):
+    import torch
+    if t.dtype != torch.float32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be (sequences, tokens) fp32 with contiguous rows" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def sequence_logp(logits, labels, stream=None):
+    """(total, tokens): log probabilities of the labels, summed over each
+    sequence and for each token. logits (S, T, V) fp32 or bf16 with any row
+    strides; labels (S, T) int64, negative where masked."""
+    import torch
+    x = _logits(logits, labels)
+    tokens = torch.empty((x.sequences, x.tokens), dtype=torch.float32, device=logits.device)
+    total = torch.empty((x.sequences,), dtype=torch.float32, device=logits.device)
+    _raise(load().ks_sequence_logp(x, tokens.data_ptr(), total.data_ptr(), None, _stream(stream, logits)),
+           "ks_sequence_logp", True)
+    return total, tokens
+
+
+def _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream):
+    import torch
+    x = _logits(logits, labels)
+    if tuple(ref.shape) != tuple(labels.shape) or ref.device != logits.device:
+        raise ValueError("ref must be (sequences, tokens) on the logits' device")
+    ref_stride = _seq_stride(ref, "ref")
+    if dlogits is not None:
+        if tuple(dlogits.shape) != tuple(logits.shape) or dlogits.dtype != logits.dtype \
+                or dlogits.device != logits.device:
+            raise ValueError("dlogits must have the logits' shape, type and device")
+    S, T = x.sequences, x.tokens
+    buf = torch.empty(1 + 2 * S + 3 * S * T, dtype=torch.float32, device=logits.device)
+    loss, rewards, grad = buf[0], buf[1:1 + S], buf[1 + S:1 + 2 * S]
+    tokens = buf[1 + 2 * S:1 + 2 * S + S * T].view(S, T)
+    stats = buf[1 + 2 * S + S * T:]
+    d_seq = d_row = 0
+    if dlogits is not None:
+        d = _logits(dlogits, labels)
+        d_seq, d_row = d.seq_stride, d.row_stride
+    _raise(load().ks_preference_loss(x, ref.data_ptr(), ref_stride, float(beta), float(smoothing), loss.data_ptr(),
+                                     rewards.data_ptr(), tokens.data_ptr(), grad.data_ptr(), stats.data_ptr(),
+                                     _ptr(dlogits), d_seq, d_row, _stream(stream, logits)),
+           "ks_preference_loss", True)
+    return loss, rewards, tokens, grad, stats
+
+
+def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, stream=None):
+    """(loss, rewards, tokens, dlogits) of the paired preference loss: sequences
+    0..P-1 of the logits (2P, T, V) are the chosen answers, P..2P-1 the rejected
+    ones, ref (2P, T) fp32 the reference model's token log probabilities.
+    dlogits may be given (the logits themselves too: then it replaces them)."""
+    import torch
+    if dlogits is None:
+        dlogits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+    loss, rewards, tokens, _, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
+    return loss, rewards, tokens, dlogits
+
+
+def _preference_backward(logits, labels, stats, grad, upstream, stream=None):
+    import torch
+    dlogits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+    x, d = _logits(logits, labels), _logits(dlogits, labels)
+    _raise(load().ks_preference_backward(x, stats.data_ptr(), grad.data_ptr(), _ptr(upstream), dlogits.data_ptr(),
+                                         d.seq_stride, d.row_stride, _stream(stream, logits)),
+           "ks_preference_backward", True)
+    return dlogits
+
+
+# ---------------------------------------------------------------- optimizer
+
+ADAMW_BLOCK = 256   # values that share a scale in 8 bits
+
+
+class AdamW:
+    """One AdamW step over many tensors. The handle keeps the tensors it was
+    given (params, grads and the moments ms, vs, changed in place) and their
+    addresses. Moments are fp32, or with `scales` int8 (ms) and uint8 (vs) with
+    scales[i] of shape (ceil(n / 256), 2), fp32."""
+
+    def __init__(self, params, grads, ms, vs, scales=None):
+        import torch
+        n = len(params)
+        if not (len(grads) == len(ms) == len(vs) == n) or (scales is not None and len(scales) != n):
+            raise ValueError("params, grads, ms, vs and scales must have one entry a tensor")
+        self.bits = 32 if scales is None else 8
+        types = (torch.float32, torch.float32) if scales is None else (torch.int8, torch.uint8)
+        self._t = (ks_adamw_tensor_t * max(n, 1))()
+        self._n = n
+        self.device = params[0].device if n else None
+        spans = []
+        for i in range(n):
+            p, g, m, v = params[i], grads[i], ms[i], vs[i]
+            for t, name in ((p, "params"), (g, "grads"), (m, "ms"), (v, "vs")):
+                _check_tensor(t, "%s[%d]" % (name, i))
+                if t.numel() != p.numel() or t.device != self.device:
+                    raise ValueError("%s[%d] must have its parameter's size, on one device" % (name, i))
+            if (m.dtype, v.dtype) != types:
+                raise TypeError("moments must be %s and %s" % types)
+            s = None
+            if scales is not None:
+                s = scales[i]
+                _check_out(s, (-(-p.numel() // ADAMW_BLOCK), 2), torch.float32, self.device, "scales[%d]" % i)
+            self._t[i] = ks_adamw_tensor_t(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(s), p.numel(),
+                                           _elem(p.dtype, "params"), _elem(g.dtype, "grads"))
+            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (p, m, v, s)
+                      if t is not None and t.numel()]
+        spans.sort()
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters and moments must not share memory")
+        self._keep = (list(params), list(grads), list(ms), list(vs), list(scales or ()))
+        self._lib = load()
+        size = ctypes.c_size_t(0)
+        _raise(self._lib.ks_grad_norm_workspace_size(self._t, n, size), "ks_grad_norm_workspace_size", True)
+        self._ws_bytes = size.value
+
+    def grad_norm(self, out=None, stream=None):
+        """The 2-norm over all gradients, a device scalar."""
+        import torch
+        if out is None:
+            out = torch.empty((), dtype=torch.float32, device=self.device)
+        ws = torch.empty(max(self._ws_bytes, 1), dtype=torch.uint8, device=self.device)
+        _raise(self._lib.ks_grad_norm(self._t, self._n, out.data_ptr(), ws.data_ptr(), self._ws_bytes,
+                                      _stream(stream, out)), "ks_grad_norm", True)
+        return out
+
+    def step(self, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None, norm=None, seed=0,
+             stream=None):
+        """The step number `step` (from 1). max_norm: scale the gradients to at
+        most that norm, `norm` (a device scalar) or grad_norm(); a norm that is
+        not finite leaves everything as it was. Returns the norm used, or
+        None."""
+        if self._n == 0:
+            return norm
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be positive")
+        if max_norm is not None and norm is None:
+            norm = self.grad_norm(stream=stream)
+        o = ks_adamw_options_t(float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
+                               float(max_norm or 0.0), int(step), int(seed) & 0xFFFFFFFF, self.bits)
+        _raise(self._lib.ks_adamw_step(self._t, self._n, o, _ptr(norm) if max_norm is not None else None,
+                                       _stream(stream, self._keep[0][0])), "ks_adamw_step", True)
+        return norm
+
+    def state_values(self, ms_out, vs_out, stream=None):
+        """The values that 8-bit moments stand for, into fp32 tensors."""
+        import torch
+        if self.bits != 8:
+            raise ValueError("32-bit moments are their own values")
+        if len(ms_out) != self._n or len(vs_out) != self._n:
+            raise ValueError("one output a tensor")
+        for i in range(self._n):
+            for t in (ms_out[i], vs_out[i]):
+                _check_tensor(t, "state_values output")
+                if t.dtype != torch.float32 or t.numel() != self._t[i].n or t.device != self.device:
+                    raise ValueError("outputs must be fp32 of their parameter's size")
+        if self._n == 0:
+            return
+        mp = (ctypes.c_void_p * self._n)(*[t.data_ptr() for t in ms_out])
+        vp = (ctypes.c_void_p * self._n)(*[t.data_ptr() for t in vs_out])
+        _raise(self._lib.ks_adamw_state_values(self._t, self._n, mp, vp, _stream(stream, ms_out[0])),
+               "ks_adamw_state_values", True)
