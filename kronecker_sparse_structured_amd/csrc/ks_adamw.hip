@@ -65,7 +65,7 @@ struct Table {
 
 struct Step {
     float b1, c1, b2, c2;      // beta and 1 - beta
-    float decay;               // 1 - lr wd
+    float decay;               // lr wd
     float rate;                // lr / (1 - b1^t)
     float root;                // 1 / sqrt(1 - b2^t)
     float eps;
@@ -237,7 +237,8 @@ __device__ __forceinline__ void step_lane(const Entry& e, const Step& s, float c
         m[j] = m[j] * s.b1 + gj * s.c1;
         v[j] = v[j] * s.b2 + (gj * gj) * s.c2;
         const float root = __builtin_amdgcn_sqrtf(v[j]) * s.root + s.eps;
-        x[j] = x[j] * s.decay - (m[j] * __builtin_amdgcn_rcpf(root)) * s.rate;
+        // the small terms first: p itself is rounded once
+        x[j] = x[j] - (x[j] * s.decay + (m[j] * __builtin_amdgcn_rcpf(root)) * s.rate);
     }
     store_lane(p, valid, wide, x);
     if constexpr (BITS == 32) {
@@ -449,7 +450,7 @@ ks_status_t launch_adamw(const ks_adamw_tensor_t* t, int n, const ks_adamw_optio
     s.c1 = static_cast<float>(1.0 - o.beta1);
     s.b2 = static_cast<float>(o.beta2);
     s.c2 = static_cast<float>(1.0 - o.beta2);
-    s.decay = static_cast<float>(1.0 - o.lr * o.weight_decay);
+    s.decay = static_cast<float>(o.lr * o.weight_decay);
     s.rate = static_cast<float>(o.lr / (1.0 - std::pow(o.beta1, static_cast<double>(o.step))));
     s.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(o.beta2, static_cast<double>(o.step))));
     s.eps = static_cast<float>(o.eps);

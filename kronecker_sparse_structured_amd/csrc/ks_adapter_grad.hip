@@ -59,7 +59,6 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     const int i0 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(wave) * per));
     const int i1 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(i0) + per));
     int own = 0, less = 0;
-#pragma unroll 8
     for (int i = i0; i < i1; i += 64) {
         const int id = i + lane < i1 ? ids[i + lane] : -1;
         own += __popcll(__ballot(id == g));

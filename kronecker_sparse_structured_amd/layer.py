@@ -118,12 +118,13 @@ def make_adapter_class():
         def forward(ctx, X, A, B, chain, ids):
             Y, H = chain.matmul(X, ids, keep=True)
             ctx.chain = chain
-            ctx.save_for_backward(X, H, ids)
+            # A and B are saved for autograd's check of in-place changes
+            ctx.save_for_backward(X, H, ids, A, B)
             return Y
 
         @staticmethod
         def backward(ctx, dY):
-            X, H, ids = ctx.saved_tensors
+            X, H, ids = ctx.saved_tensors[:3]
             weights = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
             dX, dA, dB = ctx.chain.backward(dY.float().contiguous(), X, H, ids, weights=weights)
             kind = ctx.chain.weight_dtype

@@ -84,7 +84,7 @@ def make_class():
                 norm = every.grad_norm()
             for k, ((group, t, _), h) in enumerate(zip(sets, handles)):
                 # another stream of random numbers for each step and set
-                seed = (self.seed * 0x9E3779B1 + t * 0x85EBCA77 + k * 0xC2B2AE3D) & 0xFFFFFFFF
+                seed = (self.seed * 0x9E3779B1 + t * 0xAADDE6A9 + k * 0xBEDE544D) & 0xFFFFFFFF
                 h.step(t, group["lr"], group["betas"], group["eps"], group["weight_decay"], self.max_norm, norm, seed)
             return loss
 
