@@ -473,8 +473,7 @@ ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, 
  *   stats   device fp32, 2P x T x 2: as ks_sequence_logp writes them.
  *   dlogits NULL: the loss alone. Else the gradient of the loss, of x's element
  *           type, at dlogits[s * d_seq_stride + t * d_row_stride + v]; it may
- *           be x's own memory with x's strides. Long batches run in ranges of
- *           pairs, so that the gradient finds a pair's logits in the last cache.
+ *           be x's own memory with x's strides.
  * beta > 0 and 0 <= smoothing <= 1, else KS_ERR_INVALID.
  *
  * ks_preference_backward: that gradient from stats and grad of an earlier

@@ -350,8 +350,24 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(const Table t, flo
     const int64_t start = static_cast<int64_t>(wg - e.first) * (kStep * kNormIters) + threadIdx.x * kLane;
     const bool wide = e.flags & kWide;
     float sum = 0.0f;
-#pragma unroll 4
-    for (int it = 0; it < kNormIters; ++it) {
+    const bool whole = wide && start - threadIdx.x * kLane + kStep * kNormIters <= e.n;
+    if (whole && !(e.flags & kGBF16)) {
+        // every load of the workgroup's share in flight
+        const f32x4* g = reinterpret_cast<const f32x4*>(static_cast<const float*>(e.g) + start);
+        f32x4 x[kNormIters][2];
+#pragma unroll
+        for (int it = 0; it < kNormIters; ++it) {
+            x[it][0] = g[it * (kStep / 4)];
+            x[it][1] = g[it * (kStep / 4) + 1];
+        }
+#pragma unroll
+        for (int it = 0; it < kNormIters; ++it) {
+            float part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part += x[it][j / 4][j % 4] * x[it][j / 4][j % 4];
+            sum += part;
+        }
+    } else for (int it = 0; it < kNormIters; ++it) {
         const int64_t i = start + it * kStep;
         if (i < e.n) {
             const int valid = static_cast<int>(e.n - i < kLane ? e.n - i : kLane);

@@ -66,7 +66,33 @@ __device__ __forceinline__ void load4(const T* p, int valid, float (&x)[4]) {
 
 // ---------------------------------------------------------------- few rows
 
-template <typename TX, typename TW, bool WIDE_K, bool WIDE_R>
+// Eight consecutive values: 16-byte loads (WIDE), or element-wise with zeros
+// from `valid` on.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
+    if (WIDE && valid >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = a[i];
+                x[4 + i] = b[i];
+            }
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(a[i]);
+                x[2 * i + 1] = bf16_hi(a[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < valid ? to_f32(p[i]) : 0.0f;
+    }
+}
+
+template <typename TX, typename TW, bool WIDE>
 __global__ __launch_bounds__(kThreads) void adapter_rows_kernel(const Args a, int slice) {
     __shared__ float h[KS_ADAPTER_MAX_RANK];
     const int64_t n = blockIdx.x;
@@ -81,48 +107,69 @@ __global__ __launch_bounds__(kThreads) void adapter_rows_kernel(const Args a, in
     const TW* A = static_cast<const TW*>(a.A) + static_cast<int64_t>(g) * a.rank * a.n_in;
     const TW* B = static_cast<const TW*>(a.B) + static_cast<int64_t>(g) * a.n_out * a.rank;
     const float scale = a.scale[g];
+    const int o0 = blockIdx.y * slice;
+    const int o1 = min(a.n_out, o0 + slice);
+    float* y = a.Y + n * a.n_out;
+    // the first output's values of B and Y are on their way during the dot
+    // products
+    constexpr int kAhead = 2;
+    float ahead[kAhead][8], y0 = 0.0f;
+    {
+        const int o = min(o0 + tid, o1 - 1);
+        y0 = y[o];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) load8<WIDE>(B + static_cast<int64_t>(o) * a.rank + 8 * q, a.rank - 8 * q, ahead[q]);
+    }
     // h: a wave takes four ranks at a time, its lanes the inputs
     for (int r0 = wave * 4; r0 < a.rank; r0 += 16) {
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = lane * 4; k < a.n_in; k += 256) {
-            float xv[4];
-            load4<WIDE_K>(x + k, a.n_in - k, xv);
+#pragma unroll 2
+        for (int k = lane * 8; k < a.n_in; k += 512) {
+            float xv[8], av[4][8];
+            load8<WIDE>(x + k, a.n_in - k, xv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                load8<WIDE>(A + static_cast<int64_t>(min(r0 + j, a.rank - 1)) * a.n_in + k, a.n_in - k, av[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[j] += xv[i] * av[j][i];
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], d, 64);
+        if (lane == 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (r0 + j < a.rank) {
-                    float av[4];
-                    load4<WIDE_K>(A + static_cast<int64_t>(r0 + j) * a.n_in + k, a.n_in - k, av);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j] += xv[i] * av[i];
+                    const float v = scale * acc[j];
+                    h[r0 + j] = v;
+                    if (a.H && blockIdx.y == 0) a.H[n * a.rank + r0 + j] = v;
                 }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) acc[j] += __shfl_xor(acc[j], d, 64);
-            if (lane == 0 && r0 + j < a.rank) {
-                const float v = scale * acc[j];
-                h[r0 + j] = v;
-                if (a.H && blockIdx.y == 0) a.H[n * a.rank + r0 + j] = v;
             }
         }
     }
     __syncthreads();
-    const int o0 = blockIdx.y * slice;
-    const int o1 = min(a.n_out, o0 + slice);
-    float* y = a.Y + n * a.n_out;
     for (int o = o0 + tid; o < o1; o += kThreads) {
         const TW* b = B + static_cast<int64_t>(o) * a.rank;
+        const bool first = o < o0 + kThreads;
         float sum = 0.0f;
-        for (int r = 0; r < a.rank; r += 4) {
-            float bv[4];
-            load4<WIDE_R>(b + r, a.rank - r, bv);
+        if (first) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (8 * q + i < a.rank) sum += ahead[q][i] * h[8 * q + i];
+        }
+        for (int r = first ? 8 * kAhead : 0; r < a.rank; r += 8) {
+            float bv[8];
+            load8<WIDE>(b + r, a.rank - r, bv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
                 if (r + i < a.rank) sum += bv[i] * h[r + i];
         }
-        y[o] += sum;
+        y[o] = (first ? y0 : y[o]) + sum;
     }
 }
 
@@ -255,24 +302,35 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a) {
 
 // Y += H B^T: 64 rows and 64 outputs a wave, 256 outputs a workgroup. The
 // products are formed transposed, outputs along the instruction's rows: lane
-// (li, lg) holds outputs 4 lg .. 4 lg + 3 of tile row li. B's values of the
-// current adapter stay in registers while the row tiles keep that adapter.
-constexpr int kUpRows = 64, kUpCols = 256;
+// (li, lg) holds outputs 4 lg .. 4 lg + 3 of tile row li, 64 bytes of 16 rows an
+// instruction. They cross a small LDS tile of the wave's own, so that Y is read
+// and written in runs of 256 bytes: lane (l / 16, l % 16) takes rows
+// 4 q + l / 16, outputs 4 (l % 16) .. + 3.
+constexpr int kUpRows = 64, kUpCols = 256, kUpPitch = 68;
+
+// Orders the wave's LDS accesses before and after it: its lanes exchange values.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 template <typename TW, int RT, bool WIDE>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a) {
+    __shared__ __align__(16) float cross[4][16 * kUpPitch];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int li = lane % 16, lg = lane / 16;
-    const int o0 = blockIdx.y * kUpCols + wave * 64;
+    // neighbouring workgroups take neighbouring columns of the same rows: with
+    // rows fastest, all that run together would meet in a few memory channels
+    const unsigned slabs = (a.n_out + kUpCols - 1) / kUpCols;
+    const int o0 = blockIdx.x % slabs * kUpCols + wave * 64;
     if (o0 >= a.n_out) return;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kUpRows;
+    const int64_t first = static_cast<int64_t>(blockIdx.x / slabs) * kUpRows;
     const TW* B = static_cast<const TW*>(a.B);
+    float* mine_lds = cross[wave];
+    const int left = a.n_out - (o0 + 4 * li);          // this lane's outputs of Y inside the matrix
     float bv[4][RT][4];
-    int held_g = -1, held_r = -1;
     auto hold = [&](int g, int r0) {
-        if (g == held_g && r0 == held_r) return;
-        held_g = g;
-        held_r = r0;
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
             const int o = min(o0 + 16 * ct + li, a.n_out - 1);
@@ -284,38 +342,78 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a) {
             }
         }
     };
-#pragma unroll 2
+    // the product of 16 rows, from D's layout to Y's
+    auto turn = [&](const f32x4 (&sum)[4], f32x4 (&out)[4]) {
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(mine_lds + li * kUpPitch + 16 * ct + 4 * lg) = sum[ct];
+        wave_fence();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) out[q] = *reinterpret_cast<const f32x4*>(mine_lds + (4 * q + lg) * kUpPitch + 4 * li);
+        wave_fence();
+    };
+    // 64 rows of one adapter and whole vectors everywhere: every load of the
+    // wave is in flight before the first product
+    if constexpr (WIDE) {
+        const int id = first + lane < a.batch ? a.ids[first + lane] : -1;
+        const int g = __builtin_amdgcn_readfirstlane(id);
+        if (a.rank <= 16 * RT && o0 + 64 <= a.n_out && g >= 0 && g < a.count && __all(id == g)) {
+            f32x4 y[4][4];
+            float hv[4][RT][4];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    y[rt][q] = *reinterpret_cast<const f32x4*>(a.Y + (first + 16 * rt + 4 * q + lg) * a.n_out + o0 + 4 * li);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int r = 16 * t + 4 * lg;
+                    load4<true>(a.H + (first + 16 * rt + li) * a.rank + r, a.rank - r, hv[rt][t]);
+                }
+            }
+            hold(g, 0);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                f32x4 sum[4], out[4];
+#pragma unroll
+                for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int ct = 0; ct < 4; ++ct)
+                            sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][t][i], hv[rt][t][i], sum[ct], 0, 0, 0);
+                turn(sum, out);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4*>(a.Y + (first + 16 * rt + 4 * q + lg) * a.n_out + o0 + 4 * li) = y[rt][q] + out[q];
+            }
+            return;
+        }
+    }
+#pragma unroll 1
     for (int rt = 0; rt < kUpRows / 16; ++rt) {
         const int64_t row0 = first + 16 * rt;
         if (row0 >= a.batch) return;
         const int rows = static_cast<int>(a.batch - row0 < 16 ? a.batch - row0 : 16);
         Mix mix(a.ids, row0, rows, a.count);
         if (!mix.left) continue;
-        const int64_t row = row0 + (li < rows ? li : rows - 1);
-        float* y = a.Y + row * a.n_out + o0 + 4 * lg;
-        f32x4 acc[4];
+        const float* h = a.H + (row0 + (li < rows ? li : rows - 1)) * a.rank;
+        f32x4 all[4], out[4];
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-            const int left = a.n_out - (o0 + 16 * ct + 4 * lg);
-            float v[4];
-            load4<WIDE>(y + 16 * ct, left, v);
-            acc[ct] = f32x4{v[0], v[1], v[2], v[3]};
-        }
+        for (int ct = 0; ct < 4; ++ct) all[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         while (mix.left) {
             const int g = mix.next();
-            const bool mine = mix.id == g;
-            // a lane's column of the product is one row of Y: rows of other
-            // adapters take nothing from it, not even its NaN
             f32x4 sum[4];
 #pragma unroll
-            for (int ct = 0; ct < 4; ++ct) sum[ct] = mine ? acc[ct] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             for (int r0 = 0; r0 < a.rank; r0 += 16 * RT) {
                 hold(g, r0);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     const int r = r0 + 16 * t + 4 * lg;
                     float hv[4];
-                    load4<WIDE>(a.H + row * a.rank + r, a.rank - r, hv);
+                    load4<WIDE>(h + r, a.rank - r, hv);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -323,20 +421,25 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a) {
                             sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][t][i], hv[i], sum[ct], 0, 0, 0);
                 }
             }
+            // a lane's column of the product is one row of Y: a row takes its
+            // own adapter's, and nothing of the others', not even their NaN
 #pragma unroll
             for (int ct = 0; ct < 4; ++ct)
-                if (mine) acc[ct] = sum[ct];
+                if (mix.id == g) all[ct] = sum[ct];
         }
-        if (mix.id < 0) continue;
+        turn(all, out);
+        const uint64_t on = __ballot(mix.id >= 0);     // bit r: row r has an adapter
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-            const int left = a.n_out - (o0 + 16 * ct + 4 * lg);
+        for (int q = 0; q < 4; ++q) {
+            const int r = 4 * q + lg;
+            if (!(on >> r & 1)) continue;
+            float* y = a.Y + (row0 + r) * a.n_out + o0 + 4 * li;
             if (WIDE && left >= 4) {
-                *reinterpret_cast<f32x4*>(y + 16 * ct) = acc[ct];
+                *reinterpret_cast<f32x4*>(y) += out[q];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (i < left) y[16 * ct + i] = acc[ct][i];
+                    if (i < left) y[i] += out[q][i];
             }
         }
     }
@@ -346,16 +449,15 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <typename TX, typename TW>
 ks_status_t launch_rows(const Args& a, hipStream_t stream, int num_cus) {
-    const bool wide_k = on16(a.X) && on16(a.A) && a.n_in % (16 / sizeof(TX)) == 0 && a.n_in % (16 / sizeof(TW)) == 0;
-    const bool wide_r = on16(a.B) && a.rank % 4 == 0;
-    // slices of the outputs until the card has about two workgroups a unit
-    int slices = static_cast<int>(std::max<int64_t>(1, 2 * num_cus / a.batch));
-    slices = std::max(1, std::min({slices, (a.n_out + kThreads - 1) / kThreads, 64}));
+    const bool wide = on16(a.X) && on16(a.A) && on16(a.B) && a.n_in % 8 == 0 && a.rank % 8 == 0;
+    // slices of the outputs until the card has about four workgroups a unit;
+    // at most one output a thread
+    int slices = static_cast<int>(std::max<int64_t>(1, 4 * num_cus / a.batch));
+    slices = std::min(slices, (a.n_out + kThreads - 1) / kThreads);
     const int slice = (a.n_out + slices - 1) / slices;
     const dim3 grid(static_cast<unsigned>(a.batch), static_cast<unsigned>((a.n_out + slice - 1) / slice));
-    return launch_kernel(wide_k && wide_r ? adapter_rows_kernel<TX, TW, true, true>
-                                          : adapter_rows_kernel<TX, TW, false, false>,
-                         grid, dim3(kThreads), 0, stream, a, slice);
+    return launch_kernel(wide ? adapter_rows_kernel<TX, TW, true> : adapter_rows_kernel<TX, TW, false>, grid, dim3(kThreads), 0,
+                         stream, a, slice);
 }
 
 template <typename TX, typename TW>
@@ -371,8 +473,9 @@ ks_status_t launch_down(const Args& a, hipStream_t stream) {
 template <typename TW>
 ks_status_t launch_up(const Args& a, hipStream_t stream) {
     const bool wide = on16(a.B) && on16(a.H) && on16(a.Y) && a.rank % 4 == 0 && a.n_out % 4 == 0;
-    const dim3 grid(static_cast<unsigned>((a.batch + kUpRows - 1) / kUpRows),
-                    static_cast<unsigned>((a.n_out + kUpCols - 1) / kUpCols));
+    const int64_t blocks = (a.batch + kUpRows - 1) / kUpRows * ((a.n_out + kUpCols - 1) / kUpCols);
+    if (blocks >= int64_t(1) << 31) return KS_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(blocks));
     void (*kernel)(Args);
     if (a.rank <= 16) kernel = wide ? adapter_up_kernel<TW, 1, true> : adapter_up_kernel<TW, 1, false>;
     else kernel = wide ? adapter_up_kernel<TW, 2, true> : adapter_up_kernel<TW, 2, false>;

@@ -58,11 +58,17 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     const int per = ((batch + 15) / 16 + 63) / 64 * 64;
     const int i0 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(wave) * per));
     const int i1 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(i0) + per));
+    constexpr int kBatch = 8;       // loads in flight
     int own = 0, less = 0;
-    for (int i = i0; i < i1; i += 64) {
-        const int id = i + lane < i1 ? ids[i + lane] : -1;
-        own += __popcll(__ballot(id == g));
-        less += __popcll(__ballot(id >= 0 && id < g));
+    for (int i = i0; i < i1; i += 64 * kBatch) {
+        int id[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            own += __popcll(__ballot(id[u] == g));
+            less += __popcll(__ballot(id[u] >= 0 && id[u] < g));
+        }
     }
     if (lane == 0) {
         wave_own[wave] = own;
@@ -77,11 +83,16 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     }
     at += start;
     if (own) {
-        for (int i = i0; i < i1; i += 64) {
-            const bool mine = i + lane < i1 && ids[i + lane] == g;
-            const uint64_t all = __ballot(mine);
-            if (mine) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = i + lane;
-            at += __popcll(all);
+        for (int i = i0; i < i1; i += 64 * kBatch) {
+            int id[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint64_t all = __ballot(id[u] == g);
+                if (id[u] == g) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = i + 64 * u + lane;
+                at += __popcll(all);
+            }
         }
     }
     const Segment seg = {start, total};
@@ -113,26 +124,25 @@ __device__ __forceinline__ float value_at(const T* p, int64_t row, int64_t width
 template <typename TW, int RT>
 __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const TW* B, const float* H,
                                                           const float* scale, const int* order, const Slot* slots,
-                                                          int64_t batch, int n_out, int rank, float* e_part,
+                                                          int64_t batch, int n_out, int rank, unsigned splits, float* e_part,
                                                           float* db_part) {
     constexpr int kR = 16 * RT + 1;
+    constexpr int kB = 16 * RT + (sizeof(TW) == 4 ? 1 : 2);   // bf16 pairs: an odd number of 4-byte words
     __shared__ float tile[64 * kPitch];
-    __shared__ float bt[kColsY * kR];      // B[o][r], all columns of the workgroup
+    __shared__ TW bt[kColsY * kB];         // B[o][r], all columns of the workgroup
     __shared__ float ht[64 * kR];          // H[n][r], the row tile's
     __shared__ int row_of[kMaxRows];
-    const Slot s = slots[blockIdx.x];
+    // neighbouring workgroups take neighbouring columns of the same rows
+    const int split = blockIdx.x % splits, slot = blockIdx.x / splits;
+    const Slot s = slots[slot];
     if (s.len == 0) return;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, li = lane % 16, lg = lane / 16;
-    const int r0 = blockIdx.z * 16 * RT, base = blockIdx.y * kColsY;
+    const int r0 = blockIdx.z * 16 * RT, base = split * kColsY;
     const TW* b = B + static_cast<int64_t>(s.adapter) * n_out * rank;
     const bool wide = n_out % 4 == 0 && reinterpret_cast<uintptr_t>(dY) % 16 == 0;
     const float factor = scale[s.adapter];
     const int row_tiles = (s.len + 63) / 64, col_tiles = min(kColsY / 64, (n_out - base + 63) / 64);
     for (int i = tid; i < kMaxRows; i += kThreads) row_of[i] = order[s.start + min(i, s.len - 1)];
-    for (int i = tid; i < kColsY * 16 * RT; i += kThreads) {
-        const int o = i / (16 * RT), r = i % (16 * RT);
-        bt[o * kR + r] = value_at(b, base + o, rank, r0 + r, base + o < n_out && r0 + r < rank);
-    }
     __syncthreads();
     // thread: rows tid / 16 + 16 q of a tile, four columns from 4 (tid % 16)
     float next[4][4], hnext[4 * RT];
@@ -165,6 +175,13 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
 #pragma unroll
         for (int t = 0; t < RT; ++t) d[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     load(0, 0);
+#pragma unroll 16
+    for (int i = tid; i < kColsY * 16 * RT; i += kThreads) {
+        const int o = i / (16 * RT), r = i % (16 * RT);
+        const bool in = base + o < n_out && r0 + r < rank;
+        const TW w = b[in ? static_cast<int64_t>(base + o) * rank + r0 + r : 0];
+        bt[o * kB + r] = in ? w : TW(0);
+    }
     for (int rt = 0; rt < row_tiles; ++rt) {
         f32x4 e[RT];
 #pragma unroll
@@ -190,8 +207,8 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
                 const float x = tile[(16 * wave + li) * kPitch + 16 * lg + j];
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    e[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, bt[(ct * 64 + 16 * lg + j) * kR + 16 * t + li], e[t],
-                                                                0, 0, 0);
+                    e[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, to_f32(bt[(ct * 64 + 16 * lg + j) * kB + 16 * t + li]),
+                                                                e[t], 0, 0, 0);
             }
             if (db_part) {
 #pragma unroll
@@ -210,7 +227,7 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
             for (int i = 0; i < 4; ++i) {
                 const int at = rt * 64 + 16 * wave + 4 * lg + i, r = r0 + 16 * t + li;
                 if (at < s.len && r < rank)
-                    e_part[(static_cast<int64_t>(blockIdx.y) * batch + s.start + at) * rank + r] = factor * e[t][i];
+                    e_part[(static_cast<int64_t>(split) * batch + s.start + at) * rank + r] = factor * e[t][i];
             }
     }
     if (!db_part) return;
@@ -222,108 +239,170 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
             for (int i = 0; i < 4; ++i) {
                 const int o = base + ct * 64 + 16 * wave + 4 * lg + i, r = r0 + 16 * t + li;
                 if (o < n_out && r < rank)
-                    db_part[(static_cast<int64_t>(blockIdx.x) * n_out + o) * rank + r] = d[ct][t][i];
+                    db_part[(static_cast<int64_t>(slot) * n_out + o) * rank + r] = d[ct][t][i];
             }
 }
 
-// dX and partial dA of one block of rows and 128 columns of X. A value of X is
-// used once, so it goes straight to the lane that multiplies it.
+// Orders the wave's LDS accesses before and after it: its lanes exchange values.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// dX and partial dA of one block of rows and 128 columns of X, in tiles of
+// 64 x 64. X goes through LDS for dA (inner index: the rows; a wave takes 16
+// columns); for dX a wave takes 16 rows, forms its product with the columns
+// along the instruction's rows and turns it in LDS, so that dX is read and
+// written in runs of 256 bytes.
 template <typename TX, typename TW, int RT>
 __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW* A, const float* E, const int* order,
-                                                          const Slot* slots, int n_in, int rank, float* dX,
-                                                          float* da_part) {
+                                                          const Slot* slots, int n_in, int rank, unsigned splits,
+                                                          float* dX, float* da_part) {
+    constexpr int kR = 16 * RT + 1, kTiles = kColsX / 64, kTurn = 68;
+    __shared__ float tile[64 * kPitch];
+    __shared__ float et[64 * kR];                       // E[n][r] of the row tile
+    __shared__ __align__(16) float cross[4][16 * kTurn];
     __shared__ int row_of[kMaxRows];
-    const Slot s = slots[blockIdx.x];
+    const int split = blockIdx.x % splits, slot = blockIdx.x / splits;
+    const Slot s = slots[slot];
     if (s.len == 0) return;
-    constexpr int kTiles = kColsX / 64;
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, li = lane % 16, lg = lane / 16;
     const TW* a = A + static_cast<int64_t>(s.adapter) * rank * n_in;
-    const bool wide = n_in % 4 == 0 && reinterpret_cast<uintptr_t>(dX) % 16 == 0;
-    const int row_tiles = (s.len + 63) / 64, base = blockIdx.y * kColsX;
+    const bool wide_x = n_in % 4 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
+    const bool wide_d = n_in % 4 == 0 && reinterpret_cast<uintptr_t>(dX) % 16 == 0;
+    const int row_tiles = (s.len + 63) / 64, base = split * kColsX;
+    const int col_tiles = min(kTiles, (n_in - base + 63) / 64);
     for (int i = tid; i < kMaxRows; i += kThreads) row_of[i] = order[s.start + min(i, s.len - 1)];
     __syncthreads();
     for (int r0 = 0; r0 < rank; r0 += 16 * RT) {
-        // A[r][k] of the workgroup's columns, for dX
-        float av[kTiles][RT][4];
+        // A[r][k], inner index r, of both column tiles
+        float av[kTiles][4][RT][4];
+        if (dX) {
 #pragma unroll
-        for (int ct = 0; ct < kTiles; ++ct)
+            for (int ct = 0; ct < kTiles; ++ct)
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = r0 + 16 * t + 4 * lg + j, k = base + ct * 64 + 16 * wave + li;
-                    av[ct][t][j] = value_at(a, r, n_in, k, r < rank && k < n_in);
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = r0 + 16 * t + 4 * lg + j, k = base + ct * 64 + 16 * c + li;
+                            av[ct][c][t][j] = value_at(a, r, n_in, k, r < rank && k < n_in);
+                        }
+        }
+        // thread: rows tid / 16 + 16 q of a tile, four columns from 4 (tid % 16)
+        float next[4][4], enext[4 * RT];
+        auto load = [&](int rt, int ct) {
+            if (ct == 0) {
+#pragma unroll
+                for (int q = 0; q < 4 * RT; ++q) {
+                    const int n = (q * kThreads + tid) / (16 * RT), r = r0 + (q * kThreads + tid) % (16 * RT);
+                    const int at = rt * 64 + n;
+                    enext[q] = value_at(E, s.start + at, rank, r, at < s.len && r < rank);
                 }
+            }
+            if (!da_part) return;
+            const int k = base + ct * 64 + 4 * (tid % 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int at = rt * 64 + tid / 16 + 16 * q;
+                const TX* src = X + static_cast<int64_t>(row_of[at]) * n_in + k;
+                const int valid = at < s.len ? n_in - k : 0;
+                if (wide_x && valid >= 4) {
+                    load4_f32(src, next[q]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) next[q][i] = i < valid ? to_f32(src[i]) : 0.0f;
+                }
+            }
+        };
         f32x4 d[kTiles][RT];
 #pragma unroll
         for (int c = 0; c < kTiles; ++c)
 #pragma unroll
             for (int t = 0; t < RT; ++t) d[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        load(0, 0);
         for (int rt = 0; rt < row_tiles; ++rt) {
-            if (da_part) {
-                float en[RT][16];
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
+            for (int ct = 0; ct < kTiles; ++ct) {
+                if (ct >= col_tiles) break;
+                // this wave's rows of dX, four runs of 256 bytes
+                f32x4 y[4];
+                const int k = base + ct * 64 + 4 * li;
+                if (dX) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = rt * 64 + 16 * wave + 4 * q + lg;
+                        const float* src = dX + static_cast<int64_t>(row_of[at]) * n_in + k;
+                        const int valid = at < s.len ? n_in - k : 0;
+                        y[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (wide_d && valid >= 4) {
+                            y[q] = *reinterpret_cast<const f32x4*>(src);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < valid) y[q][i] = src[i];
+                        }
+                    }
+                }
+                __syncthreads();
+                if (da_part) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tile[(tid / 16 + 16 * q) * kPitch + 4 * (tid % 16) + i] = next[q][i];
+                }
+                if (ct == 0) {
+#pragma unroll
+                    for (int q = 0; q < 4 * RT; ++q)
+                        et[(q * kThreads + tid) / (16 * RT) * kR + (q * kThreads + tid) % (16 * RT)] = enext[q];
+                }
+                __syncthreads();
+                if (ct + 1 < col_tiles) load(rt, ct + 1);
+                else if (rt + 1 < row_tiles) load(rt + 1, 0);
+                if (da_part) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int at = rt * 64 + 16 * lg + j, r = r0 + 16 * t + li;
-                        en[t][j] = value_at(E, s.start + at, rank, r, at < s.len && r < rank);
-                    }
-#pragma unroll
-                for (int ct = 0; ct < kTiles; ++ct) {
-                    const int k = base + ct * 64 + 16 * wave + li;
-                    float x[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int at = rt * 64 + 16 * lg + j;
-                        x[j] = value_at(X, row_of[at], n_in, k, at < s.len && k < n_in);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                        const float x = tile[(16 * lg + j) * kPitch + 16 * wave + li];
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
-                            d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(en[t][j], x[j], d[ct][t], 0, 0, 0);
+                            d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(et[(16 * lg + j) * kR + 16 * t + li], x,
+                                                                            d[ct][t], 0, 0, 0);
+                    }
                 }
-            }
-            if (dX) {
+                if (dX) {
+                    f32x4 sum[4];
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int at = rt * 64 + 16 * nt + li;
-                    float ev[RT][4];
+                    for (int c = 0; c < 4; ++c) sum[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int r = r0 + 16 * t + 4 * lg + j;
-                            ev[t][j] = value_at(E, s.start + at, rank, r, at < s.len && r < rank);
-                        }
-                    float* row = dX + static_cast<int64_t>(row_of[at]) * n_in;
+                            const float ev = et[(16 * wave + li) * kR + 16 * t + 4 * lg + j];
 #pragma unroll
-                    for (int ct = 0; ct < kTiles; ++ct) {
-                        // lane: columns k .. k + 3 of its row
-                        const int k = base + ct * 64 + 16 * wave + 4 * lg;
+                            for (int c = 0; c < 4; ++c)
+                                sum[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[ct][c][t][j], ev, sum[c], 0, 0, 0);
+                        }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<f32x4*>(cross[wave] + li * kTurn + 16 * c + 4 * lg) = sum[c];
+                    wave_fence();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = rt * 64 + 16 * wave + 4 * q + lg;
+                        const f32x4 add = *reinterpret_cast<const f32x4*>(cross[wave] + (4 * q + lg) * kTurn + 4 * li);
+                        float* dst = dX + static_cast<int64_t>(row_of[at]) * n_in + k;
                         const int valid = at < s.len ? n_in - k : 0;
-                        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if (wide && valid >= 4) {
-                            acc = *reinterpret_cast<const f32x4*>(row + k);
+                        if (wide_d && valid >= 4) {
+                            *reinterpret_cast<f32x4*>(dst) = y[q] + add;
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (i < valid) acc[i] = row[k + i];
-                        }
-#pragma unroll
-                        for (int t = 0; t < RT; ++t)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(av[ct][t][j], ev[t][j], acc, 0, 0, 0);
-                        if (wide && valid >= 4) {
-                            *reinterpret_cast<f32x4*>(row + k) = acc;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (i < valid) row[k + i] = acc[i];
+                                if (i < valid) dst[i] = y[q][i] + add[i];
                         }
                     }
+                    wave_fence();
                 }
             }
         }
@@ -337,10 +416,26 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                         const int r = r0 + 16 * t + 4 * lg + i;
                         const int k = base + ct * 64 + 16 * wave + li;
                         if (r < rank && k < n_in)
-                            da_part[(static_cast<int64_t>(blockIdx.x) * rank + r) * n_in + k] = d[ct][t][i];
+                            da_part[(static_cast<int64_t>(slot) * rank + r) * n_in + k] = d[ct][t][i];
                     }
         }
+        __syncthreads();   // the next ranks' tiles go over these
     }
+}
+
+// n values `stride` apart, added in order; eight loads in flight.
+__device__ __forceinline__ float sum_of(const float* p, int64_t stride, int n) {
+    float sum = 0.0f;
+    int i = 0;
+    for (; i + 8 <= n; i += 8) {
+        float x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = p[(i + u) * stride];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += x[u];
+    }
+    for (; i < n; ++i) sum += p[i * stride];
+    return sum;
 }
 
 // E[i] = sum over the column ranges; `parts` planes of `stride` values.
@@ -348,9 +443,7 @@ __global__ __launch_bounds__(kThreads) void sum_planes_kernel(const float* part,
                                                               float* out) {
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        float sum = 0.0f;
-        for (int p = 0; p < parts; ++p) sum += part[p * stride + i];
-        out[i] = sum;
+        out[i] = sum_of(part + i, stride, parts);
     }
 }
 
@@ -363,9 +456,7 @@ __global__ __launch_bounds__(kThreads) void sum_slots_kernel(const float* part, 
     const int s0 = first_slot(seg, g, block), blocks = (seg.len + block - 1) / block;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < size;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        float sum = 0.0f;
-        for (int b = 0; b < blocks; ++b) sum += part[(s0 + b) * size + i];
-        out[g * size + i] = sum;
+        out[g * size + i] = sum_of(part + s0 * size + i, size, blocks);
     }
 }
 
@@ -374,12 +465,12 @@ struct Layout {
     int block, n_slots, splits;
 };
 
-// Rows of a block: as many as leave each pass about two workgroups a compute
-// unit of the card's 256 (fewer partial sums against more of the card busy).
+// Rows of a block: as many as leave the passes about four and two workgroups a
+// compute unit of the card's 256 (fewer partial sums against loads in flight).
 int block_rows(int n_in, int n_out, int64_t batch) {
     int block = kMaxRows;
-    while (block > 64 && (batch / block * ((n_out + kColsY - 1) / kColsY) < 512 ||
-                          batch / block * ((n_in + kColsX - 1) / kColsX) < 256))
+    while (block > 64 && (batch / block * ((n_out + kColsY - 1) / kColsY) < 1024 ||
+                          batch / block * ((n_in + kColsX - 1) / kColsX) < 512))
         block /= 2;
     return block;
 }
@@ -425,10 +516,12 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
         return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 16384));
     };
     if (c.batch > 0) {
-        const dim3 gy(static_cast<unsigned>(l.n_slots), static_cast<unsigned>(l.splits),
+        if (static_cast<int64_t>(l.n_slots) * std::max(l.splits, (c.n_in + kColsX - 1) / kColsX) >= int64_t(1) << 31)
+            return KS_ERR_UNSUPPORTED;
+        const dim3 gy(static_cast<unsigned>(l.n_slots) * l.splits, 1,
                       static_cast<unsigned>((c.rank + 16 * RT - 1) / (16 * RT)));
         st = launch_kernel(grad_y_kernel<TW, RT>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
-                           c.batch, c.n_out, c.rank, e_part, dB ? w_part : static_cast<float*>(nullptr));
+                           c.batch, c.n_out, c.rank, static_cast<unsigned>(l.splits), e_part, dB ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
         if (l.splits > 1) {
             const int64_t n = c.batch * c.rank;
@@ -444,9 +537,10 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
         if (st != KS_OK) return st;
     }
     if (c.batch > 0) {
-        const dim3 gx(static_cast<unsigned>(l.n_slots), static_cast<unsigned>((c.n_in + kColsX - 1) / kColsX));
+        const unsigned splits = static_cast<unsigned>((c.n_in + kColsX - 1) / kColsX);
+        const dim3 gx(static_cast<unsigned>(l.n_slots) * splits);
         st = launch_kernel(grad_x_kernel<TX, TW, RT>, gx, dim3(kThreads), 0, c.stream, static_cast<const TX*>(X), A, E,
-                           order, slots, c.n_in, c.rank, dX, dA ? w_part : static_cast<float*>(nullptr));
+                           order, slots, c.n_in, c.rank, splits, dX, dA ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
     }
     if (dA) {

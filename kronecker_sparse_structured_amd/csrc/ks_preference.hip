@@ -9,8 +9,10 @@
 // A row of logits is 8 KB to 200 KB and everything else is small, so the work
 // is one stream over the logits for l and a second one for dx: the gradient's
 // factor c[s] depends on every row of both sequences of a pair, so no row can
-// be finished in the first stream. The caller runs ranges of pairs whose
-// logits fit the last cache, so that the second stream does not come from HBM.
+// be finished in the first stream. The second stream takes the rows in the
+// opposite order and finds those read last in the 256 MB last cache. (Ranges of
+// pairs small enough for that cache, one after another, were slower: a launch
+// of 1024 rows of 100 KB reached 3.8 TB/s where one of 8192 reaches 5.4.)
 //
 // One workgroup a row. The maximum and the sum of exponentials are kept
 // together in one pass: each lane keeps its own running pair (m, s), rescales
@@ -87,19 +89,6 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
 
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
-struct Rows {
-    ks_logits_t x;
-    int64_t s0, half;   // block of sequences [s0, s0 + n) and, beside it, + half
-    int n;              // sequences in the first block
-};
-
-// The sequence and position of a row number of the launch.
-__device__ __forceinline__ void row_of(const Rows& r, int64_t row, int64_t* s, int64_t* t) {
-    const int64_t q = row / r.x.tokens;
-    *t = row - q * r.x.tokens;
-    *s = q < r.n ? r.s0 + q : r.s0 + r.half + (q - r.n);
-}
-
 // Joins (m2, s2) to (m, s).
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     const float top = fmaxf(m, m2);
@@ -108,13 +97,11 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void token_logp_kernel(const Rows r, float* tokens, float* stats) {
+__global__ __launch_bounds__(kThreads) void token_logp_kernel(const ks_logits_t x_, float* tokens, float* stats) {
     __shared__ float wave_m[kWaves], wave_s[kWaves];
     constexpr int E = kVec<T>;
-    int64_t s_, t_;
-    row_of(r, blockIdx.x, &s_, &t_);
-    const int64_t at = s_ * r.x.tokens + t_;
-    const int64_t label = r.x.labels[s_ * r.x.label_stride + t_];
+    const int64_t at = blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
+    const int64_t label = x_.labels[s_ * x_.label_stride + t_];
     if (label < 0) {
         if (threadIdx.x == 0) {
             tokens[at] = 0.0f;
@@ -125,8 +112,8 @@ __global__ __launch_bounds__(kThreads) void token_logp_kernel(const Rows r, floa
         }
         return;
     }
-    const T* row = static_cast<const T*>(r.x.data) + s_ * r.x.seq_stride + t_ * r.x.row_stride;
-    const int V = static_cast<int>(r.x.vocab);
+    const T* row = static_cast<const T*>(x_.data) + s_ * x_.seq_stride + t_ * x_.row_stride;
+    const int V = static_cast<int>(x_.vocab);
     const int head = head_of(row, V);
     const int vecs = (V - head) / E;
     const int tail = head + vecs * E;
@@ -191,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void token_logp_kernel(const Rows r, floa
     if (tid == 0) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) join(m, s, wave_m[w], wave_s[w]);
-        const float x = label < r.x.vocab ? to_f32(row[label]) : __builtin_nanf("");
+        const float x = label < x_.vocab ? to_f32(row[label]) : __builtin_nanf("");
         tokens[at] = static_cast<float>((static_cast<double>(x) - static_cast<double>(m)) -
                                         log(static_cast<double>(s)));
         if (stats) {
@@ -217,46 +204,49 @@ __global__ __launch_bounds__(kThreads) void sequence_sum_kernel(const float* tok
     if (threadIdx.x % 64 == 0) total[s] = static_cast<float>(x);
 }
 
-__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
-
-// Rewards and gradient factors of pairs [p0, p0 + n), a wave a pair; with the
-// last range the loss over all pairs, from the rewards. One workgroup: a few
-// thousand values beside megabytes of logits.
-__global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, int64_t p0, int64_t n, const float* tokens,
-                                                         const float* ref, int64_t ref_stride, float beta,
-                                                         float smoothing, float* loss, float* rewards, float* grad) {
+// Rewards, the loss and the gradient's factors. One workgroup, a wave a
+// sequence at a time and eight tokens a lane in flight: a few thousand values
+// beside megabytes of logits (4 us at 16 x 512 tokens).
+__global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, const float* tokens, const float* ref,
+                                                         int64_t ref_stride, float beta, float smoothing, float* loss,
+                                                         float* rewards, float* grad) {
     __shared__ double sums[16];
-    const int64_t P = x.sequences / 2, T = x.tokens;
+    const int64_t S = x.sequences, P = S / 2, T = x.tokens;
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    for (int64_t p = p0 + wave; p < p0 + n; p += 16) {
-        double R[2];
+    constexpr int U = 8;
+    for (int64_t s = wave; s < S; s += 16) {
+        const int64_t* labels = x.labels + s * x.label_stride;
+        const float* l = tokens + s * T;
+        const float* r = ref + s * ref_stride;
+        double sum = 0.0;
+        for (int64_t t0 = 0; t0 < T; t0 += 64 * U) {
+            int64_t label[U];
+            float a[U], b[U];
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int64_t s = p + side * P;
-            double sum = 0.0;
-            for (int64_t t = lane; t < T; t += 64) {
-                if (x.labels[s * x.label_stride + t] >= 0)
-                    sum += static_cast<double>(tokens[s * T + t]) - static_cast<double>(ref[s * ref_stride + t]);
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t0 + 64 * u + lane, in = t < T ? t : 0;
+                label[u] = t < T ? labels[in] : -1;
+                a[u] = l[in];
+                b[u] = r[in];
             }
-            R[side] = static_cast<double>(beta) * wave_sum(sum);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (label[u] >= 0) sum += static_cast<double>(a[u]) - static_cast<double>(b[u]);
         }
-        if (lane == 0) {
-            const double z = R[0] - R[1], e = smoothing;
-            const double up = 1.0 / (1.0 + exp(-z)), un = 1.0 / (1.0 + exp(z));
-            const double c = static_cast<double>(beta) * (e * up - (1.0 - e) * un) / static_cast<double>(P);
-            rewards[p] = static_cast<float>(R[0]);
-            rewards[p + P] = static_cast<float>(R[1]);
-            grad[p] = static_cast<float>(c);
-            grad[p + P] = static_cast<float>(-c);
-        }
+        sum = wave_sum(sum);
+        if (lane == 0) rewards[s] = static_cast<float>(static_cast<double>(beta) * sum);
     }
-    if (p0 + n < P) return;
-    __threadfence_block();
     __syncthreads();
     double sum = 0.0;
     for (int64_t p = threadIdx.x; p < P; p += 1024) {
         const double z = static_cast<double>(rewards[p]) - static_cast<double>(rewards[p + P]), e = smoothing;
-        sum += (1.0 - e) * softplus(-z) + e * softplus(z);
+        // exp(-|z|) gives both sigmoids and both logarithms without overflow
+        const double d = exp(-fabs(z)), near = 1.0 / (1.0 + d), far = d / (1.0 + d), more = log1p(d);
+        const double up = z >= 0.0 ? near : far, un = z >= 0.0 ? far : near;
+        sum += (1.0 - e) * (more + fmax(-z, 0.0)) + e * (more + fmax(z, 0.0));
+        const double c = static_cast<double>(beta) * (e * up - (1.0 - e) * un) / static_cast<double>(P);
+        grad[p] = static_cast<float>(c);
+        grad[p + P] = static_cast<float>(-c);
     }
     sum = wave_sum(sum);
     if (lane == 0) sums[wave] = sum;
@@ -271,17 +261,17 @@ __global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, in
 // dx of one row. The output row may start at another place of a 16-byte
 // granule than the input row: then it goes element-wise.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logit_grad_kernel(const Rows r, const float* stats, const float* grad,
+__global__ __launch_bounds__(kThreads) void logit_grad_kernel(const ks_logits_t x_, const float* stats, const float* grad,
                                                               const float* upstream, T* d, int64_t d_seq,
                                                               int64_t d_row) {
     constexpr int E = kVec<T>;
-    int64_t s_, t_;
-    row_of(r, blockIdx.x, &s_, &t_);
-    const int64_t at = s_ * r.x.tokens + t_;
-    const int64_t label = r.x.labels[s_ * r.x.label_stride + t_];
-    const T* row = static_cast<const T*>(r.x.data) + s_ * r.x.seq_stride + t_ * r.x.row_stride;
+    // the rows that the first stream read last come first: the last cache still
+    // holds some 200 MB of them
+    const int64_t at = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
+    const int64_t label = x_.labels[s_ * x_.label_stride + t_];
+    const T* row = static_cast<const T*>(x_.data) + s_ * x_.seq_stride + t_ * x_.row_stride;
     T* out = d + s_ * d_seq + t_ * d_row;
-    const int V = static_cast<int>(r.x.vocab);
+    const int V = static_cast<int>(x_.vocab);
     const int head = head_of(out, V);
     const int vecs = (V - head) / E;
     const int tail = head + vecs * E;
@@ -299,8 +289,8 @@ __global__ __launch_bounds__(kThreads) void logit_grad_kernel(const Rows r, cons
     if (upstream) c *= *upstream;
     const float scale = -c / stats[2 * at + 1];
     // a label outside the vocabulary has no place to go: the whole row says so
-    const float c_label = label < r.x.vocab ? c : __builtin_nanf("");
-    const int place = label < r.x.vocab ? static_cast<int>(label) : 0;
+    const float c_label = label < x_.vocab ? c : __builtin_nanf("");
+    const int place = label < x_.vocab ? static_cast<int>(label) : 0;
     auto one = [&](int v) {
         float y = scale * exp_of(to_f32(row[v]) - m);
         if (v == place) y += c_label;
@@ -338,50 +328,36 @@ __global__ __launch_bounds__(kThreads) void logit_grad_kernel(const Rows r, cons
     for (; v < vecs; v += kThreads) vec(v, body[v]);
 }
 
-Rows rows_of(const LogitsCall& c, int64_t s0, int64_t n, int64_t half) {
-    Rows r;
-    r.x = c.x;
-    r.s0 = s0;
-    r.n = static_cast<int>(n);
-    r.half = half;
-    return r;
-}
-
 }  // namespace
 
-ks_status_t launch_token_logp(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, float* tokens, float* stats) {
-    const int64_t rows = (half ? 2 * n : n) * c.x.tokens;
+ks_status_t launch_token_logp(const ks_logits_t& x, float* tokens, float* stats, hipStream_t stream) {
+    const int64_t rows = x.sequences * x.tokens;
     if (rows == 0) return KS_OK;
-    const Rows r = rows_of(c, s0, n, half);
-    const dim3 grid(static_cast<unsigned>(rows));
-    return c.x.elem == KS_ELEM_BF16
-               ? launch_kernel(token_logp_kernel<bf16_t>, grid, dim3(kThreads), 0, c.stream, r, tokens, stats)
-               : launch_kernel(token_logp_kernel<float>, grid, dim3(kThreads), 0, c.stream, r, tokens, stats);
+    return launch_kernel(x.elem == KS_ELEM_BF16 ? token_logp_kernel<bf16_t> : token_logp_kernel<float>,
+                         dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, x, tokens, stats);
 }
 
-ks_status_t launch_sequence_sum(const LogitsCall& c, const float* tokens, float* total) {
-    if (c.x.sequences == 0) return KS_OK;
-    return launch_kernel(sequence_sum_kernel, dim3(static_cast<unsigned>((c.x.sequences + kWaves - 1) / kWaves)),
-                         dim3(kThreads), 0, c.stream, tokens, c.x.tokens, c.x.sequences, total);
+ks_status_t launch_sequence_sum(const ks_logits_t& x, const float* tokens, float* total, hipStream_t stream) {
+    return launch_kernel(sequence_sum_kernel, dim3(static_cast<unsigned>((x.sequences + kWaves - 1) / kWaves)),
+                         dim3(kThreads), 0, stream, tokens, x.tokens, x.sequences, total);
 }
 
-ks_status_t launch_pair_loss(const LogitsCall& c, int64_t p0, int64_t n, const float* tokens, const float* ref,
-                             int64_t ref_stride, float beta, float smoothing, float* loss, float* rewards,
-                             float* grad) {
-    return launch_kernel(pair_loss_kernel, dim3(1), dim3(1024), 0, c.stream, c.x, p0, n, tokens, ref, ref_stride, beta,
-                         smoothing, loss, rewards, grad);
+ks_status_t launch_pair_loss(const ks_logits_t& x, const float* tokens, const float* ref, int64_t ref_stride,
+                             float beta, float smoothing, float* loss, float* rewards, float* grad,
+                             hipStream_t stream) {
+    return launch_kernel(pair_loss_kernel, dim3(1), dim3(1024), 0, stream, x, tokens, ref, ref_stride, beta, smoothing,
+                         loss, rewards, grad);
 }
 
-ks_status_t launch_logit_grad(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, const float* stats,
-                              const float* grad, const float* upstream, void* d, int64_t d_seq, int64_t d_row) {
-    const int64_t rows = (half ? 2 * n : n) * c.x.tokens;
+ks_status_t launch_logit_grad(const ks_logits_t& x, const float* stats, const float* grad, const float* upstream,
+                              void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
+    const int64_t rows = x.sequences * x.tokens;
     if (rows == 0) return KS_OK;
-    const Rows r = rows_of(c, s0, n, half);
     const dim3 grid(static_cast<unsigned>(rows));
-    if (c.x.elem == KS_ELEM_BF16)
-        return launch_kernel(logit_grad_kernel<bf16_t>, grid, dim3(kThreads), 0, c.stream, r, stats, grad, upstream,
+    if (x.elem == KS_ELEM_BF16)
+        return launch_kernel(logit_grad_kernel<bf16_t>, grid, dim3(kThreads), 0, stream, x, stats, grad, upstream,
                              static_cast<bf16_t*>(d), d_seq, d_row);
-    return launch_kernel(logit_grad_kernel<float>, grid, dim3(kThreads), 0, c.stream, r, stats, grad, upstream,
+    return launch_kernel(logit_grad_kernel<float>, grid, dim3(kThreads), 0, stream, x, stats, grad, upstream,
                          static_cast<float*>(d), d_seq, d_row);
 }
 

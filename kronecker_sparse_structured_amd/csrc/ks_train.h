@@ -34,19 +34,15 @@ ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const voi
 
 // ---- preference loss (ks_preference.hip)
 
-struct LogitsCall {
-    ks_logits_t x;
-    hipStream_t stream;
-};
-
-// Rows of sequences [s0, s0 + n) and, if pairs > 0, of [s0 + half, s0 + half + n).
-ks_status_t launch_token_logp(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, float* tokens, float* stats);
-ks_status_t launch_sequence_sum(const LogitsCall& c, const float* tokens, float* total);
-ks_status_t launch_pair_loss(const LogitsCall& c, int64_t p0, int64_t n, const float* tokens, const float* ref,
-                             int64_t ref_stride, float beta, float smoothing, float* loss, float* rewards,
-                             float* grad);
-ks_status_t launch_logit_grad(const LogitsCall& c, int64_t s0, int64_t n, int64_t half, const float* stats,
-                              const float* grad, const float* upstream, void* d, int64_t d_seq, int64_t d_row);
+// One row of logits a workgroup (none: nothing is launched); the pair loss is
+// one workgroup.
+ks_status_t launch_token_logp(const ks_logits_t& x, float* tokens, float* stats, hipStream_t stream);
+ks_status_t launch_sequence_sum(const ks_logits_t& x, const float* tokens, float* total, hipStream_t stream);
+ks_status_t launch_pair_loss(const ks_logits_t& x, const float* tokens, const float* ref, int64_t ref_stride,
+                             float beta, float smoothing, float* loss, float* rewards, float* grad,
+                             hipStream_t stream);
+ks_status_t launch_logit_grad(const ks_logits_t& x, const float* stats, const float* grad, const float* upstream,
+                              void* d, int64_t d_seq, int64_t d_row, hipStream_t stream);
 
 // ---- optimizer (ks_adamw.hip)
 

@@ -147,16 +147,6 @@ ks_status_t check_backward(const ks_adapters_t* ad, const int32_t* ids, const fl
     return KS_OK;
 }
 
-// Rows of a range: Y's part of it stays in the 256 MB last cache (with X's and
-// the chain's intermediate beside it) until the adapters have added to it.
-constexpr int64_t kRangeBytes = int64_t(64) << 20;
-
-int64_t range_rows(int64_t n_out, int64_t batch) {
-    int64_t rows = std::max<int64_t>(1, kRangeBytes / (n_out * 4));
-    rows = std::max<int64_t>(256, rows / 256 * 256);
-    return std::min(rows, batch);
-}
-
 ks_status_t chain_widths(const ks_pattern_t* p, int n, const ks_adapters_t* ad) {
     const int64_t in = static_cast<int64_t>(p[0].a) * p[0].c * p[0].d;
     const int64_t out = static_cast<int64_t>(p[n - 1].a) * p[n - 1].b * p[n - 1].d;
@@ -252,10 +242,6 @@ uint64_t dlogit_bytes(const ks_logits_t* x, int64_t d_seq, int64_t d_row) {
 bool in_place(const ks_logits_t* x, const void* d, int64_t d_seq, int64_t d_row) {
     return d == x->data && d_row == x->row_stride && (x->sequences <= 1 || d_seq == x->seq_stride);
 }
-
-// Pairs of a range: both sequences' logits and their gradient's lines stay in
-// the 256 MB last cache between the two passes.
-constexpr int64_t kPairBytes = int64_t(96) << 20;
 
 // ---------------------------------------------------------------- optimizer
 
@@ -354,9 +340,6 @@ ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const 
     if (st != KS_OK) return st;
     st = chain_widths(p, n, ad);
     if (st != KS_OK) return st;
-    const int64_t rows = range_rows(ad->n_out, batch);
-    st = ks_chain_workspace_size(p, n, rows, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &need);
-    if (st != KS_OK) return st;
     // H, for callers that do not keep it
     *bytes = round256(need) + (ks::adapter_one_launch(batch) ? 0 : round256(static_cast<uint64_t>(batch) * ad->rank * 4));
     return KS_OK;
@@ -385,33 +368,21 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
                                  {ad->B, b_bytes(ad, wt)}}))
         return KS_ERR_OVERLAP;
     if (need > 0 && !aligned(ws, 16)) return KS_ERR_ALIGN;
-    const int64_t step = range_rows(ad->n_out, batch);
-    const bool one = ks::adapter_one_launch(batch);
     size_t chain_ws = 0;
-    st = ks_chain_workspace_size(p, n, step, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
+    st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
     if (st != KS_OK) return st;
-    if (!one && !H) H = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(chain_ws));
+    // the chain's own checks (weights, alignment, overlaps) come first: an
+    // argument error launches nothing
+    st = ks_chain_matmul(p, n, W, X, Y, batch, static_cast<ks_dtype_t>(code), ws, chain_ws, KS_CHAIN_AUTO, stream);
+    if (st != KS_OK) return st;
     int cus = 0;
-    for (int64_t r = 0; r < batch; r += step) {
-        const int64_t rows = std::min(step, batch - r);
-        const char* x = static_cast<const char*>(X) + r * ad->n_in * ks::elem_bytes(xt);
-        float* y = Y + r * ad->n_out;
-        // the chain's checks (weights, alignment, overlaps) come with its first range
-        st = ks_chain_matmul(p, n, W, x, y, rows, static_cast<ks_dtype_t>(code), ws, chain_ws, KS_CHAIN_AUTO, stream);
-        if (st != KS_OK) return st;
-        if (r == 0) {
-            st = current_cus(&cus);
-            if (st != KS_OK) return st;
-            // H for all rows at once, after the chain's checks: an argument
-            // error launches nothing
-            if (!one) st = ks::launch_adapter_down(adapter_call(ad, ids, xt, wt, batch, stream, cus), X, H);
-            if (st != KS_OK) return st;
-        }
-        const ks::AdapterCall c = adapter_call(ad, ids + r, xt, wt, rows, stream, cus);
-        st = one ? ks::launch_adapter_rows(c, x, y, H) : ks::launch_adapter_up(c, H + r * ad->rank, y);
-        if (st != KS_OK) return st;
-    }
-    return KS_OK;
+    st = current_cus(&cus);
+    if (st != KS_OK) return st;
+    const ks::AdapterCall c = adapter_call(ad, ids, xt, wt, batch, stream, cus);
+    if (ks::adapter_one_launch(batch)) return ks::launch_adapter_rows(c, X, Y, H);
+    if (!H) H = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(chain_ws));
+    st = ks::launch_adapter_down(c, X, H);
+    return st != KS_OK ? st : ks::launch_adapter_up(c, H, Y);
 }
 
 ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
@@ -473,9 +444,8 @@ ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, 
     if (any_overlap({{tokens, rows * 4}, {total, static_cast<uint64_t>(x->sequences) * 4}, {stats, rows * 8}},
                     {{x->data, logit_bytes(x)}, {x->labels, label_bytes(x)}}))
         return KS_ERR_OVERLAP;
-    const ks::LogitsCall c{*x, stream};
-    const ks_status_t run = ks::launch_token_logp(c, 0, x->sequences, 0, tokens, stats);
-    return run != KS_OK ? run : ks::launch_sequence_sum(c, tokens, total);
+    const ks_status_t run = ks::launch_token_logp(*x, tokens, stats, stream);
+    return run != KS_OK ? run : ks::launch_sequence_sum(*x, tokens, total, stream);
 }
 
 ks_status_t ks_preference_loss(const ks_logits_t* x, const float* ref, int64_t ref_stride, float beta, float smoothing,
@@ -507,21 +477,11 @@ ks_status_t ks_preference_loss(const ks_logits_t* x, const float* ref, int64_t r
                      {ref, span_bytes(x->sequences, ref_stride, 1, 0, x->tokens, 4)}}) ||
         any_overlap({{loss, 4}, {rewards, seqs}, {grad, seqs}, {tokens, rows * 4}, {stats, rows * 8}}, {logits}))
         return KS_ERR_OVERLAP;
-    const ks::LogitsCall c{*x, stream};
-    const int64_t P = x->sequences / 2;
-    const int64_t pair = std::max<int64_t>(1, 2 * x->tokens * x->row_stride * (x->elem == KS_ELEM_BF16 ? 2 : 4));
-    const int64_t step = dlogits ? std::max<int64_t>(1, kPairBytes / pair) : std::max<int64_t>(1, P);
-    int64_t p = 0;
-    do {
-        const int64_t n = std::min(step, P - p);
-        st = ks::launch_token_logp(c, p, n, P, tokens, stats);
-        if (st == KS_OK) st = ks::launch_pair_loss(c, p, n, tokens, ref, ref_stride, beta, smoothing, loss, rewards, grad);
-        if (st == KS_OK && dlogits)
-            st = ks::launch_logit_grad(c, p, n, P, stats, grad, nullptr, dlogits, d_seq_stride, d_row_stride);
-        if (st != KS_OK) return st;
-        p += n;
-    } while (p < P);
-    return KS_OK;
+    st = ks::launch_token_logp(*x, tokens, stats, stream);
+    if (st == KS_OK) st = ks::launch_pair_loss(*x, tokens, ref, ref_stride, beta, smoothing, loss, rewards, grad, stream);
+    if (st == KS_OK && dlogits)
+        st = ks::launch_logit_grad(*x, stats, grad, nullptr, dlogits, d_seq_stride, d_row_stride, stream);
+    return st;
 }
 
 ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, const float* grad, const float* upstream,
@@ -540,8 +500,7 @@ ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, con
                     {in_place(x, dlogits, d_seq_stride, d_row_stride) ? none : logits, {x->labels, label_bytes(x)},
                      {stats, rows * 8}, {grad, static_cast<uint64_t>(x->sequences) * 4}, {upstream, 4}}))
         return KS_ERR_OVERLAP;
-    return ks::launch_logit_grad(ks::LogitsCall{*x, stream}, 0, x->sequences, 0, stats, grad, upstream, dlogits,
-                                 d_seq_stride, d_row_stride);
+    return ks::launch_logit_grad(*x, stats, grad, upstream, dlogits, d_seq_stride, d_row_stride, stream);
 }
 
 ks_status_t ks_grad_norm_workspace_size(const ks_adamw_tensor_t* t, int n, size_t* bytes) {

@@ -176,16 +176,15 @@ def make_preference_function():
 
         @staticmethod
         def forward(ctx, logits, labels, ref, beta, smoothing):
-            loss, rewards, tokens, grad, stats = libks._preference_forward(logits, labels, ref, beta, smoothing, None,
-                                                                           None)
-            ctx.save_for_backward(logits, labels, stats, grad)
+            loss, rewards, tokens, scratch = libks._preference_forward(logits, labels, ref, beta, smoothing, None, None)
+            ctx.save_for_backward(logits, labels, scratch)
             ctx.mark_non_differentiable(rewards, tokens)
             return loss, rewards, tokens
 
         @staticmethod
         def backward(ctx, upstream, _rewards, _tokens):
-            logits, labels, stats, grad = ctx.saved_tensors
-            return libks._preference_backward(logits, labels, stats, grad, upstream.float().contiguous()), None, None, \
+            logits, labels, scratch = ctx.saved_tensors
+            return libks._preference_backward(logits, labels, scratch, upstream.float().contiguous()), None, None, \
                 None, None
 
     return PreferenceFunction

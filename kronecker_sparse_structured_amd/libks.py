@@ -217,6 +217,16 @@ def _stream(stream, *tensors) -> Optional[int]:
     return int(stream.cuda_stream)
 
 
+def _raw_stream(stream, index: int):
+    """_stream for a device index (no stream object where torch has the handle
+    at hand)."""
+    if stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return get(index) if get is not None else int(torch.cuda.current_stream(index).cuda_stream)
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
 def _raise(status: int, where: str, check: bool) -> int:
     if check and status != 0:
         raise KSError(status, where)
@@ -500,6 +510,24 @@ class AdapterChain:
         self._ad = ks_adapters_t(A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.n_in, self.n_out, self.rank,
                                  self.count)
         self._lib = load()
+        self._index = A.get_device()
+        self._sizes = {}
+
+    def _workspace(self, name, batch, code):
+        """A workspace and its size; the size of a batch is asked for once."""
+        import torch
+        key = (name, batch, code)
+        n = self._sizes.get(key)
+        if n is None:
+            size = ctypes.c_size_t(0)
+            _raise(getattr(self._lib, name)(self._p, self._n, self._ad, batch, code, size), name, True)
+            if len(self._sizes) > 256:
+                self._sizes.clear()
+            n = self._sizes[key] = size.value
+        if n == 0:
+            return None, 0, None
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return ws.data_ptr(), n, ws
 
     def _rows(self, X, ids):
         import torch
@@ -507,7 +535,7 @@ class AdapterChain:
             raise ValueError("X must be (batch, %d)" % self.n_in)
         if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
             raise ValueError("ids must be (batch,) int32")
-        if X.device != self.device or ids.device != self.device:
+        if X.get_device() != self._index or ids.get_device() != self._index:
             raise ValueError("X and ids must be on the weights' device")
         if not X.is_contiguous() or not ids.is_contiguous():
             raise ValueError("X and ids must be contiguous")
@@ -526,13 +554,10 @@ class AdapterChain:
         else:
             _check_out(out, (batch, self.n_out), torch.float32, self.device, "out")
         H = torch.empty((batch, self.rank), dtype=torch.float32, device=self.device) if keep else None
-        size = ctypes.c_size_t(0)
-        _raise(self._lib.ks_chain_adapter_workspace_size(self._p, self._n, self._ad, batch, code, size),
-               "ks_chain_adapter_workspace_size", True)
-        ws = torch.empty(size.value, dtype=torch.uint8, device=self.device) if size.value else None
+        ws, size, _keep = self._workspace("ks_chain_adapter_workspace_size", batch, code)
         _raise(self._lib.ks_chain_adapter_matmul(
             self._p, self._n, self._w, self._ad, ids.data_ptr(), X.data_ptr(), out.data_ptr(), _ptr(H), batch, code,
-            _ptr(ws), size.value, _stream(stream, X)), "ks_chain_adapter_matmul", True)
+            ws, size, _raw_stream(stream, self._index)), "ks_chain_adapter_matmul", True)
         return (out, H) if keep else out
 
     def backward(self, dY, X, H, ids, weights=True, stream=None):
@@ -548,13 +573,10 @@ class AdapterChain:
         if weights:
             dA = torch.empty((self.count, self.rank, self.n_in), dtype=torch.float32, device=self.device)
             dB = torch.empty((self.count, self.n_out, self.rank), dtype=torch.float32, device=self.device)
-        size = ctypes.c_size_t(0)
-        _raise(self._lib.ks_chain_adapter_backward_workspace_size(self._p, self._n, self._ad, batch, code, size),
-               "ks_chain_adapter_backward_workspace_size", True)
-        ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=self.device)
+        ws, size, _keep = self._workspace("ks_chain_adapter_backward_workspace_size", batch, code)
         _raise(self._lib.ks_chain_adapter_backward(
             self._p, self._n, self._w, self._ad, ids.data_ptr(), dY.data_ptr(), X.data_ptr(), H.data_ptr(),
-            dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws.data_ptr(), size.value, _stream(stream, dY)),
+            dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws, size, _raw_stream(stream, self._index)),
             "ks_chain_adapter_backward", True)
         return dX, dA, dB
 
@@ -632,30 +654,39 @@ def _elem(dtype, name) -> int:
     raise TypeError("%s must be fp32 or bf16, not %s" % (name, dtype))
 
 
+def _layout(x, name):
+    """(sequence stride, row stride) of (S, T, V) values with contiguous rows."""
+    S, T, V = x.shape
+    seq, row, one = x.stride()
+    if V > 1 and one != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    # strides of dimensions with at most one entry say nothing
+    if T <= 1:
+        row = max(V, 1)
+    if S <= 1:
+        seq = max((T - 1) * row + V, 0)
+    return seq, row
+
+
+def _rows_stride(t, name):
+    S, T = t.shape
+    seq, one = t.stride()
+    if T > 1 and one != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    return seq if S > 1 else T
+
+
 def _logits(x, labels) -> ks_logits_t:
     import torch
-    if x.dim() != 3 or tuple(labels.shape) != tuple(x.shape[:2]):
+    if x.dim() != 3 or labels.shape != x.shape[:2]:
         raise ValueError("logits must be (sequences, tokens, vocab) and labels (sequences, tokens)")
     if labels.dtype != torch.int64:
         raise TypeError("labels must be int64")
-    if not x.is_cuda or labels.device != x.device:
+    if not x.is_cuda or labels.get_device() != x.get_device():
         raise ValueError("logits and labels must be device tensors on one device")
-    elem = _elem(x.dtype, "logits")
-    S, T, V = x.shape
-    if (V > 1 and x.stride(2) != 1) or (T > 1 and labels.stride(1) != 1):
-        raise ValueError("the last dimension of logits and labels must be contiguous")
-    # strides of dimensions with at most one entry say nothing
-    row = x.stride(1) if T > 1 else max(V, 1)
-    seq = x.stride(0) if S > 1 else max((T - 1) * row + V, 0)
-    lab = labels.stride(0) if S > 1 else T
-    return ks_logits_t(x.data_ptr(), labels.data_ptr(), seq, row, lab, S, T, V, elem, 0)
-
-
-def _seq_stride(t, name):
-    import torch
-    if t.dtype != torch.float32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be (sequences, tokens) fp32 with contiguous rows" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    seq, row = _layout(x, "logits")
+    return ks_logits_t(x.data_ptr(), labels.data_ptr(), seq, row, _rows_stride(labels, "labels"), *x.shape,
+                       _elem(x.dtype, "logits"), 0)
 
 
 def sequence_logp(logits, labels, stream=None):
@@ -666,35 +697,36 @@ def sequence_logp(logits, labels, stream=None):
     x = _logits(logits, labels)
     tokens = torch.empty((x.sequences, x.tokens), dtype=torch.float32, device=logits.device)
     total = torch.empty((x.sequences,), dtype=torch.float32, device=logits.device)
-    _raise(load().ks_sequence_logp(x, tokens.data_ptr(), total.data_ptr(), None, _stream(stream, logits)),
-           "ks_sequence_logp", True)
+    _raise(load().ks_sequence_logp(x, tokens.data_ptr(), total.data_ptr(), None,
+                                   _raw_stream(stream, logits.get_device())), "ks_sequence_logp", True)
     return total, tokens
 
 
 def _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream):
+    """(loss, rewards, tokens, scratch): scratch holds d loss / d total, then
+    the rows' statistics."""
     import torch
     x = _logits(logits, labels)
-    if tuple(ref.shape) != tuple(labels.shape) or ref.device != logits.device:
-        raise ValueError("ref must be (sequences, tokens) on the logits' device")
-    ref_stride = _seq_stride(ref, "ref")
-    if dlogits is not None:
-        if tuple(dlogits.shape) != tuple(logits.shape) or dlogits.dtype != logits.dtype \
-                or dlogits.device != logits.device:
-            raise ValueError("dlogits must have the logits' shape, type and device")
-    S, T = x.sequences, x.tokens
-    buf = torch.empty(1 + 2 * S + 3 * S * T, dtype=torch.float32, device=logits.device)
-    loss, rewards, grad = buf[0], buf[1:1 + S], buf[1 + S:1 + 2 * S]
-    tokens = buf[1 + 2 * S:1 + 2 * S + S * T].view(S, T)
-    stats = buf[1 + 2 * S + S * T:]
+    if ref.dtype != torch.float32 or ref.shape != labels.shape or ref.get_device() != logits.get_device():
+        raise ValueError("ref must be (sequences, tokens) fp32 on the logits' device")
     d_seq = d_row = 0
     if dlogits is not None:
-        d = _logits(dlogits, labels)
-        d_seq, d_row = d.seq_stride, d.row_stride
-    _raise(load().ks_preference_loss(x, ref.data_ptr(), ref_stride, float(beta), float(smoothing), loss.data_ptr(),
-                                     rewards.data_ptr(), tokens.data_ptr(), grad.data_ptr(), stats.data_ptr(),
-                                     _ptr(dlogits), d_seq, d_row, _stream(stream, logits)),
+        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype \
+                or dlogits.get_device() != logits.get_device():
+            raise ValueError("dlogits must have the logits' shape, type and device")
+        d_seq, d_row = _layout(dlogits, "dlogits")
+    S, T = x.sequences, x.tokens
+    f32, device = torch.float32, logits.device
+    loss = torch.empty((), dtype=f32, device=device)
+    rewards = torch.empty((S,), dtype=f32, device=device)
+    tokens = torch.empty((S, T), dtype=f32, device=device)
+    scratch = torch.empty((S + 2 * S * T,), dtype=f32, device=device)
+    at = scratch.data_ptr()
+    _raise(load().ks_preference_loss(x, ref.data_ptr(), _rows_stride(ref, "ref"), float(beta), float(smoothing),
+                                     loss.data_ptr(), rewards.data_ptr(), tokens.data_ptr(), at, at + 4 * S,
+                                     _ptr(dlogits), d_seq, d_row, _raw_stream(stream, logits.get_device())),
            "ks_preference_loss", True)
-    return loss, rewards, tokens, grad, stats
+    return loss, rewards, tokens, scratch
 
 
 def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, stream=None):
@@ -704,18 +736,19 @@ def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, 
     dlogits may be given (the logits themselves too: then it replaces them)."""
     import torch
     if dlogits is None:
-        dlogits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
-    loss, rewards, tokens, _, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    loss, rewards, tokens, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
     return loss, rewards, tokens, dlogits
 
 
-def _preference_backward(logits, labels, stats, grad, upstream, stream=None):
+def _preference_backward(logits, labels, scratch, upstream, stream=None):
     import torch
-    dlogits = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
-    x, d = _logits(logits, labels), _logits(dlogits, labels)
-    _raise(load().ks_preference_backward(x, stats.data_ptr(), grad.data_ptr(), _ptr(upstream), dlogits.data_ptr(),
-                                         d.seq_stride, d.row_stride, _stream(stream, logits)),
-           "ks_preference_backward", True)
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    x = _logits(logits, labels)
+    d_seq, d_row = _layout(dlogits, "dlogits")
+    at = scratch.data_ptr()
+    _raise(load().ks_preference_backward(x, at + 4 * x.sequences, at, _ptr(upstream), dlogits.data_ptr(), d_seq, d_row,
+                                         _raw_stream(stream, logits.get_device())), "ks_preference_backward", True)
     return dlogits
 
 
@@ -737,27 +770,29 @@ class AdamW:
             raise ValueError("params, grads, ms, vs and scales must have one entry a tensor")
         self.bits = 32 if scales is None else 8
         types = (torch.float32, torch.float32) if scales is None else (torch.int8, torch.uint8)
-        self._t = (ks_adamw_tensor_t * max(n, 1))()
         self._n = n
         self.device = params[0].device if n else None
-        spans = []
-        for i in range(n):
-            p, g, m, v = params[i], grads[i], ms[i], vs[i]
-            for t, name in ((p, "params"), (g, "grads"), (m, "ms"), (v, "vs")):
+        T = torch.Tensor
+        self._sizes = list(map(T.numel, params))
+        index = self.device.index if n else None
+        for ts, name in ((params, "params"), (grads, "grads"), (ms, "ms"), (vs, "vs")):
+            for i, t in enumerate(ts):
                 _check_tensor(t, "%s[%d]" % (name, i))
-                if t.numel() != p.numel() or t.device != self.device:
-                    raise ValueError("%s[%d] must have its parameter's size, on one device" % (name, i))
-            if (m.dtype, v.dtype) != types:
-                raise TypeError("moments must be %s and %s" % types)
-            s = None
-            if scales is not None:
-                s = scales[i]
-                _check_out(s, (-(-p.numel() // ADAMW_BLOCK), 2), torch.float32, self.device, "scales[%d]" % i)
-            self._t[i] = ks_adamw_tensor_t(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(s), p.numel(),
-                                           _elem(p.dtype, "params"), _elem(g.dtype, "grads"))
-            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (p, m, v, s)
-                      if t is not None and t.numel()]
-        spans.sort()
+            if list(map(T.numel, ts)) != self._sizes or any(d != index for d in map(T.get_device, ts)):
+                raise ValueError("%s must have their parameters' sizes, on one device" % name)
+        if any(t.dtype is not types[0] for t in ms) or any(t.dtype is not types[1] for t in vs):
+            raise TypeError("moments must be %s and %s" % types)
+        if scales is not None:
+            for i, s in enumerate(scales):
+                _check_out(s, (-(-self._sizes[i] // ADAMW_BLOCK), 2), torch.float32, self.device, "scales[%d]" % i)
+        at = [list(map(T.data_ptr, ts)) for ts in (params, grads, ms, vs)]
+        at.append(list(map(T.data_ptr, scales)) if scales is not None else [None] * n)
+        self._t = (ks_adamw_tensor_t * max(n, 1))(*[
+            ks_adamw_tensor_t(*a, size, _elem(p.dtype, "params"), _elem(g.dtype, "grads"))
+            for *a, size, p, g in zip(*at, self._sizes, params, grads)])
+        spans = sorted((a, a + t.numel() * t.element_size())
+                       for ts, addr in zip((params, ms, vs, scales or []), (at[0], at[2], at[3], at[4]))
+                       for t, a in zip(ts, addr) if t.numel())
         if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
             raise ValueError("parameters and moments must not share memory")
         self._keep = (list(params), list(grads), list(ms), list(vs), list(scales or ()))
@@ -773,7 +808,7 @@ class AdamW:
             out = torch.empty((), dtype=torch.float32, device=self.device)
         ws = torch.empty(max(self._ws_bytes, 1), dtype=torch.uint8, device=self.device)
         _raise(self._lib.ks_grad_norm(self._t, self._n, out.data_ptr(), ws.data_ptr(), self._ws_bytes,
-                                      _stream(stream, out)), "ks_grad_norm", True)
+                                      _raw_stream(stream, self.device.index)), "ks_grad_norm", True)
         return out
 
     def step(self, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None, norm=None, seed=0,
@@ -791,7 +826,7 @@ class AdamW:
         o = ks_adamw_options_t(float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
                                float(max_norm or 0.0), int(step), int(seed) & 0xFFFFFFFF, self.bits)
         _raise(self._lib.ks_adamw_step(self._t, self._n, o, _ptr(norm) if max_norm is not None else None,
-                                       _stream(stream, self._keep[0][0])), "ks_adamw_step", True)
+                                       _raw_stream(stream, self.device.index)), "ks_adamw_step", True)
         return norm
 
     def state_values(self, ms_out, vs_out, stream=None):
@@ -801,14 +836,15 @@ class AdamW:
             raise ValueError("32-bit moments are their own values")
         if len(ms_out) != self._n or len(vs_out) != self._n:
             raise ValueError("one output a tensor")
-        for i in range(self._n):
-            for t in (ms_out[i], vs_out[i]):
-                _check_tensor(t, "state_values output")
-                if t.dtype != torch.float32 or t.numel() != self._t[i].n or t.device != self.device:
-                    raise ValueError("outputs must be fp32 of their parameter's size")
         if self._n == 0:
             return
-        mp = (ctypes.c_void_p * self._n)(*[t.data_ptr() for t in ms_out])
-        vp = (ctypes.c_void_p * self._n)(*[t.data_ptr() for t in vs_out])
-        _raise(self._lib.ks_adamw_state_values(self._t, self._n, mp, vp, _stream(stream, ms_out[0])),
+        T, index = torch.Tensor, self.device.index
+        for outs in (ms_out, vs_out):
+            if list(map(T.numel, outs)) != self._sizes or any(t.dtype is not torch.float32 for t in outs):
+                raise ValueError("outputs must be fp32 of their parameter's size")
+            if set(map(T.get_device, outs)) != {index} or not all(map(T.is_contiguous, outs)):
+                raise ValueError("outputs must be contiguous, on the parameters' device")
+        mp = (ctypes.c_void_p * self._n)(*map(T.data_ptr, ms_out))
+        vp = (ctypes.c_void_p * self._n)(*map(T.data_ptr, vs_out))
+        _raise(self._lib.ks_adamw_state_values(self._t, self._n, mp, vp, _raw_stream(stream, index)),
                "ks_adamw_state_values", True)
