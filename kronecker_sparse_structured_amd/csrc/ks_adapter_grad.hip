@@ -29,13 +29,14 @@ namespace ks {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 256;    // most rows of a block
 constexpr int kColsY = 256;      // columns of dY a workgroup takes
-constexpr int kColsX = 128;      // columns of X a workgroup takes
-constexpr int kPitch = 65;       // LDS row of a 64-wide tile: odd, so that row and column reads of 16 + 16 j
-                                 // places fall into 64 different banks
+constexpr int kColsX = 64;       // columns of X a workgroup takes (25216 x 384: 108 us a call, 118 with 128)
+constexpr int kPitch = 72;       // LDS row of a 64-wide tile: 16-byte runs of a row for the row operand, and
+                                 // 4 rows x 16 columns over all banks, two lanes each, for the column operand
 
 struct Slot {
     int adapter, start, len, reserved;   // rows order[start .. start + len); len 0: empty
@@ -118,9 +119,8 @@ __device__ __forceinline__ float value_at(const T* p, int64_t row, int64_t width
 //
 // dY goes through LDS in tiles of 64 x 64, the next tile's loads in flight
 // while this one is multiplied. A wave takes 16 rows of the tile for E (inner
-// index: the columns) and 16 columns for dB (inner index: the rows); lane group
-// lg takes the inner values 16 lg + j, which the odd pitch spreads over all
-// banks for both.
+// index: the columns, 16 lg + j for lane group lg) and 16 columns for dB (inner
+// index: the rows, 4 j + lg).
 template <typename TW, int RT>
 __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const TW* B, const float* H,
                                                           const float* scale, const int* order, const Slot* slots,
@@ -128,8 +128,8 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
                                                           float* db_part) {
     constexpr int kR = 16 * RT + 1;
     constexpr int kB = 16 * RT + (sizeof(TW) == 4 ? 1 : 2);   // bf16 pairs: an odd number of 4-byte words
-    __shared__ float tile[64 * kPitch];
-    __shared__ TW bt[kColsY * kB];         // B[o][r], all columns of the workgroup
+    __shared__ __align__(16) float tile[64 * kPitch];
+    __shared__ __align__(4) TW bt[kColsY * kB];         // B[o][r], all columns of the workgroup
     __shared__ float ht[64 * kR];          // H[n][r], the row tile's
     __shared__ int row_of[kMaxRows];
     // neighbouring workgroups take neighbouring columns of the same rows
@@ -175,15 +175,36 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
 #pragma unroll
         for (int t = 0; t < RT; ++t) d[c][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     load(0, 0);
-#pragma unroll 16
-    for (int i = tid; i < kColsY * 16 * RT; i += kThreads) {
-        const int o = i / (16 * RT), r = i % (16 * RT);
-        const bool in = base + o < n_out && r0 + r < rank;
-        const TW w = b[in ? static_cast<int64_t>(base + o) * rank + r0 + r : 0];
-        bt[o * kB + r] = in ? w : TW(0);
+    // B of all columns: 16-byte vectors of ranks where they are whole
+    constexpr int kV = 16 / static_cast<int>(sizeof(TW)), kVecs = kColsY * 16 * RT / kV / kThreads;
+    if (rank % kV == 0 && reinterpret_cast<uintptr_t>(B) % 16 == 0) {
+        u32x4 w[kVecs];
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int v = q * kThreads + tid, o = v / (16 * RT / kV), r = v % (16 * RT / kV) * kV;
+            const bool in = base + o < n_out && r0 + r < rank;
+            w[q] = *reinterpret_cast<const u32x4*>(b + (in ? static_cast<int64_t>(base + o) * rank + r0 + r : 0));
+            if (!in) w[q] = u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int v = q * kThreads + tid, o = v / (16 * RT / kV), r = v % (16 * RT / kV) * kV;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(bt + o * kB + r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = w[q][i];
+        }
+    } else {
+#pragma unroll 8
+        for (int i = tid; i < kColsY * 16 * RT; i += kThreads) {
+            const int o = i / (16 * RT), r = i % (16 * RT);
+            const bool in = base + o < n_out && r0 + r < rank;
+            const TW w = b[in ? static_cast<int64_t>(base + o) * rank + r0 + r : 0];
+            bt[o * kB + r] = in ? w : TW(0);
+        }
     }
     for (int rt = 0; rt < row_tiles; ++rt) {
         f32x4 e[RT];
+        float hv[RT][16];                  // H with inner index n, for all column tiles
 #pragma unroll
         for (int t = 0; t < RT; ++t) e[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -192,8 +213,8 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tile[(tid / 16 + 16 * q) * kPitch + 4 * (tid % 16) + i] = next[q][i];
+                *reinterpret_cast<f32x4*>(tile + (tid / 16 + 16 * q) * kPitch + 4 * (tid % 16)) =
+                    f32x4{next[q][0], next[q][1], next[q][2], next[q][3]};
             if (ct == 0 && db_part) {
 #pragma unroll
                 for (int q = 0; q < 4 * RT; ++q)
@@ -203,21 +224,28 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
             if (ct + 1 < col_tiles) load(rt, ct + 1);
             else if (rt + 1 < row_tiles) load(rt + 1, 0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float x = tile[(16 * wave + li) * kPitch + 16 * lg + j];
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(tile + (16 * wave + li) * kPitch + 16 * lg + 4 * q);
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
-                    e[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, to_f32(bt[(ct * 64 + 16 * lg + j) * kB + 16 * t + li]),
-                                                                e[t], 0, 0, 0);
-            }
-            if (db_part) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x = tile[(16 * lg + j) * kPitch + 16 * wave + li];
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, ht[(16 * lg + j) * kR + 16 * t + li], d[ct][t],
-                                                                        0, 0, 0);
+                        e[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            x[j], to_f32(bt[(ct * 64 + 16 * lg + 4 * q + j) * kB + 16 * t + li]), e[t], 0, 0, 0);
+            }
+            if (db_part) {
+                if (ct == 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) hv[t][j] = ht[(4 * j + lg) * kR + 16 * t + li];
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = tile[(4 * j + lg) * kPitch + 16 * wave + li];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, hv[t][j], d[ct][t], 0, 0, 0);
                 }
             }
         }
@@ -250,7 +278,7 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// dX and partial dA of one block of rows and 128 columns of X, in tiles of
+// dX and partial dA of one block of rows and 64 columns of X, in tiles of
 // 64 x 64. X goes through LDS for dA (inner index: the rows; a wave takes 16
 // columns); for dX a wave takes 16 rows, forms its product with the columns
 // along the instruction's rows and turns it in LDS, so that dX is read and
@@ -260,7 +288,7 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                                                           const Slot* slots, int n_in, int rank, unsigned splits,
                                                           float* dX, float* da_part) {
     constexpr int kR = 16 * RT + 1, kTiles = kColsX / 64, kTurn = 68;
-    __shared__ float tile[64 * kPitch];
+    __shared__ __align__(16) float tile[64 * kPitch];
     __shared__ float et[64 * kR];                       // E[n][r] of the row tile
     __shared__ __align__(16) float cross[4][16 * kTurn];
     __shared__ int row_of[kMaxRows];
@@ -350,8 +378,8 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                 if (da_part) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) tile[(tid / 16 + 16 * q) * kPitch + 4 * (tid % 16) + i] = next[q][i];
+                        *reinterpret_cast<f32x4*>(tile + (tid / 16 + 16 * q) * kPitch + 4 * (tid % 16)) =
+                            f32x4{next[q][0], next[q][1], next[q][2], next[q][3]};
                 }
                 if (ct == 0) {
 #pragma unroll
@@ -364,10 +392,10 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                 if (da_part) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float x = tile[(16 * lg + j) * kPitch + 16 * wave + li];
+                        const float x = tile[(4 * j + lg) * kPitch + 16 * wave + li];
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
-                            d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(et[(16 * lg + j) * kR + 16 * t + li], x,
+                            d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(et[(4 * j + lg) * kR + 16 * t + li], x,
                                                                             d[ct][t], 0, 0, 0);
                     }
                 }
@@ -465,12 +493,12 @@ struct Layout {
     int block, n_slots, splits;
 };
 
-// Rows of a block: as many as leave the passes about four and two workgroups a
+// Rows of a block: as many as leave the passes about two and one workgroups a
 // compute unit of the card's 256 (fewer partial sums against loads in flight).
 int block_rows(int n_in, int n_out, int64_t batch) {
     int block = kMaxRows;
-    while (block > 64 && (batch / block * ((n_out + kColsY - 1) / kColsY) < 1024 ||
-                          batch / block * ((n_in + kColsX - 1) / kColsX) < 512))
+    while (block > 64 && (batch / block * ((n_out + kColsY - 1) / kColsY) < 512 ||
+                          batch / block * ((n_in + kColsX - 1) / kColsX) < 256))
         block /= 2;
     return block;
 }
