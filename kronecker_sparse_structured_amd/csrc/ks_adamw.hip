@@ -352,19 +352,17 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(const Table t, flo
     float sum = 0.0f;
     const bool whole = wide && start - threadIdx.x * kLane + kStep * kNormIters <= e.n;
     if (whole && !(e.flags & kGBF16)) {
-        // every load of the workgroup's share in flight
-        const f32x4* g = reinterpret_cast<const f32x4*>(static_cast<const float*>(e.g) + start);
-        f32x4 x[kNormIters][2];
+        // every load of the workgroup's share in flight, each in whole lines
+        const f32x4* g = reinterpret_cast<const f32x4*>(static_cast<const float*>(e.g) + (start - threadIdx.x * kLane)) +
+                         threadIdx.x;
+        f32x4 x[2 * kNormIters];
 #pragma unroll
-        for (int it = 0; it < kNormIters; ++it) {
-            x[it][0] = g[it * (kStep / 4)];
-            x[it][1] = g[it * (kStep / 4) + 1];
-        }
+        for (int it = 0; it < 2 * kNormIters; ++it) x[it] = g[it * kThreads];
 #pragma unroll
-        for (int it = 0; it < kNormIters; ++it) {
+        for (int it = 0; it < 2 * kNormIters; ++it) {
             float part = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) part += x[it][j / 4][j % 4] * x[it][j / 4][j % 4];
+            for (int j = 0; j < 4; ++j) part += x[it][j] * x[it][j];
             sum += part;
         }
     } else for (int it = 0; it < kNormIters; ++it) {

@@ -64,6 +64,19 @@ __device__ __forceinline__ void load4(const T* p, int valid, float (&x)[4]) {
     }
 }
 
+// Ranks r .. r + 3 of a row of `rank` values. WIDE (rank a multiple of 4): one
+// unconditional load, so that the loads of a wave go out together.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load_ranks(const T* row, int r, int rank, float (&x)[4]) {
+    if constexpr (WIDE) {
+        load4_f32(row + min(r, rank - 4), x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = r < rank ? x[i] : 0.0f;
+    } else {
+        load4<false>(row + r, rank - r, x);
+    }
+}
+
 // ---------------------------------------------------------------- few rows
 
 // Eight consecutive values: 16-byte loads (WIDE), or element-wise with zeros
@@ -300,13 +313,15 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a) {
     }
 }
 
-// Y += H B^T: 64 rows and 64 outputs a wave, 256 outputs a workgroup. The
+// Y += H B^T: 16 rows and 64 outputs a wave, 256 outputs a workgroup. The
 // products are formed transposed, outputs along the instruction's rows: lane
 // (li, lg) holds outputs 4 lg .. 4 lg + 3 of tile row li, 64 bytes of 16 rows an
 // instruction. They cross a small LDS tile of the wave's own, so that Y is read
-// and written in runs of 256 bytes: lane (l / 16, l % 16) takes rows
-// 4 q + l / 16, outputs 4 (l % 16) .. + 3.
-constexpr int kUpRows = 64, kUpCols = 256, kUpPitch = 68;
+// and written in runs of 256 bytes: lane (li, lg) takes rows 4 q + lg, outputs
+// 4 li .. + 3. Y's values are on their way from the start. Bound by HBM: Y is
+// read and written once, 5.7 TB/s at 16384 x 4096 (64 rows a wave: 5.4, and a
+// third slower on 4099 rows, where a round of waves does not fill the card).
+constexpr int kUpCols = 256, kUpPitch = 68;
 
 // Orders the wave's LDS accesses before and after it: its lanes exchange values.
 __device__ __forceinline__ void wave_fence() {
@@ -325,122 +340,84 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a) {
     const unsigned slabs = (a.n_out + kUpCols - 1) / kUpCols;
     const int o0 = blockIdx.x % slabs * kUpCols + wave * 64;
     if (o0 >= a.n_out) return;
-    const int64_t first = static_cast<int64_t>(blockIdx.x / slabs) * kUpRows;
-    const TW* B = static_cast<const TW*>(a.B);
-    float* mine_lds = cross[wave];
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / slabs) * kTile;
+    const int rows = static_cast<int>(a.batch - row0 < kTile ? a.batch - row0 : kTile);
+    float* mine = cross[wave];
     const int left = a.n_out - (o0 + 4 * li);          // this lane's outputs of Y inside the matrix
-    float bv[4][RT][4];
-    auto hold = [&](int g, int r0) {
+    const bool whole = WIDE && rows == kTile && o0 + 64 <= a.n_out;      // every lane's vectors, for the whole wave
+    f32x4 y[4];
+    if (whole) {
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-            const int o = min(o0 + 16 * ct + li, a.n_out - 1);
-            const TW* b = B + (static_cast<int64_t>(g) * a.n_out + o) * a.rank;
+        for (int q = 0; q < 4; ++q)
+            y[q] = *reinterpret_cast<const f32x4*>(a.Y + (row0 + 4 * q + lg) * a.n_out + o0 + 4 * li);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[4];
+            load4<WIDE>(a.Y + (row0 + 4 * q + lg) * a.n_out + o0 + 4 * li, 4 * q + lg < rows ? left : 0, v);
+            y[q] = f32x4{v[0], v[1], v[2], v[3]};
+        }
+    }
+    const float* h = a.H + (row0 + (li < rows ? li : rows - 1)) * a.rank;
+    float hv[RT][4];                                   // H of the first ranks: all of them up to 16 RT
+#pragma unroll
+    for (int t = 0; t < RT; ++t) load_ranks<WIDE>(h, 16 * t + 4 * lg, a.rank, hv[t]);
+    Mix mix(a.ids, row0, rows, a.count);
+    if (!mix.left) return;
+    f32x4 all[4];
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) all[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    while (mix.left) {
+        const int g = mix.next();
+        f32x4 sum[4];
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r0 = 0; r0 < a.rank; r0 += 16 * RT) {
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
                 const int r = r0 + 16 * t + 4 * lg;
-                load4<WIDE>(b + r, a.rank - r, bv[ct][t]);
-            }
-        }
-    };
-    // the product of 16 rows, from D's layout to Y's
-    auto turn = [&](const f32x4 (&sum)[4], f32x4 (&out)[4]) {
+                float hr[4], bv[4][4];
+                if (r0 == 0) {
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(mine_lds + li * kUpPitch + 16 * ct + 4 * lg) = sum[ct];
-        wave_fence();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) out[q] = *reinterpret_cast<const f32x4*>(mine_lds + (4 * q + lg) * kUpPitch + 4 * li);
-        wave_fence();
-    };
-    // 64 rows of one adapter and whole vectors everywhere: every load of the
-    // wave is in flight before the first product
-    if constexpr (WIDE) {
-        const int id = first + lane < a.batch ? a.ids[first + lane] : -1;
-        const int g = __builtin_amdgcn_readfirstlane(id);
-        if (a.rank <= 16 * RT && o0 + 64 <= a.n_out && g >= 0 && g < a.count && __all(id == g)) {
-            f32x4 y[4][4];
-            float hv[4][RT][4];
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    y[rt][q] = *reinterpret_cast<const f32x4*>(a.Y + (first + 16 * rt + 4 * q + lg) * a.n_out + o0 + 4 * li);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const int r = 16 * t + 4 * lg;
-                    load4<true>(a.H + (first + 16 * rt + li) * a.rank + r, a.rank - r, hv[rt][t]);
+                    for (int i = 0; i < 4; ++i) hr[i] = hv[t][i];
+                } else {
+                    load_ranks<WIDE>(h, r, a.rank, hr);
                 }
-            }
-            hold(g, 0);
 #pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                f32x4 sum[4], out[4];
-#pragma unroll
-                for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int ct = 0; ct < 4; ++ct)
-                            sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][t][i], hv[rt][t][i], sum[ct], 0, 0, 0);
-                turn(sum, out);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<f32x4*>(a.Y + (first + 16 * rt + 4 * q + lg) * a.n_out + o0 + 4 * li) = y[rt][q] + out[q];
-            }
-            return;
-        }
-    }
-#pragma unroll 1
-    for (int rt = 0; rt < kUpRows / 16; ++rt) {
-        const int64_t row0 = first + 16 * rt;
-        if (row0 >= a.batch) return;
-        const int rows = static_cast<int>(a.batch - row0 < 16 ? a.batch - row0 : 16);
-        Mix mix(a.ids, row0, rows, a.count);
-        if (!mix.left) continue;
-        const float* h = a.H + (row0 + (li < rows ? li : rows - 1)) * a.rank;
-        f32x4 all[4], out[4];
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct) all[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        while (mix.left) {
-            const int g = mix.next();
-            f32x4 sum[4];
-#pragma unroll
-            for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int r0 = 0; r0 < a.rank; r0 += 16 * RT) {
-                hold(g, r0);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const int r = r0 + 16 * t + 4 * lg;
-                    float hv[4];
-                    load4<WIDE>(h + r, a.rank - r, hv);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int ct = 0; ct < 4; ++ct)
-                            sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][t][i], hv[i], sum[ct], 0, 0, 0);
+                for (int ct = 0; ct < 4; ++ct) {
+                    const int o = min(o0 + 16 * ct + li, a.n_out - 1);
+                    load_ranks<WIDE>(static_cast<const TW*>(a.B) + (static_cast<int64_t>(g) * a.n_out + o) * a.rank, r,
+                                     a.rank, bv[ct]);
                 }
-            }
-            // a lane's column of the product is one row of Y: a row takes its
-            // own adapter's, and nothing of the others', not even their NaN
-#pragma unroll
-            for (int ct = 0; ct < 4; ++ct)
-                if (mix.id == g) all[ct] = sum[ct];
-        }
-        turn(all, out);
-        const uint64_t on = __ballot(mix.id >= 0);     // bit r: row r has an adapter
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = 4 * q + lg;
-            if (!(on >> r & 1)) continue;
-            float* y = a.Y + (row0 + r) * a.n_out + o0 + 4 * li;
-            if (WIDE && left >= 4) {
-                *reinterpret_cast<f32x4*>(y) += out[q];
-            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (i < left) y[i] += out[q][i];
+#pragma unroll
+                    for (int ct = 0; ct < 4; ++ct)
+                        sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][i], hr[i], sum[ct], 0, 0, 0);
             }
+        }
+        // a lane's column of the product is one row of Y: a row takes its own
+        // adapter's, and nothing of the others', not even their NaN
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct)
+            if (mix.id == g) all[ct] = sum[ct];
+    }
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(mine + li * kUpPitch + 16 * ct + 4 * lg) = all[ct];
+    wave_fence();
+    const uint64_t on = __ballot(mix.id >= 0);         // bit r: row r has an adapter
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = 4 * q + lg;
+        const f32x4 add = *reinterpret_cast<const f32x4*>(mine + r * kUpPitch + 4 * li);
+        if (!(on >> r & 1)) continue;
+        float* dst = a.Y + (row0 + r) * a.n_out + o0 + 4 * li;
+        if (whole || (WIDE && left >= 4)) {
+            *reinterpret_cast<f32x4*>(dst) = y[q] + add;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) dst[i] = y[q][i] + add[i];
         }
     }
 }
@@ -473,7 +450,7 @@ ks_status_t launch_down(const Args& a, hipStream_t stream) {
 template <typename TW>
 ks_status_t launch_up(const Args& a, hipStream_t stream) {
     const bool wide = on16(a.B) && on16(a.H) && on16(a.Y) && a.rank % 4 == 0 && a.n_out % 4 == 0;
-    const int64_t blocks = (a.batch + kUpRows - 1) / kUpRows * ((a.n_out + kUpCols - 1) / kUpCols);
+    const int64_t blocks = (a.batch + kTile - 1) / kTile * ((a.n_out + kUpCols - 1) / kUpCols);
     if (blocks >= int64_t(1) << 31) return KS_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks));
     void (*kernel)(Args);

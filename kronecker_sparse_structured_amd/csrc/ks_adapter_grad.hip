@@ -288,9 +288,8 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                                                           const Slot* slots, int n_in, int rank, unsigned splits,
                                                           float* dX, float* da_part) {
     constexpr int kR = 16 * RT + 1, kTiles = kColsX / 64, kTurn = 68;
-    __shared__ __align__(16) float tile[64 * kPitch];
+    __shared__ __align__(16) float tile[64 * kPitch];   // X; after its use for dA, a quarter for each wave's turn
     __shared__ float et[64 * kR];                       // E[n][r] of the row tile
-    __shared__ __align__(16) float cross[4][16 * kTurn];
     __shared__ int row_of[kMaxRows];
     const int split = blockIdx.x % splits, slot = blockIdx.x / splits;
     const Slot s = slots[slot];
@@ -400,6 +399,8 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                     }
                 }
                 if (dX) {
+                    if (da_part) __syncthreads();
+                    float* cross = tile + wave * 16 * kPitch;
                     f32x4 sum[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -414,12 +415,12 @@ __global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW*
                         }
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<f32x4*>(cross[wave] + li * kTurn + 16 * c + 4 * lg) = sum[c];
+                        *reinterpret_cast<f32x4*>(cross + li * kTurn + 16 * c + 4 * lg) = sum[c];
                     wave_fence();
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int at = rt * 64 + 16 * wave + 4 * q + lg;
-                        const f32x4 add = *reinterpret_cast<const f32x4*>(cross[wave] + (4 * q + lg) * kTurn + 4 * li);
+                        const f32x4 add = *reinterpret_cast<const f32x4*>(cross + (4 * q + lg) * kTurn + 4 * li);
                         float* dst = dX + static_cast<int64_t>(row_of[at]) * n_in + k;
                         const int valid = at < s.len ? n_in - k : 0;
                         if (wide_d && valid >= 4) {

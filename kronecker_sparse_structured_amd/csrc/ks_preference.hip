@@ -18,8 +18,8 @@
 // together in one pass: each lane keeps its own running pair (m, s), rescales
 // s when m grows, and the lanes' pairs are joined at the end. Rows start at
 // any element (an odd vocabulary in bf16 puts them at any even byte), so a
-// row's head up to the next 16-byte boundary and its tail go element-wise and
-// the rest in 16-byte loads.
+// row's head up to the next 128-byte line and its tail go element-wise, one
+// value a thread, and the rest in 16-byte vectors that fill whole lines.
 //
 // exp(x - m) is exp2((x - m) log2 e): the difference is taken first, so that a
 // maximum at the type's lowest value (a fully masked vocabulary) cannot
@@ -80,10 +80,10 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kVec<T>]) {
     return w;
 }
 
-// Elements before the first 16-byte boundary at or after p, at most n.
+// Elements before the first 128-byte line that starts at or after p, at most n.
 template <typename T>
 __device__ __forceinline__ int head_of(const T* p, int n) {
-    const int bytes = static_cast<int>((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16);
+    const int bytes = static_cast<int>((128 - reinterpret_cast<uintptr_t>(p) % 128) % 128);
     return min(n, bytes / static_cast<int>(sizeof(T)));
 }
 
