@@ -379,12 +379,15 @@ typedef struct ks_adapters_t {
  *   Y      device fp32, batch x n_out; added to.
  *   H      device fp32, batch x rank: fully overwritten, zeros for rows
  *          without an adapter. ks_adapter_backward reads it.
+ *   ws     device workspace of ks_adapter_workspace_size bytes, 16-byte
+ *          aligned (may be NULL when that is 0).
  * The intermediate H is fp32 in every case. Pointers need the alignment of
  * their element; 16 bytes select wider loads. Y and H must not overlap any
  * input or each other (KS_ERR_OVERLAP).
  */
+ks_status_t ks_adapter_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes);
 ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const void* X, float* Y, float* H,
-                              int64_t batch, ks_dtype_t dt, hipStream_t stream);
+                              int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * ks_adapter_backward: gradients of ks_adapter_matmul. With

@@ -286,28 +286,25 @@ __device__ __forceinline__ void step_lane(const Entry& e, const Step& s, float c
     }
 }
 
-// Workgroup w of a tensor takes values [w chunk, (w + 1) chunk).
-template <int BITS, int ITERS>
+// Workgroup w of a tensor takes values [w kStep, (w + 1) kStep): one step, as
+// two or four were 1 to 9 % slower.
+template <int BITS>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Table t, const Step s) {
     bool skip;
     const float clip = clip_of(s, &skip);
     if (skip) return;
     const int wg = blockIdx.x;
     const Entry& e = t.e[find_entry(t, wg)];
-    const int64_t start = static_cast<int64_t>(wg - e.first) * (kStep * ITERS) + threadIdx.x * kLane;
-#pragma unroll 1
-    for (int it = 0; it < ITERS; ++it) {
-        const int64_t i = start + it * kStep;
-        const int64_t left = e.n - i;
-        // whole half waves go on together: their maxima need every lane
-        if (i / kBlock * kBlock >= e.n) return;
-        const int valid = static_cast<int>(left < 0 ? 0 : (left < kLane ? left : kLane));
-        const uint32_t types = e.flags & (kPBF16 | kGBF16);
-        if (types == 0) step_lane<BITS, float, float>(e, s, clip, i, valid);
-        else if (types == kPBF16) step_lane<BITS, bf16_t, float>(e, s, clip, i, valid);
-        else if (types == kGBF16) step_lane<BITS, float, bf16_t>(e, s, clip, i, valid);
-        else step_lane<BITS, bf16_t, bf16_t>(e, s, clip, i, valid);
-    }
+    const int64_t i = static_cast<int64_t>(wg - e.first) * kStep + threadIdx.x * kLane;
+    // whole half waves go on together: their maxima need every lane
+    if (i / kBlock * kBlock >= e.n) return;
+    const int64_t left = e.n - i;
+    const int valid = static_cast<int>(left < 0 ? 0 : (left < kLane ? left : kLane));
+    const uint32_t types = e.flags & (kPBF16 | kGBF16);
+    if (types == 0) step_lane<BITS, float, float>(e, s, clip, i, valid);
+    else if (types == kPBF16) step_lane<BITS, bf16_t, float>(e, s, clip, i, valid);
+    else if (types == kGBF16) step_lane<BITS, float, bf16_t>(e, s, clip, i, valid);
+    else step_lane<BITS, bf16_t, bf16_t>(e, s, clip, i, valid);
 }
 
 // Values of 8-bit states: p and g of the entries are the fp32 outputs.
@@ -352,12 +349,14 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(const Table t, flo
     float sum = 0.0f;
     const bool whole = wide && start - threadIdx.x * kLane + kStep * kNormIters <= e.n;
     if (whole && !(e.flags & kGBF16)) {
-        // every load of the workgroup's share in flight, each in whole lines
+        // every load of the workgroup's share in flight, each in whole lines and
+        // past the last cache: 206 MB in 34 us (68 with ordinary loads, which
+        // first push other tensors' changed lines out to memory)
         const f32x4* g = reinterpret_cast<const f32x4*>(static_cast<const float*>(e.g) + (start - threadIdx.x * kLane)) +
                          threadIdx.x;
         f32x4 x[2 * kNormIters];
 #pragma unroll
-        for (int it = 0; it < 2 * kNormIters; ++it) x[it] = g[it * kThreads];
+        for (int it = 0; it < 2 * kNormIters; ++it) x[it] = __builtin_nontemporal_load(&g[it * kThreads]);
 #pragma unroll
         for (int it = 0; it < 2 * kNormIters; ++it) {
             float part = 0.0f;
@@ -471,15 +470,14 @@ ks_status_t launch_adamw(const ks_adamw_tensor_t* t, int n, const ks_adamw_optio
     s.max_norm = static_cast<float>(o.max_norm);
     s.seed = o.seed;
     s.norm = norm;
-    constexpr int kIters = 2;
     const bool small = o.state_bits == 8;
     return for_tables(
-        t, n, kStep * kIters,
+        t, n, kStep,
         [&](Entry& e, int) {
             e.flags |= (on16(e.p) && on16(e.g) && on16(e.m) && on16(e.v)) ? kWide : 0u;
         },
         [&](const Table& table, unsigned wgs) {
-            return launch_kernel(small ? adamw_kernel<8, kIters> : adamw_kernel<32, kIters>, dim3(wgs),
+            return launch_kernel(small ? adamw_kernel<8> : adamw_kernel<32>, dim3(wgs),
                                  dim3(kThreads), 0, stream, table, s);
         });
 }

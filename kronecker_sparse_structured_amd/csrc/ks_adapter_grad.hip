@@ -38,15 +38,9 @@ constexpr int kColsX = 64;       // columns of X a workgroup takes (25216 x 384:
 constexpr int kPitch = 72;       // LDS row of a 64-wide tile: 16-byte runs of a row for the row operand, and
                                  // 4 rows x 16 columns over all banks, two lanes each, for the column operand
 
-struct Slot {
-    int adapter, start, len, reserved;   // rows order[start .. start + len); len 0: empty
-};
-struct Segment {
-    int start, len;                      // an adapter's rows in the order
-};
+using Slot = AdapterSlot;
+using Segment = AdapterSegment;
 
-// Blocks of adapter g start at slot floor(start / block) + g: at most one slot
-// an adapter is left empty, and no slot is claimed twice.
 __device__ __forceinline__ int first_slot(Segment s, int g, int block) { return s.start / block + g; }
 
 // One workgroup an adapter: its rows' places in the order are the rows of
@@ -490,8 +484,9 @@ __global__ __launch_bounds__(kThreads) void sum_slots_kernel(const float* part, 
 }
 
 struct Layout {
-    size_t order, segs, slots, e, e_part, w_part, total;
-    int block, n_slots, splits;
+    AdapterOrder o;
+    size_t e, e_part, w_part, total;
+    int splits;
 };
 
 // Rows of a block: as many as leave the passes about two and one workgroups a
@@ -504,24 +499,19 @@ int block_rows(int n_in, int n_out, int64_t batch) {
     return block;
 }
 
-Layout layout_of(int n_in, int n_out, int rank, int count, int64_t batch) {
+Layout layout_of(int n_in, int n_out, int rank, int count, int64_t batch, char* ws) {
     Layout l;
-    size_t at = 0;
+    size_t at = adapter_order_layout(batch, block_rows(n_in, n_out, batch), count, ws, &l.o);
     auto take = [&](size_t bytes) {
         const size_t here = at;
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    l.block = block_rows(n_in, n_out, batch);
-    l.n_slots = static_cast<int>(batch / l.block) + count;
     l.splits = (n_out + kColsY - 1) / kColsY;
-    l.order = take(static_cast<size_t>(batch) * 4);
-    l.segs = take(static_cast<size_t>(count) * sizeof(Segment));
-    l.slots = take(static_cast<size_t>(l.n_slots) * sizeof(Slot));
     l.e = take(static_cast<size_t>(batch) * rank * 4);
     l.e_part = take(l.splits > 1 ? static_cast<size_t>(l.splits) * batch * rank * 4 : 0);
     // dB's partial sums are added before dA's are written
-    l.w_part = take(static_cast<size_t>(l.n_slots) * rank * std::max(n_in, n_out) * 4);
+    l.w_part = take(static_cast<size_t>(l.o.n_slots) * rank * std::max(n_in, n_out) * 4);
     l.total = at;
     return l;
 }
@@ -529,25 +519,24 @@ Layout layout_of(int n_in, int n_out, int rank, int count, int64_t batch) {
 template <typename TX, typename TW, int RT>
 ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX, float* dA, float* dB,
                 char* ws) {
-    const Layout l = layout_of(c.n_in, c.n_out, c.rank, c.count, c.batch);
-    int* order = reinterpret_cast<int*>(ws + l.order);
-    Segment* segs = reinterpret_cast<Segment*>(ws + l.segs);
-    Slot* slots = reinterpret_cast<Slot*>(ws + l.slots);
+    const Layout l = layout_of(c.n_in, c.n_out, c.rank, c.count, c.batch, ws);
+    const int* order = l.o.order;
+    const Segment* segs = l.o.segs;
+    const Slot* slots = l.o.slots;
     float* E = reinterpret_cast<float*>(ws + l.e);
     float* e_part = l.splits > 1 ? reinterpret_cast<float*>(ws + l.e_part) : E;
     float* w_part = reinterpret_cast<float*>(ws + l.w_part);
     const TW* A = static_cast<const TW*>(c.A);
     const TW* B = static_cast<const TW*>(c.B);
-    ks_status_t st = launch_kernel(sort_kernel, dim3(static_cast<unsigned>(c.count)), dim3(1024), 0, c.stream, c.ids,
-                                   static_cast<int>(c.batch), c.count, l.block, order, segs, slots, l.n_slots);
+    ks_status_t st = launch_adapter_order(c, l.o);
     if (st != KS_OK) return st;
     auto blocks_for = [](int64_t n) {
         return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 16384));
     };
     if (c.batch > 0) {
-        if (static_cast<int64_t>(l.n_slots) * std::max(l.splits, (c.n_in + kColsX - 1) / kColsX) >= int64_t(1) << 31)
+        if (static_cast<int64_t>(l.o.n_slots) * std::max(l.splits, (c.n_in + kColsX - 1) / kColsX) >= int64_t(1) << 31)
             return KS_ERR_UNSUPPORTED;
-        const dim3 gy(static_cast<unsigned>(l.n_slots) * l.splits, 1,
+        const dim3 gy(static_cast<unsigned>(l.o.n_slots) * l.splits, 1,
                       static_cast<unsigned>((c.rank + 16 * RT - 1) / (16 * RT)));
         st = launch_kernel(grad_y_kernel<TW, RT>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
                            c.batch, c.n_out, c.rank, static_cast<unsigned>(l.splits), e_part, dB ? w_part : static_cast<float*>(nullptr));
@@ -562,12 +551,12 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
     if (dB) {
         const int64_t size = static_cast<int64_t>(c.n_out) * c.rank;
         st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
-                           c.stream, w_part, segs, size, l.block, dB);
+                           c.stream, w_part, segs, size, l.o.block, dB);
         if (st != KS_OK) return st;
     }
     if (c.batch > 0) {
         const unsigned splits = static_cast<unsigned>((c.n_in + kColsX - 1) / kColsX);
-        const dim3 gx(static_cast<unsigned>(l.n_slots) * splits);
+        const dim3 gx(static_cast<unsigned>(l.o.n_slots) * splits);
         st = launch_kernel(grad_x_kernel<TX, TW, RT>, gx, dim3(kThreads), 0, c.stream, static_cast<const TX*>(X), A, E,
                            order, slots, c.n_in, c.rank, splits, dX, dA ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
@@ -575,7 +564,7 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
     if (dA) {
         const int64_t size = static_cast<int64_t>(c.n_in) * c.rank;
         st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
-                           c.stream, w_part, segs, size, l.block, dA);
+                           c.stream, w_part, segs, size, l.o.block, dA);
     }
     return st;
 }
@@ -589,8 +578,28 @@ ks_status_t run_rank(const AdapterCall& c, const float* dY, const void* X, const
 
 }  // namespace
 
+size_t adapter_order_layout(int64_t batch, int block, int count, char* ws, AdapterOrder* out) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* here = ws ? ws + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    out->block = block;
+    out->n_slots = adapter_slots(batch, block, count);
+    out->order = reinterpret_cast<int*>(take(static_cast<size_t>(batch) * 4));
+    out->segs = reinterpret_cast<Segment*>(take(static_cast<size_t>(count) * sizeof(Segment)));
+    out->slots = reinterpret_cast<Slot*>(take(static_cast<size_t>(out->n_slots) * sizeof(Slot)));
+    return at;
+}
+
+ks_status_t launch_adapter_order(const AdapterCall& c, const AdapterOrder& o) {
+    return launch_kernel(sort_kernel, dim3(static_cast<unsigned>(c.count)), dim3(1024), 0, c.stream, c.ids,
+                         static_cast<int>(c.batch), c.count, o.block, o.order, o.segs, o.slots, o.n_slots);
+}
+
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch) {
-    return layout_of(n_in, n_out, rank, count, batch).total;
+    return layout_of(n_in, n_out, rank, count, batch, nullptr).total;
 }
 
 ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,

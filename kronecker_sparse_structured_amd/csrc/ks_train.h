@@ -21,12 +21,34 @@ struct AdapterCall {
     int num_cus;
 };
 
-// Whether a batch runs as one launch (launch_adapter_rows, H optional) or as
-// the two products, H = X A^T and Y += H B^T.
-bool adapter_one_launch(int64_t batch);
-ks_status_t launch_adapter_rows(const AdapterCall& c, const void* X, float* Y, float* H);
-ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H);
-ks_status_t launch_adapter_up(const AdapterCall& c, const float* H, float* Y);
+// Rows by adapter (stable; rows without an adapter left out), cut into blocks
+// of `block` rows of one adapter each.
+struct AdapterSlot {
+    int adapter, start, len, reserved;   // rows order[start .. start + len); len 0: empty
+};
+struct AdapterSegment {
+    int start, len;                      // an adapter's rows in the order
+};
+struct AdapterOrder {
+    int* order;
+    AdapterSegment* segs;
+    AdapterSlot* slots;
+    int block, n_slots;
+};
+// Blocks of adapter g start at slot floor(start / block) + g: at most one slot
+// an adapter is left empty, and no slot is claimed twice.
+inline int adapter_slots(int64_t batch, int block, int count) { return static_cast<int>(batch / block) + count; }
+// Bytes and layout (from `ws`) of an order for this batch.
+size_t adapter_order_layout(int64_t batch, int block, int count, char* ws, AdapterOrder* out);
+ks_status_t launch_adapter_order(const AdapterCall& c, const AdapterOrder& o);
+
+// How a batch runs: one launch for few rows (H optional); the two products
+// H = X A^T and Y += H B^T over rows sorted by adapter for more; over rows as
+// they lie for many.
+enum AdapterPath : int { kAdapterRows = 0, kAdapterSorted = 1, kAdapterRuns = 2 };
+AdapterPath adapter_path(int64_t batch);
+size_t adapter_workspace(int64_t batch, int count);
+ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float* Y, void* ws);
 
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch);
 ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,

@@ -108,15 +108,18 @@ ks::AdapterCall adapter_call(const ks_adapters_t* ad, const int32_t* ids, int xt
     return c;
 }
 
-// Pointers of the adapters and of a forward call (batch > 0).
+// Pointers of the adapters and of a forward call (batch > 0), and its
+// workspace.
 ks_status_t check_forward(const ks_adapters_t* ad, const int32_t* ids, const void* X, const float* Y, const float* H,
-                          int64_t batch, int xt, int wt) {
+                          int64_t batch, int xt, int wt, const void* ws, size_t ws_bytes, size_t need) {
     if (!ad->A || !ad->B || !ad->scale || !ids || !X || !Y) return KS_ERR_NULL;
+    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
     if (!aligned(ad->A, ks::elem_bytes(wt)) || !aligned(ad->B, ks::elem_bytes(wt)) || !aligned(ad->scale, 4) ||
-        !aligned(ids, 4) || !aligned(X, ks::elem_bytes(xt)) || !aligned(Y, 4) || !aligned(H, 4))
+        !aligned(ids, 4) || !aligned(X, ks::elem_bytes(xt)) || !aligned(Y, 4) || !aligned(H, 4) ||
+        (need > 0 && !aligned(ws, 16)))
         return KS_ERR_ALIGN;
     const uint64_t n = static_cast<uint64_t>(batch);
-    if (any_overlap({{Y, n * ad->n_out * 4}, {H, n * ad->rank * 4}},
+    if (any_overlap({{Y, n * ad->n_out * 4}, {H, n * ad->rank * 4}, {need > 0 ? ws : nullptr, need}},
                     {{X, n * ad->n_in * ks::elem_bytes(xt)}, {ids, n * 4}, {ad->A, a_bytes(ad, wt)},
                      {ad->B, b_bytes(ad, wt)}, {ad->scale, static_cast<uint64_t>(ad->count) * 4}}))
         return KS_ERR_OVERLAP;
@@ -281,24 +284,30 @@ ks_status_t check_states(const ks_adamw_tensor_t& t, int bits, bool step) {
 
 extern "C" {
 
+ks_status_t ks_adapter_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    const ks_status_t st = check_adapters(ad, batch);
+    if (st != KS_OK) return st;
+    *bytes = ks::adapter_workspace(batch, ad->count);
+    return KS_OK;
+}
+
 ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const void* X, float* Y, float* H,
-                              int64_t batch, ks_dtype_t dt, hipStream_t stream) {
-    ks_status_t st = check_adapters(ad, batch);
+                              int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+    size_t need = 0;
+    ks_status_t st = ks_adapter_workspace_size(ad, batch, &need);
     if (st != KS_OK) return st;
     int xt = 0, wt = 0;
     st = adapter_types(enum_value(&dt), &xt, &wt);
     if (st != KS_OK) return st;
     if (batch == 0) return KS_OK;
     if (!H) return KS_ERR_NULL;
-    st = check_forward(ad, ids, X, Y, H, batch, xt, wt);
+    st = check_forward(ad, ids, X, Y, H, batch, xt, wt, ws, ws_bytes, need);
     if (st != KS_OK) return st;
     int cus = 0;
     st = current_cus(&cus);
     if (st != KS_OK) return st;
-    const ks::AdapterCall c = adapter_call(ad, ids, xt, wt, batch, stream, cus);
-    if (ks::adapter_one_launch(batch)) return ks::launch_adapter_rows(c, X, Y, H);
-    st = ks::launch_adapter_down(c, X, H);
-    return st != KS_OK ? st : ks::launch_adapter_up(c, H, Y);
+    return ks::launch_adapter(adapter_call(ad, ids, xt, wt, batch, stream, cus), X, H, Y, ws);
 }
 
 ks_status_t ks_adapter_backward_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes) {
@@ -340,15 +349,16 @@ ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const 
     if (st != KS_OK) return st;
     st = chain_widths(p, n, ad);
     if (st != KS_OK) return st;
-    // H, for callers that do not keep it
-    *bytes = round256(need) + (ks::adapter_one_launch(batch) ? 0 : round256(static_cast<uint64_t>(batch) * ad->rank * 4));
+    // the adapters' own, and H for callers that do not keep it
+    *bytes = round256(need) + round256(ks::adapter_workspace(batch, ad->count)) +
+             (ks::adapter_path(batch) == ks::kAdapterRows ? 0 : round256(static_cast<uint64_t>(batch) * ad->rank * 4));
     return KS_OK;
 }
 
 ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
                                     const int32_t* ids, const void* X, float* Y, float* H, int64_t batch,
                                     ks_dtype_t dt, void* ws, size_t ws_bytes, hipStream_t stream) {
-    size_t need = 0;
+    size_t need = 0, chain_ws = 0;
     const int code = enum_value(&dt);
     ks_status_t st = ks_chain_adapter_workspace_size(p, n, ad, batch, static_cast<ks_dtype_t>(code), &need);
     if (st != KS_OK) return st;
@@ -356,19 +366,8 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     st = adapter_types(code, &xt, &wt);
     if (st != KS_OK) return st;
     if (batch == 0) return KS_OK;
-    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
-    st = check_forward(ad, ids, X, Y, H, batch, xt, wt);
+    st = check_forward(ad, ids, X, Y, H, batch, xt, wt, ws, ws_bytes, need);
     if (st != KS_OK) return st;
-    if (need > 0 && any_overlap({{ws, need}},
-                                {{X, static_cast<uint64_t>(batch) * ad->n_in * ks::elem_bytes(xt)},
-                                 {Y, static_cast<uint64_t>(batch) * ad->n_out * 4},
-                                 {H, static_cast<uint64_t>(batch) * ad->rank * 4},
-                                 {ids, static_cast<uint64_t>(batch) * 4},
-                                 {ad->A, a_bytes(ad, wt)},
-                                 {ad->B, b_bytes(ad, wt)}}))
-        return KS_ERR_OVERLAP;
-    if (need > 0 && !aligned(ws, 16)) return KS_ERR_ALIGN;
-    size_t chain_ws = 0;
     st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
     if (st != KS_OK) return st;
     // the chain's own checks (weights, alignment, overlaps) come first: an
@@ -378,11 +377,10 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     int cus = 0;
     st = current_cus(&cus);
     if (st != KS_OK) return st;
-    const ks::AdapterCall c = adapter_call(ad, ids, xt, wt, batch, stream, cus);
-    if (ks::adapter_one_launch(batch)) return ks::launch_adapter_rows(c, X, Y, H);
-    if (!H) H = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(chain_ws));
-    st = ks::launch_adapter_down(c, X, H);
-    return st != KS_OK ? st : ks::launch_adapter_up(c, H, Y);
+    char* rest = static_cast<char*>(ws) + round256(chain_ws);
+    if (!H && ks::adapter_path(batch) != ks::kAdapterRows)
+        H = reinterpret_cast<float*>(rest + round256(ks::adapter_workspace(batch, ad->count)));
+    return ks::launch_adapter(adapter_call(ad, ids, xt, wt, batch, stream, cus), X, H, Y, rest);
 }
 
 ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,

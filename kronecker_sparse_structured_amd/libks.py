@@ -164,7 +164,8 @@ def load(path: str = LIB_PATH):
     pp, pa, pl, pt = (ctypes.POINTER(t) for t in (ks_pattern_t, ks_adapters_t, ks_logits_t, ks_adamw_tensor_t))
     f32, size, psize = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     for name, args in {
-        "ks_adapter_matmul": [pa, vp, vp, vp, vp, i64, i32, vp],
+        "ks_adapter_workspace_size": [pa, i64, psize],
+        "ks_adapter_matmul": [pa, vp, vp, vp, vp, i64, i32, vp, size, vp],
         "ks_adapter_backward_workspace_size": [pa, i64, psize],
         "ks_adapter_backward": [pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size, vp],
         "ks_chain_adapter_workspace_size": [pp, i32, pa, i64, i32, psize],
@@ -613,8 +614,12 @@ def adapter_matmul(X, A, B, scale, ids, out, keep=False, stream=None):
         raise ValueError("ids must be (batch,) int32")
     ad = _adapters(A, B, scale, X.shape[1], out.shape[1])
     H = torch.empty((X.shape[0], ad.rank), dtype=torch.float32, device=X.device)
+    size = ctypes.c_size_t(0)
+    _raise(load().ks_adapter_workspace_size(ad, X.shape[0], size), "ks_adapter_workspace_size", True)
+    ws = torch.empty(size.value, dtype=torch.uint8, device=X.device) if size.value else None
     _raise(load().ks_adapter_matmul(ad, _ptr(ids), _ptr(X), _ptr(out), _ptr(H), X.shape[0],
-                                    dtype_code(X.dtype, A.dtype), _stream(stream, X)), "ks_adapter_matmul", True)
+                                    dtype_code(X.dtype, A.dtype), _ptr(ws), size.value, _stream(stream, X)),
+           "ks_adapter_matmul", True)
     return (out, H) if keep else out
 
 

@@ -16,10 +16,10 @@ def adapters(n_in=16, n_out=24, rank=4, count=3, **kw):
     return libks.ks_adapters_t(v["A"], v["B"], v["scale"], n_in, n_out, rank, count)
 
 
-def forward(ad=None, batch=8, dt=F32, **kw):
+def forward(ad=None, batch=8, dt=F32, ws_bytes=1 << 30, **kw):
     v = {**P, **kw}
     return libks.load().ks_adapter_matmul(ad if ad is not None else adapters(), v["ids"], v["X"], v["Y"], v["H"], batch,
-                                          dt, None)
+                                          dt, v["ws"], ws_bytes, None)
 
 
 def test_adapter_refusals():
@@ -38,7 +38,13 @@ def test_adapter_refusals():
     assert forward(Y=P["X"] + 8 * 16 * 4 - 4) == libks.KS_ERR_OVERLAP
     assert forward(H=P["Y"] + 4) == libks.KS_ERR_OVERLAP
     assert forward(Y=P["ids"]) == libks.KS_ERR_OVERLAP
-    assert libks.load().ks_adapter_matmul(None, P["ids"], P["X"], P["Y"], P["H"], 8, F32, None) == libks.KS_ERR_NULL
+    assert libks.load().ks_adapter_matmul(None, P["ids"], P["X"], P["Y"], P["H"], 8, F32, None, 0,
+                                          None) == libks.KS_ERR_NULL
+    size = ctypes.c_size_t(0)
+    assert libks.load().ks_adapter_workspace_size(adapters(), 1000, size) == libks.KS_OK and size.value >= 4000
+    assert forward(batch=1000, ws_bytes=size.value - 1) == libks.KS_ERR_WORKSPACE
+    assert forward(batch=1000, ws=P["ws"] + 4) == libks.KS_ERR_ALIGN
+    assert forward(batch=1000, ws=P["X"]) == libks.KS_ERR_OVERLAP
     assert forward(batch=0, X=None, Y=None, ids=None, H=None) == libks.KS_OK
 
 
