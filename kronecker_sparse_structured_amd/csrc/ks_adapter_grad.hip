@@ -10,7 +10,7 @@
 //   1. sort    rows by adapter (stable), cut into blocks of rows that belong
 //              to one adapter each: the rest never meets a mixed block.
 //   2. grad_y  a pass over dY: partial E and dB.
-//   3. sum     the partial sums, in order.
+//   3. sum     dB and E from their partial sums, in order.
 //   4. grad_x  a pass over X and dX: dX, partial dA.
 //   5. sum     dA.
 // No atomics; the order of every sum is fixed by ids alone.
@@ -53,14 +53,13 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     const int per = ((batch + 15) / 16 + 63) / 64 * 64;
     const int i0 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(wave) * per));
     const int i1 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(i0) + per));
-    constexpr int kBatch = 8;       // loads in flight
-    int own = 0, less = 0;
-    for (int i = i0; i < i1; i += 64 * kBatch) {
-        int id[kBatch];
+    constexpr int kHeld = 32;       // ids a lane holds: one read of up to 32768 rows
+    int own = 0, less = 0, id[kHeld];
+    for (int i = i0; i < i1; i += 64 * kHeld) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
+        for (int u = 0; u < kHeld; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kHeld; ++u) {
             own += __popcll(__ballot(id[u] == g));
             less += __popcll(__ballot(id[u] >= 0 && id[u] < g));
         }
@@ -78,12 +77,14 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     }
     at += start;
     if (own) {
-        for (int i = i0; i < i1; i += 64 * kBatch) {
-            int id[kBatch];
+        const bool held = i1 - i0 <= 64 * kHeld;
+        for (int i = i0; i < i1; i += 64 * kHeld) {
+            if (!held) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
+                for (int u = 0; u < kHeld; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
+            }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
+            for (int u = 0; u < kHeld; ++u) {
                 const uint64_t all = __ballot(id[u] == g);
                 if (id[u] == g) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = i + 64 * u + lane;
                 at += __popcll(all);
@@ -115,7 +116,8 @@ __device__ __forceinline__ float value_at(const T* p, int64_t row, int64_t width
 // while this one is multiplied. A wave takes 16 rows of the tile for E (inner
 // index: the columns, 16 lg + j for lane group lg) and 16 columns for dB (inner
 // index: the rows, 4 j + lg).
-template <typename TW, int RT>
+// PAST: dY goes past the last cache.
+template <typename TW, int RT, bool PAST>
 __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const TW* B, const float* H,
                                                           const float* scale, const int* order, const Slot* slots,
                                                           int64_t batch, int n_out, int rank, unsigned splits, float* e_part,
@@ -148,7 +150,10 @@ __global__ __launch_bounds__(kThreads) void grad_y_kernel(const float* dY, const
             const float* src = dY + static_cast<int64_t>(row_of[at]) * n_out + o;
             const int valid = at < s.len ? n_out - o : 0;
             if (wide && valid >= 4) {
-                load4_f32(src, next[q]);
+                const f32x4 v = PAST ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src))
+                                     : *reinterpret_cast<const f32x4*>(src);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) next[q][i] = v[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) next[q][i] = i < valid ? src[i] : 0.0f;
@@ -276,9 +281,10 @@ __device__ __forceinline__ void wave_fence() {
 // 64 x 64. X goes through LDS for dA (inner index: the rows; a wave takes 16
 // columns); for dX a wave takes 16 rows, forms its product with the columns
 // along the instruction's rows and turns it in LDS, so that dX is read and
-// written in runs of 256 bytes.
+// written in runs of 256 bytes. (Two waves a SIMD at least: without that bound the
+// compiler takes more registers, 38 us against 27 at 25216 x 384 in fp32.)
 template <typename TX, typename TW, int RT>
-__global__ __launch_bounds__(kThreads) void grad_x_kernel(const TX* X, const TW* A, const float* E, const int* order,
+__global__ __launch_bounds__(kThreads, 2) void grad_x_kernel(const TX* X, const TW* A, const float* E, const int* order,
                                                           const Slot* slots, int n_in, int rank, unsigned splits,
                                                           float* dX, float* da_part) {
     constexpr int kR = 16 * RT + 1, kTiles = kColsX / 64, kTurn = 68;
@@ -461,26 +467,24 @@ __device__ __forceinline__ float sum_of(const float* p, int64_t stride, int n) {
     return sum;
 }
 
-// E[i] = sum over the column ranges; `parts` planes of `stride` values.
-__global__ __launch_bounds__(kThreads) void sum_planes_kernel(const float* part, int64_t n, int64_t stride, int parts,
-                                                              float* out) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        out[i] = sum_of(part + i, stride, parts);
+// Gradient of the adapters' weights (`size` values each): the sum over an
+// adapter's blocks of rows, zeros without any; and, in the workgroups past
+// those (part_e not NULL), E as the sum over the column ranges: `planes` of
+// `n_e` values.
+__global__ __launch_bounds__(kThreads) void sum_kernel(const float* part, const Segment* segs, int64_t size, int block,
+                                                       int per_adapter, int count, float* out, const float* part_e,
+                                                       int64_t n_e, int planes, float* E) {
+    const int64_t wg = blockIdx.x, weights = static_cast<int64_t>(per_adapter) * count;
+    if (wg >= weights) {
+        const int64_t i = (wg - weights) * kThreads + threadIdx.x;
+        if (i < n_e) E[i] = sum_of(part_e + i, n_e, planes);
+        return;
     }
-}
-
-// Gradient of one adapter's weights (`size` values each): the sum over its
-// blocks of rows, zeros without any.
-__global__ __launch_bounds__(kThreads) void sum_slots_kernel(const float* part, const Segment* segs, int64_t size,
-                                                             int block, float* out) {
-    const int g = blockIdx.y;
+    const int g = static_cast<int>(wg / per_adapter);
+    const int64_t i = wg % per_adapter * kThreads + threadIdx.x;
+    if (i >= size) return;
     const Segment seg = segs[g];
-    const int s0 = first_slot(seg, g, block), blocks = (seg.len + block - 1) / block;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < size;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        out[g * size + i] = sum_of(part + s0 * size + i, size, blocks);
-    }
+    out[g * size + i] = sum_of(part + first_slot(seg, g, block) * size + i, size, (seg.len + block - 1) / block);
 }
 
 struct Layout {
@@ -530,30 +534,29 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
     const TW* B = static_cast<const TW*>(c.B);
     ks_status_t st = launch_adapter_order(c, l.o);
     if (st != KS_OK) return st;
-    auto blocks_for = [](int64_t n) {
-        return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 16384));
+    // one launch for dB (or dA) and, with planes > 1, for E
+    auto sum = [&](int64_t size, float* out, int planes) {
+        const int64_t per = out ? (size + kThreads - 1) / kThreads : 0, n_e = planes > 1 ? c.batch * c.rank : 0;
+        const int64_t blocks = per * c.count + (n_e + kThreads - 1) / kThreads;
+        if (blocks == 0) return KS_OK;
+        if (blocks >= int64_t(1) << 31) return KS_ERR_UNSUPPORTED;
+        return launch_kernel(sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, c.stream, w_part, segs,
+                             size, l.o.block, static_cast<int>(per), out ? c.count : 0, out, e_part, n_e, planes, E);
     };
     if (c.batch > 0) {
         if (static_cast<int64_t>(l.o.n_slots) * std::max(l.splits, (c.n_in + kColsX - 1) / kColsX) >= int64_t(1) << 31)
             return KS_ERR_UNSUPPORTED;
         const dim3 gy(static_cast<unsigned>(l.o.n_slots) * l.splits, 1,
                       static_cast<unsigned>((c.rank + 16 * RT - 1) / (16 * RT)));
-        st = launch_kernel(grad_y_kernel<TW, RT>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
+        // a dY that the last cache cannot hold goes past it (16384 x 4096: 130 us a
+        // call, 155 through it; smaller ones are there from the projection's pass)
+        const bool past_cache = c.batch * c.n_out * 4 > int64_t(192) << 20;
+        st = launch_kernel(past_cache ? grad_y_kernel<TW, RT, true> : grad_y_kernel<TW, RT, false>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
                            c.batch, c.n_out, c.rank, static_cast<unsigned>(l.splits), e_part, dB ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
-        if (l.splits > 1) {
-            const int64_t n = c.batch * c.rank;
-            st = launch_kernel(sum_planes_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, c.stream, e_part, n, n,
-                               l.splits, E);
-            if (st != KS_OK) return st;
-        }
     }
-    if (dB) {
-        const int64_t size = static_cast<int64_t>(c.n_out) * c.rank;
-        st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
-                           c.stream, w_part, segs, size, l.o.block, dB);
-        if (st != KS_OK) return st;
-    }
+    st = sum(static_cast<int64_t>(c.n_out) * c.rank, dB, c.batch > 0 ? l.splits : 0);
+    if (st != KS_OK) return st;
     if (c.batch > 0) {
         const unsigned splits = static_cast<unsigned>((c.n_in + kColsX - 1) / kColsX);
         const dim3 gx(static_cast<unsigned>(l.o.n_slots) * splits);
@@ -561,12 +564,7 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
                            order, slots, c.n_in, c.rank, splits, dX, dA ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
     }
-    if (dA) {
-        const int64_t size = static_cast<int64_t>(c.n_in) * c.rank;
-        st = launch_kernel(sum_slots_kernel, dim3(blocks_for(size), static_cast<unsigned>(c.count)), dim3(kThreads), 0,
-                           c.stream, w_part, segs, size, l.o.block, dA);
-    }
-    return st;
+    return sum(static_cast<int64_t>(c.n_in) * c.rank, dA, 0);
 }
 
 template <typename TX, typename TW>
