@@ -111,13 +111,6 @@ __device__ __forceinline__ void load_lane(const T* src, int valid, bool wide, fl
     }
 }
 
-// fp32 to bf16, nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    return x != x ? 0x7fc0u : r;
-}
-
 template <typename T>
 __device__ __forceinline__ void store_lane(T* dst, int valid, bool wide, const float (&x)[kLane]) {
     if (wide && valid == kLane) {
@@ -133,7 +126,7 @@ __device__ __forceinline__ void store_lane(T* dst, int valid, bool wide, const f
         } else {
             u32x4 a;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+            for (int i = 0; i < 4; ++i) a[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
             *reinterpret_cast<u32x4*>(dst) = a;
         }
     } else {
@@ -141,7 +134,7 @@ __device__ __forceinline__ void store_lane(T* dst, int valid, bool wide, const f
         for (int i = 0; i < kLane; ++i) {
             if (i < valid) {
                 if constexpr (sizeof(T) == 4) dst[i] = x[i];
-                else dst[i] = static_cast<bf16_t>(bf16_bits(x[i]));
+                else dst[i] = to_bf16(x[i]);
             }
         }
     }

@@ -36,6 +36,15 @@ __device__ __forceinline__ void load4_f32(const bf16_t* p, float (&v)[4]) {
     v[3] = bf16_hi(w[1]);
 }
 
+// fp32 to bf16, nearest even (NaN stays NaN): one value's bits, or two in a
+// word (the conversion instruction takes pairs).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+__device__ __forceinline__ bf16_t to_bf16(float x) { return static_cast<bf16_t>(pack_bf16(x, 0.0f)); }
+
 template <int N>
 __device__ __forceinline__ void zero(float (&v)[N]) {
 #pragma unroll

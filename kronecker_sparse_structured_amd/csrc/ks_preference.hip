@@ -35,7 +35,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr float kLog2e = 1.44269504088896340736f;
+// log2 e in two parts: the fp32 value alone is 1.3e-8 too small, which a sum of
+// terms near exp(-6) shows as 8e-8, the same way in every row
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f;
 constexpr float kLowest = -3.402823466e38f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -57,16 +59,10 @@ __device__ __forceinline__ void widen(u32x4 w, float (&x)[kVec<T>]) {
     }
 }
 
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    return x != x ? 0x7fc0u : r;
-}
-
 template <typename T>
 __device__ __forceinline__ T narrow(float x) {
     if constexpr (sizeof(T) == 4) return x;
-    else return static_cast<bf16_t>(bf16_bits(x));
+    else return to_bf16(x);
 }
 
 template <typename T>
@@ -75,7 +71,7 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kVec<T>]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
-        else w[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+        else w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     }
     return w;
 }
@@ -87,7 +83,9 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
     return min(n, bytes / static_cast<int>(sizeof(T)));
 }
 
-__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+__device__ __forceinline__ float exp_of(float d) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kLog2e, d * kLog2eLow));
+}
 
 // Joins (m2, s2) to (m, s).
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
