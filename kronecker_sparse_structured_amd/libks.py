@@ -14,7 +14,9 @@ allocate the output (and the chain workspace) with torch.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -721,16 +723,16 @@ def _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream):
             raise ValueError("dlogits must have the logits' shape, type and device")
         d_seq, d_row = _layout(dlogits, "dlogits")
     S, T = x.sequences, x.tokens
-    f32, device = torch.float32, logits.device
-    loss = torch.empty((), dtype=f32, device=device)
-    rewards = torch.empty((S,), dtype=f32, device=device)
-    tokens = torch.empty((S, T), dtype=f32, device=device)
-    scratch = torch.empty((S + 2 * S * T,), dtype=f32, device=device)
-    at = scratch.data_ptr()
+    # one allocation: loss, rewards, tokens, and what backward reads
+    n, f32 = S * T, torch.float32
+    buf = torch.empty((1 + 2 * S + 3 * n,), dtype=f32, device=logits.device)
+    loss, rewards = buf.as_strided((), (), 0), buf.as_strided((S,), (1,), 1)
+    tokens, scratch = buf.as_strided((S, T), (T, 1), 1 + S), buf.as_strided((S + 2 * n,), (1,), 1 + S + n)
+    first = buf.data_ptr()
+    at = first + 4 * (1 + S + n)
     _raise(load().ks_preference_loss(x, ref.data_ptr(), _rows_stride(ref, "ref"), float(beta), float(smoothing),
-                                     loss.data_ptr(), rewards.data_ptr(), tokens.data_ptr(), at, at + 4 * S,
-                                     _ptr(dlogits), d_seq, d_row, _raw_stream(stream, logits.get_device())),
-           "ks_preference_loss", True)
+                                     first, first + 4, first + 4 * (1 + S), at, at + 4 * S, _ptr(dlogits),
+                                     d_seq, d_row, _raw_stream(stream, logits.get_device())), "ks_preference_loss", True)
     return loss, rewards, tokens, scratch
 
 
@@ -741,7 +743,7 @@ def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, 
     dlogits may be given (the logits themselves too: then it replaces them)."""
     import torch
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     loss, rewards, tokens, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
     return loss, rewards, tokens, dlogits
 
@@ -760,6 +762,7 @@ def _preference_backward(logits, labels, scratch, upstream, stream=None):
 # ---------------------------------------------------------------- optimizer
 
 ADAMW_BLOCK = 256   # values that share a scale in 8 bits
+_dtype_of = operator.attrgetter("dtype")
 
 
 class AdamW:
@@ -780,24 +783,30 @@ class AdamW:
         T = torch.Tensor
         self._sizes = list(map(T.numel, params))
         index = self.device.index if n else None
-        for ts, name in ((params, "params"), (grads, "grads"), (ms, "ms"), (vs, "vs")):
-            for i, t in enumerate(ts):
-                _check_tensor(t, "%s[%d]" % (name, i))
-            if list(map(T.numel, ts)) != self._sizes or any(d != index for d in map(T.get_device, ts)):
-                raise ValueError("%s must have their parameters' sizes, on one device" % name)
+        sets = [(params, "params"), (grads, "grads"), (ms, "ms"), (vs, "vs")]
+        for ts, name in sets:
+            if list(map(T.numel, ts)) != self._sizes:
+                raise ValueError("%s must have their parameters' sizes" % name)
+        if scales is not None:
+            sets.append((scales, "scales"))
+            if [t.shape for t in scales] != [(-(-size // ADAMW_BLOCK), 2) for size in self._sizes] \
+                    or any(t.dtype is not torch.float32 for t in scales):
+                raise ValueError("scales must be (ceil(n / %d), 2) fp32" % ADAMW_BLOCK)
+        for ts, name in sets:
+            if not all(t.is_cuda for t in ts) or not all(map(T.is_contiguous, ts)) \
+                    or any(d != index for d in map(T.get_device, ts)):
+                raise ValueError("%s must be contiguous, on one device" % name)
         if any(t.dtype is not types[0] for t in ms) or any(t.dtype is not types[1] for t in vs):
             raise TypeError("moments must be %s and %s" % types)
-        if scales is not None:
-            for i, s in enumerate(scales):
-                _check_out(s, (-(-self._sizes[i] // ADAMW_BLOCK), 2), torch.float32, self.device, "scales[%d]" % i)
         at = [list(map(T.data_ptr, ts)) for ts in (params, grads, ms, vs)]
         at.append(list(map(T.data_ptr, scales)) if scales is not None else [None] * n)
         self._t = (ks_adamw_tensor_t * max(n, 1))(*[
             ks_adamw_tensor_t(*a, size, _elem(p.dtype, "params"), _elem(g.dtype, "grads"))
             for *a, size, p, g in zip(*at, self._sizes, params, grads)])
-        spans = sorted((a, a + t.numel() * t.element_size())
-                       for ts, addr in zip((params, ms, vs, scales or []), (at[0], at[2], at[3], at[4]))
-                       for t, a in zip(ts, addr) if t.numel())
+        spans = []
+        for ts, addr in ((params, at[0]), (ms, at[2]), (vs, at[3]), (scales or [], at[4])):
+            spans += [(a, a + b) for a, b in zip(addr, [t.nbytes for t in ts]) if b]
+        spans.sort()
         if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
             raise ValueError("parameters and moments must not share memory")
         self._keep = (list(params), list(grads), list(ms), list(vs), list(scales or ()))
@@ -843,13 +852,12 @@ class AdamW:
             raise ValueError("one output a tensor")
         if self._n == 0:
             return
-        T, index = torch.Tensor, self.device.index
+        T, index, ptrs = torch.Tensor, self.device.index, []
         for outs in (ms_out, vs_out):
-            if list(map(T.numel, outs)) != self._sizes or any(t.dtype is not torch.float32 for t in outs):
+            if list(map(T.numel, outs)) != self._sizes or set(map(_dtype_of, outs)) != {torch.float32}:
                 raise ValueError("outputs must be fp32 of their parameter's size")
             if set(map(T.get_device, outs)) != {index} or not all(map(T.is_contiguous, outs)):
                 raise ValueError("outputs must be contiguous, on the parameters' device")
-        mp = (ctypes.c_void_p * self._n)(*map(T.data_ptr, ms_out))
-        vp = (ctypes.c_void_p * self._n)(*map(T.data_ptr, vs_out))
-        _raise(self._lib.ks_adamw_state_values(self._t, self._n, mp, vp, _raw_stream(stream, index)),
+            ptrs.append((ctypes.c_void_p * self._n).from_buffer(array.array("Q", map(T.data_ptr, outs))))
+        _raise(self._lib.ks_adamw_state_values(self._t, self._n, *ptrs, _raw_stream(stream, index)),
                "ks_adamw_state_values", True)
