@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kTensors = 60;      // a launch: 60 * 56 bytes + options stay under 4 KB of arguments
 constexpr int kThreads = 256;
+constexpr int64_t kMaxGroups = int64_t(1) << 23;   // workgroups a launch: a grid counts its threads in 32 bits
 constexpr int kBlock = 256;       // values that share a scale
 constexpr int kLane = 8;          // consecutive values a lane holds: half a wave covers a block
 constexpr int kStep = kThreads * kLane;
@@ -402,7 +403,7 @@ ks_status_t for_tables(const ks_adamw_tensor_t* t, int n, int64_t chunk, Fill fi
     for (int i = 0; i < n; ++i) {
         const int64_t groups = (t[i].n + chunk - 1) / chunk;
         if (groups > 0) {
-            if (table.count == kTensors || wgs + groups >= (int64_t(1) << 31)) {
+            if (table.count == kTensors || wgs + groups > kMaxGroups) {
                 const ks_status_t st = run(table, static_cast<unsigned>(wgs));
                 if (st != KS_OK) return st;
                 table.count = 0;

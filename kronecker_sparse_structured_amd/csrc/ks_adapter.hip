@@ -53,6 +53,7 @@ struct Args {
     float* H;
     int64_t batch;
     int n_in, n_out, rank, count;
+    int64_t first;           // first workgroup of a launch among all of the batch's
 };
 
 // Four consecutive values from an address that is aligned to them (WIDE), or
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a, co
     __shared__ int id_of[kTile];
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
     const int li = lane % 16, lg = lane / 16;
-    const int64_t block = blockIdx.x;
+    const int64_t block = a.first + blockIdx.x;
     if (o.order && block >= o.n_slots) {
         // a row a thread; a wave clears the rows it has found
         const int64_t row0 = (block - o.n_slots) * kThreads + wave * 64, i = row0 + lane;
@@ -381,9 +382,10 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
     // neighbouring workgroups take neighbouring columns of the same rows: with
     // rows fastest, all that run together would meet in a few memory channels
     const unsigned slabs = (a.n_out + kUpCols - 1) / kUpCols;
-    const int o0 = blockIdx.x % slabs * kUpCols + wave * 64;
+    const int64_t group = a.first + blockIdx.x;
+    const int o0 = static_cast<int>(group % slabs) * kUpCols + wave * 64;
     if (o0 >= a.n_out) return;
-    const int64_t block = blockIdx.x / slabs;
+    const int64_t block = group / slabs;
     Tile tile = o.order ? Tile(o.order, o.slots[block]) : Tile(a.ids, a.batch, a.count, block * kTile);
     if (!tile.left) return;
     const int rows = tile.rows;
@@ -484,15 +486,26 @@ ks_status_t launch_rows(const Args& a, hipStream_t stream, int num_cus) {
                          stream, a, slice);
 }
 
+// A grid counts its threads in 32 bits: at most 2^23 workgroups a launch.
+ks_status_t launch_groups(void (*kernel)(Args, AdapterOrder), int64_t blocks, Args a, const AdapterOrder& o,
+                          hipStream_t stream) {
+    constexpr int64_t kMost = int64_t(1) << 23;
+    for (a.first = 0; a.first < blocks; a.first += kMost) {
+        const ks_status_t st = launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(kMost, blocks - a.first))),
+                                             dim3(kThreads), 0, stream, a, o);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
 template <typename TX, typename TW>
 ks_status_t launch_down(const Args& a, const AdapterOrder& o, hipStream_t stream) {
     const bool wide = on16(a.X) && on16(a.A) && a.n_in % (16 / sizeof(TX)) == 0 && a.n_in % (16 / sizeof(TW)) == 0;
-    const dim3 grid(static_cast<unsigned>(o.order ? o.n_slots + (a.batch + kThreads - 1) / kThreads
-                                                  : (a.batch + kTile - 1) / kTile));
+    const int64_t blocks = o.order ? o.n_slots + (a.batch + kThreads - 1) / kThreads : (a.batch + kTile - 1) / kTile;
     void (*kernel)(Args, AdapterOrder);
     if (a.rank <= 16) kernel = wide ? adapter_down_kernel<TX, TW, 1, true> : adapter_down_kernel<TX, TW, 1, false>;
     else kernel = wide ? adapter_down_kernel<TX, TW, 2, true> : adapter_down_kernel<TX, TW, 2, false>;
-    return launch_kernel(kernel, grid, dim3(kThreads), 0, stream, a, o);
+    return launch_groups(kernel, blocks, a, o, stream);
 }
 
 template <typename TW>
@@ -500,12 +513,10 @@ ks_status_t launch_up(const Args& a, const AdapterOrder& o, hipStream_t stream) 
     const bool wide = on16(a.B) && on16(a.H) && on16(a.Y) && a.rank % 4 == 0 && a.n_out % 4 == 0;
     const int64_t tiles = o.order ? o.n_slots : (a.batch + kTile - 1) / kTile;
     const int64_t blocks = tiles * ((a.n_out + kUpCols - 1) / kUpCols);
-    if (blocks >= int64_t(1) << 31) return KS_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(blocks));
     void (*kernel)(Args, AdapterOrder);
     if (a.rank <= 16) kernel = wide ? adapter_up_kernel<TW, 1, true> : adapter_up_kernel<TW, 1, false>;
     else kernel = wide ? adapter_up_kernel<TW, 2, true> : adapter_up_kernel<TW, 2, false>;
-    return launch_kernel(kernel, grid, dim3(kThreads), 0, stream, a, o);
+    return launch_groups(kernel, blocks, a, o, stream);
 }
 
 template <typename TX, typename TW>
@@ -540,7 +551,7 @@ size_t adapter_workspace(int64_t batch, int count) {
 }
 
 ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float* Y, void* ws) {
-    const Args a{c.A, c.B, c.scale, c.ids, X, Y, H, c.batch, c.n_in, c.n_out, c.rank, c.count};
+    const Args a{c.A, c.B, c.scale, c.ids, X, Y, H, c.batch, c.n_in, c.n_out, c.rank, c.count, 0};
     if (c.xt == kBF16) return launch_types<bf16_t, bf16_t>(c, a, ws);
     if (c.wt == kBF16) return launch_types<float, bf16_t>(c, a, ws);
     return launch_types<float, float>(c, a, ws);

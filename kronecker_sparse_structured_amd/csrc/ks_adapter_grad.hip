@@ -50,12 +50,11 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
                                                     Segment* segs, Slot* slots, int n_slots) {
     __shared__ int wave_own[16], wave_less[16];
     const int g = blockIdx.x, tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    const int per = ((batch + 15) / 16 + 63) / 64 * 64;
-    const int i0 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(wave) * per));
-    const int i1 = static_cast<int>(min(static_cast<int64_t>(batch), static_cast<int64_t>(i0) + per));
+    const int64_t per = ((static_cast<int64_t>(batch) + 15) / 16 + 63) / 64 * 64;
+    const int64_t i0 = min(static_cast<int64_t>(batch), wave * per), i1 = min(static_cast<int64_t>(batch), i0 + per);
     constexpr int kHeld = 32;       // ids a lane holds: one read of up to 32768 rows
     int own = 0, less = 0, id[kHeld];
-    for (int i = i0; i < i1; i += 64 * kHeld) {
+    for (int64_t i = i0; i < i1; i += 64 * kHeld) {
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
 #pragma unroll
@@ -78,7 +77,7 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
     at += start;
     if (own) {
         const bool held = i1 - i0 <= 64 * kHeld;
-        for (int i = i0; i < i1; i += 64 * kHeld) {
+        for (int64_t i = i0; i < i1; i += 64 * kHeld) {
             if (!held) {
 #pragma unroll
                 for (int u = 0; u < kHeld; ++u) id[u] = i + 64 * u + lane < i1 ? ids[i + 64 * u + lane] : -1;
@@ -86,7 +85,7 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* ids, int batc
 #pragma unroll
             for (int u = 0; u < kHeld; ++u) {
                 const uint64_t all = __ballot(id[u] == g);
-                if (id[u] == g) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = i + 64 * u + lane;
+                if (id[u] == g) order[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = static_cast<int>(i + 64 * u + lane);
                 at += __popcll(all);
             }
         }
@@ -532,6 +531,11 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
     float* w_part = reinterpret_cast<float*>(ws + l.w_part);
     const TW* A = static_cast<const TW*>(c.A);
     const TW* B = static_cast<const TW*>(c.B);
+    // a grid counts its threads in 32 bits: 2^24 workgroups of 256 are one too many
+    const int64_t most = (int64_t(1) << 24) - 1, wide = std::max(c.n_in, c.n_out);
+    if (static_cast<int64_t>(l.o.n_slots) * ((wide + kColsX - 1) / kColsX) > most ||
+        (wide * c.rank + kThreads - 1) / kThreads * c.count + (c.batch * c.rank + kThreads - 1) / kThreads > most)
+        return KS_ERR_UNSUPPORTED;
     ks_status_t st = launch_adapter_order(c, l.o);
     if (st != KS_OK) return st;
     // one launch for dB (or dA) and, with planes > 1, for E
@@ -539,20 +543,18 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
         const int64_t per = out ? (size + kThreads - 1) / kThreads : 0, n_e = planes > 1 ? c.batch * c.rank : 0;
         const int64_t blocks = per * c.count + (n_e + kThreads - 1) / kThreads;
         if (blocks == 0) return KS_OK;
-        if (blocks >= int64_t(1) << 31) return KS_ERR_UNSUPPORTED;
         return launch_kernel(sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, c.stream, w_part, segs,
                              size, l.o.block, static_cast<int>(per), out ? c.count : 0, out, e_part, n_e, planes, E);
     };
     if (c.batch > 0) {
-        if (static_cast<int64_t>(l.o.n_slots) * std::max(l.splits, (c.n_in + kColsX - 1) / kColsX) >= int64_t(1) << 31)
-            return KS_ERR_UNSUPPORTED;
         const dim3 gy(static_cast<unsigned>(l.o.n_slots) * l.splits, 1,
                       static_cast<unsigned>((c.rank + 16 * RT - 1) / (16 * RT)));
         // a dY that the last cache cannot hold goes past it (16384 x 4096: 130 us a
         // call, 155 through it; smaller ones are there from the projection's pass)
         const bool past_cache = c.batch * c.n_out * 4 > int64_t(192) << 20;
-        st = launch_kernel(past_cache ? grad_y_kernel<TW, RT, true> : grad_y_kernel<TW, RT, false>, gy, dim3(kThreads), 0, c.stream, dY, B, H, c.scale, order, slots,
-                           c.batch, c.n_out, c.rank, static_cast<unsigned>(l.splits), e_part, dB ? w_part : static_cast<float*>(nullptr));
+        st = launch_kernel(past_cache ? grad_y_kernel<TW, RT, true> : grad_y_kernel<TW, RT, false>, gy, dim3(kThreads),
+                           0, c.stream, dY, B, H, c.scale, order, slots, c.batch, c.n_out, c.rank,
+                           static_cast<unsigned>(l.splits), e_part, dB ? w_part : static_cast<float*>(nullptr));
         if (st != KS_OK) return st;
     }
     st = sum(static_cast<int64_t>(c.n_out) * c.rank, dB, c.batch > 0 ? l.splits : 0);

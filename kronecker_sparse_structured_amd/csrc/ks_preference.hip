@@ -34,6 +34,7 @@ namespace ks {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxRows = int64_t(1) << 23;   // rows a launch: a grid counts its threads in 32 bits
 constexpr int kWaves = kThreads / 64;
 // log2 e in two parts: the fp32 value alone is 1.3e-8 too small, which a sum of
 // terms near exp(-6) shows as 8e-8, the same way in every row
@@ -97,10 +98,10 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 // KEEP: a gradient may follow and read these logits again; else they go past the
 // last cache (16 x 512 rows of 32000 in bf16: 74 us, 80 through it).
 template <typename T, bool KEEP>
-__global__ __launch_bounds__(kThreads) void token_logp_kernel(const ks_logits_t x_, float* tokens, float* stats) {
+__global__ __launch_bounds__(kThreads) void token_logp_kernel(const ks_logits_t x_, int64_t row0, float* tokens, float* stats) {
     __shared__ float wave_m[kWaves], wave_s[kWaves];
     constexpr int E = kVec<T>;
-    const int64_t at = blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
+    const int64_t at = row0 + blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
     const int64_t label = x_.labels[s_ * x_.label_stride + t_];
     if (label < 0) {
         if (threadIdx.x == 0) {
@@ -264,13 +265,13 @@ __global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, co
 // output row may start at another place of a 16-byte
 // granule than the input row: then it goes element-wise.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logit_grad_kernel(const ks_logits_t x_, const float* stats, const float* grad,
+__global__ __launch_bounds__(kThreads) void logit_grad_kernel(const ks_logits_t x_, int64_t row0, const float* stats, const float* grad,
                                                               const float* upstream, T* d, int64_t d_seq,
                                                               int64_t d_row) {
     constexpr int E = kVec<T>;
     // the rows that the first stream read last come first: the last cache still
     // holds some 200 MB of them
-    const int64_t at = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
+    const int64_t at = row0 + gridDim.x - 1 - blockIdx.x, s_ = at / x_.tokens, t_ = at - s_ * x_.tokens;
     const int64_t label = x_.labels[s_ * x_.label_stride + t_];
     const T* row = static_cast<const T*>(x_.data) + s_ * x_.seq_stride + t_ * x_.row_stride;
     T* out = d + s_ * d_seq + t_ * d_row;
@@ -334,12 +335,16 @@ __global__ __launch_bounds__(kThreads) void logit_grad_kernel(const ks_logits_t 
 }  // namespace
 
 ks_status_t launch_token_logp(const ks_logits_t& x, float* tokens, float* stats, hipStream_t stream) {
-    const int64_t rows = x.sequences * x.tokens;
-    if (rows == 0) return KS_OK;
-    void (*kernel)(ks_logits_t, float*, float*);
+    void (*kernel)(ks_logits_t, int64_t, float*, float*);
     if (x.elem == KS_ELEM_BF16) kernel = stats ? token_logp_kernel<bf16_t, true> : token_logp_kernel<bf16_t, false>;
     else kernel = stats ? token_logp_kernel<float, true> : token_logp_kernel<float, false>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, x, tokens, stats);
+    const int64_t rows = x.sequences * x.tokens;
+    for (int64_t r = 0; r < rows; r += kMaxRows) {
+        const ks_status_t st = launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(kMaxRows, rows - r))),
+                                             dim3(kThreads), 0, stream, x, r, tokens, stats);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
 }
 
 ks_status_t launch_sequence_sum(const ks_logits_t& x, const float* tokens, float* total, hipStream_t stream) {
@@ -357,13 +362,18 @@ ks_status_t launch_pair_loss(const ks_logits_t& x, const float* tokens, const fl
 ks_status_t launch_logit_grad(const ks_logits_t& x, const float* stats, const float* grad, const float* upstream,
                               void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
     const int64_t rows = x.sequences * x.tokens;
-    if (rows == 0) return KS_OK;
-    const dim3 grid(static_cast<unsigned>(rows));
-    if (x.elem == KS_ELEM_BF16)
-        return launch_kernel(logit_grad_kernel<bf16_t>, grid, dim3(kThreads), 0, stream, x, stats, grad, upstream,
-                             static_cast<bf16_t*>(d), d_seq, d_row);
-    return launch_kernel(logit_grad_kernel<float>, grid, dim3(kThreads), 0, stream, x, stats, grad, upstream,
-                         static_cast<float*>(d), d_seq, d_row);
+    for (int64_t end = rows; end > 0; end -= std::min(kMaxRows, end)) {
+        const int64_t n = std::min(kMaxRows, end);
+        const dim3 grid(static_cast<unsigned>(n));
+        const ks_status_t st =
+            x.elem == KS_ELEM_BF16
+                ? launch_kernel(logit_grad_kernel<bf16_t>, grid, dim3(kThreads), 0, stream, x, end - n, stats, grad,
+                                upstream, static_cast<bf16_t*>(d), d_seq, d_row)
+                : launch_kernel(logit_grad_kernel<float>, grid, dim3(kThreads), 0, stream, x, end - n, stats, grad,
+                                upstream, static_cast<float*>(d), d_seq, d_row);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
 }
 
 }  // namespace ks
