@@ -425,14 +425,26 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
 
 /*
  * ks_chain_adapter_backward: dX of the chain (dY W_{n-1} ... W_0, W frozen)
- * plus the adapters', and dA and dB (both NULL: not computed).
+ * plus the adapters', and dA and dB (both NULL: not computed). The chain's part
+ * is the chain of the factors in reverse with every block transposed, planned as
+ * ks_chain_matmul plans it.
+ *   Wt     NULL: W's blocks are transposed in the workspace by each call. Else
+ *          device, what ks_chain_transpose wrote for the same p, n and weights
+ *          (ks_chain_transpose_size bytes, 16-byte aligned): a layer whose W does
+ *          not change makes it once; W may then be NULL.
+ *   ws     of ks_chain_adapter_backward_workspace_size bytes, which has to be
+ *          told whether Wt will be given.
  */
+ks_status_t ks_chain_transpose_size(const ks_pattern_t* p, int n, ks_dtype_t dt, size_t* bytes);
+ks_status_t ks_chain_transpose(const ks_pattern_t* p, int n, const void* const* W, void* Wt, ks_dtype_t dt,
+                               hipStream_t stream);
 ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
-                                                     int64_t batch, ks_dtype_t dt, size_t* bytes);
-ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
-                                      const int32_t* ids, const float* dY, const void* X, const float* H, float* dX,
-                                      float* dA, float* dB, int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes,
-                                      hipStream_t stream);
+                                                     int64_t batch, ks_dtype_t dt, int have_transposed,
+                                                     size_t* bytes);
+ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const void* Wt,
+                                      const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X,
+                                      const float* H, float* dX, float* dA, float* dB, int64_t batch, ks_dtype_t dt,
+                                      void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Token logits. x[s][t][v] of `sequences` x `tokens` x `vocab` values lies at

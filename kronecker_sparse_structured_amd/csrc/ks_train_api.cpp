@@ -156,44 +156,72 @@ ks_status_t chain_widths(const ks_pattern_t* p, int n, const ks_adapters_t* ad) 
     return in == ad->n_in && out == ad->n_out ? KS_OK : KS_ERR_CHAIN_MISMATCH;
 }
 
-// The chain's gradient goes factor by factor: dY is fp32, so the products run
-// with the weights' type alone.
-ks_dtype_t grad_dtype(int wt) { return wt == ks::kBF16 ? KS_DTYPE_BF16W : KS_DTYPE_F32; }
-
+// dX = dY W_{n-1} ... W_0 is the chain of the factors in reverse, each with its
+// blocks transposed (pattern (a, c, b, d)): it runs as ks_chain_matmul does, with
+// its fused launches. dY is fp32, so it runs with the weights' type alone.
 struct ChainGrad {
-    size_t factor_ws;      // transposed blocks of one factor
-    size_t buffer;         // one intermediate
-    int buffers;
-    size_t adapter_ws;
-    size_t total;
+    std::vector<ks_pattern_t> p;     // in application order
+    std::vector<size_t> at;          // of each factor's transposed blocks, in application order
+    size_t blocks;                   // bytes of all of them
+    ks_dtype_t dt;
+    int wt;
 };
 
-ks_status_t chain_grad(const ks_pattern_t* p, int n, const ks_adapters_t* ad, int64_t batch, int dt, ChainGrad* out) {
+ks_status_t reversed_chain(const ks_pattern_t* p, int n, int64_t batch, int dt, ChainGrad* out) {
     size_t bytes = 0;
     // the chain's own checks of patterns, batch and type
     ks_status_t st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(dt), KS_CHAIN_NO_FUSE, &bytes);
     if (st != KS_OK) return st;
-    st = check_adapters(ad, batch);
+    int xt = 0;
+    st = adapter_types(dt, &xt, &out->wt);
     if (st != KS_OK) return st;
-    st = chain_widths(p, n, ad);
-    if (st != KS_OK) return st;
-    int xt = 0, wt = 0;
-    st = adapter_types(dt, &xt, &wt);
-    if (st != KS_OK) return st;
-    uint64_t widest = 0;
-    out->factor_ws = 0;
-    for (int k = 0; k < n; ++k) {
-        st = ks_matmul_dx_workspace_size(p[k], grad_dtype(wt), &bytes);
+    out->dt = out->wt == ks::kBF16 ? KS_DTYPE_BF16W : KS_DTYPE_F32;
+    out->blocks = 0;
+    for (int k = n - 1; k >= 0; --k) {
+        st = ks_matmul_dx_workspace_size(p[k], out->dt, &bytes);
         if (st != KS_OK) return st;
-        out->factor_ws = std::max(out->factor_ws, bytes);
-        if (k > 0) widest = std::max<uint64_t>(widest, static_cast<uint64_t>(p[k].a) * p[k].c * p[k].d);
+        out->p.push_back({p[k].a, p[k].c, p[k].b, p[k].d});
+        out->at.push_back(out->blocks);
+        out->blocks += bytes;
     }
-    out->buffers = n <= 1 ? 0 : (n == 2 ? 1 : 2);
-    out->buffer = round256(widest * static_cast<uint64_t>(batch) * 4);
-    st = ks_adapter_backward_workspace_size(ad, batch, &out->adapter_ws);
+    return KS_OK;
+}
+
+ks::Shape shape_of(const ks_pattern_t& p) {
+    ks::Shape s;
+    s.a = p.a; s.b = p.b; s.c = p.c; s.d = p.d;
+    s.n_in = static_cast<int64_t>(p.a) * p.c * p.d;
+    s.n_out = static_cast<int64_t>(p.a) * p.b * p.d;
+    s.nnz = s.n_in * p.b;
+    return s;
+}
+
+// W's blocks transposed into Wt, in the order of the reversed chain.
+ks_status_t transpose_chain(const ks_pattern_t* p, int n, const void* const* W, const ChainGrad& g, char* wt,
+                            hipStream_t stream) {
+    for (int k = 0; k < n; ++k) {
+        const ks_status_t st =
+            ks::launch_transpose_blocks(shape_of(p[n - 1 - k]), g.wt, W[n - 1 - k], wt + g.at[k], stream);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
+// Workspace of the chain's part of a backward call: transposed blocks, unless
+// the caller has them, then the reversed chain's own.
+struct ChainGradWs {
+    size_t chain, adapters, total;
+};
+
+ks_status_t chain_grad_ws(const ChainGrad& g, const ks_adapters_t* ad, int64_t batch, bool have_blocks,
+                          ChainGradWs* out) {
+    ks_status_t st = ks_chain_workspace_size(g.p.data(), static_cast<int>(g.p.size()), batch, g.dt, KS_CHAIN_AUTO,
+                                             &out->chain);
+    if (st != KS_OK) return st;
+    st = ks_adapter_backward_workspace_size(ad, batch, &out->adapters);
     if (st != KS_OK) return st;
     // the adapters run after the chain, over the same memory
-    out->total = std::max(out->factor_ws + out->buffers * out->buffer, out->adapter_ws);
+    out->total = std::max((have_blocks ? 0 : g.blocks) + round256(out->chain), out->adapters);
     return KS_OK;
 }
 
@@ -383,47 +411,89 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     return ks::launch_adapter(adapter_call(ad, ids, xt, wt, batch, stream, cus), X, H, Y, rest);
 }
 
-ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
-                                                     int64_t batch, ks_dtype_t dt, size_t* bytes) {
+ks_status_t ks_chain_transpose_size(const ks_pattern_t* p, int n, ks_dtype_t dt, size_t* bytes) {
     if (!bytes) return KS_ERR_NULL;
     ChainGrad g;
-    const ks_status_t st = chain_grad(p, n, ad, batch, enum_value(&dt), &g);
+    const ks_status_t st = reversed_chain(p, n, 0, enum_value(&dt), &g);
     if (st != KS_OK) return st;
-    *bytes = g.total;
+    *bytes = g.blocks;
     return KS_OK;
 }
 
-ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const ks_adapters_t* ad,
-                                      const int32_t* ids, const float* dY, const void* X, const float* H, float* dX,
-                                      float* dA, float* dB, int64_t batch, ks_dtype_t dt, void* ws, size_t ws_bytes,
-                                      hipStream_t stream) {
+ks_status_t ks_chain_transpose(const ks_pattern_t* p, int n, const void* const* W, void* Wt, ks_dtype_t dt,
+                               hipStream_t stream) {
     ChainGrad g;
+    const ks_status_t st = reversed_chain(p, n, 0, enum_value(&dt), &g);
+    if (st != KS_OK) return st;
+    if (!W || !Wt) return KS_ERR_NULL;
+    if (!aligned(Wt, 16)) return KS_ERR_ALIGN;
+    for (int k = 0; k < n; ++k) {
+        if (!W[k]) return KS_ERR_NULL;
+        if (!aligned(W[k], ks::elem_bytes(g.wt))) return KS_ERR_ALIGN;
+        if (overlap(Wt, g.blocks, W[k], static_cast<uint64_t>(shape_of(p[k]).nnz) * ks::elem_bytes(g.wt)))
+            return KS_ERR_OVERLAP;
+    }
+    return transpose_chain(p, n, W, g, static_cast<char*>(Wt), stream);
+}
+
+ks_status_t ks_chain_adapter_backward_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad,
+                                                     int64_t batch, ks_dtype_t dt, int have_transposed,
+                                                     size_t* bytes) {
+    if (!bytes) return KS_ERR_NULL;
+    ChainGrad g;
+    ChainGradWs w;
+    ks_status_t st = reversed_chain(p, n, batch, enum_value(&dt), &g);
+    if (st == KS_OK) st = check_adapters(ad, batch);
+    if (st == KS_OK) st = chain_widths(p, n, ad);
+    if (st == KS_OK) st = chain_grad_ws(g, ad, batch, have_transposed != 0, &w);
+    if (st != KS_OK) return st;
+    *bytes = w.total;
+    return KS_OK;
+}
+
+ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* const* W, const void* Wt,
+                                      const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X,
+                                      const float* H, float* dX, float* dA, float* dB, int64_t batch, ks_dtype_t dt,
+                                      void* ws, size_t ws_bytes, hipStream_t stream) {
+    ChainGrad g;
+    ChainGradWs w;
     const int code = enum_value(&dt);
-    ks_status_t st = chain_grad(p, n, ad, batch, code, &g);
+    ks_status_t st = reversed_chain(p, n, batch, code, &g);
+    if (st == KS_OK) st = check_adapters(ad, batch);
+    if (st == KS_OK) st = chain_widths(p, n, ad);
+    if (st == KS_OK) st = chain_grad_ws(g, ad, batch, Wt != nullptr, &w);
     if (st != KS_OK) return st;
     int xt = 0, wt = 0;
     st = adapter_types(code, &xt, &wt);
     if (st != KS_OK) return st;
-    if (batch > 0 && (!W || !dX)) return KS_ERR_NULL;
+    if (batch > 0 && ((!W && !Wt) || !dX)) return KS_ERR_NULL;
     if (batch == 0 && !dA && !dB) return KS_OK;
-    if (!ws || ws_bytes < g.total) return KS_ERR_WORKSPACE;
-    st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, g.total);
+    if (!ws || ws_bytes < w.total) return KS_ERR_WORKSPACE;
+    st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, w.total);
     if (st != KS_OK) return st;
+    if (!aligned(Wt, 16)) return KS_ERR_ALIGN;
     char* base = static_cast<char*>(ws);
     if (batch > 0) {
-        for (int k = 0; k < n; ++k) {
+        const uint64_t dx_bytes = static_cast<uint64_t>(batch) * ad->n_in * 4;
+        if (Wt && any_overlap({{dX, dx_bytes}, {ws, w.total}}, {{Wt, g.blocks}})) return KS_ERR_OVERLAP;
+        for (int k = 0; k < n && !Wt; ++k) {
             if (!W[k]) return KS_ERR_NULL;
-            const uint64_t bytes = static_cast<uint64_t>(p[k].a) * p[k].b * p[k].c * p[k].d * ks::elem_bytes(wt);
-            if (any_overlap({{dX, static_cast<uint64_t>(batch) * ad->n_in * 4}, {ws, g.total}}, {{W[k], bytes}}))
-                return KS_ERR_OVERLAP;
+            if (!aligned(W[k], ks::elem_bytes(wt))) return KS_ERR_ALIGN;
+            const uint64_t bytes = static_cast<uint64_t>(shape_of(p[k]).nnz) * ks::elem_bytes(wt);
+            if (any_overlap({{dX, dx_bytes}, {ws, w.total}}, {{W[k], bytes}})) return KS_ERR_OVERLAP;
         }
-        const float* cur = dY;
-        for (int k = n - 1; k >= 0; --k) {
-            float* out = k == 0 ? dX : reinterpret_cast<float*>(base + g.factor_ws + (k % 2) * (g.buffers - 1) * g.buffer);
-            st = ks_matmul_dx(p[k], W[k], cur, out, batch, grad_dtype(wt), base, g.factor_ws, stream);
+        const char* blocks = static_cast<const char*>(Wt);
+        char* chain_ws = base;
+        if (!blocks) {
+            st = transpose_chain(p, n, W, g, base, stream);
             if (st != KS_OK) return st;
-            cur = out;
+            blocks = base;
+            chain_ws = base + g.blocks;
         }
+        std::vector<const void*> factors(n);
+        for (int k = 0; k < n; ++k) factors[k] = blocks + g.at[k];
+        st = ks_chain_matmul(g.p.data(), n, factors.data(), dY, dX, batch, g.dt, chain_ws, w.chain, KS_CHAIN_AUTO, stream);
+        if (st != KS_OK) return st;
     }
     int cus = 0;
     st = current_cus(&cus);

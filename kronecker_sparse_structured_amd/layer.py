@@ -158,7 +158,7 @@ def make_adapter_class():
             ids2 = ids.reshape(-1).contiguous()
             # the handle holds addresses, so it is made for the tensors of this call
             chain = libks.AdapterChain([w.detach() for w in self.layer.weights], self.layer.patterns,
-                                       self.A.detach(), self.B.detach(), self.scale)
+                                       self.A.detach(), self.B.detach(), self.scale, transposed=False)
             if torch.is_grad_enabled() and (x2.requires_grad or self.A.requires_grad or self.B.requires_grad):
                 y = AdapterFunction.apply(x2, self.A, self.B, chain, ids2)
             else:

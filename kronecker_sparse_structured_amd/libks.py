@@ -172,8 +172,10 @@ def load(path: str = LIB_PATH):
         "ks_adapter_backward": [pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size, vp],
         "ks_chain_adapter_workspace_size": [pp, i32, pa, i64, i32, psize],
         "ks_chain_adapter_matmul": [pp, i32, ctypes.POINTER(vp), pa, vp, vp, vp, vp, i64, i32, vp, size, vp],
-        "ks_chain_adapter_backward_workspace_size": [pp, i32, pa, i64, i32, psize],
-        "ks_chain_adapter_backward": [pp, i32, ctypes.POINTER(vp), pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size,
+        "ks_chain_transpose_size": [pp, i32, i32, psize],
+        "ks_chain_transpose": [pp, i32, ctypes.POINTER(vp), vp, i32, vp],
+        "ks_chain_adapter_backward_workspace_size": [pp, i32, pa, i64, i32, i32, psize],
+        "ks_chain_adapter_backward": [pp, i32, ctypes.POINTER(vp), vp, pa, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, size,
                                       vp],
         "ks_sequence_logp": [pl, vp, vp, vp, vp],
         "ks_preference_loss": [pl, vp, i64, f32, f32, vp, vp, vp, vp, vp, vp, i64, i64, vp],
@@ -472,12 +474,15 @@ class AdapterChain:
     Y[n] = X[n] W^T + H[n] B[g]^T, H[n] = scale[g] X[n] A[g]^T, g = ids[n]
     (no adapter for an id outside [0, G)).
 
-    The handle keeps its weights (no copies: later in-place changes of them are
-    seen) and their addresses, so that a call only marshals its rows. W_k has
-    shape (a, d, b, c); A (G, rank, n_in); B (G, n_out, rank); scale (G,) fp32;
-    W, A and B have one type, fp32 or bf16; X has that type, or is fp32."""
+    The handle keeps its weights and their addresses, so that a call only
+    marshals its rows; later in-place changes of them are seen. For backward()
+    it also keeps W's blocks transposed, if `transposed` (made here, and left
+    unused once an in-place operation has changed a W; then, as without them,
+    each call transposes). W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
+    n_out, rank); scale (G,) fp32; W, A and B have one type, fp32 or bf16; X has
+    that type, or is fp32."""
 
-    def __init__(self, Ws, patterns, A, B, scale):
+    def __init__(self, Ws, patterns, A, B, scale, transposed=True):
         import torch
         self.patterns = [tuple(int(v) for v in p) for p in patterns]
         if not self.patterns or len(Ws) != len(self.patterns):
@@ -515,15 +520,25 @@ class AdapterChain:
         self._lib = load()
         self._index = A.get_device()
         self._sizes = {}
+        self._wt = self._versions = None
+        if transposed and not torch.cuda.is_current_stream_capturing():
+            code, size = self._codes[torch.float32], ctypes.c_size_t(0)
+            _raise(self._lib.ks_chain_transpose_size(self._p, self._n, code, size), "ks_chain_transpose_size", True)
+            self._wt = torch.empty(size.value, dtype=torch.uint8, device=self.device)
+            self._versions = [w._version for w in Ws]
+            _raise(self._lib.ks_chain_transpose(self._p, self._n, self._w, self._wt.data_ptr(), code,
+                                                _raw_stream(None, self._index)), "ks_chain_transpose", True)
+            # calls may come on any stream
+            torch.cuda.current_stream(self._index).synchronize()
 
-    def _workspace(self, name, batch, code):
+    def _workspace(self, name, batch, *args):
         """A workspace and its size; the size of a batch is asked for once."""
         import torch
-        key = (name, batch, code)
+        key = (name, batch, *args)
         n = self._sizes.get(key)
         if n is None:
             size = ctypes.c_size_t(0)
-            _raise(getattr(self._lib, name)(self._p, self._n, self._ad, batch, code, size), name, True)
+            _raise(getattr(self._lib, name)(self._p, self._n, self._ad, batch, *args, size), name, True)
             if len(self._sizes) > 256:
                 self._sizes.clear()
             n = self._sizes[key] = size.value
@@ -576,9 +591,12 @@ class AdapterChain:
         if weights:
             dA = torch.empty((self.count, self.rank, self.n_in), dtype=torch.float32, device=self.device)
             dB = torch.empty((self.count, self.n_out, self.rank), dtype=torch.float32, device=self.device)
-        ws, size, _keep = self._workspace("ks_chain_adapter_backward_workspace_size", batch, code)
+        wt = None
+        if self._wt is not None and [w._version for w in self._keep[0]] == self._versions:
+            wt = self._wt.data_ptr()
+        ws, size, _keep = self._workspace("ks_chain_adapter_backward_workspace_size", batch, code, int(wt is not None))
         _raise(self._lib.ks_chain_adapter_backward(
-            self._p, self._n, self._w, self._ad, ids.data_ptr(), dY.data_ptr(), X.data_ptr(), H.data_ptr(),
+            self._p, self._n, self._w, wt, self._ad, ids.data_ptr(), dY.data_ptr(), X.data_ptr(), H.data_ptr(),
             dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws, size, _raw_stream(stream, self._index)),
             "ks_chain_adapter_backward", True)
         return dX, dA, dB

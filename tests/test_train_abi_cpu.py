@@ -93,15 +93,25 @@ def test_chain_refusals():
     assert chain(batch=0, X=None) == libks.KS_OK
     lib = libks.load()
 
-    def back(ws_bytes=1 << 30, w=WP, dx=P["dX"], **kw):
+    def back(ws_bytes=1 << 30, w=WP, dx=P["dX"], wt=None, **kw):
         v = {**P, **kw}
-        return lib.ks_chain_adapter_backward(pats, 2, w, adapters(), v["ids"], v["dY"], v["X"], v["H"], dx, v["dA"],
+        return lib.ks_chain_adapter_backward(pats, 2, w, wt, adapters(), v["ids"], v["dY"], v["X"], v["H"], dx, v["dA"],
                                              v["dB"], 8, F32, v["ws"], ws_bytes, None)
 
-    assert lib.ks_chain_adapter_backward_workspace_size(pats, 2, adapters(), 8, F32, size) == libks.KS_OK
+    assert lib.ks_chain_adapter_backward_workspace_size(pats, 2, adapters(), 8, F32, 0, size) == libks.KS_OK
     assert back(ws_bytes=size.value - 1) == libks.KS_ERR_WORKSPACE
     assert back(dx=None) == libks.KS_ERR_NULL and back(w=None) == libks.KS_ERR_NULL
     assert back(dx=0xC0000000) == libks.KS_ERR_OVERLAP and back(dB=None) == libks.KS_ERR_NULL
+    assert back(wt=0xE0000008) == libks.KS_ERR_ALIGN and back(wt=P["dX"]) == libks.KS_ERR_OVERLAP
+    less = ctypes.c_size_t(0)
+    assert lib.ks_chain_adapter_backward_workspace_size(pats, 2, adapters(), 8, F32, 1, less) == libks.KS_OK
+    assert less.value <= size.value
+    assert lib.ks_chain_transpose_size(pats, 2, F32, less) == libks.KS_OK and less.value >= (64 + 96) * 4
+    assert lib.ks_chain_transpose_size(pats, 2, 5, less) == libks.KS_ERR_DTYPE
+    assert lib.ks_chain_transpose(pats, 2, WP, None, F32, None) == libks.KS_ERR_NULL
+    assert lib.ks_chain_transpose(pats, 2, WP, 0xE0000004, F32, None) == libks.KS_ERR_ALIGN
+    assert lib.ks_chain_transpose(pats, 2, WP, 0xC0000000, F32, None) == libks.KS_ERR_OVERLAP
+    assert lib.ks_chain_transpose(pats, 2, (ctypes.c_void_p * 2)(None, 16), 0xE0000000, F32, None) == libks.KS_ERR_NULL
 
 
 def logits(**kw):
