@@ -475,14 +475,14 @@ class AdapterChain:
     (no adapter for an id outside [0, G)).
 
     The handle keeps its weights and their addresses, so that a call only
-    marshals its rows; later in-place changes of them are seen. For backward()
-    it also keeps W's blocks transposed, if `transposed` (made here, and left
-    unused once an in-place operation has changed a W; then, as without them,
-    each call transposes). W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
+    marshals its rows; later in-place changes of them are seen. With `transposed`
+    it also keeps W's blocks transposed, for the backward() calls of a training
+    loop: made here once, where each call makes its own otherwise, and left unused
+    after an in-place operation on a W. W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
     n_out, rank); scale (G,) fp32; W, A and B have one type, fp32 or bf16; X has
     that type, or is fp32."""
 
-    def __init__(self, Ws, patterns, A, B, scale, transposed=True):
+    def __init__(self, Ws, patterns, A, B, scale, transposed=False):
         import torch
         self.patterns = [tuple(int(v) for v in p) for p in patterns]
         if not self.patterns or len(Ws) != len(self.patterns):
@@ -818,9 +818,10 @@ class AdamW:
             raise TypeError("moments must be %s and %s" % types)
         at = [list(map(T.data_ptr, ts)) for ts in (params, grads, ms, vs)]
         at.append(list(map(T.data_ptr, scales)) if scales is not None else [None] * n)
-        self._t = (ks_adamw_tensor_t * max(n, 1))(*[
-            ks_adamw_tensor_t(*a, size, _elem(p.dtype, "params"), _elem(g.dtype, "grads"))
-            for *a, size, p, g in zip(*at, self._sizes, params, grads)])
+        for ts, name in ((params, "params"), (grads, "grads")):
+            codes = {t: _elem(t, name) for t in set(map(_dtype_of, ts))}
+            at.append([codes[t] for t in map(_dtype_of, ts)])
+        self._t = (ks_adamw_tensor_t * max(n, 1))(*zip(*at[:5], self._sizes, *at[5:]))
         spans = []
         for ts, addr in ((params, at[0]), (ms, at[2]), (vs, at[3]), (scales or [], at[4])):
             spans += [(a, a + b) for a, b in zip(addr, [t.nbytes for t in ts]) if b]

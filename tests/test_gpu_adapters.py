@@ -224,12 +224,12 @@ def test_chain_with_adapters(case):
         assert err <= FP32_REL_TOL, err
     only = chain.backward(dY, X, H, ids, weights=False)
     assert torch.equal(only[0], dX) and only[1] is None and only[2] is None
-    # without transposed blocks at hand: the same bits; after a change of W: its gradient
-    plain = libks.AdapterChain(Ws, ps, A, B, scale, transposed=False)
-    assert all(torch.equal(a, b) for a, b in zip(plain.backward(dY, X, H, ids), (dX, dA, dB)))
+    # with transposed blocks at hand: the same bits; after a change of W: its gradient
+    ready = libks.AdapterChain(Ws, ps, A, B, scale, transposed=True)
+    assert all(torch.equal(a, b) for a, b in zip(ready.backward(dY, X, H, ids), (dX, dA, dB)))
     Ws[0].mul_(-1.5)
-    changed = chain.backward(dY, X, H, ids)[0]
-    assert torch.equal(changed, plain.backward(dY, X, H, ids)[0]) and not torch.equal(changed, dX)
+    changed = ready.backward(dY, X, H, ids)[0]
+    assert torch.equal(changed, chain.backward(dY, X, H, ids)[0]) and not torch.equal(changed, dX)
 
 
 def test_layer_autograd_other_stream_and_graph():
