@@ -83,32 +83,6 @@ __device__ __forceinline__ void load_ranks(const T* row, int r, int rank, float 
 
 // ---------------------------------------------------------------- few rows
 
-// Eight consecutive values: 16-byte loads (WIDE), or element-wise with zeros
-// from `valid` on.
-template <bool WIDE, typename T>
-__device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
-    if (WIDE && valid >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = a[i];
-                x[4 + i] = b[i];
-            }
-        } else {
-            const u32x4 a = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(a[i]);
-                x[2 * i + 1] = bf16_hi(a[i]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < valid ? to_f32(p[i]) : 0.0f;
-    }
-}
-
 // Sum over the wave's 64 lanes, in lane 63: four steps inside rows of 16 lanes,
 // then the rows' totals from one to the next.
 template <int CTRL>

@@ -36,6 +36,34 @@ __device__ __forceinline__ void load4_f32(const bf16_t* p, float (&v)[4]) {
     v[3] = bf16_hi(w[1]);
 }
 
+// Eight consecutive values: 16-byte loads (WIDE), or element-wise with zeros
+// from `valid` on.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load8(const T* p, int valid, float (&x)[8]) {
+    if (WIDE && valid >= 8) {
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        if constexpr (sizeof(T) == 4) {
+            const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = a[i];
+                x[4 + i] = b[i];
+            }
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(a[i]);
+                x[2 * i + 1] = bf16_hi(a[i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < valid ? to_f32(p[i]) : 0.0f;
+    }
+}
+
 // fp32 to bf16, nearest even (NaN stays NaN): one value's bits, or two in a
 // word (the conversion instruction takes pairs).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -83,6 +83,10 @@ CASES = [
     (2049, 384, 1536, 2, 8, (F32, F32), "runs"), (3000, 1024, 256, 4, 33, (BF16, BF16), "runs"),
     (1040, 64, 64, 3, 200, (F32, F32), "random"), (1100, 128, 64, 3, 16, (F32, F32), "none"),
     (4099, 64, 1000, 2, 32, (BF16, BF16), "one"),
+    # both sides of the gradients' limit of rows for two small launches
+    (64, 300, 520, 1, 16, (BF16, BF16), "one"), (65, 300, 520, 3, 16, (BF16, BF16), "random"),
+    (4, 260, 1, 2, 256, (F32, F32), "random"), (12, 1, 300, 5, 67, (F32, BF16), "random"),
+    (9, 512, 96, 3, 100, (BF16, BF16), "none"),
 ]
 
 
