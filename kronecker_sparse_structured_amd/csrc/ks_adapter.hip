@@ -53,6 +53,8 @@ struct Args {
     float* H;
     int64_t batch;
     int n_in, n_out, rank, count;
+    bf16_t* parts;           // H in three parts, chunks of 4 ranks (null: not wanted)
+    int32_t* groups;         // with parts: the adapter of each group of rows
     int64_t first;           // first workgroup of a launch among all of the batch's
 };
 
@@ -208,6 +210,12 @@ struct Tile {
         id = li < rows ? slot.adapter : -1;
         left = __ballot(id >= 0) & 0xffffu;
     }
+    // The adapter that the rows of this lane's group of kPairGroup share, or -1.
+    __device__ __forceinline__ int shared() const {
+        const int lane = threadIdx.x % 64, first = __shfl(id, lane & ~(kPairGroup - 1), 64);
+        const uint64_t same = __ballot(lane % 16 >= rows || id == first);
+        return (same >> (lane & ~(kPairGroup - 1)) & ((1u << kPairGroup) - 1)) == (1u << kPairGroup) - 1 ? first : -1;
+    }
     // The rows' adapters one after another.
     __device__ __forceinline__ int next() {
         const int g = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
@@ -215,6 +223,21 @@ struct Tile {
         return g;
     }
 };
+
+// A value of H as three bf16 values, each the leading bits of what the ones before
+// leave: their sum is the value exactly. Infinity and NaN stay in the first.
+__device__ __forceinline__ void keep_parts(const Args& a, int64_t row, int r, float h) {
+    bf16_t* to = a.parts + row * (kLowPartsBytes / 2) + r / 4 * 12 + r % 4;
+    float first = __uint_as_float(__float_as_uint(h) & 0xffff0000u), rest = h - first;
+    if (!(fabsf(h) < __builtin_inff())) {
+        first = h;
+        rest = 0.0f;
+    }
+    const float second = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+    to[0] = to_bf16(first);
+    to[4] = to_bf16(second);
+    to[8] = to_bf16(rest - second);
+}
 
 // H of 16 rows a workgroup. RT: rank tiles of 16 that a pass over X keeps in
 // registers. With sorted rows, workgroups past the slots look for rows without
@@ -248,6 +271,10 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a, co
     const TX* x = static_cast<const TX*>(a.X) + tile.row * a.n_in;
     const int quarter = (a.n_in + 4 * kStepK<TX> - 1) / (4 * kStepK<TX>) * kStepK<TX>;
     const int k0 = wave * quarter, k1 = min(a.n_in, k0 + quarter);
+    if (a.parts) {
+        const int g = tile.shared();
+        if (tid < rows && tid % kPairGroup == 0) a.groups[(block * kTile + tid) / kPairGroup] = g;
+    }
     if (!o.order) {
         // rows without an adapter
         for (int i = tid; i < rows * a.rank; i += kThreads)
@@ -321,9 +348,11 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a, co
             __syncthreads();
             for (int i = tid; i < kTile * 16 * RT; i += kThreads) {
                 const int row = i / (16 * RT), r = i % (16 * RT);
-                if (id_of[row] == g && r0 + r < a.rank)
-                    a.H[row_of[row] * a.rank + r0 + r] =
-                        scale * ((part[0][row][r] + part[1][row][r]) + (part[2][row][r] + part[3][row][r]));
+                if (id_of[row] != g) continue;
+                const bool in = r0 + r < a.rank;
+                const float h = scale * ((part[0][row][r] + part[1][row][r]) + (part[2][row][r] + part[3][row][r]));
+                if (in) a.H[row_of[row] * a.rank + r0 + r] = h;
+                if (a.parts) keep_parts(a, row_of[row], r0 + r, in ? h : 0.0f);
             }
             __syncthreads();
         }
@@ -348,7 +377,14 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <typename TW, int RT, bool WIDE>
+// kRest: only rows whose group shares no adapter (a fused launch has added the
+// others'), kRestTiles tiles a workgroup: mostly there are few or none, and the
+// launch costs its workgroups' starts. 16384 rows in runs of whole groups: 82 us
+// the whole chain with one tile each, 77 with 4, 75 with 16; 4099 rows in random
+// order: 104, 105, 138.
+constexpr int kRestTiles = 4;
+
+template <typename TW, int RT, bool WIDE, bool kRest>
 __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, const AdapterOrder o) {
     __shared__ __align__(16) float cross[4][16 * kUpPitch];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
@@ -359,89 +395,118 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
     const int64_t group = a.first + blockIdx.x;
     const int o0 = static_cast<int>(group % slabs) * kUpCols + wave * 64;
     if (o0 >= a.n_out) return;
-    const int64_t block = group / slabs;
-    Tile tile = o.order ? Tile(o.order, o.slots[block]) : Tile(a.ids, a.batch, a.count, block * kTile);
-    if (!tile.left) return;
-    const int rows = tile.rows;
-    int64_t row_of[4];                                 // of this lane's runs of Y
+    const int64_t first = group / slabs * (kRest ? kRestTiles : 1);
+    uint64_t todo = 1;                                 // a bit a tile; with REST kTile / kPairGroup bits, a group each
+    constexpr int kBits = kRest ? kTile / kPairGroup : 1;
+    if (kRest) {
+        static_assert(kRestTiles * kTile <= 64 * kPairGroup, "a group a lane");
+        const int64_t n = first * kTile + lane * kPairGroup;
+        int id[kPairGroup];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        row_of[q] = o.order ? __shfl(static_cast<int>(tile.row), 4 * q + lg, 64) : block * kTile + 4 * q + lg;
-    float* mine = cross[wave];
-    const int left = a.n_out - (o0 + 4 * li);          // this lane's outputs of Y inside the matrix
-    const bool whole = WIDE && rows == kTile && o0 + 64 <= a.n_out;      // every lane's vectors, for the whole wave
-    f32x4 y[4];
-    if (whole) {
+        for (int i = 0; i < kPairGroup; ++i) id[i] = a.ids[min(n + i, a.batch - 1)];
+        bool mixed = false, any = false;
+        const int64_t end = min(a.batch, (first + kRestTiles) * kTile);
+#pragma unroll
+        for (int i = 0; i < kPairGroup; ++i) {
+            if (n + i >= end) continue;
+            if (id[i] < 0 || id[i] >= a.count) id[i] = -1;
+            any |= id[i] >= 0;
+            mixed |= id[i] != id[0];
+        }
+        todo = __ballot(mixed && any);
+    }
+    while (todo) {
+        const int at = __builtin_ctzll(todo) / kBits;
+        todo &= ~(((uint64_t(1) << kBits) - 1) << (at * kBits));
+        const int64_t block = first + at;
+        Tile tile = o.order ? Tile(o.order, o.slots[block]) : Tile(a.ids, a.batch, a.count, block * kTile);
+        if (kRest) {
+            if (tile.shared() >= 0) tile.id = -1;
+            tile.left = __ballot(tile.id >= 0) & 0xffffu;
+        }
+        if (!tile.left) continue;
+        const int rows = tile.rows;
+        int64_t row_of[4];                                 // of this lane's runs of Y
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            y[q] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.Y + row_of[q] * a.n_out + o0 + 4 * li));
-    } else {
+            row_of[q] = o.order ? __shfl(static_cast<int>(tile.row), 4 * q + lg, 64) : block * kTile + 4 * q + lg;
+        float* mine = cross[wave];
+        const int left = a.n_out - (o0 + 4 * li);          // this lane's outputs of Y inside the matrix
+        const bool whole = WIDE && rows == kTile && o0 + 64 <= a.n_out;      // every lane's vectors, for the whole wave
+        f32x4 y[4];
+        if (whole) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[4];
-            load4<WIDE>(a.Y + row_of[q] * a.n_out + o0 + 4 * li, 4 * q + lg < rows ? left : 0, v);
-            y[q] = f32x4{v[0], v[1], v[2], v[3]};
-        }
-    }
-    const float* h = a.H + tile.row * a.rank;
-    float hv[RT][4];                                   // H of the first ranks: all of them up to 16 RT
-#pragma unroll
-    for (int t = 0; t < RT; ++t) load_ranks<WIDE>(h, 16 * t + 4 * lg, a.rank, hv[t]);
-    f32x4 all[4];
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) all[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    while (tile.left) {
-        const int g = tile.next();
-        f32x4 sum[4];
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int r0 = 0; r0 < a.rank; r0 += 16 * RT) {
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int r = r0 + 16 * t + 4 * lg;
-                float hr[4], bv[4][4];
-                if (r0 == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) hr[i] = hv[t][i];
-                } else {
-                    load_ranks<WIDE>(h, r, a.rank, hr);
-                }
-#pragma unroll
-                for (int ct = 0; ct < 4; ++ct) {
-                    const int c = min(o0 + 16 * ct + li, a.n_out - 1);
-                    load_ranks<WIDE>(static_cast<const TW*>(a.B) + (static_cast<int64_t>(g) * a.n_out + c) * a.rank, r,
-                                     a.rank, bv[ct]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int ct = 0; ct < 4; ++ct)
-                        sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][i], hr[i], sum[ct], 0, 0, 0);
-            }
-        }
-        // a lane's column of the product is one row of Y: a row takes its own
-        // adapter's, and nothing of the others', not even their NaN
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
-            if (tile.id == g) all[ct] = sum[ct];
-    }
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(mine + li * kUpPitch + 16 * ct + 4 * lg) = all[ct];
-    wave_fence();
-    const uint64_t on = __ballot(tile.id >= 0);         // bit r: row r has an adapter
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int r = 4 * q + lg;
-        const f32x4 add = *reinterpret_cast<const f32x4*>(mine + r * kUpPitch + 4 * li);
-        if (!(on >> r & 1)) continue;
-        float* dst = a.Y + row_of[q] * a.n_out + o0 + 4 * li;
-        if (whole || (WIDE && left >= 4)) {
-            __builtin_nontemporal_store(y[q] + add, reinterpret_cast<f32x4*>(dst));
+            for (int q = 0; q < 4; ++q)
+                y[q] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.Y + row_of[q] * a.n_out + o0 + 4 * li));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) dst[i] = y[q][i] + add[i];
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+                load4<WIDE>(a.Y + row_of[q] * a.n_out + o0 + 4 * li, 4 * q + lg < rows ? left : 0, v);
+                y[q] = f32x4{v[0], v[1], v[2], v[3]};
+            }
         }
+        const float* h = a.H + tile.row * a.rank;
+        float hv[RT][4];                                   // H of the first ranks: all of them up to 16 RT
+#pragma unroll
+        for (int t = 0; t < RT; ++t) load_ranks<WIDE>(h, 16 * t + 4 * lg, a.rank, hv[t]);
+        f32x4 all[4];
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) all[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        while (tile.left) {
+            const int g = tile.next();
+            f32x4 sum[4];
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct) sum[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r0 = 0; r0 < a.rank; r0 += 16 * RT) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int r = r0 + 16 * t + 4 * lg;
+                    float hr[4], bv[4][4];
+                    if (r0 == 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hr[i] = hv[t][i];
+                    } else {
+                        load_ranks<WIDE>(h, r, a.rank, hr);
+                    }
+#pragma unroll
+                    for (int ct = 0; ct < 4; ++ct) {
+                        const int c = min(o0 + 16 * ct + li, a.n_out - 1);
+                        load_ranks<WIDE>(static_cast<const TW*>(a.B) + (static_cast<int64_t>(g) * a.n_out + c) * a.rank, r,
+                                         a.rank, bv[ct]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int ct = 0; ct < 4; ++ct)
+                            sum[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[ct][i], hr[i], sum[ct], 0, 0, 0);
+                }
+            }
+            // a lane's column of the product is one row of Y: a row takes its own
+            // adapter's, and nothing of the others', not even their NaN
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct)
+                if (tile.id == g) all[ct] = sum[ct];
+        }
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(mine + li * kUpPitch + 16 * ct + 4 * lg) = all[ct];
+        wave_fence();
+        const uint64_t on = __ballot(tile.id >= 0);         // bit r: row r has an adapter
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = 4 * q + lg;
+            const f32x4 add = *reinterpret_cast<const f32x4*>(mine + r * kUpPitch + 4 * li);
+            if (!(on >> r & 1)) continue;
+            float* dst = a.Y + row_of[q] * a.n_out + o0 + 4 * li;
+            if (whole || (WIDE && left >= 4)) {
+                __builtin_nontemporal_store(y[q] + add, reinterpret_cast<f32x4*>(dst));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < left) dst[i] = y[q][i] + add[i];
+            }
+        }
+        wave_fence();
     }
 }
 
@@ -482,14 +547,18 @@ ks_status_t launch_down(const Args& a, const AdapterOrder& o, hipStream_t stream
     return launch_groups(kernel, blocks, a, o, stream);
 }
 
+bool up_wide(const Args& a) {
+    return on16(a.B) && on16(a.H) && on16(a.Y) && a.rank % 4 == 0 && a.n_out % 4 == 0;
+}
+
 template <typename TW>
 ks_status_t launch_up(const Args& a, const AdapterOrder& o, hipStream_t stream) {
-    const bool wide = on16(a.B) && on16(a.H) && on16(a.Y) && a.rank % 4 == 0 && a.n_out % 4 == 0;
+    const bool wide = up_wide(a);
     const int64_t tiles = o.order ? o.n_slots : (a.batch + kTile - 1) / kTile;
     const int64_t blocks = tiles * ((a.n_out + kUpCols - 1) / kUpCols);
     void (*kernel)(Args, AdapterOrder);
-    if (a.rank <= 16) kernel = wide ? adapter_up_kernel<TW, 1, true> : adapter_up_kernel<TW, 1, false>;
-    else kernel = wide ? adapter_up_kernel<TW, 2, true> : adapter_up_kernel<TW, 2, false>;
+    if (a.rank <= 16) kernel = wide ? adapter_up_kernel<TW, 1, true, false> : adapter_up_kernel<TW, 1, false, false>;
+    else kernel = wide ? adapter_up_kernel<TW, 2, true, false> : adapter_up_kernel<TW, 2, false, false>;
     return launch_groups(kernel, blocks, a, o, stream);
 }
 
@@ -525,10 +594,27 @@ size_t adapter_workspace(int64_t batch, int count) {
 }
 
 ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float* Y, void* ws) {
-    const Args a{c.A, c.B, c.scale, c.ids, X, Y, H, c.batch, c.n_in, c.n_out, c.rank, c.count, 0};
+    const Args a{c.A, c.B, c.scale, c.ids, X, Y, H, c.batch, c.n_in, c.n_out, c.rank, c.count, nullptr, nullptr, 0};
     if (c.xt == kBF16) return launch_types<bf16_t, bf16_t>(c, a, ws);
     if (c.wt == kBF16) return launch_types<float, bf16_t>(c, a, ws);
     return launch_types<float, float>(c, a, ws);
+}
+
+ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, int32_t* groups) {
+    const Args a{c.A, c.B, c.scale, c.ids, X, nullptr, H, c.batch, c.n_in, c.n_out, c.rank, c.count,
+                 static_cast<bf16_t*>(parts), groups, 0};
+    if (c.xt == kBF16) return launch_down<bf16_t, bf16_t>(a, {}, c.stream);
+    if (c.wt == kBF16) return launch_down<float, bf16_t>(a, {}, c.stream);
+    return launch_down<float, float>(a, {}, c.stream);
+}
+
+ks_status_t launch_adapter_rest(const AdapterCall& c, const float* H, float* Y) {
+    if (c.wt != kBF16 || c.rank > kLowPartsRank) return KS_ERR_UNSUPPORTED;
+    const Args a{c.A, c.B, c.scale, c.ids, nullptr, Y, const_cast<float*>(H), c.batch, c.n_in, c.n_out, c.rank,
+                 c.count, nullptr, nullptr, 0};
+    constexpr int kRows = kRestTiles * kTile;
+    return launch_groups(up_wide(a) ? adapter_up_kernel<bf16_t, 1, true, true> : adapter_up_kernel<bf16_t, 1, false, true>,
+                         (c.batch + kRows - 1) / kRows * ((c.n_out + kUpCols - 1) / kUpCols), a, {}, c.stream);
 }
 
 }  // namespace ks

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "ks_internal.h"
+#include "ks_train.h"
 
 namespace {
 
@@ -361,6 +362,107 @@ ks_status_t dw_check(ks_pattern_t p, const void* dY, const void* X, const void* 
 
 }  // namespace
 
+// ks_chain_matmul; with `extra`, a last launch that can add the adapters does so.
+ks_status_t ks::chain_matmul(const ks_pattern_t* p, int n, const void* const* W, const void* X, void* Y,
+                             int64_t batch, int dt, void* ws, size_t ws_bytes, unsigned flags, hipStream_t stream,
+                             ChainAdapters* extra) {
+    ChainPlan plan;
+    ks_status_t st = plan_chain(p, n, batch, dt, flags, &plan);
+    if (st != KS_OK) return st;
+    if (batch == 0) return KS_OK;
+    if (!W || !X || !Y) return KS_ERR_NULL;
+    for (int k = 0; k < n; ++k)
+        if (!W[k]) return KS_ERR_NULL;
+    const size_t need = static_cast<size_t>(plan.nbuf) * plan.buf_bytes;
+    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
+    const int xe = ks::elem_bytes(plan.xt0), we = ks::elem_bytes(plan.wt);
+    if (!aligned(X, xe) || !aligned(Y, 4)) return KS_ERR_ALIGN;
+    for (int k = 0; k < n; ++k)
+        if (!aligned(W[k], we)) return KS_ERR_ALIGN;
+    if (need > 0 && !aligned(ws, 16)) return KS_ERR_ALIGN;
+    const uint64_t xb = static_cast<uint64_t>(batch) * plan.shapes[0].n_in * xe;
+    const uint64_t yb = static_cast<uint64_t>(batch) * plan.shapes[n - 1].n_out * 4u;
+    if (overlap(Y, yb, X, xb)) return KS_ERR_OVERLAP;
+    if (need > 0 && (overlap(ws, need, X, xb) || overlap(ws, need, Y, yb))) return KS_ERR_OVERLAP;
+    for (int k = 0; k < n; ++k) {
+        const uint64_t wb = static_cast<uint64_t>(plan.shapes[k].nnz) * we;
+        if (overlap(Y, yb, W[k], wb)) return KS_ERR_OVERLAP;
+        if (need > 0 && overlap(ws, need, W[k], wb)) return KS_ERR_OVERLAP;
+    }
+
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != KS_OK) return st;
+    if (extra) {
+        // the last launch adds them if it is a fused pair that can
+        const int last = plan.group_start.back();
+        extra->added = plan.group_kind.back() == 1 &&
+                       ks::fused_pair_adds(plan.shapes[last], plan.shapes[last + 1], last == 0 ? plan.xt0 : ks::kF32,
+                                           plan.wt, extra->pair.B, extra->pair.rank);
+        if (extra->added) {
+            st = ks::launch_adapter_down(extra->call, X, extra->H, const_cast<void*>(extra->pair.H),
+                                         const_cast<int32_t*>(extra->pair.groups));
+            if (st != KS_OK) return st;
+        }
+    }
+    char* bufs[2] = {static_cast<char*>(ws), static_cast<char*>(ws) + plan.buf_bytes};
+    const void* cur = X;
+    int cur_t = plan.xt0;
+    const int groups = static_cast<int>(plan.group_start.size());
+    for (int g = 0; g < groups; ++g) {
+        const int k = plan.group_start[g];
+        float* out = (g == groups - 1) ? static_cast<float*>(Y)
+                                       : reinterpret_cast<float*>(bufs[g % 2]);
+        if (plan.group_kind[g] == 1 && g == groups - 1 && extra && extra->added) {
+            st = ks::launch_fused_pair_adapters(plan.shapes[k], plan.shapes[k + 1], W[k], W[k + 1], cur, out, batch,
+                                                extra->pair, stream, cus);
+            if (st == KS_OK) st = ks::launch_adapter_rest(extra->call, extra->H, out);
+        } else if (plan.group_kind[g] == 1) {
+            st = ks::launch_fused_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt,
+                                       W[k], W[k + 1], cur, out, batch, stream, cus);
+        } else if (plan.group_kind[g] == 2) {
+            st = ks::launch_slab_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt,
+                                      W[k], W[k + 1], cur, out, batch, stream, cus);
+        } else if (plan.group_kind[g] == 3) {
+            st = ks::launch_row_chain(&plan.shapes[k], plan.group_len[g], cur_t, plan.wt, W + k, cur, out, batch,
+                                      stream, cus);
+        } else if (plan.group_kind[g] == 4 && ks::strided_pair_aligned(cur, out)) {
+            st = ks::launch_strided_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt, W[k], W[k + 1],
+                                         cur, out, batch, stream, cus);
+        } else if (plan.group_kind[g] == 5 && ks::monarch_pair_aligned(cur, out)) {
+            st = ks::launch_monarch_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt, W[k], W[k + 1],
+                                         cur, out, batch, stream, cus);
+        } else if (aligned_pair_kind(plan.group_kind[g])) {
+            // X or Y not 16-byte aligned: the two factors one at a time,
+            // through the buffer that is neither this group's input nor output
+            float* mid = reinterpret_cast<float*>(
+                (cur == bufs[0] || out == reinterpret_cast<float*>(bufs[0])) ? bufs[1] : bufs[0]);
+            // only the first or last group can see an unaligned pointer, and
+            // the plan keeps a spare buffer for it
+            if (plan.nbuf == 0 || static_cast<const void*>(mid) == cur || mid == out) return KS_ERR_UNSUPPORTED;
+            ks::FactorCall f;
+            f.s = plan.shapes[k]; f.xt = cur_t; f.wt = plan.wt; f.W = W[k]; f.X = cur; f.Y = mid;
+            f.batch = batch; f.stream = stream; f.num_cus = cus; f.rows_per_block = 0;
+            f.store_waves = KS_STORE_AUTO;
+            st = run_factor(KS_KERNEL_AUTO, f);
+            if (st == KS_OK) {
+                f.s = plan.shapes[k + 1]; f.xt = ks::kF32; f.W = W[k + 1]; f.X = mid; f.Y = out;
+                st = run_factor(KS_KERNEL_AUTO, f);
+            }
+        } else {
+            ks::FactorCall f;
+            f.s = plan.shapes[k]; f.xt = cur_t; f.wt = plan.wt; f.W = W[k]; f.X = cur; f.Y = out;
+            f.batch = batch; f.stream = stream; f.num_cus = cus; f.rows_per_block = 0;
+            f.store_waves = KS_STORE_AUTO;
+            st = run_factor(KS_KERNEL_AUTO, f);
+        }
+        if (st != KS_OK) return st;
+        cur = out;
+        cur_t = ks::kF32;
+    }
+    return KS_OK;
+}
+
 extern "C" {
 
 const char* ks_status_string(ks_status_t status) {
@@ -518,85 +620,7 @@ ks_status_t ks_chain_matmul(const ks_pattern_t* p, int n, const void* const* W,
                             const void* X, void* Y, int64_t batch, ks_dtype_t dt,
                             void* ws, size_t ws_bytes, unsigned flags,
                             hipStream_t stream) {
-    ChainPlan plan;
-    ks_status_t st = plan_chain(p, n, batch, enum_value(&dt), flags, &plan);
-    if (st != KS_OK) return st;
-    if (batch == 0) return KS_OK;
-    if (!W || !X || !Y) return KS_ERR_NULL;
-    for (int k = 0; k < n; ++k)
-        if (!W[k]) return KS_ERR_NULL;
-    const size_t need = static_cast<size_t>(plan.nbuf) * plan.buf_bytes;
-    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
-    const int xe = ks::elem_bytes(plan.xt0), we = ks::elem_bytes(plan.wt);
-    if (!aligned(X, xe) || !aligned(Y, 4)) return KS_ERR_ALIGN;
-    for (int k = 0; k < n; ++k)
-        if (!aligned(W[k], we)) return KS_ERR_ALIGN;
-    if (need > 0 && !aligned(ws, 16)) return KS_ERR_ALIGN;
-    const uint64_t xb = static_cast<uint64_t>(batch) * plan.shapes[0].n_in * xe;
-    const uint64_t yb = static_cast<uint64_t>(batch) * plan.shapes[n - 1].n_out * 4u;
-    if (overlap(Y, yb, X, xb)) return KS_ERR_OVERLAP;
-    if (need > 0 && (overlap(ws, need, X, xb) || overlap(ws, need, Y, yb))) return KS_ERR_OVERLAP;
-    for (int k = 0; k < n; ++k) {
-        const uint64_t wb = static_cast<uint64_t>(plan.shapes[k].nnz) * we;
-        if (overlap(Y, yb, W[k], wb)) return KS_ERR_OVERLAP;
-        if (need > 0 && overlap(ws, need, W[k], wb)) return KS_ERR_OVERLAP;
-    }
-
-    int cus = 0;
-    st = current_cus(&cus);
-    if (st != KS_OK) return st;
-    char* bufs[2] = {static_cast<char*>(ws), static_cast<char*>(ws) + plan.buf_bytes};
-    const void* cur = X;
-    int cur_t = plan.xt0;
-    const int groups = static_cast<int>(plan.group_start.size());
-    for (int g = 0; g < groups; ++g) {
-        const int k = plan.group_start[g];
-        float* out = (g == groups - 1) ? static_cast<float*>(Y)
-                                       : reinterpret_cast<float*>(bufs[g % 2]);
-        if (plan.group_kind[g] == 1) {
-            st = ks::launch_fused_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt,
-                                       W[k], W[k + 1], cur, out, batch, stream, cus);
-        } else if (plan.group_kind[g] == 2) {
-            st = ks::launch_slab_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt,
-                                      W[k], W[k + 1], cur, out, batch, stream, cus);
-        } else if (plan.group_kind[g] == 3) {
-            st = ks::launch_row_chain(&plan.shapes[k], plan.group_len[g], cur_t, plan.wt, W + k, cur, out, batch,
-                                      stream, cus);
-        } else if (plan.group_kind[g] == 4 && ks::strided_pair_aligned(cur, out)) {
-            st = ks::launch_strided_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt, W[k], W[k + 1],
-                                         cur, out, batch, stream, cus);
-        } else if (plan.group_kind[g] == 5 && ks::monarch_pair_aligned(cur, out)) {
-            st = ks::launch_monarch_pair(plan.shapes[k], plan.shapes[k + 1], cur_t, plan.wt, plan.wt, W[k], W[k + 1],
-                                         cur, out, batch, stream, cus);
-        } else if (aligned_pair_kind(plan.group_kind[g])) {
-            // X or Y not 16-byte aligned: the two factors one at a time,
-            // through the buffer that is neither this group's input nor output
-            float* mid = reinterpret_cast<float*>(
-                (cur == bufs[0] || out == reinterpret_cast<float*>(bufs[0])) ? bufs[1] : bufs[0]);
-            // only the first or last group can see an unaligned pointer, and
-            // the plan keeps a spare buffer for it
-            if (plan.nbuf == 0 || static_cast<const void*>(mid) == cur || mid == out) return KS_ERR_UNSUPPORTED;
-            ks::FactorCall f;
-            f.s = plan.shapes[k]; f.xt = cur_t; f.wt = plan.wt; f.W = W[k]; f.X = cur; f.Y = mid;
-            f.batch = batch; f.stream = stream; f.num_cus = cus; f.rows_per_block = 0;
-            f.store_waves = KS_STORE_AUTO;
-            st = run_factor(KS_KERNEL_AUTO, f);
-            if (st == KS_OK) {
-                f.s = plan.shapes[k + 1]; f.xt = ks::kF32; f.W = W[k + 1]; f.X = mid; f.Y = out;
-                st = run_factor(KS_KERNEL_AUTO, f);
-            }
-        } else {
-            ks::FactorCall f;
-            f.s = plan.shapes[k]; f.xt = cur_t; f.wt = plan.wt; f.W = W[k]; f.X = cur; f.Y = out;
-            f.batch = batch; f.stream = stream; f.num_cus = cus; f.rows_per_block = 0;
-            f.store_waves = KS_STORE_AUTO;
-            st = run_factor(KS_KERNEL_AUTO, f);
-        }
-        if (st != KS_OK) return st;
-        cur = out;
-        cur_t = ks::kF32;
-    }
-    return KS_OK;
+    return ks::chain_matmul(p, n, W, X, Y, batch, enum_value(&dt), ws, ws_bytes, flags, stream, nullptr);
 }
 
 ks_status_t ks_plan_describe(ks_pattern_t p, int64_t batch, ks_dtype_t dt, char* buf, size_t len) {

@@ -31,6 +31,26 @@
 // Z never leaves the chip: the pair moves |X| + |Y| + weights through HBM
 // instead of |X| + 2|Z| + |Y|.
 //
+// Adapters. With bf16 operands the same launch can add the low-rank adapters of
+// the rows' requests, Y[n] += H[n] B[g]^T with g = ids[n], H from an earlier launch,
+// for stages whose four rows share an adapter: there Y is written once and never
+// read. H comes as three bf16 values whose sum is the fp32 value exactly, so its
+// products with B are those of fp32; the loader streams the stage's rows of them
+// and the stage's adapter along with X. A thread of phase B keeps its four outputs'
+// values of B in registers, and the products run on the 16-block 4x4x4 bf16 MFMA,
+// whose lanes are given their own outputs as the columns: each receives the stage's
+// four rows of its own output, which is where phase B has them. Phase A uses the
+// same instruction there, four gammas at a time (products of bf16 values are exact
+// in fp32): the kernel is bound by its two phases on the chip more than by HBM, and
+// that saves 17 us of 16384 rows. With it and rank 16 they take 75 us (63 for the
+// chain alone, 4.0 TB/s); with the adapters added by a pass over Y, 63 and 98.
+// Weights stay packed in registers: nine waves leave 168 a wave, and spilled ones
+// come back through the vector-memory counter behind the stores (B of 32 ranks does
+// not fit: 64 us on 4099 rows for the two passes' 53).
+// Stages of several adapters are left to another launch: going through a stage's
+// adapters here, each loading its B, took 524 us on 16384 rows in random order of 8
+// adapters, the other launch 340.
+//
 // Alignment. X and Y need only be aligned to their element size. When X
 // starts xshift elements past a 16-byte boundary, the loader streams the
 // 16-byte granules that cover each row, from the boundary below it (a
@@ -78,6 +98,8 @@ struct FusedTile {
                   "phase A: 4x4 MFMA blocks of rows x beta0, 16 delta0 per block group");
 };
 
+static_assert(kRows == kPairGroup, "an adapter a stage");
+
 // Loader instructions (1 KB each) for one stage of rows of elem_bytes-wide
 // elements with kXPadBytes after each row.
 constexpr int stage_insts(int eb) { return (kRows * (kC0 * kD0 * eb + kXPadBytes) + 1023) / 1024; }
@@ -85,8 +107,12 @@ constexpr int stage_bytes(int eb) { return stage_insts(eb) * 1024; }
 constexpr int kStagesF32 = 3;              // LDS ring depth for fp32 rows
 constexpr int kStagesBF16 = 4;             // ... and for bf16 rows (half the bytes)
 constexpr int stages_for(int eb) { return eb == 4 ? kStagesF32 : kStagesBF16; }
-constexpr size_t fused_lds_bytes(int eb, int bt) {
-    return size_t(stages_for(eb)) * stage_bytes(eb) + size_t(kZBufs) * kRows * (bt * kZPitch + 8) * sizeof(float);
+// With adapters, a ring of the stages' rows of H and ids, one loader instruction
+// each. Phase B reads them one stage after phase A has read X: one slot more.
+constexpr int kLowBytes = 1024 + 256;
+constexpr size_t fused_lds_bytes(int eb, int bt, bool low) {
+    return size_t(stages_for(eb)) * stage_bytes(eb) + (low ? size_t(stages_for(eb) + 1) * kLowBytes : 0) +
+           size_t(kZBufs) * kRows * (bt * kZPitch + 8) * sizeof(float);
 }
 
 struct FusedArgs {
@@ -98,6 +124,39 @@ struct FusedArgs {
     int xshift;             // elements from the 16-byte boundary below X to X (the same in every row)
 };
 
+// N weights of a thread: fp32 values, or the packed words of bf16 ones, widened
+// where they are used (hold: widened once, ahead of the loop over the stages, they
+// would take twice the registers).
+template <int N, bool PACKED>
+struct Weights {
+    float v[N];
+    template <typename TW>
+    __device__ __forceinline__ void load(const TW* p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f32(p[i]);
+    }
+    __device__ __forceinline__ float at(int i) const { return v[i]; }
+    __device__ __forceinline__ void hold() {}
+};
+typedef short short4v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ short4v four_bf16(uint32_t lo, uint32_t hi) {
+    return __builtin_bit_cast(short4v, uint64_t(lo) | uint64_t(hi) << 32);
+}
+template <int N>
+struct Weights<N, true> {
+    uint32_t w[N / 2];
+    __device__ __forceinline__ void load(const bf16_t* p) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = uint32_t(p[2 * i]) | uint32_t(p[2 * i + 1]) << 16;
+    }
+    __device__ __forceinline__ float at(int i) const { return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
+    __device__ __forceinline__ void hold() {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ short4v four(int c) const { return four_bf16(w[2 * c], w[2 * c + 1]); }
+};
+
 // The byte limit of issue_stage when rows start xshift elements past a
 // 16-byte boundary: the granule holding the last elements of the stage's last
 // row is one past the usual limit.
@@ -105,15 +164,20 @@ __device__ __forceinline__ uint32_t shifted_limit(uint32_t limit, int xshift) {
     return (xshift == 0 || limit > kNoVector - 16u) ? limit : limit + 16u;
 }
 
-// kYVec: Y is 16-byte aligned (vector stores in phase B); BT: beta0 per tile.
-template <typename TX, typename TW, bool kYVec, int BT>
+// kYVec: Y is 16-byte aligned (vector stores in phase B); BT: beta0 per tile;
+// ADD: adapters as well.
+template <typename TX, typename TW, bool kYVec, int BT, bool ADD>
 __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __restrict__ X,
                                                                    const TW* __restrict__ K0,
                                                                    const TW* __restrict__ K1,
-                                                                   float* __restrict__ Y, FusedArgs args) {
+                                                                   float* __restrict__ Y, FusedArgs args,
+                                                                   PairAdapters ad) {
+    static_assert(!ADD || (sizeof(TX) == 2 && sizeof(TW) == 2 && BT == 32), "adapters: bf16, a thread all rows of a stage");
     constexpr int EB = int(sizeof(TX));
     constexpr int VW = 16 / EB;
     constexpr int INSTS = stage_insts(EB);
+    constexpr int kLowRow = kLowPartsBytes;                  // bytes of a row's parts of H
+    constexpr int kLoads = INSTS + (ADD ? 2 : 0);            // loader instructions of a stage
     constexpr int kStageBytes = stage_bytes(EB);
     constexpr int kStages = stages_for(EB);
     constexpr int kRowBytes = kC0 * kD0 * EB + kXPadBytes;   // LDS pitch of a row of X
@@ -124,6 +188,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     constexpr int kRowsPerPass = Tile::kRowsPerPass;
     extern __shared__ __align__(16) unsigned char lds[];
     float* const zs = reinterpret_cast<float*>(lds + kStages * kStageBytes);   // kZBufs x [kRows][BT][kZPitch]
+    unsigned char* const lows = reinterpret_cast<unsigned char*>(zs + kZBufs * kZFloats);   // kStages + 1 slots (ADD)
 
     const int t = threadIdx.x;
     const int blk = xcd_logical_block(blockIdx.x, gridDim.x);
@@ -156,10 +221,23 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             issue_stage<INSTS>(lp, INSTS, xbase + n0 * args.n_in,
                                shifted_limit(stage_limit(n0, row_end, args.n_in, EB), args.xshift),
                                lds + (s % kStages) * kStageBytes);
+            if constexpr (ADD) {
+                // the rows' parts of H, one after another, and their adapter; lanes past
+                // the last row read its end again, which nobody uses
+                const int lane = t - kFusedConsumers * 64;
+                unsigned char* low = lows + (s % (kStages + 1)) * kLowBytes;
+                const int bytes = static_cast<int>(min(row_end - n0, int64_t(kRows))) * kLowRow;
+                __builtin_amdgcn_global_load_lds(
+                    reinterpret_cast<const void*>(reinterpret_cast<const char*>(ad.H) + n0 * kLowRow +
+                                                  min(lane * 16, bytes - 16)),
+                    low, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(ad.groups + n0 / kRows), low + 1024, 4, 0,
+                                                 0);
+            }
         };
         for (int s = 0; s < kStages - 1 && s < nsteps; ++s) issue(s);
         for (int s = 0; s <= nsteps; ++s) {
-            if (s < nsteps) wait_vmcnt_upto(min(kStages - 2, nsteps - 1 - s) * INSTS);
+            if (s < nsteps) wait_vmcnt_upto(min(kStages - 2, nsteps - 1 - s) * kLoads);
             lds_barrier();                                   // stage s ready, Z of stage s - 1 written
             if (s + kStages - 1 < nsteps) issue(s + kStages - 1);
         }
@@ -180,17 +258,36 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     // groups of 4 beta0, all kRows rows
     const int a_d0 = 16 * (wave & 3) + (lane >> 2);        // delta0 of this lane's block
     const int a_b0 = (wave >> 2) * kSetsPerWave * 4;       // first beta0 (within the tile) of the wave
-    float k0r[kSetsPerWave][kC0];
+    Weights<kC0, ADD> k0r[kSetsPerWave];
 #pragma unroll
-    for (int j = 0; j < kSetsPerWave; ++j) {
-        const TW* kp = K0 + (int64_t(a_d0) * args.b0 + beta0 + a_b0 + 4 * j + q) * kC0;   // K0[0][d0][beta][:]
-#pragma unroll
-        for (int g = 0; g < kC0; ++g) k0r[j][g] = to_f32(kp[g]);
-    }
+    for (int j = 0; j < kSetsPerWave; ++j)                  // K0[0][d0][beta][:]
+        k0r[j].load(K0 + (int64_t(a_d0) * args.b0 + beta0 + a_b0 + 4 * j + q) * kC0);
 
     // (A) Z[r][beta0][d0] = sum_g K0[0][d0][beta0][g] * X[r][g][d0] for stage s
     auto phase_a = [&](int s, float* zb) {
         const unsigned char* xs = lds + (s % kStages) * kStageBytes;
+        if constexpr (ADD) {
+            static_assert(kRows == 4, "one row a lane of a block");
+            const TX* xa = reinterpret_cast<const TX*>(xs + q * kRowBytes) + args.xshift + a_d0;
+            short4v x[kC0 / 4];
+#pragma unroll
+            for (int g = 0; g < kC0; ++g) x[g / 4][g % 4] = static_cast<short>(xa[g * kD0]);
+            floatx4 z[kSetsPerWave];
+#pragma unroll
+            for (int j = 0; j < kSetsPerWave; ++j) z[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < kC0 / 4; ++c)
+#pragma unroll
+                for (int j = 0; j < kSetsPerWave; ++j)
+                    z[j] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(x[c], k0r[j].four(c), z[j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < kSetsPerWave; ++j) {
+                float* zw = zb + (a_b0 + 4 * j + q) * kZPitch + a_d0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) zw[i * kZRow] = z[j][i];
+            }
+            return;
+        } else {
 #pragma unroll
         for (int rg = 0; rg < kRows; rg += 4) {
             const TX* xa = reinterpret_cast<const TX*>(xs + (rg + q) * kRowBytes) + args.xshift + a_d0;
@@ -201,7 +298,8 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             for (int g = 0; g < kC0; ++g) {
                 const float x = to_f32(xa[g * kD0]);
 #pragma unroll
-                for (int j = 0; j < kSetsPerWave; ++j) z[j] = __builtin_amdgcn_mfma_f32_4x4x1f32(x, k0r[j][g], z[j], 0, 0, 0);
+                for (int j = 0; j < kSetsPerWave; ++j)
+                    z[j] = __builtin_amdgcn_mfma_f32_4x4x1f32(x, k0r[j].at(g), z[j], 0, 0, 0);
             }
 #pragma unroll
             for (int j = 0; j < kSetsPerWave; ++j) {
@@ -209,6 +307,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
 #pragma unroll
                 for (int i = 0; i < 4; ++i) zw[i * kZRow] = z[j][i];
             }
+        }
         }
     };
 
@@ -230,17 +329,81 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     const int b1 = (t >> 1) & (kB1 - 1);
     const int a1 = (t >> 4) & (BT - 1);                // alpha1 within the tile
     const int e10 = run * 4;                           // first delta1 of the run
-    float k1r[4][kC1];
+    Weights<kC1, ADD> k1r[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const TW* kp = K1 + ((int64_t(beta0 + a1) * kD1 + e10 + k) * kB1 + b1) * kC1;   // K1[a][e][b][:]
-#pragma unroll
-        for (int g = 0; g < kC1; ++g) k1r[k][g] = to_f32(kp[g]);
-    }
+    for (int k = 0; k < 4; ++k)                              // K1[a][e][b][:]
+        k1r[k].load(K1 + ((int64_t(beta0 + a1) * kD1 + e10 + k) * kB1 + b1) * kC1);
     const int64_t yoff = int64_t(beta0 + a1) * (kB1 * kD1) + b1 * kD1 + e10;
+    // low[k][r]: the adapter's part of output k of the run in row r of the stage. The
+    // adapter's B of these four outputs stays from stage to stage.
+    uint32_t bw[4][ADD ? 8 : 1];
+    int held = -1;
+    auto adapter = [&](int s, floatx4 (&low)[4]) {
+        const unsigned char* at = lows + (s % (kStages + 1)) * kLowBytes;
+        const uint4* h = reinterpret_cast<const uint4*>(at + q * kLowRow);   // of row q: [chunk of 4 ranks][part][4]
+        const int g = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int*>(at + 1024));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) low[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (g < 0) return;
+        if (g != held) {
+            held = g;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bf16_t* b = static_cast<const bf16_t*>(ad.B) + (int64_t(g) * args.n_out + yoff + k) * ad.rank;
+#pragma unroll
+                for (int w = 0; w < 8; w += 2) {
+                    uint2 v = *reinterpret_cast<const uint2*>(b + min(2 * w, ad.rank - 4));
+                    if (2 * w >= ad.rank) v = uint2{0u, 0u};
+                    bw[k][w] = v.x;
+                    bw[k][w + 1] = v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {                   // two chunks of 4 ranks
+            const uint4 v[3] = {h[3 * c / 2], h[3 * c / 2 + 1], h[3 * c / 2 + 2]};
+            const short4v part[6] = {four_bf16(v[0].x, v[0].y), four_bf16(v[0].z, v[0].w), four_bf16(v[1].x, v[1].y),
+                                     four_bf16(v[1].z, v[1].w), four_bf16(v[2].x, v[2].y), four_bf16(v[2].z, v[2].w)};
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    low[k] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                        part[i], four_bf16(bw[k][2 * (c + i / 3)], bw[k][2 * (c + i / 3) + 1]), low[k], 0, 0, 0);
+        }
+    };
     auto phase_b = [&](int s, const float* zb) {
         const int64_t n0 = row_begin + int64_t(s) * kRows;
         const int rows = static_cast<int>(min(int64_t(kRows), row_end - n0));
+        if constexpr (ADD) {
+            // on top of the adapter's part, all rows of a gamma1 together: what
+            // the other order holds at a time does not fit the registers
+            floatx4 y[4];
+            adapter(s, y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) k1r[k].hold();
+#pragma unroll
+            for (int g = 0; g < kC1; ++g)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const floatx4 z = *reinterpret_cast<const floatx4*>(zb + r * kZRow + a1 * kZPitch + e10 + g * kD1);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k][r] = fmaf(k1r[k].at(g), z[k], y[k][r]);
+                }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (r >= rows) break;
+                const floatx4 out = {y[0][r], y[1][r], y[2][r], y[3][r]};
+                float* yr = Y + (n0 + r) * args.n_out + yoff;
+                if constexpr (kYVec) {
+                    __builtin_nontemporal_store(out, reinterpret_cast<floatx4*>(yr));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) __builtin_nontemporal_store(out[k], yr + k);
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int r0 = 0; r0 < kRows; r0 += kRowsPerPass) {
             const int r = r0 + rsub;
@@ -250,7 +413,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             for (int g = 0; g < kC1; ++g) {
                 const floatx4 z = *reinterpret_cast<const floatx4*>(zr + g * kD1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = fmaf(k1r[k][g], z[k], y[k]);
+                for (int k = 0; k < 4; ++k) y[k] = fmaf(k1r[k].at(g), z[k], y[k]);
             }
             if (r < rows) {
                 float* yr = Y + (n0 + r) * args.n_out + yoff;
@@ -271,9 +434,9 @@ bool shape_ok(const Shape& s0, const Shape& s1) {
            s1.c == kC1 && s1.d == kD1;
 }
 
-template <typename TX, typename TW, int BT>
+template <typename TX, typename TW, int BT, bool ADD>
 ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const void* W1, const void* X,
-                        float* Y, int64_t batch, hipStream_t stream, int num_cus) {
+                        float* Y, int64_t batch, const PairAdapters& ad, hipStream_t stream, int num_cus) {
     FusedArgs args;
     args.b0 = s0.b;
     args.n_in = s0.n_in;
@@ -283,7 +446,7 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
     args.n_tiles = s0.b / BT;
     args.xshift = static_cast<int>((reinterpret_cast<uintptr_t>(X) & 15u) / sizeof(TX));
     // about one resident wave of workgroups (as many per compute unit as fit its 160 KB of LDS)
-    const size_t lds = fused_lds_bytes(int(sizeof(TX)), BT);
+    const size_t lds = fused_lds_bytes(int(sizeof(TX)), BT, ADD);
     const int per_cu = std::max(1, std::min(4, int((160 * 1024) / lds)));
     const int64_t steps_total = (batch + kRows - 1) / kRows;
     const int64_t splits = std::max<int64_t>(1, int64_t(std::max(num_cus, 1)) * per_cu / args.n_tiles);
@@ -293,9 +456,9 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
     const int64_t blocks = nsplit * args.n_tiles;
     if (blocks > 0x7fffffff) return KS_ERR_UNSUPPORTED;
     const bool y_vec = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0;
-    auto kernel = y_vec ? fused_pair_kernel<TX, TW, true, BT> : fused_pair_kernel<TX, TW, false, BT>;
+    auto kernel = y_vec ? fused_pair_kernel<TX, TW, true, BT, ADD> : fused_pair_kernel<TX, TW, false, BT, ADD>;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFusedThreads), lds, stream,
-                         static_cast<const TX*>(X), static_cast<const TW*>(W0), static_cast<const TW*>(W1), Y, args);
+                         static_cast<const TX*>(X), static_cast<const TW*>(W0), static_cast<const TW*>(W1), Y, args, ad);
 }
 
 // The widest tile that divides b0: 32 beta0 per workgroup on GPT-2-medium's
@@ -304,9 +467,9 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
 template <typename TX, typename TW>
 ks_status_t launch_typed(const Shape& s0, const Shape& s1, const void* W0, const void* W1, const void* X,
                          float* Y, int64_t batch, hipStream_t stream, int num_cus) {
-    if (s0.b % 32 == 0) return launch_tile<TX, TW, 32>(s0, s1, W0, W1, X, Y, batch, stream, num_cus);
-    if (s0.b % 16 == 0) return launch_tile<TX, TW, 16>(s0, s1, W0, W1, X, Y, batch, stream, num_cus);
-    return launch_tile<TX, TW, 8>(s0, s1, W0, W1, X, Y, batch, stream, num_cus);
+    if (s0.b % 32 == 0) return launch_tile<TX, TW, 32, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
+    if (s0.b % 16 == 0) return launch_tile<TX, TW, 16, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
+    return launch_tile<TX, TW, 8, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
 }
 
 }  // namespace
@@ -332,6 +495,18 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
     if (xt == kBF16 && wt0 == kBF16) return launch_typed<bf16_t, bf16_t>(s0, s1, W0, W1, X, Y, batch, stream, num_cus);
     if (xt == kF32 && wt0 == kBF16) return launch_typed<float, bf16_t>(s0, s1, W0, W1, X, Y, batch, stream, num_cus);
     return KS_ERR_UNSUPPORTED;
+}
+
+bool fused_pair_adds(const Shape& s0, const Shape& s1, int xt, int wt, const void* B, int rank) {
+    return xt == kBF16 && wt == kBF16 && s0.b % 32 == 0 && fused_pair_supports(s0, s1, xt, wt, wt) && rank <= 16 &&
+           rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0;
+}
+
+ks_status_t launch_fused_pair_adapters(const Shape& s0, const Shape& s1, const void* W0, const void* W1,
+                                       const void* X, float* Y, int64_t batch, const PairAdapters& ad,
+                                       hipStream_t stream, int num_cus) {
+    if (!fused_pair_adds(s0, s1, kBF16, kBF16, ad.B, ad.rank)) return KS_ERR_UNSUPPORTED;
+    return launch_tile<bf16_t, bf16_t, 32, true>(s0, s1, W0, W1, X, Y, batch, ad, stream, num_cus);
 }
 
 }  // namespace ks

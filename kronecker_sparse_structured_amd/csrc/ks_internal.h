@@ -92,6 +92,23 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
                               const void* W0, const void* W1, const void* X, float* Y,
                               int64_t batch, hipStream_t stream, int num_cus);
 
+// The same pair of bf16 operands with low-rank adapters added to its output,
+// Y[n] += H[n] B[g]^T with g = groups[n / kPairGroup] (< 0: nothing is added to these
+// rows). H: per row (kLowPartsBytes, 16-byte aligned), for every four of 16 ranks,
+// zeros past the adapters' own, three times four bf16 values whose sums are the fp32
+// values. B [count, n_out, rank]. fused_pair_adds: whether it runs them.
+constexpr int kPairGroup = 4, kLowPartsBytes = 96, kLowPartsRank = 16;
+struct PairAdapters {
+    const void* H;
+    const int32_t* groups;
+    const void* B;
+    int rank;
+};
+bool fused_pair_adds(const Shape& s0, const Shape& s1, int xt, int wt, const void* B, int rank);
+ks_status_t launch_fused_pair_adapters(const Shape& s0, const Shape& s1, const void* W0, const void* W1,
+                                       const void* X, float* Y, int64_t batch, const PairAdapters& ad,
+                                       hipStream_t stream, int num_cus);
+
 // Fused pair whose second factor works inside the first one's output slabs:
 // F = (a, 16, 16, 16) then G = (16 a, 16, 16, 1). KS_ERR_UNSUPPORTED when the
 // pair is not of that family.

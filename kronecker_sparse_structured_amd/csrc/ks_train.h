@@ -50,6 +50,24 @@ AdapterPath adapter_path(int64_t batch);
 size_t adapter_workspace(int64_t batch, int count);
 ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float* Y, void* ws);
 
+// The first product alone, over rows as they lie: H, its values in parts as the
+// fused pair takes them, and the adapter of each kPairGroup rows (-1 unless they
+// share one); then the second product for the other groups' rows.
+ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, int32_t* groups);
+ks_status_t launch_adapter_rest(const AdapterCall& c, const float* H, float* Y);
+
+// Adapters beside a chain: chain_matmul (ks_chain_matmul with the dtype as an int)
+// runs them around its last launch where that is a fused pair that adds them
+// (added); the caller runs them otherwise.
+struct ChainAdapters {
+    AdapterCall call;
+    PairAdapters pair;
+    float* H;
+    bool added;
+};
+ks_status_t chain_matmul(const ks_pattern_t* p, int n, const void* const* W, const void* X, void* Y, int64_t batch,
+                         int dt, void* ws, size_t ws_bytes, unsigned flags, hipStream_t stream, ChainAdapters* extra);
+
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch);
 ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,
                                 float* dA, float* dB, void* ws);

@@ -236,6 +236,39 @@ def test_chain_with_adapters(case):
     assert torch.equal(changed, chain.backward(dY, X, H, ids)[0]) and not torch.equal(changed, dX)
 
 
+PAIR = [(1, 64, 16, 64), (64, 8, 8, 8)]
+
+
+@pytest.mark.parametrize("rank,xt,mix,batch", [
+    (16, BF16, "runs", 1025), (8, BF16, "random", 1026), (4, BF16, "runs", 4099), (12, BF16, "random", 4098), (16, BF16, "runs", 5001), (16, F32, "random", 4097),
+    (20, F32, "runs", 4110), (32, BF16, "random", 4097), (32, BF16, "runs", 4999), (16, BF16, "none", 4100),
+    (13, BF16, "runs", 4100), (48, BF16, "runs", 4100)])
+def test_pair_adds_adapters(rank, xt, mix, batch):
+    """Many rows through the fused pair of factors, which adds the adapters itself
+    where it can: against 64 bits, rows of several adapters in a tile, NaN in the
+    adapters of other rows."""
+    require_gpu()
+    X, A, B, scale, ids = draw(batch, 1024, 4096, 6, rank, xt, BF16, seed=rank + batch, mix=mix)
+    ids[ids == 4] = 3
+    A[4], B[4] = float("nan"), float("inf")                  # of no row
+    A[5], B[5] = float("nan"), float("nan")
+    Ws = [(torch.randn(a, d, b, c) / c ** 0.5).to(BF16).to(DEV) for a, b, c, d in PAIR]
+    chain = libks.AdapterChain(Ws, PAIR, A, B, scale)
+    Y, H = chain.matmul(X, ids, keep=True)
+    assert torch.equal(Y.view(torch.int32), chain.matmul(X, ids).view(torch.int32))
+    bad = ids == 5
+    assert not torch.isfinite(Y[bad]).any() and torch.isfinite(Y[~bad]).all()
+    A[4:], B[4:] = 0.0, 0.0
+    ok = ~bad
+    ref = formula(X[ok], A, B, scale, ids[ok])
+    mag = formula(X[ok].abs(), A.abs(), B.abs(), scale, ids[ok])
+    near(H[ok], ref["H"], mag["H"], 1024 + 2, "H")
+    Wn, x = [w.double().cpu().numpy() for w in Ws], X[ok].double().cpu().numpy()
+    base = torch.from_numpy(oracle.ks_chain_matmul(PAIR, Wn, x))
+    size = torch.from_numpy(oracle.ks_chain_matmul(PAIR, [abs(w) for w in Wn], abs(x)))
+    near(Y[ok], base + ref["D"], size + mag["D"], 1024 + rank + 26 + 4, "Y")
+
+
 def test_layer_autograd_other_stream_and_graph():
     require_gpu()
     base = layer.KSLinear([(4, 64, 16, 6)], device=DEV, seed=3)
