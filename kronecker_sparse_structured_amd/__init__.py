@@ -5,14 +5,17 @@ nonzeros are stored as an (a, d, b, c) tensor (KS abstract page,
 taxoreview.com "dblp:303/4794", first paragraph). The compute path is the
 HIP library libks.so (C ABI in include/ks.h); ``libks`` is its ctypes
 binding. Importing this package loads nothing; the first call does.
+``layer`` and ``optim`` hold what a model trains with: KS layers, low-rank
+adapters beside them, a preference loss and AdamW (``finetune`` runs them
+together).
 """
 from . import datagen  # noqa: F401  (seeded inputs; no KS arithmetic)
 
-__all__ = ["datagen", "libks"]
+__all__ = ["datagen", "layer", "libks", "optim"]
 
 
 def __getattr__(name):
-    if name == "libks":
+    if name in ("layer", "libks", "optim"):
         import importlib
-        return importlib.import_module(__name__ + ".libks")
+        return importlib.import_module(__name__ + "." + name)
     raise AttributeError(name)

@@ -137,8 +137,8 @@ def make_adapter_class():
         y = layer(x) + alpha / rank x A[g]^T B[g]^T, where ids gives the
         adapter g of each row (any id outside [0, adapters): none, the layer
         alone). A is drawn N(0, 1/n_in) and B starts at zero, so a new adapter
-        changes nothing. Input (..., n_in) with ids (...), int32; output
-        (..., n_out), fp32."""
+        changes nothing (more than 1024 rows: nothing beyond rounding). Input
+        (..., n_in) with ids (...), int32; output (..., n_out), fp32."""
 
         def __init__(self, layer, adapters: int, rank: int, alpha: float = 16.0, seed: int = 0):
             super().__init__()
