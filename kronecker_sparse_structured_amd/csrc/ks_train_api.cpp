@@ -411,15 +411,12 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     if (st != KS_OK) return st;
     st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
     if (st != KS_OK) return st;
-    int cus = 0;
-    st = current_cus(&cus);
-    if (st != KS_OK) return st;
     char* rest = static_cast<char*>(ws) + round256(chain_ws);
     char* low = rest + round256(ks::adapter_workspace(batch, ad->count));
     if (!H && ks::adapter_path(batch) != ks::kAdapterRows) H = reinterpret_cast<float*>(low);
     char* parts = low + round256(static_cast<uint64_t>(batch) * ad->rank * 4);
     ks::ChainAdapters extra;
-    extra.call = adapter_call(ad, ids, xt, wt, batch, stream, cus);
+    extra.call = adapter_call(ad, ids, xt, wt, batch, stream, 0);
     extra.pair = {parts, reinterpret_cast<int32_t*>(parts + parts_bytes(batch)), ad->B, ad->rank};
     extra.H = H;
     extra.added = false;
@@ -428,6 +425,8 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     st = ks::chain_matmul(p, n, W, X, Y, batch, code, ws, chain_ws, KS_CHAIN_AUTO, stream,
                           takes_parts(ad->rank, batch) ? &extra : nullptr);
     if (st != KS_OK || extra.added) return st;
+    st = current_cus(&extra.call.num_cus);
+    if (st != KS_OK) return st;
     return ks::launch_adapter(extra.call, X, H, Y, rest);
 }
 
