@@ -409,6 +409,12 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     if (batch == 0) return KS_OK;
     st = check_forward(ad, ids, X, Y, H, batch, xt, wt, ws, ws_bytes, need);
     if (st != KS_OK) return st;
+    for (int k = 0; W && k < n; ++k) {
+        // the chain's own checks take in Y and its part of the workspace
+        const uint64_t bytes = static_cast<uint64_t>(shape_of(p[k]).nnz) * ks::elem_bytes(wt);
+        if (any_overlap({{H, static_cast<uint64_t>(batch) * ad->rank * 4}, {need > 0 ? ws : nullptr, need}}, {{W[k], bytes}}))
+            return KS_ERR_OVERLAP;
+    }
     st = ks_chain_workspace_size(p, n, batch, static_cast<ks_dtype_t>(code), KS_CHAIN_AUTO, &chain_ws);
     if (st != KS_OK) return st;
     char* rest = static_cast<char*>(ws) + round256(chain_ws);
@@ -494,12 +500,14 @@ ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* 
     char* base = static_cast<char*>(ws);
     if (batch > 0) {
         const uint64_t dx_bytes = static_cast<uint64_t>(batch) * ad->n_in * 4;
-        if (Wt && any_overlap({{dX, dx_bytes}, {ws, w.total}}, {{Wt, g.blocks}})) return KS_ERR_OVERLAP;
+        const uint64_t each = static_cast<uint64_t>(ad->count) * ad->rank * 4;
+        const Range da{dA, each * ad->n_in}, db{dB, each * ad->n_out};
+        if (Wt && any_overlap({{dX, dx_bytes}, da, db, {ws, w.total}}, {{Wt, g.blocks}})) return KS_ERR_OVERLAP;
         for (int k = 0; k < n && !Wt; ++k) {
             if (!W[k]) return KS_ERR_NULL;
             if (!aligned(W[k], ks::elem_bytes(wt))) return KS_ERR_ALIGN;
             const uint64_t bytes = static_cast<uint64_t>(shape_of(p[k]).nnz) * ks::elem_bytes(wt);
-            if (any_overlap({{dX, dx_bytes}, {ws, w.total}}, {{W[k], bytes}})) return KS_ERR_OVERLAP;
+            if (any_overlap({{dX, dx_bytes}, da, db, {ws, w.total}}, {{W[k], bytes}})) return KS_ERR_OVERLAP;
         }
         const char* blocks = static_cast<const char*>(Wt);
         char* chain_ws = base;

@@ -114,6 +114,20 @@ def test_chain_refusals():
     assert lib.ks_chain_transpose(pats, 2, (ctypes.c_void_p * 2)(None, 16), 0xE0000000, F32, None) == libks.KS_ERR_NULL
 
 
+def test_weights_of_the_chain_apart_from_everything_written():
+    size = ctypes.c_size_t(0)
+    pats = libks._patterns(PS)
+    lib = libks.load()
+    assert lib.ks_chain_adapter_workspace_size(pats, 2, adapters(), 2000, F32, size) == libks.KS_OK
+    at = lambda a: (ctypes.c_void_p * 2)(a, WP[1])
+    assert chain(w=at(P["H"])) == libks.KS_ERR_OVERLAP
+    assert chain(batch=2000, w=at(P["ws"] + size.value - 16)) == libks.KS_ERR_OVERLAP
+    for name in ("dA", "dB"):
+        assert lib.ks_chain_adapter_backward(pats, 2, at(P[name]), None, adapters(), P["ids"], P["dY"], P["X"], P["H"],
+                                             P["dX"], P["dA"], P["dB"], 8, F32, P["ws"], 1 << 30, None) == \
+            libks.KS_ERR_OVERLAP
+
+
 def logits(**kw):
     v = dict(data=0x10000000, labels=0x20000000, seq_stride=40, row_stride=10, label_stride=4, sequences=2, tokens=4,
              vocab=10, elem=libks.ELEM_F32, reserved=0)
