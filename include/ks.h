@@ -435,7 +435,10 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
  *   Wt     NULL: W's blocks are transposed in the workspace by each call. Else
  *          device, what ks_chain_transpose wrote for the same p, n and weights
  *          (ks_chain_transpose_size bytes, 16-byte aligned): a layer whose W does
- *          not change makes it once; W may then be NULL.
+ *          not change makes it once; W may then be NULL. Where both are given
+ *          either is read: the pair (1, b, 16, 64), (b, 8, 8, 8) with bf16 weights,
+ *          b up to 64 and a multiple of 16 runs as one launch on W itself (W and
+ *          dY 16-byte aligned).
  *   ws     of ks_chain_adapter_backward_workspace_size bytes, which has to be
  *          told whether Wt will be given.
  */

@@ -68,6 +68,12 @@ struct ChainAdapters {
 ks_status_t chain_matmul(const ks_pattern_t* p, int n, const void* const* W, const void* X, void* Y, int64_t batch,
                          int dt, void* ws, size_t ws_bytes, unsigned flags, hipStream_t stream, ChainAdapters* extra);
 
+// dX of a pair of factors (1, b0, 16, 64), (b0, 8, 8, 8) with bf16 weights in one
+// launch (ks_pair_grad.hip).
+bool pair_dx_supports(const Shape& s0, const Shape& s1, int wt, const void* W0, const void* W1, const float* dY);
+ks_status_t launch_pair_dx(const Shape& s0, const void* W0, const void* W1, const float* dY, float* dX, int64_t batch,
+                           hipStream_t stream, int num_cus);
+
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch);
 ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,
                                 float* dA, float* dB, void* ws);

@@ -498,31 +498,41 @@ ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* 
     if (st != KS_OK) return st;
     if (!aligned(Wt, 16)) return KS_ERR_ALIGN;
     char* base = static_cast<char*>(ws);
+    int cus = 0;
     if (batch > 0) {
         const uint64_t dx_bytes = static_cast<uint64_t>(batch) * ad->n_in * 4;
         const uint64_t each = static_cast<uint64_t>(ad->count) * ad->rank * 4;
         const Range da{dA, each * ad->n_in}, db{dB, each * ad->n_out};
         if (Wt && any_overlap({{dX, dx_bytes}, da, db, {ws, w.total}}, {{Wt, g.blocks}})) return KS_ERR_OVERLAP;
-        for (int k = 0; k < n && !Wt; ++k) {
-            if (!W[k]) return KS_ERR_NULL;
+        bool have = W != nullptr;                            // every factor as it is
+        for (int k = 0; k < n && W; ++k) {
+            have = have && W[k];
+            if (!W[k] && !Wt) return KS_ERR_NULL;
+            if (!W[k]) continue;
             if (!aligned(W[k], ks::elem_bytes(wt))) return KS_ERR_ALIGN;
             const uint64_t bytes = static_cast<uint64_t>(shape_of(p[k]).nnz) * ks::elem_bytes(wt);
             if (any_overlap({{dX, dx_bytes}, da, db, {ws, w.total}}, {{W[k], bytes}})) return KS_ERR_OVERLAP;
         }
-        const char* blocks = static_cast<const char*>(Wt);
-        char* chain_ws = base;
-        if (!blocks) {
-            st = transpose_chain(p, n, W, g, base, stream);
-            if (st != KS_OK) return st;
-            blocks = base;
-            chain_ws = base + g.blocks;
+        st = current_cus(&cus);
+        if (st != KS_OK) return st;
+        if (n == 2 && have && ks::pair_dx_supports(shape_of(p[0]), shape_of(p[1]), wt, W[0], W[1], dY)) {
+            st = ks::launch_pair_dx(shape_of(p[0]), W[0], W[1], dY, dX, batch, stream, cus);
+        } else {
+            const char* blocks = static_cast<const char*>(Wt);
+            char* chain_ws = base;
+            if (!blocks) {
+                st = transpose_chain(p, n, W, g, base, stream);
+                if (st != KS_OK) return st;
+                blocks = base;
+                chain_ws = base + g.blocks;
+            }
+            std::vector<const void*> factors(n);
+            for (int k = 0; k < n; ++k) factors[k] = blocks + g.at[k];
+            st = ks_chain_matmul(g.p.data(), n, factors.data(), dY, dX, batch, g.dt, chain_ws, w.chain, KS_CHAIN_AUTO,
+                                 stream);
         }
-        std::vector<const void*> factors(n);
-        for (int k = 0; k < n; ++k) factors[k] = blocks + g.at[k];
-        st = ks_chain_matmul(g.p.data(), n, factors.data(), dY, dX, batch, g.dt, chain_ws, w.chain, KS_CHAIN_AUTO, stream);
         if (st != KS_OK) return st;
     }
-    int cus = 0;
     st = current_cus(&cus);
     if (st != KS_OK) return st;
     return ks::launch_adapter_grad(adapter_call(ad, ids, xt, wt, batch, stream, cus), dY, X, H,

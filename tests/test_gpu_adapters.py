@@ -269,6 +269,30 @@ def test_pair_adds_adapters(rank, xt, mix, batch):
     near(Y[ok], base + ref["D"], size + mag["D"], 1024 + rank + 26 + 4, "Y")
 
 
+@pytest.mark.parametrize("b0,batch,xt,shift", [(64, 1, BF16, 0), (64, 3, F32, 0), (64, 1027, BF16, 0), (48, 70, BF16, 0),
+                                               (32, 2050, F32, 0), (16, 9, BF16, 0), (80, 33, BF16, 0), (64, 21, BF16, 1)])
+def test_gradient_of_the_pair(b0, batch, xt, shift):
+    """dX of the fused pair's gradient, of other widths and of a dY that is not
+    16-byte aligned, against 64 bits."""
+    require_gpu()
+    ps = [(1, b0, 16, 64), (b0, 8, 8, 8)]
+    n_out = b0 * 64
+    X, A, B, scale, ids = draw(batch, 1024, n_out, 2, 4, xt, BF16, seed=b0 + batch, mix="random")
+    Ws = [(torch.randn(a, d, b, c) / c ** 0.5).to(BF16).to(DEV) for a, b, c, d in ps]
+    chain = libks.AdapterChain(Ws, ps, A, B, scale)
+    flat = torch.randn(batch * n_out + shift, device=DEV)
+    dY = flat[shift:].view(batch, n_out)
+    _, H = chain.matmul(X, ids, keep=True)
+    dX = chain.backward(dY, X, H, ids)[0]
+    assert torch.equal(dX, chain.backward(dY, X, H, ids)[0])
+    ref, mag = formula(X, A, B, scale, ids, dY), formula(X.abs(), A.abs(), B.abs(), scale, ids, dY.abs())
+    Wn = [w.double().cpu().numpy() for w in Ws]
+    back, size = dY.double().cpu().numpy(), dY.double().cpu().abs().numpy()
+    for p, w in zip(ps[::-1], Wn[::-1]):
+        back, size = oracle.ks_matmul_dx(p, w, back), oracle.ks_matmul_dx(p, abs(w), size)
+    near(dX, torch.from_numpy(back) + ref["dX"], torch.from_numpy(size) + mag["dX"], n_out + b0 + 8 + 4 + 4, "dX")
+
+
 def test_layer_autograd_other_stream_and_graph():
     require_gpu()
     base = layer.KSLinear([(4, 64, 16, 6)], device=DEV, seed=3)
