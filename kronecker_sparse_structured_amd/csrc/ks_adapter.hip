@@ -227,7 +227,7 @@ struct Tile {
 // A value of H as three bf16 values, each the leading bits of what the ones before
 // leave: their sum is the value exactly. Infinity and NaN stay in the first.
 __device__ __forceinline__ void keep_parts(const Args& a, int64_t row, int r, float h) {
-    bf16_t* to = a.parts + row * (kLowPartsBytes / 2) + r / 4 * 12 + r % 4;
+    bf16_t* to = a.parts + row * (low_parts_bytes(a.rank) / 2) + r / 4 * 12 + r % 4;
     float first = __uint_as_float(__float_as_uint(h) & 0xffff0000u), rest = h - first;
     if (!(fabsf(h) < __builtin_inff())) {
         first = h;

@@ -45,8 +45,8 @@
 // that saves 17 us of 16384 rows. With it and rank 16 they take 75 us (63 for the
 // chain alone, 4.0 TB/s); with the adapters added by a pass over Y, 63 and 98.
 // Weights stay packed in registers: nine waves leave 168 a wave, and spilled ones
-// come back through the vector-memory counter behind the stores (B of 32 ranks does
-// not fit: 64 us on 4099 rows for the two passes' 53).
+// come back through the vector-memory counter behind the stores. Rank 32: 96 us for
+// 180.
 // Stages of several adapters are left to another launch: going through a stage's
 // adapters here, each loading its B, took 524 us on 16384 rows in random order of 8
 // adapters, the other launch 340.
@@ -165,19 +165,19 @@ __device__ __forceinline__ uint32_t shifted_limit(uint32_t limit, int xshift) {
 }
 
 // kYVec: Y is 16-byte aligned (vector stores in phase B); BT: beta0 per tile;
-// ADD: adapters as well.
-template <typename TX, typename TW, bool kYVec, int BT, bool ADD>
+// RT: tiles of 16 ranks of adapters that are added (0: none).
+template <typename TX, typename TW, bool kYVec, int BT, int RT>
 __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __restrict__ X,
                                                                    const TW* __restrict__ K0,
                                                                    const TW* __restrict__ K1,
                                                                    float* __restrict__ Y, FusedArgs args,
                                                                    PairAdapters ad) {
-    static_assert(!ADD || (sizeof(TX) == 2 && sizeof(TW) == 2 && BT == 32), "adapters: bf16, a thread all rows of a stage");
+    static_assert(RT == 0 || (sizeof(TX) == 2 && sizeof(TW) == 2 && BT == 32), "adapters: bf16, a thread all rows of a stage");
     constexpr int EB = int(sizeof(TX));
     constexpr int VW = 16 / EB;
     constexpr int INSTS = stage_insts(EB);
-    constexpr int kLowRow = kLowPartsBytes;                  // bytes of a row's parts of H
-    constexpr int kLoads = INSTS + (ADD ? 2 : 0);            // loader instructions of a stage
+    constexpr int kLowRow = low_parts_bytes(16 * RT);                  // bytes of a row's parts of H
+    constexpr int kLoads = INSTS + (RT > 0 ? 2 : 0);            // loader instructions of a stage
     constexpr int kStageBytes = stage_bytes(EB);
     constexpr int kStages = stages_for(EB);
     constexpr int kRowBytes = kC0 * kD0 * EB + kXPadBytes;   // LDS pitch of a row of X
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     constexpr int kRowsPerPass = Tile::kRowsPerPass;
     extern __shared__ __align__(16) unsigned char lds[];
     float* const zs = reinterpret_cast<float*>(lds + kStages * kStageBytes);   // kZBufs x [kRows][BT][kZPitch]
-    unsigned char* const lows = reinterpret_cast<unsigned char*>(zs + kZBufs * kZFloats);   // kStages + 1 slots (ADD)
+    unsigned char* const lows = reinterpret_cast<unsigned char*>(zs + kZBufs * kZFloats);   // kStages + 1 slots (RT > 0)
 
     const int t = threadIdx.x;
     const int blk = xcd_logical_block(blockIdx.x, gridDim.x);
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             issue_stage<INSTS>(lp, INSTS, xbase + n0 * args.n_in,
                                shifted_limit(stage_limit(n0, row_end, args.n_in, EB), args.xshift),
                                lds + (s % kStages) * kStageBytes);
-            if constexpr (ADD) {
+            if constexpr (RT > 0) {
                 // the rows' parts of H, one after another, and their adapter; lanes past
                 // the last row read its end again, which nobody uses
                 const int lane = t - kFusedConsumers * 64;
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     // groups of 4 beta0, all kRows rows
     const int a_d0 = 16 * (wave & 3) + (lane >> 2);        // delta0 of this lane's block
     const int a_b0 = (wave >> 2) * kSetsPerWave * 4;       // first beta0 (within the tile) of the wave
-    Weights<kC0, ADD> k0r[kSetsPerWave];
+    Weights<kC0, (RT > 0)> k0r[kSetsPerWave];
 #pragma unroll
     for (int j = 0; j < kSetsPerWave; ++j)                  // K0[0][d0][beta][:]
         k0r[j].load(K0 + (int64_t(a_d0) * args.b0 + beta0 + a_b0 + 4 * j + q) * kC0);
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     // (A) Z[r][beta0][d0] = sum_g K0[0][d0][beta0][g] * X[r][g][d0] for stage s
     auto phase_a = [&](int s, float* zb) {
         const unsigned char* xs = lds + (s % kStages) * kStageBytes;
-        if constexpr (ADD) {
+        if constexpr (RT > 0) {
             static_assert(kRows == 4, "one row a lane of a block");
             const TX* xa = reinterpret_cast<const TX*>(xs + q * kRowBytes) + args.xshift + a_d0;
             short4v x[kC0 / 4];
@@ -329,14 +329,14 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     const int b1 = (t >> 1) & (kB1 - 1);
     const int a1 = (t >> 4) & (BT - 1);                // alpha1 within the tile
     const int e10 = run * 4;                           // first delta1 of the run
-    Weights<kC1, ADD> k1r[4];
+    Weights<kC1, (RT > 0)> k1r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)                              // K1[a][e][b][:]
         k1r[k].load(K1 + ((int64_t(beta0 + a1) * kD1 + e10 + k) * kB1 + b1) * kC1);
     const int64_t yoff = int64_t(beta0 + a1) * (kB1 * kD1) + b1 * kD1 + e10;
     // low[k][r]: the adapter's part of output k of the run in row r of the stage. The
     // adapter's B of these four outputs stays from stage to stage.
-    uint32_t bw[4][ADD ? 8 : 1];
+    uint32_t bw[4][RT > 0 ? 8 * RT : 1];
     int held = -1;
     auto adapter = [&](int s, floatx4 (&low)[4]) {
         const unsigned char* at = lows + (s % (kStages + 1)) * kLowBytes;
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             for (int k = 0; k < 4; ++k) {
                 const bf16_t* b = static_cast<const bf16_t*>(ad.B) + (int64_t(g) * args.n_out + yoff + k) * ad.rank;
 #pragma unroll
-                for (int w = 0; w < 8; w += 2) {
+                for (int w = 0; w < 8 * RT; w += 2) {
                     uint2 v = *reinterpret_cast<const uint2*>(b + min(2 * w, ad.rank - 4));
                     if (2 * w >= ad.rank) v = uint2{0u, 0u};
                     bw[k][w] = v.x;
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             }
         }
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {                   // two chunks of 4 ranks
+        for (int c = 0; c < 4 * RT; c += 2) {                   // two chunks of 4 ranks
             const uint4 v[3] = {h[3 * c / 2], h[3 * c / 2 + 1], h[3 * c / 2 + 2]};
             const short4v part[6] = {four_bf16(v[0].x, v[0].y), four_bf16(v[0].z, v[0].w), four_bf16(v[1].x, v[1].y),
                                      four_bf16(v[1].z, v[1].w), four_bf16(v[2].x, v[2].y), four_bf16(v[2].z, v[2].w)};
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     auto phase_b = [&](int s, const float* zb) {
         const int64_t n0 = row_begin + int64_t(s) * kRows;
         const int rows = static_cast<int>(min(int64_t(kRows), row_end - n0));
-        if constexpr (ADD) {
+        if constexpr (RT > 0) {
             // on top of the adapter's part, all rows of a gamma1 together: what
             // the other order holds at a time does not fit the registers
             floatx4 y[4];
@@ -390,6 +390,16 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
 #pragma unroll
                     for (int k = 0; k < 4; ++k) y[k][r] = fmaf(k1r[k].at(g), z[k], y[k][r]);
                 }
+            // With 32 ranks every row is finished here. Otherwise the compiler sinks
+            // the sums of rows 1 to 3 into the tests below and keeps all that they
+            // need in registers, which at 16 ranks has Z's reads under way early
+            // (16384 rows 77 us, 92 with this) and at 32 spills (4099 rows 64 us, 37).
+            if constexpr (RT > 1) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(y[k][r]));
+            }
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (r >= rows) break;
@@ -434,7 +444,7 @@ bool shape_ok(const Shape& s0, const Shape& s1) {
            s1.c == kC1 && s1.d == kD1;
 }
 
-template <typename TX, typename TW, int BT, bool ADD>
+template <typename TX, typename TW, int BT, int RT>
 ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const void* W1, const void* X,
                         float* Y, int64_t batch, const PairAdapters& ad, hipStream_t stream, int num_cus) {
     FusedArgs args;
@@ -446,7 +456,7 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
     args.n_tiles = s0.b / BT;
     args.xshift = static_cast<int>((reinterpret_cast<uintptr_t>(X) & 15u) / sizeof(TX));
     // about one resident wave of workgroups (as many per compute unit as fit its 160 KB of LDS)
-    const size_t lds = fused_lds_bytes(int(sizeof(TX)), BT, ADD);
+    const size_t lds = fused_lds_bytes(int(sizeof(TX)), BT, RT > 0);
     const int per_cu = std::max(1, std::min(4, int((160 * 1024) / lds)));
     const int64_t steps_total = (batch + kRows - 1) / kRows;
     const int64_t splits = std::max<int64_t>(1, int64_t(std::max(num_cus, 1)) * per_cu / args.n_tiles);
@@ -456,7 +466,7 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
     const int64_t blocks = nsplit * args.n_tiles;
     if (blocks > 0x7fffffff) return KS_ERR_UNSUPPORTED;
     const bool y_vec = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0;
-    auto kernel = y_vec ? fused_pair_kernel<TX, TW, true, BT, ADD> : fused_pair_kernel<TX, TW, false, BT, ADD>;
+    auto kernel = y_vec ? fused_pair_kernel<TX, TW, true, BT, RT> : fused_pair_kernel<TX, TW, false, BT, RT>;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFusedThreads), lds, stream,
                          static_cast<const TX*>(X), static_cast<const TW*>(W0), static_cast<const TW*>(W1), Y, args, ad);
 }
@@ -467,9 +477,9 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
 template <typename TX, typename TW>
 ks_status_t launch_typed(const Shape& s0, const Shape& s1, const void* W0, const void* W1, const void* X,
                          float* Y, int64_t batch, hipStream_t stream, int num_cus) {
-    if (s0.b % 32 == 0) return launch_tile<TX, TW, 32, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
-    if (s0.b % 16 == 0) return launch_tile<TX, TW, 16, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
-    return launch_tile<TX, TW, 8, false>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
+    if (s0.b % 32 == 0) return launch_tile<TX, TW, 32, 0>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
+    if (s0.b % 16 == 0) return launch_tile<TX, TW, 16, 0>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
+    return launch_tile<TX, TW, 8, 0>(s0, s1, W0, W1, X, Y, batch, {}, stream, num_cus);
 }
 
 }  // namespace
@@ -498,15 +508,16 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
 }
 
 bool fused_pair_adds(const Shape& s0, const Shape& s1, int xt, int wt, const void* B, int rank) {
-    return xt == kBF16 && wt == kBF16 && s0.b % 32 == 0 && fused_pair_supports(s0, s1, xt, wt, wt) && rank <= 16 &&
-           rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0;
+    return xt == kBF16 && wt == kBF16 && s0.b % 32 == 0 && fused_pair_supports(s0, s1, xt, wt, wt) &&
+           rank <= kLowPartsRank && rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0;
 }
 
 ks_status_t launch_fused_pair_adapters(const Shape& s0, const Shape& s1, const void* W0, const void* W1,
                                        const void* X, float* Y, int64_t batch, const PairAdapters& ad,
                                        hipStream_t stream, int num_cus) {
     if (!fused_pair_adds(s0, s1, kBF16, kBF16, ad.B, ad.rank)) return KS_ERR_UNSUPPORTED;
-    return launch_tile<bf16_t, bf16_t, 32, true>(s0, s1, W0, W1, X, Y, batch, ad, stream, num_cus);
+    return ad.rank <= 16 ? launch_tile<bf16_t, bf16_t, 32, 1>(s0, s1, W0, W1, X, Y, batch, ad, stream, num_cus)
+                         : launch_tile<bf16_t, bf16_t, 32, 2>(s0, s1, W0, W1, X, Y, batch, ad, stream, num_cus);
 }
 
 }  // namespace ks

@@ -94,10 +94,12 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
 
 // The same pair of bf16 operands with low-rank adapters added to its output,
 // Y[n] += H[n] B[g]^T with g = groups[n / kPairGroup] (< 0: nothing is added to these
-// rows). H: per row (kLowPartsBytes, 16-byte aligned), for every four of 16 ranks,
-// zeros past the adapters' own, three times four bf16 values whose sums are the fp32
-// values. B [count, n_out, rank]. fused_pair_adds: whether it runs them.
-constexpr int kPairGroup = 4, kLowPartsBytes = 96, kLowPartsRank = 16;
+// rows). H: per row (low_parts_bytes, 16-byte aligned), for every four ranks up to the
+// next multiple of 16, zeros past the adapters' own, three times four bf16 values
+// whose sums are the fp32 values. B [count, n_out, rank]. fused_pair_adds: whether it
+// runs them.
+constexpr int kPairGroup = 4, kLowPartsRank = 32;
+constexpr int low_parts_bytes(int rank) { return (rank + 15) / 16 * 96; }
 struct PairAdapters {
     const void* H;
     const int32_t* groups;

@@ -242,7 +242,7 @@ PAIR = [(1, 64, 16, 64), (64, 8, 8, 8)]
 @pytest.mark.parametrize("rank,xt,mix,batch", [
     (16, BF16, "runs", 1025), (8, BF16, "random", 1026), (4, BF16, "runs", 4099), (12, BF16, "random", 4098), (16, BF16, "runs", 5001), (16, F32, "random", 4097),
     (20, F32, "runs", 4110), (32, BF16, "random", 4097), (32, BF16, "runs", 4999), (16, BF16, "none", 4100),
-    (13, BF16, "runs", 4100), (48, BF16, "runs", 4100)])
+    (20, BF16, "runs", 1030), (28, BF16, "random", 1027), (13, BF16, "runs", 4100), (48, BF16, "runs", 4100)])
 def test_pair_adds_adapters(rank, xt, mix, batch):
     """Many rows through the fused pair of factors, which adds the adapters itself
     where it can: against 64 bits, rows of several adapters in a tile, NaN in the
