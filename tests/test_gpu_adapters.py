@@ -354,3 +354,62 @@ def test_batches_whose_output_passes_4_gib():
     back = formula(X[rows], A, B, scale, ids[rows], Y[rows])
     bmag = formula(X[rows].abs(), A.abs(), B.abs(), scale, ids[rows], Y[rows].abs())
     near(dX[rows], back["dX"], bmag["dX"], n_out + 8, "dX")
+
+
+def test_pair_on_another_stream_and_in_a_graph():
+    """The fused pair with adapters and its gradient: bits of the call on the default
+    stream, from another stream and from replays of a graph with eager work between."""
+    require_gpu()
+    batch = 1410
+    X, A, B, scale, ids = draw(batch, 1024, 4096, 5, 16, BF16, BF16, seed=3, mix="runs")
+    Ws = [(torch.randn(a, d, b, c) / c ** 0.5).to(BF16).to(DEV) for a, b, c, d in PAIR]
+    chain = libks.AdapterChain(Ws, PAIR, A, B, scale)
+    dY = torch.randn(batch, 4096, device=DEV)
+
+    def both():
+        Y, H = chain.matmul(X, ids, keep=True)
+        return (Y, H) + chain.backward(dY, X, H, ids)
+
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = both()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for k in range(4):
+        X.normal_()
+        dY.normal_()
+        ids.copy_(((torch.arange(batch, device=DEV) + 37 * k) // (50 + k)) % 6)
+        want = both()
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_pair_past_32_bit_offsets():
+    """The fused pair with adapters and its gradient where Y and dY pass 4 GiB."""
+    require_gpu()
+    batch = 270_003
+    g = torch.Generator(device=DEV).manual_seed(1)
+    X = torch.randn(batch, 1024, device=DEV, generator=g, dtype=BF16)
+    A = (torch.randn(3, 8, 1024, device=DEV, generator=g) / 32).to(BF16)
+    B = torch.randn(3, 4096, 8, device=DEV, generator=g).to(BF16)
+    Ws = [(torch.randn(a, d, b, c) / c ** 0.5).to(BF16).to(DEV) for a, b, c, d in PAIR]
+    scale = torch.ones(3, device=DEV)
+    ids = (torch.arange(batch, device=DEV) // 1001 % 4).to(torch.int32)
+    chain = libks.AdapterChain(Ws, PAIR, A, B, scale)
+    Y, H = chain.matmul(X, ids, keep=True)
+    dX = chain.backward(Y, X, H, ids, weights=False)[0]
+    # the same rows in a short batch of their own: the neighbours of a row do not matter
+    for n0 in (0, 131_064, 262_136, batch - 1203):
+        rows = slice(n0, n0 + 1203)
+        Ys, Hs = chain.matmul(X[rows].clone(), ids[rows].clone(), keep=True)
+        dXs = chain.backward(Y[rows].clone(), X[rows].clone(), Hs, ids[rows].clone(), weights=False)[0]
+        for whole, part in ((Y[rows], Ys), (H[rows], Hs), (dX[rows], dXs)):
+            assert float((whole.double() - part.double()).norm() / part.double().norm()) <= FP32_REL_TOL
