@@ -512,6 +512,7 @@ class AdapterChain:
         if A.dtype == torch.bfloat16:
             self._codes[torch.bfloat16] = DTYPE_BF16
         self._keep = (list(Ws), A, B, scale)
+        self._f32 = scale.new_empty          # an fp32 tensor beside the weights, without torch.empty's keywords
         self._n = len(self.patterns)
         self._p = _patterns(self.patterns)
         self._w = (ctypes.c_void_p * self._n)(*[w.data_ptr() for w in Ws])
@@ -533,7 +534,6 @@ class AdapterChain:
 
     def _workspace(self, name, batch, *args):
         """A workspace and its size; the size of a batch is asked for once."""
-        import torch
         key = (name, batch, *args)
         n = self._sizes.get(key)
         if n is None:
@@ -544,7 +544,7 @@ class AdapterChain:
             n = self._sizes[key] = size.value
         if n == 0:
             return None, 0, None
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        ws = self._f32((n + 3) // 4)
         return ws.data_ptr(), n, ws
 
     def _rows(self, X, ids):
@@ -568,10 +568,10 @@ class AdapterChain:
         import torch
         batch, code = self._rows(X, ids)
         if out is None:
-            out = torch.empty((batch, self.n_out), dtype=torch.float32, device=self.device)
+            out = self._f32(batch, self.n_out)
         else:
             _check_out(out, (batch, self.n_out), torch.float32, self.device, "out")
-        H = torch.empty((batch, self.rank), dtype=torch.float32, device=self.device) if keep else None
+        H = self._f32(batch, self.rank) if keep else None
         ws, size, _keep = self._workspace("ks_chain_adapter_workspace_size", batch, code)
         _raise(self._lib.ks_chain_adapter_matmul(
             self._p, self._n, self._w, self._ad, ids.data_ptr(), X.data_ptr(), out.data_ptr(), _ptr(H), batch, code,
@@ -586,11 +586,11 @@ class AdapterChain:
         batch, code = self._rows(X, ids)
         _check_out(dY, (batch, self.n_out), torch.float32, self.device, "dY")
         _check_out(H, (batch, self.rank), torch.float32, self.device, "H")
-        dX = torch.empty((batch, self.n_in), dtype=torch.float32, device=self.device)
+        dX = self._f32(batch, self.n_in)
         dA = dB = None
         if weights:
-            dA = torch.empty((self.count, self.rank, self.n_in), dtype=torch.float32, device=self.device)
-            dB = torch.empty((self.count, self.n_out, self.rank), dtype=torch.float32, device=self.device)
+            dA = self._f32(self.count, self.rank, self.n_in)
+            dB = self._f32(self.count, self.n_out, self.rank)
         wt = None
         if self._wt is not None and [w._version for w in self._keep[0]] == self._versions:
             wt = self._wt.data_ptr()
