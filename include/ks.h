@@ -415,11 +415,11 @@ ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, con
  * kept). Above 1024 rows, a chain that ends in a fused pair of a GPT-2-medium
  * MLP's kind, (1, b, 16, 64) then (b, 8, 8, 8) with b a multiple of 32, adds
  * bf16 adapters of a rank that is a multiple of 4 and at most 32 in that launch
- * wherever four rows, counted from the first, share one; the sums are then
- * taken in another order, so a row without an adapter has the chain's value up
- * to rounding. Y is fully overwritten; ad->n_in and ad->n_out have to be the
- * chain's (KS_ERR_CHAIN_MISMATCH). Workspace as for ks_chain_matmul, of the
- * size that ks_chain_adapter_workspace_size gives.
+ * to every four rows, counted from the first, that share one or change it once;
+ * the sums are then taken in another order, so a row without an adapter has the
+ * chain's value up to rounding. Y is fully overwritten; ad->n_in and ad->n_out
+ * have to be the chain's (KS_ERR_CHAIN_MISMATCH). Workspace as for
+ * ks_chain_matmul, of the size that ks_chain_adapter_workspace_size gives.
  */
 ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const ks_adapters_t* ad, int64_t batch,
                                             ks_dtype_t dt, size_t* bytes);

@@ -54,7 +54,7 @@ struct Args {
     int64_t batch;
     int n_in, n_out, rank, count;
     bf16_t* parts;           // H in three parts, chunks of 4 ranks (null: not wanted)
-    int32_t* groups;         // with parts: the adapter of each group of rows
+    PairGroup* groups;       // with parts: the adapters of each group of rows
     int64_t first;           // first workgroup of a launch among all of the batch's
 };
 
@@ -210,11 +210,20 @@ struct Tile {
         id = li < rows ? slot.adapter : -1;
         left = __ballot(id >= 0) & 0xffffu;
     }
-    // The adapter that the rows of this lane's group of kPairGroup share, or -1.
-    __device__ __forceinline__ int shared() const {
-        const int lane = threadIdx.x % 64, first = __shfl(id, lane & ~(kPairGroup - 1), 64);
-        const uint64_t same = __ballot(lane % 16 >= rows || id == first);
-        return (same >> (lane & ~(kPairGroup - 1)) & ((1u << kPairGroup) - 1)) == (1u << kPairGroup) - 1 ? first : -1;
+    // Whether the adapters of this lane's group of kPairGroup rows change at most
+    // once, and them (none if not).
+    __device__ __forceinline__ bool plain(PairGroup* g) const {
+        constexpr unsigned kAll = (1u << kPairGroup) - 1;
+        const int lane = threadIdx.x % 64, base = lane & ~(kPairGroup - 1);
+        const int last = max(min(kPairGroup, rows - base % 16) - 1, 0);
+        const int first = __shfl(id, base, 64), then = __shfl(id, base + last, 64);
+        const bool past = lane % 16 >= rows;
+        const unsigned as_first = __ballot(past || id == first) >> base & kAll;
+        const unsigned as_then = __ballot(past || id == then) >> base & kAll;
+        const int split = as_first == kAll ? kPairGroup : __builtin_ctz(~as_first);
+        const bool ok = as_then >> split == kAll >> split;
+        *g = PairGroup{ok ? first : -1, (ok ? split : kPairGroup) << 17 | (then + 1)};
+        return ok;
     }
     // The rows' adapters one after another.
     __device__ __forceinline__ int next() {
@@ -272,7 +281,8 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a, co
     const int quarter = (a.n_in + 4 * kStepK<TX> - 1) / (4 * kStepK<TX>) * kStepK<TX>;
     const int k0 = wave * quarter, k1 = min(a.n_in, k0 + quarter);
     if (a.parts) {
-        const int g = tile.shared();
+        PairGroup g;
+        tile.plain(&g);
         if (tid < rows && tid % kPairGroup == 0) a.groups[(block * kTile + tid) / kPairGroup] = g;
     }
     if (!o.order) {
@@ -377,8 +387,8 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// kRest: only rows whose group shares no adapter (a fused launch has added the
-// others'), kRestTiles tiles a workgroup: mostly there are few or none, and the
+// kRest: only rows of groups whose adapters change more than once (a fused launch
+// has added the others'), kRestTiles tiles a workgroup: mostly there are few or none, and the
 // launch costs its workgroups' starts. 16384 rows in runs of whole groups: 82 us
 // the whole chain with one tile each, 77 with 4, 75 with 16; 4099 rows in random
 // order: 104, 105, 138.
@@ -396,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
     const int o0 = static_cast<int>(group % slabs) * kUpCols + wave * 64;
     if (o0 >= a.n_out) return;
     const int64_t first = group / slabs * (kRest ? kRestTiles : 1);
-    uint64_t todo = 1;                                 // a bit a tile; with REST kTile / kPairGroup bits, a group each
+    uint64_t todo = 1;                                 // a bit a tile; with kRest kTile / kPairGroup bits, a group each
     constexpr int kBits = kRest ? kTile / kPairGroup : 1;
     if (kRest) {
         static_assert(kRestTiles * kTile <= 64 * kPairGroup, "a group a lane");
@@ -404,16 +414,14 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
         int id[kPairGroup];
 #pragma unroll
         for (int i = 0; i < kPairGroup; ++i) id[i] = a.ids[min(n + i, a.batch - 1)];
-        bool mixed = false, any = false;
         const int64_t end = min(a.batch, (first + kRestTiles) * kTile);
+        int changes = 0;
 #pragma unroll
         for (int i = 0; i < kPairGroup; ++i) {
-            if (n + i >= end) continue;
             if (id[i] < 0 || id[i] >= a.count) id[i] = -1;
-            any |= id[i] >= 0;
-            mixed |= id[i] != id[0];
+            if (i > 0 && n + i < end && id[i] != id[i - 1]) ++changes;
         }
-        todo = __ballot(mixed && any);
+        todo = __ballot(changes > 1);
     }
     while (todo) {
         const int at = __builtin_ctzll(todo) / kBits;
@@ -421,7 +429,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
         const int64_t block = first + at;
         Tile tile = o.order ? Tile(o.order, o.slots[block]) : Tile(a.ids, a.batch, a.count, block * kTile);
         if (kRest) {
-            if (tile.shared() >= 0) tile.id = -1;
+            PairGroup g;
+            if (tile.plain(&g)) tile.id = -1;
             tile.left = __ballot(tile.id >= 0) & 0xffffu;
         }
         if (!tile.left) continue;
@@ -600,7 +609,7 @@ ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float*
     return launch_types<float, float>(c, a, ws);
 }
 
-ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, int32_t* groups) {
+ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, PairGroup* groups) {
     const Args a{c.A, c.B, c.scale, c.ids, X, nullptr, H, c.batch, c.n_in, c.n_out, c.rank, c.count,
                  static_cast<bf16_t*>(parts), groups, 0};
     if (c.xt == kBF16) return launch_down<bf16_t, bf16_t>(a, {}, c.stream);

@@ -401,7 +401,7 @@ ks_status_t ks::chain_matmul(const ks_pattern_t* p, int n, const void* const* W,
                                            plan.wt, extra->pair.B, extra->pair.rank);
         if (extra->added) {
             st = ks::launch_adapter_down(extra->call, X, extra->H, const_cast<void*>(extra->pair.H),
-                                         const_cast<int32_t*>(extra->pair.groups));
+                                         const_cast<PairGroup*>(extra->pair.groups));
             if (st != KS_OK) return st;
         }
     }

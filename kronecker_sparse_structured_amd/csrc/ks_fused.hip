@@ -33,23 +33,22 @@
 //
 // Adapters. With bf16 operands the same launch can add the low-rank adapters of
 // the rows' requests, Y[n] += H[n] B[g]^T with g = ids[n], H from an earlier launch,
-// for stages whose four rows share an adapter: there Y is written once and never
-// read. H comes as three bf16 values whose sum is the fp32 value exactly, so its
+// for stages whose four rows share an adapter or pass once from one to another:
+// there Y is written once and never read. H comes as three bf16 values whose sum is the fp32 value exactly, so its
 // products with B are those of fp32; the loader streams the stage's rows of them
-// and the stage's adapter along with X. A thread of phase B keeps its four outputs'
+// and the stage's adapters along with X. A thread of phase B keeps its four outputs'
 // values of B in registers, and the products run on the 16-block 4x4x4 bf16 MFMA,
 // whose lanes are given their own outputs as the columns: each receives the stage's
 // four rows of its own output, which is where phase B has them. Phase A uses the
 // same instruction there, four gammas at a time (products of bf16 values are exact
 // in fp32): the kernel is bound by its two phases on the chip more than by HBM, and
-// that saves 17 us of 16384 rows. With it and rank 16 they take 75 us (63 for the
-// chain alone, 4.0 TB/s); with the adapters added by a pass over Y, 63 and 98.
+// that saves 17 us of 16384 rows. With H, 16384 rows take 78 us at rank 16 and 97 at
+// 32 (63 for the chain alone); with the adapters added by a pass over Y, 157 and 180.
 // Weights stay packed in registers: nine waves leave 168 a wave, and spilled ones
-// come back through the vector-memory counter behind the stores. Rank 32: 96 us for
-// 180.
-// Stages of several adapters are left to another launch: going through a stage's
-// adapters here, each loading its B, took 524 us on 16384 rows in random order of 8
-// adapters, the other launch 340.
+// come back through the vector-memory counter behind the stores.
+// Other stages are left to another launch: going through all of a stage's adapters
+// here, each loading its B, took 524 us on 16384 rows in random order of 8 adapters,
+// 368 now.
 //
 // Alignment. X and Y need only be aligned to their element size. When X
 // starts xshift elements past a 16-byte boundary, the loader streams the
@@ -167,11 +166,8 @@ __device__ __forceinline__ uint32_t shifted_limit(uint32_t limit, int xshift) {
 // kYVec: Y is 16-byte aligned (vector stores in phase B); BT: beta0 per tile;
 // RT: tiles of 16 ranks of adapters that are added (0: none).
 template <typename TX, typename TW, bool kYVec, int BT, int RT>
-__global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __restrict__ X,
-                                                                   const TW* __restrict__ K0,
-                                                                   const TW* __restrict__ K1,
-                                                                   float* __restrict__ Y, FusedArgs args,
-                                                                   PairAdapters ad) {
+__device__ __forceinline__ void fused_pair(const TX* __restrict__ X, const TW* __restrict__ K0, const TW* __restrict__ K1,
+                                           float* __restrict__ Y, const FusedArgs& args, const PairAdapters& ad) {
     static_assert(RT == 0 || (sizeof(TX) == 2 && sizeof(TW) == 2 && BT == 32), "adapters: bf16, a thread all rows of a stage");
     constexpr int EB = int(sizeof(TX));
     constexpr int VW = 16 / EB;
@@ -222,7 +218,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
                                shifted_limit(stage_limit(n0, row_end, args.n_in, EB), args.xshift),
                                lds + (s % kStages) * kStageBytes);
             if constexpr (RT > 0) {
-                // the rows' parts of H, one after another, and their adapter; lanes past
+                // the rows' parts of H, one after another, and their adapters; lanes past
                 // the last row read its end again, which nobody uses
                 const int lane = t - kFusedConsumers * 64;
                 unsigned char* low = lows + (s % (kStages + 1)) * kLowBytes;
@@ -231,8 +227,8 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
                     reinterpret_cast<const void*>(reinterpret_cast<const char*>(ad.H) + n0 * kLowRow +
                                                   min(lane * 16, bytes - 16)),
                     low, 16, 0, 0);
-                __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(ad.groups + n0 / kRows), low + 1024, 4, 0,
-                                                 0);
+                __builtin_amdgcn_global_load_lds(
+                    reinterpret_cast<const void*>(&ad.groups[n0 / kRows].first + min(lane, 1)), low + 1024, 4, 0, 0);
             }
         };
         for (int s = 0; s < kStages - 1 && s < nsteps; ++s) issue(s);
@@ -334,42 +330,61 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     for (int k = 0; k < 4; ++k)                              // K1[a][e][b][:]
         k1r[k].load(K1 + ((int64_t(beta0 + a1) * kD1 + e10 + k) * kB1 + b1) * kC1);
     const int64_t yoff = int64_t(beta0 + a1) * (kB1 * kD1) + b1 * kD1 + e10;
-    // low[k][r]: the adapter's part of output k of the run in row r of the stage. The
+    // low[k][r]: the adapters' part of output k of the run in row r of the stage. An
     // adapter's B of these four outputs stays from stage to stage.
     uint32_t bw[4][RT > 0 ? 8 * RT : 1];
     int held = -1;
-    auto adapter = [&](int s, floatx4 (&low)[4]) {
+    auto adapters = [&](int s, floatx4 (&low)[4]) {
         const unsigned char* at = lows + (s % (kStages + 1)) * kLowBytes;
         const uint4* h = reinterpret_cast<const uint4*>(at + q * kLowRow);   // of row q: [chunk of 4 ranks][part][4]
-        const int g = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int*>(at + 1024));
+        PairGroup rows;
+        rows.first = __builtin_amdgcn_readfirstlane(reinterpret_cast<const int*>(at + 1024)[0]);
+        rows.second = __builtin_amdgcn_readfirstlane(reinterpret_cast<const int*>(at + 1024)[1]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) low[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (g < 0) return;
-        if (g != held) {
-            held = g;
+        int g = rows.first, row = 0, end = rows.split();         // rows [row, end) are adapter g's
+        for (;;) {
+            if (g >= 0) {
+                if (g != held) {
+                    held = g;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bf16_t* b = static_cast<const bf16_t*>(ad.B) + (int64_t(g) * args.n_out + yoff + k) * ad.rank;
+                    for (int k = 0; k < 4; ++k) {
+                        const bf16_t* b = static_cast<const bf16_t*>(ad.B) + (int64_t(g) * args.n_out + yoff + k) * ad.rank;
 #pragma unroll
-                for (int w = 0; w < 8 * RT; w += 2) {
-                    uint2 v = *reinterpret_cast<const uint2*>(b + min(2 * w, ad.rank - 4));
-                    if (2 * w >= ad.rank) v = uint2{0u, 0u};
-                    bw[k][w] = v.x;
-                    bw[k][w + 1] = v.y;
+                        for (int w = 0; w < 8 * RT; w += 2) {
+                            uint2 v = *reinterpret_cast<const uint2*>(b + min(2 * w, ad.rank - 4));
+                            if (2 * w >= ad.rank) v = uint2{0u, 0u};
+                            bw[k][w] = v.x;
+                            bw[k][w + 1] = v.y;
+                        }
+                    }
                 }
+                floatx4 sum[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4 * RT; c += 2) {              // two chunks of 4 ranks
+                    const uint4 v[3] = {h[3 * c / 2], h[3 * c / 2 + 1], h[3 * c / 2 + 2]};
+                    const short4v part[6] = {four_bf16(v[0].x, v[0].y), four_bf16(v[0].z, v[0].w),
+                                             four_bf16(v[1].x, v[1].y), four_bf16(v[1].z, v[1].w),
+                                             four_bf16(v[2].x, v[2].y), four_bf16(v[2].z, v[2].w)};
+#pragma unroll
+                    for (int i = 0; i < 6; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            sum[k] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                                part[i], four_bf16(bw[k][2 * (c + i / 3)], bw[k][2 * (c + i / 3) + 1]), sum[k], 0, 0, 0);
+                }
+                // a row takes its own adapter's, nothing of the other's NaN
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) low[k][r] = r >= row && r < end ? sum[k][r] : low[k][r];
             }
-        }
-#pragma unroll
-        for (int c = 0; c < 4 * RT; c += 2) {                   // two chunks of 4 ranks
-            const uint4 v[3] = {h[3 * c / 2], h[3 * c / 2 + 1], h[3 * c / 2 + 2]};
-            const short4v part[6] = {four_bf16(v[0].x, v[0].y), four_bf16(v[0].z, v[0].w), four_bf16(v[1].x, v[1].y),
-                                     four_bf16(v[1].z, v[1].w), four_bf16(v[2].x, v[2].y), four_bf16(v[2].z, v[2].w)};
-#pragma unroll
-            for (int i = 0; i < 6; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    low[k] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
-                        part[i], four_bf16(bw[k][2 * (c + i / 3)], bw[k][2 * (c + i / 3) + 1]), low[k], 0, 0, 0);
+            if (end >= kRows) return;
+            g = rows.then();
+            row = end;
+            end = kRows;
         }
     };
     auto phase_b = [&](int s, const float* zb) {
@@ -379,7 +394,7 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
             // on top of the adapter's part, all rows of a gamma1 together: what
             // the other order holds at a time does not fit the registers
             floatx4 y[4];
-            adapter(s, y);
+            adapters(s, y);
 #pragma unroll
             for (int k = 0; k < 4; ++k) k1r[k].hold();
 #pragma unroll
@@ -390,16 +405,13 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
 #pragma unroll
                     for (int k = 0; k < 4; ++k) y[k][r] = fmaf(k1r[k].at(g), z[k], y[k][r]);
                 }
-            // With 32 ranks every row is finished here. Otherwise the compiler sinks
-            // the sums of rows 1 to 3 into the tests below and keeps all that they
-            // need in registers, which at 16 ranks has Z's reads under way early
-            // (16384 rows 77 us, 92 with this) and at 32 spills (4099 rows 64 us, 37).
-            if constexpr (RT > 1) {
+            // Every row is finished here: sunk into the tests below, as the compiler
+            // would have them, the sums of rows 1 to 3 keep all that they need in
+            // registers (rank 32: spilled, 64 us on 4099 rows for 38).
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+            for (int r = 0; r < kRows; ++r)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(y[k][r]));
-            }
+                for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(y[k][r]));
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (r >= rows) break;
@@ -439,6 +451,27 @@ __global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __r
     pipeline(phase_b);
 }
 
+template <typename TX, typename TW, bool kYVec, int BT>
+__global__ __launch_bounds__(kFusedThreads) void fused_pair_kernel(const TX* __restrict__ X,
+                                                                   const TW* __restrict__ K0,
+                                                                   const TW* __restrict__ K1,
+                                                                   float* __restrict__ Y, FusedArgs args) {
+    fused_pair<TX, TW, kYVec, BT, 0>(X, K0, K1, Y, args, PairAdapters{});
+}
+
+// LDS holds one workgroup a compute unit, three waves on a SIMD at most: registers
+// for more waves would only hold back reads of Z (16384 rows of rank 16: 92 us with
+// four in the compiler's mind, 78 with three).
+template <bool kYVec, int RT>
+__global__ __launch_bounds__(kFusedThreads)
+    __attribute__((amdgpu_waves_per_eu(3, 3))) void fused_pair_adapters_kernel(const bf16_t* __restrict__ X,
+                                                                               const bf16_t* __restrict__ K0,
+                                                                               const bf16_t* __restrict__ K1,
+                                                                               float* __restrict__ Y, FusedArgs args,
+                                                                               PairAdapters ad) {
+    fused_pair<bf16_t, bf16_t, kYVec, 32, RT>(X, K0, K1, Y, args, ad);
+}
+
 bool shape_ok(const Shape& s0, const Shape& s1) {
     return s0.a == 1 && s0.c == kC0 && s0.d == kD0 && s0.b % 8 == 0 && s1.a == s0.b && s1.b == kB1 &&
            s1.c == kC1 && s1.d == kD1;
@@ -466,9 +499,16 @@ ks_status_t launch_tile(const Shape& s0, const Shape& s1, const void* W0, const 
     const int64_t blocks = nsplit * args.n_tiles;
     if (blocks > 0x7fffffff) return KS_ERR_UNSUPPORTED;
     const bool y_vec = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0;
-    auto kernel = y_vec ? fused_pair_kernel<TX, TW, true, BT, RT> : fused_pair_kernel<TX, TW, false, BT, RT>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFusedThreads), lds, stream,
-                         static_cast<const TX*>(X), static_cast<const TW*>(W0), static_cast<const TW*>(W1), Y, args, ad);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kFusedThreads);
+    const TX* x = static_cast<const TX*>(X);
+    const TW *w0 = static_cast<const TW*>(W0), *w1 = static_cast<const TW*>(W1);
+    if constexpr (RT > 0) {
+        return launch_kernel(y_vec ? fused_pair_adapters_kernel<true, RT> : fused_pair_adapters_kernel<false, RT>, grid,
+                             block, lds, stream, x, w0, w1, Y, args, ad);
+    } else {
+        return launch_kernel(y_vec ? fused_pair_kernel<TX, TW, true, BT> : fused_pair_kernel<TX, TW, false, BT>, grid,
+                             block, lds, stream, x, w0, w1, Y, args);
+    }
 }
 
 // The widest tile that divides b0: 32 beta0 per workgroup on GPT-2-medium's

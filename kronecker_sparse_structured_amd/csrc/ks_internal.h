@@ -93,16 +93,21 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
                               int64_t batch, hipStream_t stream, int num_cus);
 
 // The same pair of bf16 operands with low-rank adapters added to its output,
-// Y[n] += H[n] B[g]^T with g = groups[n / kPairGroup] (< 0: nothing is added to these
-// rows). H: per row (low_parts_bytes, 16-byte aligned), for every four ranks up to the
-// next multiple of 16, zeros past the adapters' own, three times four bf16 values
-// whose sums are the fp32 values. B [count, n_out, rank]. fused_pair_adds: whether it
-// runs them.
+// Y[n] += H[n] B[g]^T, rows by groups of kPairGroup: the first split() rows of a group
+// are adapter `first`'s, the others then()'s (< 0: nothing is added). H: per row
+// (low_parts_bytes, 16-byte aligned), for every four ranks up to the next multiple of
+// 16, zeros past the adapters' own, three times four bf16 values whose sums are the
+// fp32 values. B [count, n_out, rank]. fused_pair_adds: whether it runs them.
 constexpr int kPairGroup = 4, kLowPartsRank = 32;
 constexpr int low_parts_bytes(int rank) { return (rank + 15) / 16 * 96; }
+struct PairGroup {
+    int32_t first, second;               // second: split << 17 | (then + 1)
+    constexpr int split() const { return second >> 17; }
+    constexpr int then() const { return (second & 0x1ffff) - 1; }
+};
 struct PairAdapters {
     const void* H;
-    const int32_t* groups;
+    const PairGroup* groups;
     const void* B;
     int rank;
 };

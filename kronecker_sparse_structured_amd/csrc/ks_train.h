@@ -51,9 +51,9 @@ size_t adapter_workspace(int64_t batch, int count);
 ks_status_t launch_adapter(const AdapterCall& c, const void* X, float* H, float* Y, void* ws);
 
 // The first product alone, over rows as they lie: H, its values in parts as the
-// fused pair takes them, and the adapter of each kPairGroup rows (-1 unless they
-// share one); then the second product for the other groups' rows.
-ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, int32_t* groups);
+// fused pair takes them, and the adapters of each kPairGroup rows (none where they
+// change more than once); then the second product for those groups' rows.
+ks_status_t launch_adapter_down(const AdapterCall& c, const void* X, float* H, void* parts, PairGroup* groups);
 ks_status_t launch_adapter_rest(const AdapterCall& c, const float* H, float* Y);
 
 // Adapters beside a chain: chain_matmul (ks_chain_matmul with the dtype as an int)

@@ -153,10 +153,10 @@ ks_status_t check_backward(const ks_adapters_t* ad, const int32_t* ids, const fl
 // Whether a chain's last launch may add the adapters, and the bytes of H in parts.
 // It is for rows whose requests lie together, as those of prompts and of training
 // do (1024 -> 4096, rank 16, chain and adapters, against the sorted rows or the
-// rows as they lie: 1024 rows 18 us for 33, 2048 rows 22 for 40, 4096 rows 29 for
-// 58, 16384 rows 76 for 157; rank 32: 16384 rows 96 for 180). Up to this many rows the batch may as well be the next
+// rows as they lie: 1024 rows 18 us for 33, 2048 rows 22 for 40, 4096 rows 30 for
+// 58, 16384 rows 78 for 157; rank 32: 16384 rows 97 for 180). Up to this many rows the batch may as well be the next
 // tokens of as many requests in any order, which the other launch has to take (1024
-// rows 59 us for 37 sorted, 4096 rows 107 for 61).
+// rows 66 us for 36 sorted, 4096 rows 117 for 61).
 constexpr int64_t kLooseRows = 1024;
 bool takes_parts(int rank, int64_t batch) { return batch > kLooseRows && rank <= ks::kLowPartsRank; }
 uint64_t parts_bytes(int rank, int64_t batch) {
@@ -394,7 +394,7 @@ ks_status_t ks_chain_adapter_workspace_size(const ks_pattern_t* p, int n, const 
     // that adds the adapters reads
     *bytes = round256(need) + round256(ks::adapter_workspace(batch, ad->count)) +
              (ks::adapter_path(batch) == ks::kAdapterRows ? 0 : round256(static_cast<uint64_t>(batch) * ad->rank * 4)) +
-             (takes_parts(ad->rank, batch) ? parts_bytes(ad->rank, batch) + round256(static_cast<uint64_t>(batch) + 4) : 0);
+             (takes_parts(ad->rank, batch) ? parts_bytes(ad->rank, batch) + round256((static_cast<uint64_t>(batch) + 3) / 4 * 8) : 0);
     return KS_OK;
 }
 
@@ -425,7 +425,7 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
     char* parts = low + round256(static_cast<uint64_t>(batch) * ad->rank * 4);
     ks::ChainAdapters extra;
     extra.call = adapter_call(ad, ids, xt, wt, batch, stream, 0);
-    extra.pair = {parts, reinterpret_cast<int32_t*>(parts + parts_bytes(ad->rank, batch)), ad->B, ad->rank};
+    extra.pair = {parts, reinterpret_cast<ks::PairGroup*>(parts + parts_bytes(ad->rank, batch)), ad->B, ad->rank};
     extra.H = H;
     extra.added = false;
     // the chain's own checks (weights, alignment, overlaps) come first: an
