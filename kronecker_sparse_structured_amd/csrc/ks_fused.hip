@@ -34,9 +34,9 @@
 // Adapters. With bf16 operands the same launch can add the low-rank adapters of
 // the rows' requests, Y[n] += H[n] B[g]^T with g = ids[n], H from an earlier launch,
 // for stages whose four rows share an adapter or pass once from one to another:
-// there Y is written once and never read. H comes as three bf16 values whose sum is the fp32 value exactly, so its
-// products with B are those of fp32; the loader streams the stage's rows of them
-// and the stage's adapters along with X. A thread of phase B keeps its four outputs'
+// there Y is written once and never read. H comes as three bf16 values whose sum
+// is the fp32 value exactly, so its products with B are those of fp32; the loader
+// streams the stage's rows of them and the stage's adapters along with X. A thread of phase B keeps its four outputs'
 // values of B in registers, and the products run on the 16-block 4x4x4 bf16 MFMA,
 // whose lanes are given their own outputs as the columns: each receives the stage's
 // four rows of its own output, which is where phase B has them. Phase A uses the
