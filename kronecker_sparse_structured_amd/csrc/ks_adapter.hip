@@ -22,6 +22,9 @@
 //     fp32 one.
 //   adapter_up_kernel, Y += H B^T: fp32 matrix instructions on B widened to
 //     fp32, so that H is never rounded to fewer bits.
+// Beside a chain whose last launch adds the adapters itself (ks_fused.hip), the down
+// kernel gives H in the parts that it reads, and the up kernel takes the rows it
+// leaves.
 // The operands go from global memory straight to registers: A and B are read
 // by many workgroups and come from L2, X and Y are used once.
 
