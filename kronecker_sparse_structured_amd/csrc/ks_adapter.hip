@@ -108,9 +108,9 @@ template <typename TX, typename TW, bool WIDE>
 __global__ __launch_bounds__(kThreads) void adapter_rows_kernel(const Args a, int slice) {
     __shared__ float h[KS_ADAPTER_MAX_RANK];
     const int64_t n = blockIdx.x;
-    const int g = a.ids[n];
+    const int g = adapter_of(a.ids[n], a.count);
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    if (g < 0 || g >= a.count) {
+    if (g < 0) {
         if (a.H && blockIdx.y == 0)
             for (int r = tid; r < a.rank; r += kThreads) a.H[n * a.rank + r] = 0.0f;
         return;
@@ -202,8 +202,7 @@ struct Tile {
         const int li = threadIdx.x % 16;
         rows = static_cast<int>(batch - row0 < kTile ? batch - row0 : kTile);
         row = row0 + min(li, rows - 1);
-        id = li < rows ? ids[row] : -1;
-        if (id >= count) id = -1;
+        id = li < rows ? adapter_of(ids[row], count) : -1;
         left = __ballot(id >= 0) & 0xffffu;
     }
     __device__ __forceinline__ Tile(const int* order, const AdapterSlot& slot) {
@@ -225,7 +224,7 @@ struct Tile {
         const unsigned as_then = __ballot(past || id == then) >> base & kAll;
         const int split = as_first == kAll ? kPairGroup : __builtin_ctz(~as_first);
         const bool ok = as_then >> split == kAll >> split;
-        *g = PairGroup{ok ? first : -1, (ok ? split : kPairGroup) << 17 | (then + 1)};
+        *g = PairGroup::of(ok ? first : -1, ok ? split : kPairGroup, then);
         return ok;
     }
     // The rows' adapters one after another.
@@ -267,8 +266,8 @@ __global__ __launch_bounds__(kThreads) void adapter_down_kernel(const Args a, co
     if (o.order && block >= o.n_slots) {
         // a row a thread; a wave clears the rows it has found
         const int64_t row0 = (block - o.n_slots) * kThreads + wave * 64, i = row0 + lane;
-        const int id = i < a.batch ? a.ids[i] : 0;
-        for (uint64_t off = __ballot(id < 0 || id >= a.count); off; off &= off - 1)
+        const bool none = i < a.batch && adapter_of(a.ids[i], a.count) < 0;
+        for (uint64_t off = __ballot(none); off; off &= off - 1)
             for (int r = lane; r < a.rank; r += 64) a.H[(row0 + __builtin_ctzll(off)) * a.rank + r] = 0.0f;
         return;
     }
@@ -416,14 +415,12 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
         const int64_t n = first * kTile + lane * kPairGroup;
         int id[kPairGroup];
 #pragma unroll
-        for (int i = 0; i < kPairGroup; ++i) id[i] = a.ids[min(n + i, a.batch - 1)];
+        for (int i = 0; i < kPairGroup; ++i) id[i] = adapter_of(a.ids[min(n + i, a.batch - 1)], a.count);
         const int64_t end = min(a.batch, (first + kRestTiles) * kTile);
         int changes = 0;
 #pragma unroll
-        for (int i = 0; i < kPairGroup; ++i) {
-            if (id[i] < 0 || id[i] >= a.count) id[i] = -1;
-            if (i > 0 && n + i < end && id[i] != id[i - 1]) ++changes;
-        }
+        for (int i = 1; i < kPairGroup; ++i)
+            if (n + i < end && id[i] != id[i - 1]) ++changes;
         todo = __ballot(changes > 1);
     }
     while (todo) {

@@ -505,8 +505,8 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const float* dY, 
     __shared__ float part2[16 * KS_ADAPTER_MAX_RANK];
     __shared__ float e[KS_ADAPTER_MAX_RANK];
     const int64_t n = blockIdx.x;
-    const int g = ids[n], tid = threadIdx.x;
-    if (g < 0 || g >= count) return;                   // nothing reads its E
+    const int g = adapter_of(ids[n], count), tid = threadIdx.x;
+    if (g < 0) return;                                 // nothing reads its E
     const TW* a = A + static_cast<int64_t>(g) * rank * n_in;
     const TW* b = B + static_cast<int64_t>(g) * n_out * rank;
     const float* dy = dY + n * n_out;

@@ -100,8 +100,14 @@ ks_status_t launch_fused_pair(const Shape& s0, const Shape& s1, int xt, int wt0,
 // fp32 values. B [count, n_out, rank]. fused_pair_adds: whether it runs them.
 constexpr int kPairGroup = 4, kLowPartsRank = 32;
 constexpr int low_parts_bytes(int rank) { return (rank + 15) / 16 * 96; }
+// The adapter of a row with this id: any id outside [0, count) means none, -1. Kernels
+// that pack ids or compare those of neighbouring rows take them through here: -2 beside
+// -1 is no change of adapter, and would not fit the packed word.
+constexpr int adapter_of(int id, int count) { return id >= 0 && id < count ? id : -1; }
 struct PairGroup {
     int32_t first, second;               // second: split << 17 | (then + 1)
+    // first, then: from adapter_of
+    static constexpr PairGroup of(int first, int split, int then) { return {first, split << 17 | (then + 1)}; }
     constexpr int split() const { return second >> 17; }
     constexpr int then() const { return (second & 0x1ffff) - 1; }
 };
