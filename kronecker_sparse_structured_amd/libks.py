@@ -10,7 +10,10 @@ HIP kernels of libks.so; there is no fallback. If the library is not built,
 loading fails loudly.
 
 ``matmul`` and ``chain_matmul`` are conveniences over the same calls that
-allocate the output (and the chain workspace) with torch.
+allocate the output (and the chain workspace) with torch. They, the adapters,
+the preference loss and the optimizer count what they write into a caller's
+tensor as an in-place change (torch's version counter), so that autograd sees
+it; the ``ks_`` calls write through addresses and do not.
 """
 from __future__ import annotations
 
@@ -393,6 +396,14 @@ def _check_tensor(t, name):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _wrote(tensors):
+    """Counts a write through their addresses as an in-place change of these
+    tensors (one, or several), as an operation of torch's own would. Without it
+    autograd would take a changed tensor for the one it saved."""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
+
+
 def matmul(X, W, pattern, out=None, kernel="auto", stream=None):
     """Y = X W^T for one KS factor; X is (batch, a*c*d), W is (a, d, b, c)."""
     import torch
@@ -404,9 +415,12 @@ def matmul(X, W, pattern, out=None, kernel="auto", stream=None):
     if W.numel() != a * b * c * d:
         raise ValueError("W must hold a*b*c*d = %d values" % (a * b * c * d))
     batch = X.shape[0]
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((batch, a * b * d), dtype=torch.float32, device=X.device)
     ks_matmul_ex((a, b, c, d), W, X, out, batch, dtype_code(X.dtype, W.dtype), stream, kernel=kernel)
+    if given:
+        _wrote(out)
     return out
 
 
@@ -419,13 +433,16 @@ def chain_matmul(X, Ws, patterns, out=None, fuse=True, stream=None):
     dt = dtype_code(X.dtype, Ws[0].dtype)
     batch = X.shape[0]
     last = patterns[-1]
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((batch, int(last[0]) * int(last[1]) * int(last[3])),
                           dtype=torch.float32, device=X.device)
     flags = CHAIN_AUTO if fuse else CHAIN_NO_FUSE
     nbytes = ks_chain_workspace_size(patterns, batch, dt, flags)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device) if nbytes else None
     ks_chain_matmul(patterns, Ws, X, out, batch, dt, ws, nbytes, flags, stream)
+    if given:
+        _wrote(out)
     return out
 
 
@@ -439,11 +456,14 @@ def matmul_dx(dY, W, pattern, out=None, stream=None):
         raise ValueError("dY must be (batch, a*b*d) = (*, %d)" % (a * b * d))
     batch = dY.shape[0]
     dt = dtype_code(dY.dtype, W.dtype)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((batch, a * c * d), dtype=torch.float32, device=dY.device)
     nbytes = ks_matmul_dx_workspace_size((a, b, c, d), dt)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dY.device)
     ks_matmul_dx((a, b, c, d), W, dY, out, batch, dt, ws, nbytes, stream)
+    if given:
+        _wrote(out)
     return out
 
 
@@ -459,11 +479,14 @@ def matmul_dw(dY, X, pattern, out=None, stream=None):
         raise ValueError("X must be (batch, a*c*d) and dY (batch, a*b*d)")
     batch = X.shape[0]
     dt = DTYPE_BF16 if X.dtype == torch.bfloat16 else DTYPE_F32
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((a, d, b, c), dtype=torch.float32, device=X.device)
     nbytes = ks_matmul_dw_workspace_size((a, b, c, d), batch, dt)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device) if nbytes else None
     ks_matmul_dw((a, b, c, d), dY, X, out, batch, dt, ws, nbytes, stream)
+    if given:
+        _wrote(out)
     return out
 
 
@@ -478,7 +501,9 @@ class AdapterChain:
     marshals its rows; later in-place changes of them are seen. With `transposed`
     it also keeps W's blocks transposed, for the backward() calls of a training
     loop: made here once, where each call makes its own otherwise, and left unused
-    after an in-place operation on a W. W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
+    after an in-place operation on a W that torch counts, this module's optimizer
+    among them. Changes that torch does not count (through W.data, by a replayed
+    graph, by code that writes through W's address) need a new handle. W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
     n_out, rank); scale (G,) fp32; W, A and B have one type, fp32 or bf16; X has
     that type, or is fp32."""
 
@@ -567,7 +592,8 @@ class AdapterChain:
         for backward()."""
         import torch
         batch, code = self._rows(X, ids)
-        if out is None:
+        given = out is not None
+        if not given:
             out = self._f32(batch, self.n_out)
         else:
             _check_out(out, (batch, self.n_out), torch.float32, self.device, "out")
@@ -576,6 +602,8 @@ class AdapterChain:
         _raise(self._lib.ks_chain_adapter_matmul(
             self._p, self._n, self._w, self._ad, ids.data_ptr(), X.data_ptr(), out.data_ptr(), _ptr(H), batch, code,
             ws, size, _raw_stream(stream, self._index)), "ks_chain_adapter_matmul", True)
+        if given:
+            _wrote(out)
         return (out, H) if keep else out
 
     def backward(self, dY, X, H, ids, weights=True, stream=None):
@@ -640,6 +668,7 @@ def adapter_matmul(X, A, B, scale, ids, out, keep=False, stream=None):
     _raise(load().ks_adapter_matmul(ad, _ptr(ids), _ptr(X), _ptr(out), _ptr(H), X.shape[0],
                                     dtype_code(X.dtype, A.dtype), _ptr(ws), size.value, _stream(stream, X)),
            "ks_adapter_matmul", True)
+    _wrote(out)
     return (out, H) if keep else out
 
 
@@ -665,6 +694,8 @@ def adapter_backward(dY, X, H, A, B, scale, ids, dX=None, stream=None):
     _raise(load().ks_adapter_backward(ad, _ptr(ids), _ptr(dY), _ptr(X), _ptr(H), _ptr(dX), _ptr(dA), _ptr(dB),
                                       X.shape[0], dtype_code(X.dtype, A.dtype), _ptr(ws), size.value,
                                       _stream(stream, X)), "ks_adapter_backward", True)
+    if dX is not None:
+        _wrote(dX)
     return dA, dB
 
 
@@ -760,9 +791,12 @@ def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, 
     ones, ref (2P, T) fp32 the reference model's token log probabilities.
     dlogits may be given (the logits themselves too: then it replaces them)."""
     import torch
-    if dlogits is None:
+    given = dlogits is not None
+    if not given:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     loss, rewards, tokens, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
+    if given:
+        _wrote(dlogits)
     return loss, rewards, tokens, dlogits
 
 
@@ -829,19 +863,35 @@ class AdamW:
         if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
             raise ValueError("parameters and moments must not share memory")
         self._keep = (list(params), list(grads), list(ms), list(vs), list(scales or ()))
+        self._written = self._counters(params, ms, vs, scales or ())
         self._lib = load()
         size = ctypes.c_size_t(0)
         _raise(self._lib.ks_grad_norm_workspace_size(self._t, n, size), "ks_grad_norm_workspace_size", True)
         self._ws_bytes = size.value
 
+    @staticmethod
+    def _counters(*sets):
+        """Tensors that hold the version counters of all of these: views of one
+        buffer share its counter."""
+        out = []
+        for ts in sets:
+            if ts and ts[0]._base is not None:
+                bases = [t if t._base is None else t._base for t in ts]
+                ts = {id(t): t for t in bases}.values()
+            out += ts
+        return out
+
     def grad_norm(self, out=None, stream=None):
         """The 2-norm over all gradients, a device scalar."""
         import torch
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.empty((), dtype=torch.float32, device=self.device)
         ws = torch.empty(max(self._ws_bytes, 1), dtype=torch.uint8, device=self.device)
         _raise(self._lib.ks_grad_norm(self._t, self._n, out.data_ptr(), ws.data_ptr(), self._ws_bytes,
                                       _raw_stream(stream, self.device.index)), "ks_grad_norm", True)
+        if given:
+            _wrote(out)
         return out
 
     def step(self, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None, norm=None, seed=0,
@@ -860,6 +910,7 @@ class AdamW:
                                float(max_norm or 0.0), int(step), int(seed) & 0xFFFFFFFF, self.bits)
         _raise(self._lib.ks_adamw_step(self._t, self._n, o, _ptr(norm) if max_norm is not None else None,
                                        _raw_stream(stream, self.device.index)), "ks_adamw_step", True)
+        _wrote(self._written)
         return norm
 
     def state_values(self, ms_out, vs_out, stream=None):
@@ -880,3 +931,4 @@ class AdamW:
             ptrs.append((ctypes.c_void_p * self._n).from_buffer(array.array("Q", map(T.data_ptr, outs))))
         _raise(self._lib.ks_adamw_state_values(self._t, self._n, *ptrs, _raw_stream(stream, index)),
                "ks_adamw_state_values", True)
+        _wrote([*ms_out, *vs_out])
