@@ -176,7 +176,7 @@ def make_preference_function():
 
         @staticmethod
         def forward(ctx, logits, labels, ref, beta, smoothing):
-            loss, rewards, tokens, scratch = libks._preference_forward(logits, labels, ref, beta, smoothing, None, None)
+            loss, rewards, tokens, scratch = libks._preference_forward(logits, labels, ref, beta, smoothing)
             ctx.save_for_backward(logits, labels, scratch)
             ctx.mark_non_differentiable(rewards, tokens)
             return loss, rewards, tokens

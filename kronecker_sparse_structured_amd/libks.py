@@ -13,7 +13,9 @@ loading fails loudly.
 allocate the output (and the chain workspace) with torch. They, the adapters,
 the preference loss and the optimizer count what they write into a caller's
 tensor as an in-place change (torch's version counter), so that autograd sees
-it; the ``ks_`` calls write through addresses and do not.
+it; the ``ks_`` calls write through addresses and do not. Their ``stream``
+(default: torch's current one) is the one that the call launches on and
+allocates for.
 """
 from __future__ import annotations
 
@@ -225,14 +227,32 @@ def _stream(stream, *tensors) -> Optional[int]:
     return int(stream.cuda_stream)
 
 
-def _raw_stream(stream, index: int):
-    """_stream for a device index (no stream object where torch has the handle
-    at hand)."""
-    if stream is None:
-        import torch
-        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return get(index) if get is not None else int(torch.cuda.current_stream(index).cuda_stream)
-    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+def _raw_stream(index: int):
+    """Torch's current stream of a device index (no stream object where torch has
+    the handle at hand)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else int(torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_stream(stream, device, call, *args):
+    """call(*args) with `stream` (a stream object or its address) as torch's
+    current one. What the call allocates then comes from that stream's memory:
+    a workspace that it drops goes to nobody else before its kernels are done.
+    Results are held for the caller's current stream as well, which may read
+    them once it has waited for `stream`. Tensors that the caller gives are the
+    caller's to keep until then."""
+    import torch
+    raw = stream if isinstance(stream, int) else int(stream.cuda_stream)
+    here = torch.cuda.current_stream(device)
+    if raw == here.cuda_stream:
+        return call(*args)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=device)):
+        out = call(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(here)
+    return out
 
 
 def _raise(status: int, where: str, check: bool) -> int:
@@ -414,11 +434,13 @@ def matmul(X, W, pattern, out=None, kernel="auto", stream=None):
         raise ValueError("X must be (batch, a*c*d) = (*, %d)" % (a * c * d))
     if W.numel() != a * b * c * d:
         raise ValueError("W must hold a*b*c*d = %d values" % (a * b * c * d))
+    if stream is not None:
+        return _on_stream(stream, X.device, matmul, X, W, pattern, out, kernel)
     batch = X.shape[0]
     given = out is not None
     if not given:
         out = torch.empty((batch, a * b * d), dtype=torch.float32, device=X.device)
-    ks_matmul_ex((a, b, c, d), W, X, out, batch, dtype_code(X.dtype, W.dtype), stream, kernel=kernel)
+    ks_matmul_ex((a, b, c, d), W, X, out, batch, dtype_code(X.dtype, W.dtype), kernel=kernel)
     if given:
         _wrote(out)
     return out
@@ -430,6 +452,8 @@ def chain_matmul(X, Ws, patterns, out=None, fuse=True, stream=None):
     _check_tensor(X, "X")
     for i, w in enumerate(Ws):
         _check_tensor(w, "W[%d]" % i)
+    if stream is not None:
+        return _on_stream(stream, X.device, chain_matmul, X, Ws, patterns, out, fuse)
     dt = dtype_code(X.dtype, Ws[0].dtype)
     batch = X.shape[0]
     last = patterns[-1]
@@ -440,7 +464,7 @@ def chain_matmul(X, Ws, patterns, out=None, fuse=True, stream=None):
     flags = CHAIN_AUTO if fuse else CHAIN_NO_FUSE
     nbytes = ks_chain_workspace_size(patterns, batch, dt, flags)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device) if nbytes else None
-    ks_chain_matmul(patterns, Ws, X, out, batch, dt, ws, nbytes, flags, stream)
+    ks_chain_matmul(patterns, Ws, X, out, batch, dt, ws, nbytes, flags)
     if given:
         _wrote(out)
     return out
@@ -454,6 +478,8 @@ def matmul_dx(dY, W, pattern, out=None, stream=None):
     _check_tensor(W, "W")
     if dY.dim() != 2 or dY.shape[1] != a * b * d:
         raise ValueError("dY must be (batch, a*b*d) = (*, %d)" % (a * b * d))
+    if stream is not None:
+        return _on_stream(stream, dY.device, matmul_dx, dY, W, pattern, out)
     batch = dY.shape[0]
     dt = dtype_code(dY.dtype, W.dtype)
     given = out is not None
@@ -461,7 +487,7 @@ def matmul_dx(dY, W, pattern, out=None, stream=None):
         out = torch.empty((batch, a * c * d), dtype=torch.float32, device=dY.device)
     nbytes = ks_matmul_dx_workspace_size((a, b, c, d), dt)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dY.device)
-    ks_matmul_dx((a, b, c, d), W, dY, out, batch, dt, ws, nbytes, stream)
+    ks_matmul_dx((a, b, c, d), W, dY, out, batch, dt, ws, nbytes)
     if given:
         _wrote(out)
     return out
@@ -477,6 +503,8 @@ def matmul_dw(dY, X, pattern, out=None, stream=None):
         raise TypeError("dY must be fp32")
     if X.dim() != 2 or X.shape[1] != a * c * d or dY.shape != (X.shape[0], a * b * d):
         raise ValueError("X must be (batch, a*c*d) and dY (batch, a*b*d)")
+    if stream is not None:
+        return _on_stream(stream, dY.device, matmul_dw, dY, X, pattern, out)
     batch = X.shape[0]
     dt = DTYPE_BF16 if X.dtype == torch.bfloat16 else DTYPE_F32
     given = out is not None
@@ -484,7 +512,7 @@ def matmul_dw(dY, X, pattern, out=None, stream=None):
         out = torch.empty((a, d, b, c), dtype=torch.float32, device=X.device)
     nbytes = ks_matmul_dw_workspace_size((a, b, c, d), batch, dt)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=X.device) if nbytes else None
-    ks_matmul_dw((a, b, c, d), dY, X, out, batch, dt, ws, nbytes, stream)
+    ks_matmul_dw((a, b, c, d), dY, X, out, batch, dt, ws, nbytes)
     if given:
         _wrote(out)
     return out
@@ -553,9 +581,10 @@ class AdapterChain:
             self._wt = torch.empty(size.value, dtype=torch.uint8, device=self.device)
             self._versions = [w._version for w in Ws]
             _raise(self._lib.ks_chain_transpose(self._p, self._n, self._w, self._wt.data_ptr(), code,
-                                                _raw_stream(None, self._index)), "ks_chain_transpose", True)
+                                                _raw_stream(self._index)), "ks_chain_transpose", True)
             # calls may come on any stream
             torch.cuda.current_stream(self._index).synchronize()
+            self._wt_stream = _raw_stream(self._index)
 
     def _workspace(self, name, batch, *args):
         """A workspace and its size; the size of a batch is asked for once."""
@@ -591,6 +620,8 @@ class AdapterChain:
         """Y (batch, n_out) fp32; with keep=True (Y, H), H (batch, rank) fp32
         for backward()."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.device, self.matmul, X, ids, out, keep)
         batch, code = self._rows(X, ids)
         given = out is not None
         if not given:
@@ -601,7 +632,7 @@ class AdapterChain:
         ws, size, _keep = self._workspace("ks_chain_adapter_workspace_size", batch, code)
         _raise(self._lib.ks_chain_adapter_matmul(
             self._p, self._n, self._w, self._ad, ids.data_ptr(), X.data_ptr(), out.data_ptr(), _ptr(H), batch, code,
-            ws, size, _raw_stream(stream, self._index)), "ks_chain_adapter_matmul", True)
+            ws, size, _raw_stream(self._index)), "ks_chain_adapter_matmul", True)
         if given:
             _wrote(out)
         return (out, H) if keep else out
@@ -611,6 +642,8 @@ class AdapterChain:
         frozen. dY (batch, n_out) fp32; X, H and ids as matmul() had and gave
         them."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.device, self.backward, dY, X, H, ids, weights)
         batch, code = self._rows(X, ids)
         _check_out(dY, (batch, self.n_out), torch.float32, self.device, "dY")
         _check_out(H, (batch, self.rank), torch.float32, self.device, "H")
@@ -619,13 +652,15 @@ class AdapterChain:
         if weights:
             dA = self._f32(self.count, self.rank, self.n_in)
             dB = self._f32(self.count, self.n_out, self.rank)
-        wt = None
+        wt, launch = None, _raw_stream(self._index)
         if self._wt is not None and [w._version for w in self._keep[0]] == self._versions:
             wt = self._wt.data_ptr()
+            if launch != self._wt_stream:              # the handle may go before the kernels are done
+                self._wt.record_stream(torch.cuda.current_stream(self._index))
         ws, size, _keep = self._workspace("ks_chain_adapter_backward_workspace_size", batch, code, int(wt is not None))
         _raise(self._lib.ks_chain_adapter_backward(
             self._p, self._n, self._w, wt, self._ad, ids.data_ptr(), dY.data_ptr(), X.data_ptr(), H.data_ptr(),
-            dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws, size, _raw_stream(stream, self._index)),
+            dX.data_ptr(), _ptr(dA), _ptr(dB), batch, code, ws, size, launch),
             "ks_chain_adapter_backward", True)
         return dX, dA, dB
 
@@ -660,13 +695,15 @@ def adapter_matmul(X, A, B, scale, ids, out, keep=False, stream=None):
         raise ValueError("X must be (batch, n_in) and out (batch, n_out) fp32")
     if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
         raise ValueError("ids must be (batch,) int32")
+    if stream is not None:
+        return _on_stream(stream, X.device, adapter_matmul, X, A, B, scale, ids, out, keep)
     ad = _adapters(A, B, scale, X.shape[1], out.shape[1])
     H = torch.empty((X.shape[0], ad.rank), dtype=torch.float32, device=X.device)
     size = ctypes.c_size_t(0)
     _raise(load().ks_adapter_workspace_size(ad, X.shape[0], size), "ks_adapter_workspace_size", True)
     ws = torch.empty(size.value, dtype=torch.uint8, device=X.device) if size.value else None
     _raise(load().ks_adapter_matmul(ad, _ptr(ids), _ptr(X), _ptr(out), _ptr(H), X.shape[0],
-                                    dtype_code(X.dtype, A.dtype), _ptr(ws), size.value, _stream(stream, X)),
+                                    dtype_code(X.dtype, A.dtype), _ptr(ws), size.value, _stream(None, X)),
            "ks_adapter_matmul", True)
     _wrote(out)
     return (out, H) if keep else out
@@ -682,6 +719,8 @@ def adapter_backward(dY, X, H, A, B, scale, ids, dX=None, stream=None):
         raise ValueError("X must be (batch, n_in) and dY (batch, n_out) fp32")
     if ids.dtype != torch.int32 or tuple(ids.shape) != (X.shape[0],):
         raise ValueError("ids must be (batch,) int32")
+    if stream is not None:
+        return _on_stream(stream, X.device, adapter_backward, dY, X, H, A, B, scale, ids, dX)
     ad = _adapters(A, B, scale, X.shape[1], dY.shape[1])
     _check_out(H, (X.shape[0], ad.rank), torch.float32, X.device, "H")
     if dX is not None:
@@ -693,7 +732,7 @@ def adapter_backward(dY, X, H, A, B, scale, ids, dX=None, stream=None):
     ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=X.device)
     _raise(load().ks_adapter_backward(ad, _ptr(ids), _ptr(dY), _ptr(X), _ptr(H), _ptr(dX), _ptr(dA), _ptr(dB),
                                       X.shape[0], dtype_code(X.dtype, A.dtype), _ptr(ws), size.value,
-                                      _stream(stream, X)), "ks_adapter_backward", True)
+                                      _stream(None, X)), "ks_adapter_backward", True)
     if dX is not None:
         _wrote(dX)
     return dA, dB
@@ -751,14 +790,16 @@ def sequence_logp(logits, labels, stream=None):
     strides; labels (S, T) int64, negative where masked."""
     import torch
     x = _logits(logits, labels)
+    if stream is not None:
+        return _on_stream(stream, logits.device, sequence_logp, logits, labels)
     tokens = torch.empty((x.sequences, x.tokens), dtype=torch.float32, device=logits.device)
     total = torch.empty((x.sequences,), dtype=torch.float32, device=logits.device)
     _raise(load().ks_sequence_logp(x, tokens.data_ptr(), total.data_ptr(), None,
-                                   _raw_stream(stream, logits.get_device())), "ks_sequence_logp", True)
+                                   _raw_stream(logits.get_device())), "ks_sequence_logp", True)
     return total, tokens
 
 
-def _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream):
+def _preference_forward(logits, labels, ref, beta, smoothing, dlogits=None):
     """(loss, rewards, tokens, scratch): scratch holds d loss / d total, then
     the rows' statistics."""
     import torch
@@ -781,7 +822,7 @@ def _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream):
     at = first + 4 * (1 + S + n)
     _raise(load().ks_preference_loss(x, ref.data_ptr(), _rows_stride(ref, "ref"), float(beta), float(smoothing),
                                      first, first + 4, first + 4 * (1 + S), at, at + 4 * S, _ptr(dlogits),
-                                     d_seq, d_row, _raw_stream(stream, logits.get_device())), "ks_preference_loss", True)
+                                     d_seq, d_row, _raw_stream(logits.get_device())), "ks_preference_loss", True)
     return loss, rewards, tokens, scratch
 
 
@@ -791,23 +832,26 @@ def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0, dlogits=None, 
     ones, ref (2P, T) fp32 the reference model's token log probabilities.
     dlogits may be given (the logits themselves too: then it replaces them)."""
     import torch
+    if stream is not None:
+        _logits(logits, labels)
+        return _on_stream(stream, logits.device, preference_loss, logits, labels, ref, beta, smoothing, dlogits)
     given = dlogits is not None
     if not given:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
-    loss, rewards, tokens, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits, stream)
+    loss, rewards, tokens, _ = _preference_forward(logits, labels, ref, beta, smoothing, dlogits)
     if given:
         _wrote(dlogits)
     return loss, rewards, tokens, dlogits
 
 
-def _preference_backward(logits, labels, scratch, upstream, stream=None):
+def _preference_backward(logits, labels, scratch, upstream):
     import torch
     dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     x = _logits(logits, labels)
     d_seq, d_row = _layout(dlogits, "dlogits")
     at = scratch.data_ptr()
     _raise(load().ks_preference_backward(x, at + 4 * x.sequences, at, _ptr(upstream), dlogits.data_ptr(), d_seq, d_row,
-                                         _raw_stream(stream, logits.get_device())), "ks_preference_backward", True)
+                                         _raw_stream(logits.get_device())), "ks_preference_backward", True)
     return dlogits
 
 
@@ -884,12 +928,14 @@ class AdamW:
     def grad_norm(self, out=None, stream=None):
         """The 2-norm over all gradients, a device scalar."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.device, self.grad_norm, out)
         given = out is not None
         if not given:
             out = torch.empty((), dtype=torch.float32, device=self.device)
         ws = torch.empty(max(self._ws_bytes, 1), dtype=torch.uint8, device=self.device)
         _raise(self._lib.ks_grad_norm(self._t, self._n, out.data_ptr(), ws.data_ptr(), self._ws_bytes,
-                                      _raw_stream(stream, self.device.index)), "ks_grad_norm", True)
+                                      _raw_stream(self.device.index)), "ks_grad_norm", True)
         if given:
             _wrote(out)
         return out
@@ -904,18 +950,22 @@ class AdamW:
             return norm
         if max_norm is not None and not max_norm > 0:
             raise ValueError("max_norm must be positive")
+        if stream is not None:
+            return _on_stream(stream, self.device, self.step, step, lr, betas, eps, weight_decay, max_norm, norm, seed)
         if max_norm is not None and norm is None:
-            norm = self.grad_norm(stream=stream)
+            norm = self.grad_norm()
         o = ks_adamw_options_t(float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay),
                                float(max_norm or 0.0), int(step), int(seed) & 0xFFFFFFFF, self.bits)
         _raise(self._lib.ks_adamw_step(self._t, self._n, o, _ptr(norm) if max_norm is not None else None,
-                                       _raw_stream(stream, self.device.index)), "ks_adamw_step", True)
+                                       _raw_stream(self.device.index)), "ks_adamw_step", True)
         _wrote(self._written)
         return norm
 
     def state_values(self, ms_out, vs_out, stream=None):
         """The values that 8-bit moments stand for, into fp32 tensors."""
         import torch
+        if stream is not None:
+            return _on_stream(stream, self.device, self.state_values, ms_out, vs_out)
         if self.bits != 8:
             raise ValueError("32-bit moments are their own values")
         if len(ms_out) != self._n or len(vs_out) != self._n:
@@ -929,6 +979,6 @@ class AdamW:
             if set(map(T.get_device, outs)) != {index} or not all(map(T.is_contiguous, outs)):
                 raise ValueError("outputs must be contiguous, on the parameters' device")
             ptrs.append((ctypes.c_void_p * self._n).from_buffer(array.array("Q", map(T.data_ptr, outs))))
-        _raise(self._lib.ks_adamw_state_values(self._t, self._n, *ptrs, _raw_stream(stream, index)),
+        _raise(self._lib.ks_adamw_state_values(self._t, self._n, *ptrs, _raw_stream(index)),
                "ks_adamw_state_values", True)
         _wrote([*ms_out, *vs_out])
