@@ -813,16 +813,16 @@ def _preference_forward(logits, labels, ref, beta, smoothing, dlogits=None):
             raise ValueError("dlogits must have the logits' shape, type and device")
         d_seq, d_row = _layout(dlogits, "dlogits")
     S, T = x.sequences, x.tokens
-    # one allocation: loss, rewards, tokens, and what backward reads
-    n, f32 = S * T, torch.float32
-    buf = torch.empty((1 + 2 * S + 3 * n,), dtype=f32, device=logits.device)
-    loss, rewards = buf.as_strided((), (), 0), buf.as_strided((S,), (1,), 1)
-    tokens, scratch = buf.as_strided((S, T), (T, 1), 1 + S), buf.as_strided((S + 2 * n,), (1,), 1 + S + n)
-    first = buf.data_ptr()
-    at = first + 4 * (1 + S + n)
+    # memory of their own: as views of one buffer the results could not be changed
+    # in place under autograd, and would keep each other alive
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    f32 = loss.new_empty
+    rewards, tokens, scratch = f32(S), f32(S, T), f32(S + 2 * S * T)
+    at = scratch.data_ptr()
     _raise(load().ks_preference_loss(x, ref.data_ptr(), _rows_stride(ref, "ref"), float(beta), float(smoothing),
-                                     first, first + 4, first + 4 * (1 + S), at, at + 4 * S, _ptr(dlogits),
-                                     d_seq, d_row, _raw_stream(logits.get_device())), "ks_preference_loss", True)
+                                     loss.data_ptr(), rewards.data_ptr(), tokens.data_ptr(), at, at + 4 * S,
+                                     _ptr(dlogits), d_seq, d_row, _raw_stream(logits.get_device())),
+           "ks_preference_loss", True)
     return loss, rewards, tokens, scratch
 
 
