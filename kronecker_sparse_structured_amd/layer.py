@@ -118,8 +118,9 @@ def make_adapter_class():
         def forward(ctx, X, A, B, chain, ids):
             Y, H = chain.matmul(X, ids, keep=True)
             ctx.chain = chain
-            # A and B are saved for autograd's check of in-place changes
-            ctx.save_for_backward(X, H, ids, A, B)
+            # the weights are saved for autograd's check of in-place changes: H and the
+            # gradients are of the same ones (inference tensors cannot be saved)
+            ctx.save_for_backward(X, H, ids, A, B, *(t for t in chain.frozen if not t.is_inference()))
             return Y
 
         @staticmethod

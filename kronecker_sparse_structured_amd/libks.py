@@ -565,6 +565,7 @@ class AdapterChain:
         if A.dtype == torch.bfloat16:
             self._codes[torch.bfloat16] = DTYPE_BF16
         self._keep = (list(Ws), A, B, scale)
+        self.frozen = (*Ws, scale)           # what backward() reads and gives no gradient of
         self._f32 = scale.new_empty          # an fp32 tensor beside the weights, without torch.empty's keywords
         self._n = len(self.patterns)
         self._p = _patterns(self.patterns)

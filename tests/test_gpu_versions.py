@@ -120,3 +120,34 @@ def test_inference_tensors_have_no_counter():
         p, g, m, v = (torch.ones(300, device=DEV) for _ in range(4))
         libks.AdamW([p], [g], [m], [v]).step(1, lr=0.1)
         assert float(p[0]) < 1.0
+
+
+@pytest.mark.parametrize("what", ["W", "scale"])
+def test_a_change_of_what_is_frozen_between_forward_and_backward_is_seen(what):
+    """dX is formed from W, E and dX from scale, H before: all of one time."""
+    require_gpu()
+    base = layer.KSLinear(CHAIN, device=DEV)
+    m = layer.AdapterLinear(base, 3, 5)
+    x = torch.randn(70, 42, device=DEV, requires_grad=True)
+    ids = torch.zeros(70, dtype=torch.int32, device=DEV)
+    y = m(x, ids)
+    with torch.no_grad():
+        (base.weights[1] if what == "W" else m.scale).mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    m(x, ids).sum().backward()
+    assert x.grad.any()
+
+
+def test_frozen_weights_that_are_inference_tensors_train_adapters():
+    require_gpu()
+    with torch.inference_mode():
+        base = layer.KSLinear(CHAIN, device=DEV)
+        for w in base.weights:
+            w.requires_grad_(False)
+    m = layer.AdapterLinear(base, 3, 5)
+    m.A, m.B, m.scale = (torch.nn.Parameter(torch.ones_like(m.A)), torch.nn.Parameter(torch.ones_like(m.B)),
+                         torch.ones(3, device=DEV))
+    x = torch.randn(70, 42, device=DEV)
+    m(x, torch.zeros(70, dtype=torch.int32, device=DEV)).sum().backward()
+    assert m.A.grad[0].any() and m.B.grad[0].any()
