@@ -5,17 +5,46 @@ on Y = X W^T, see include/ks.h). AdapterLinear: such a layer, frozen, with
 low-rank adapters of many requests beside it. preference_loss: the paired
 preference loss on token logits.
 
-Argument marshalling only: every product runs in the HIP library. With
+Argument marshalling only: every product runs in the HIP library. The gradients
+are not differentiable themselves: a second derivative raises. With
 gradients enabled each factor is its own launch, so that the intermediates
 the backward pass needs are kept; without, the chain goes through
 ``chain_matmul`` and may run fused pairs.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Sequence
 
 from . import libks
+
+
+def _first_only(backward):
+    """A backward() whose gradients are constants to autograd: a derivative of one
+    raises, where it would silently be zero. (torch's once_differentiable raises
+    only if what backward() was given has a derivative, which a loss's 1 has
+    not.)"""
+    import torch
+
+    class Refuse(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, g):
+            return g.detach()
+
+        @staticmethod
+        def backward(ctx, _):
+            raise RuntimeError("a gradient through libks was differentiated: only first derivatives are formed")
+
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():                # without create_graph
+            return out
+        return tuple(g if g is None else Refuse.apply(g.requires_grad_()) for g in out)
+
+    return call
 
 
 def _autograd():
@@ -31,6 +60,7 @@ def _autograd():
             return libks.matmul(X, W, ctx.pattern)
 
         @staticmethod
+        @_first_only
         def backward(ctx, dY):
             X, W = ctx.saved_tensors
             dY = dY.contiguous()
@@ -124,6 +154,7 @@ def make_adapter_class():
             return Y
 
         @staticmethod
+        @_first_only
         def backward(ctx, dY):
             X, H, ids = ctx.saved_tensors[:3]
             weights = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
@@ -183,6 +214,7 @@ def make_preference_function():
             return loss, rewards, tokens
 
         @staticmethod
+        @_first_only
         def backward(ctx, upstream, _rewards, _tokens):
             logits, labels, scratch = ctx.saved_tensors
             return libks._preference_backward(logits, labels, scratch, upstream.float().contiguous()), None, None, \
