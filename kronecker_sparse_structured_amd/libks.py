@@ -531,7 +531,8 @@ class AdapterChain:
     loop: made here once, where each call makes its own otherwise, and left unused
     after an in-place operation on a W that torch counts, this module's optimizer
     among them. Changes that torch does not count (through W.data, by a replayed
-    graph, by code that writes through W's address) need a new handle. W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
+    graph, by code that writes through W's address) need a new handle; inference
+    tensors have no such count, and each call transposes them. W_k has shape (a, d, b, c); A (G, rank, n_in); B (G,
     n_out, rank); scale (G,) fp32; W, A and B have one type, fp32 or bf16; X has
     that type, or is fp32."""
 
@@ -576,7 +577,8 @@ class AdapterChain:
         self._index = A.get_device()
         self._sizes = {}
         self._wt = self._versions = None
-        if transposed and not torch.cuda.is_current_stream_capturing():
+        # inference tensors have no version to tell a change by
+        if transposed and not torch.cuda.is_current_stream_capturing() and not any(w.is_inference() for w in Ws):
             code, size = self._codes[torch.float32], ctypes.c_size_t(0)
             _raise(self._lib.ks_chain_transpose_size(self._p, self._n, code, size), "ks_chain_transpose_size", True)
             self._wt = torch.empty(size.value, dtype=torch.uint8, device=self.device)

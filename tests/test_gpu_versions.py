@@ -151,3 +151,25 @@ def test_frozen_weights_that_are_inference_tensors_train_adapters():
     x = torch.randn(70, 42, device=DEV)
     m(x, torch.zeros(70, dtype=torch.int32, device=DEV)).sum().backward()
     assert m.A.grad[0].any() and m.B.grad[0].any()
+
+
+def test_transposed_blocks_of_inference_tensors():
+    require_gpu()
+    with torch.inference_mode():
+        X, A, B, scale, ids, Ws, dY = chain_of()
+        ready = libks.AdapterChain(Ws, CHAIN, A, B, scale, transposed=True)
+        plain = libks.AdapterChain(Ws, CHAIN, A, B, scale)
+        _, H = ready.matmul(X, ids, keep=True)
+        for _ in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(ready.backward(dY, X, H, ids), plain.backward(dY, X, H, ids)))
+            Ws[0].mul_(2)
+    X, A, B, scale, ids, Ws, dY = chain_of()
+    with torch.inference_mode():                 # tensors made outside keep their version
+        ready = libks.AdapterChain(Ws, CHAIN, A, B, scale, transposed=True)
+        assert ready._wt is not None
+        _, H = ready.matmul(X, ids, keep=True)
+        before = ready.backward(dY, X, H, ids)[0]
+        Ws[0].mul_(2)
+        assert torch.equal(ready.backward(dY, X, H, ids)[0],
+                           libks.AdapterChain(Ws, CHAIN, A, B, scale).backward(dY, X, H, ids)[0])
+        assert not torch.equal(ready.backward(dY, X, H, ids)[0], before)
