@@ -400,7 +400,7 @@ ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const
  *   dA, dB fully overwritten, zeros for adapters without rows; both NULL: not
  *          computed (then X and H may be NULL).
  *   ws     device workspace of ks_adapter_backward_workspace_size bytes, 16-byte
- *          aligned.
+ *          aligned (may be NULL when that is 0).
  * Partial sums over ranges of an adapter's rows are added in a fixed order.
  * batch = 0 writes the zeros of dA and dB.
  */
@@ -440,7 +440,7 @@ ks_status_t ks_chain_adapter_matmul(const ks_pattern_t* p, int n, const void* co
  *          b up to 64 and a multiple of 16 runs as one launch on W itself (W and
  *          dY 16-byte aligned).
  *   ws     of ks_chain_adapter_backward_workspace_size bytes, which has to be
- *          told whether Wt will be given.
+ *          told whether Wt will be given (may be NULL when that is 0).
  */
 ks_status_t ks_chain_transpose_size(const ks_pattern_t* p, int n, ks_dtype_t dt, size_t* bytes);
 ks_status_t ks_chain_transpose(const ks_pattern_t* p, int n, const void* const* W, void* Wt, ks_dtype_t dt,

@@ -370,7 +370,7 @@ ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, con
     st = adapter_types(enum_value(&dt), &xt, &wt);
     if (st != KS_OK) return st;
     if (!dA && !dB && (batch == 0 || !dX)) return KS_OK;
-    if (!ws || ws_bytes < need) return KS_ERR_WORKSPACE;
+    if (need > 0 && (!ws || ws_bytes < need)) return KS_ERR_WORKSPACE;
     st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, need);
     if (st != KS_OK) return st;
     int cus = 0;
@@ -495,7 +495,7 @@ ks_status_t ks_chain_adapter_backward(const ks_pattern_t* p, int n, const void* 
     if (st != KS_OK) return st;
     if (batch > 0 && ((!W && !Wt) || !dX)) return KS_ERR_NULL;
     if (batch == 0 && !dA && !dB) return KS_OK;
-    if (!ws || ws_bytes < w.total) return KS_ERR_WORKSPACE;
+    if (w.total > 0 && (!ws || ws_bytes < w.total)) return KS_ERR_WORKSPACE;
     st = check_backward(ad, ids, dY, X, H, dX, dA, dB, batch, xt, wt, ws, w.total);
     if (st != KS_OK) return st;
     if (!aligned(Wt, 16)) return KS_ERR_ALIGN;
