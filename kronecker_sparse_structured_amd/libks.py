@@ -928,6 +928,11 @@ class AdamW:
             out += ts
         return out
 
+    def _check_scalar(self, t, name):
+        import torch
+        if not isinstance(t, torch.Tensor) or t.numel() != 1 or t.dtype is not torch.float32 or t.device != self.device:
+            raise ValueError("%s must be one fp32 value on %s" % (name, self.device))
+
     def grad_norm(self, out=None, stream=None):
         """The 2-norm over all gradients, a device scalar."""
         import torch
@@ -936,6 +941,8 @@ class AdamW:
         given = out is not None
         if not given:
             out = torch.empty((), dtype=torch.float32, device=self.device)
+        else:
+            self._check_scalar(out, "out")
         ws = torch.empty(max(self._ws_bytes, 1), dtype=torch.uint8, device=self.device)
         _raise(self._lib.ks_grad_norm(self._t, self._n, out.data_ptr(), ws.data_ptr(), self._ws_bytes,
                                       _raw_stream(self.device.index)), "ks_grad_norm", True)
@@ -953,6 +960,8 @@ class AdamW:
             return norm
         if max_norm is not None and not max_norm > 0:
             raise ValueError("max_norm must be positive")
+        if norm is not None:
+            self._check_scalar(norm, "norm")
         if stream is not None:
             return _on_stream(stream, self.device, self.step, step, lr, betas, eps, weight_decay, max_norm, norm, seed)
         if max_norm is not None and norm is None:
