@@ -403,6 +403,8 @@ ks_status_t ks_adapter_matmul(const ks_adapters_t* ad, const int32_t* ids, const
  *          aligned (may be NULL when that is 0).
  * Partial sums over ranges of an adapter's rows are added in a fixed order.
  * batch = 0 writes the zeros of dA and dB.
+ * The size query and the call give KS_ERR_UNSUPPORTED where a grid could not hold
+ * the work, e.g. 65535 adapters of more than 16320 values and over 64 rows.
  */
 ks_status_t ks_adapter_backward_workspace_size(const ks_adapters_t* ad, int64_t batch, size_t* bytes);
 ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, const float* dY, const void* X,

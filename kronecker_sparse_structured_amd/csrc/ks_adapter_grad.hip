@@ -689,11 +689,6 @@ ks_status_t run(const AdapterCall& c, const float* dY, const void* X, const floa
     float* w_part = reinterpret_cast<float*>(ws + l.w_part);
     const TW* A = static_cast<const TW*>(c.A);
     const TW* B = static_cast<const TW*>(c.B);
-    // a grid counts its threads in 32 bits: 2^24 workgroups of 256 are one too many
-    const int64_t most = (int64_t(1) << 24) - 1, wide = std::max(c.n_in, c.n_out);
-    if (static_cast<int64_t>(l.o.n_slots) * ((wide + kColsX - 1) / kColsX) > most ||
-        (wide * c.rank + kThreads - 1) / kThreads * c.count + (c.batch * c.rank + kThreads - 1) / kThreads > most)
-        return KS_ERR_UNSUPPORTED;
     ks_status_t st = launch_adapter_order(c, l.o);
     if (st != KS_OK) return st;
     // one launch for dB (or dA) and, with planes > 1, for E
@@ -754,6 +749,15 @@ size_t adapter_order_layout(int64_t batch, int block, int count, char* ws, Adapt
 ks_status_t launch_adapter_order(const AdapterCall& c, const AdapterOrder& o) {
     return launch_kernel(sort_kernel, dim3(static_cast<unsigned>(c.count)), dim3(1024), 0, c.stream, c.ids,
                          static_cast<int>(c.batch), c.count, o.block, o.order, o.segs, o.slots, o.n_slots);
+}
+
+bool adapter_grad_fits(int n_in, int n_out, int rank, int count, int64_t batch) {
+    if (few_rows(n_in, n_out, rank, batch)) return true;
+    // a grid counts its threads in 32 bits: 2^24 workgroups of 256 are one too many
+    const int64_t most = (int64_t(1) << 24) - 1, wide = std::max(n_in, n_out);
+    const int64_t slots = adapter_slots(batch, block_rows(n_in, n_out, batch), count);
+    return slots * ((wide + kColsX - 1) / kColsX) <= most &&
+           (wide * rank + kThreads - 1) / kThreads * count + (batch * rank + kThreads - 1) / kThreads <= most;
 }
 
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch) {

@@ -74,6 +74,8 @@ bool pair_dx_supports(const Shape& s0, const Shape& s1, int wt, const void* W0, 
 ks_status_t launch_pair_dx(const Shape& s0, const void* W0, const void* W1, const float* dY, float* dX, int64_t batch,
                            hipStream_t stream, int num_cus);
 
+// fits: whether the launches' grids can hold it.
+bool adapter_grad_fits(int n_in, int n_out, int rank, int count, int64_t batch);
 size_t adapter_grad_workspace(int n_in, int n_out, int rank, int count, int64_t batch);
 ks_status_t launch_adapter_grad(const AdapterCall& c, const float* dY, const void* X, const float* H, float* dX,
                                 float* dA, float* dB, void* ws);

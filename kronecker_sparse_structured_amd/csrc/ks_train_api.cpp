@@ -355,8 +355,9 @@ ks_status_t ks_adapter_backward_workspace_size(const ks_adapters_t* ad, int64_t 
     if (!bytes) return KS_ERR_NULL;
     const ks_status_t st = check_adapters(ad, batch);
     if (st != KS_OK) return st;
-    *bytes = ks::adapter_grad_workspace(static_cast<int>(ad->n_in), static_cast<int>(ad->n_out), ad->rank, ad->count,
-                                        batch);
+    const int n_in = static_cast<int>(ad->n_in), n_out = static_cast<int>(ad->n_out);
+    if (!ks::adapter_grad_fits(n_in, n_out, ad->rank, ad->count, batch)) return KS_ERR_UNSUPPORTED;
+    *bytes = ks::adapter_grad_workspace(n_in, n_out, ad->rank, ad->count, batch);
     return KS_OK;
 }
 
