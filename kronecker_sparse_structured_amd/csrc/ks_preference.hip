@@ -34,7 +34,7 @@ namespace ks {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxRows = int64_t(1) << 23;   // rows a launch: a grid counts its threads in 32 bits
+constexpr int64_t kMaxRows = int64_t(1) << 23;   // workgroups a launch: a grid counts its threads in 32 bits
 constexpr int kWaves = kThreads / 64;
 // log2 e in two parts: the fp32 value alone is 1.3e-8 too small, which a sum of
 // terms near exp(-6) shows as 8e-8, the same way in every row
@@ -197,8 +197,9 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // total[s] = sum_t tokens: one wave a sequence.
-__global__ __launch_bounds__(kThreads) void sequence_sum_kernel(const float* tokens, int64_t T, int64_t S, float* total) {
-    const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / 64;
+__global__ __launch_bounds__(kThreads) void sequence_sum_kernel(const float* tokens, int64_t T, int64_t s0, int64_t S,
+                                                               float* total) {
+    const int64_t s = s0 + static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / 64;
     if (s >= S) return;
     double x = 0.0;
     for (int64_t t = threadIdx.x % 64; t < T; t += 64) x += static_cast<double>(tokens[s * T + t]);
@@ -348,8 +349,13 @@ ks_status_t launch_token_logp(const ks_logits_t& x, float* tokens, float* stats,
 }
 
 ks_status_t launch_sequence_sum(const ks_logits_t& x, const float* tokens, float* total, hipStream_t stream) {
-    return launch_kernel(sequence_sum_kernel, dim3(static_cast<unsigned>((x.sequences + kWaves - 1) / kWaves)),
-                         dim3(kThreads), 0, stream, tokens, x.tokens, x.sequences, total);
+    for (int64_t s = 0; s < x.sequences; s += kMaxRows * kWaves) {
+        const int64_t groups = std::min(kMaxRows, (x.sequences - s + kWaves - 1) / kWaves);
+        const ks_status_t st = launch_kernel(sequence_sum_kernel, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0,
+                                             stream, tokens, x.tokens, s, x.sequences, total);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
 }
 
 ks_status_t launch_pair_loss(const ks_logits_t& x, const float* tokens, const float* ref, int64_t ref_stride,
