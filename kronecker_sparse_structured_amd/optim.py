@@ -65,9 +65,7 @@ def make_class():
                 by_step = {}
                 for p in group["params"]:
                     if p.grad is not None:
-                        s = self._state(p)
-                        s["step"] += 1
-                        by_step.setdefault(s["step"], []).append(p)
+                        by_step.setdefault(self._state(p)["step"] + 1, []).append(p)
                 sets += [(group, t, ps) for t, ps in sorted(by_step.items())]
             if not sets:
                 return loss
@@ -78,6 +76,10 @@ def make_class():
                                    [s["v"] for s in st], [s["scales"] for s in st] if self.state_bits == 8 else None)
 
             handles = [handle(ps) for _, _, ps in sets]
+            # counted once every tensor has been accepted
+            for _, t, ps in sets:
+                for p in ps:
+                    self.state[p]["step"] = t
             norm = None
             if self.max_norm is not None:
                 every = handles[0] if len(handles) == 1 else handle([p for _, _, ps in sets for p in ps])
