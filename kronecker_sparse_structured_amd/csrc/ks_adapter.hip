@@ -413,14 +413,16 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(const Args a, cons
     if (kRest) {
         static_assert(kRestTiles * kTile <= 64 * kPairGroup, "a group a lane");
         const int64_t n = first * kTile + lane * kPairGroup;
-        int id[kPairGroup];
+        int id[kPairGroup];                            // all loads first: compared as they come, 6.5 us for 5.2
 #pragma unroll
-        for (int i = 0; i < kPairGroup; ++i) id[i] = adapter_of(a.ids[min(n + i, a.batch - 1)], a.count);
+        for (int i = 0; i < kPairGroup; ++i) id[i] = a.ids[min(n + i, a.batch - 1)];
         const int64_t end = min(a.batch, (first + kRestTiles) * kTile);
         int changes = 0;
 #pragma unroll
-        for (int i = 1; i < kPairGroup; ++i)
-            if (n + i < end && id[i] != id[i - 1]) ++changes;
+        for (int i = 0; i < kPairGroup; ++i) {
+            id[i] = adapter_of(id[i], a.count);
+            if (i > 0 && n + i < end && id[i] != id[i - 1]) ++changes;
+        }
         todo = __ballot(changes > 1);
     }
     while (todo) {

@@ -103,7 +103,7 @@ constexpr int low_parts_bytes(int rank) { return (rank + 15) / 16 * 96; }
 // The adapter of a row with this id: any id outside [0, count) means none, -1. Kernels
 // that pack ids or compare those of neighbouring rows take them through here: -2 beside
 // -1 is no change of adapter, and would not fit the packed word.
-constexpr int adapter_of(int id, int count) { return id >= 0 && id < count ? id : -1; }
+constexpr int adapter_of(int id, int count) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(count) ? id : -1; }
 struct PairGroup {
     int32_t first, second;               // second: split << 17 | (then + 1)
     // first, then: from adapter_of
