@@ -861,7 +861,7 @@ def _preference_backward(logits, labels, scratch, upstream):
 # ---------------------------------------------------------------- optimizer
 
 ADAMW_BLOCK = 256   # values that share a scale in 8 bits
-_dtype_of = operator.attrgetter("dtype")
+_dtype_of, _base_of = operator.attrgetter("dtype"), operator.attrgetter("_base")
 
 
 class AdamW:
@@ -923,8 +923,9 @@ class AdamW:
         out = []
         for ts in sets:
             if ts and ts[0]._base is not None:
-                bases = [t if t._base is None else t._base for t in ts]
-                ts = {id(t): t for t in bases}.values()
+                bases = set(map(_base_of, ts))
+                ts = [t for t in ts if t._base is None] if None in bases else []
+                out += bases - {None}
             out += ts
         return out
 
