@@ -489,6 +489,7 @@ ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, 
  *   rewards[s] = beta sum_t (tokens[s][t] - ref[s][t]) over unmasked t
  *   z_i = rewards[i] - rewards[P + i]
  *   loss = 1/P sum_i (1 - smoothing) log(1 + exp(-z_i)) + smoothing log(1 + exp(z_i))
+ *   (a term of weight 0 is 0, whatever its logarithm)
  *   ref     device fp32, ref[s * ref_stride + t]: the reference's tokens of
  *           ks_sequence_logp; not read where masked.
  *   loss    device fp32, one value (0 if there is no pair).

@@ -246,7 +246,9 @@ __global__ __launch_bounds__(1024) void pair_loss_kernel(const ks_logits_t x, co
         // exp(-|z|) gives both sigmoids and both logarithms without overflow
         const double d = exp(-fabs(z)), near = 1.0 / (1.0 + d), far = d / (1.0 + d), more = log1p(d);
         const double up = z >= 0.0 ? near : far, un = z >= 0.0 ? far : near;
-        sum += (1.0 - e) * (more + fmax(-z, 0.0)) + e * (more + fmax(z, 0.0));
+        // a side of weight 0 is left out: its logarithm may be infinite
+        if (e < 1.0) sum += (1.0 - e) * (more + fmax(-z, 0.0));
+        if (e > 0.0) sum += e * (more + fmax(z, 0.0));
         const double c = static_cast<double>(beta) * (e * up - (1.0 - e) * un) / static_cast<double>(P);
         grad[p] = static_cast<float>(c);
         grad[p + P] = static_cast<float>(-c);
