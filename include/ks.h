@@ -419,7 +419,8 @@ ks_status_t ks_adapter_backward(const ks_adapters_t* ad, const int32_t* ids, con
  * bf16 adapters of a rank that is a multiple of 4 and at most 32 in that launch
  * to every four rows, counted from the first, that share one or change it once;
  * the sums are then taken in another order, so a row without an adapter has the
- * chain's value up to rounding. Y is fully overwritten; ad->n_in and ad->n_out
+ * chain's value up to rounding, and an infinite value of B may give NaN (H enters
+ * as three parts, and a part may be 0). Y is fully overwritten; ad->n_in and ad->n_out
  * have to be the chain's (KS_ERR_CHAIN_MISMATCH). Workspace as for
  * ks_chain_matmul, of the size that ks_chain_adapter_workspace_size gives.
  */
@@ -491,7 +492,7 @@ ks_status_t ks_sequence_logp(const ks_logits_t* x, float* tokens, float* total, 
  *   loss = 1/P sum_i (1 - smoothing) log(1 + exp(-z_i)) + smoothing log(1 + exp(z_i))
  *   (a term of weight 0 is 0, whatever its logarithm)
  *   ref     device fp32, ref[s * ref_stride + t]: the reference's tokens of
- *           ks_sequence_logp; not read where masked.
+ *           ks_sequence_logp; of no effect where masked.
  *   loss    device fp32, one value (0 if there is no pair).
  *   rewards device fp32, 2P.   tokens device fp32, 2P x T.
  *   grad    device fp32, 2P: d loss / d total[s], for ks_preference_backward.

@@ -35,7 +35,8 @@
 // the rows' requests, Y[n] += H[n] B[g]^T with g = ids[n], H from an earlier launch,
 // for stages whose four rows share an adapter or pass once from one to another:
 // there Y is written once and never read. H comes as three bf16 values whose sum
-// is the fp32 value exactly, so its products with B are those of fp32; the loader
+// is the fp32 value exactly, so its products with a finite B are those of fp32 (a part
+// may be 0: an infinite B can give NaN); the loader
 // streams the stage's rows of them and the stage's adapters along with X. A thread of phase B keeps its four outputs'
 // values of B in registers, and the products run on the 16-block 4x4x4 bf16 MFMA,
 // whose lanes are given their own outputs as the columns: each receives the stage's

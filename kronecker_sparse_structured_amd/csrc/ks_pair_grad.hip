@@ -10,7 +10,8 @@
 //
 // Workgroup: whole rows, four at a time, eight waves, one workgroup a compute
 // unit. All weights of the pair stay in its registers, two bf16 values a word (96
-// words a thread at b0 = 64), loaded once through LDS.
+// words a thread at b0 = 64), loaded once through LDS. Two buffers of dZ take 133 of
+// the 160 KB of LDS at b0 = 64 and would take 166 at 80: wider pairs run as a chain.
 //  (A) on the 16-block 4x4x1 fp32 MFMA: lane 4 i + q supplies row q of block i's
 //      left operand, column q of its right one, and receives column q of the
 //      block's product, the rows in its four registers. Wave w takes alpha in
