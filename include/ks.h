@@ -335,8 +335,9 @@ ks_status_t ks_chain_describe(const ks_pattern_t* p, int n, int64_t batch, ks_dt
 
 /*
  * Operators around the product, for serving and fine-tuning a layer of KS
- * factors: low-rank adapters beside a frozen projection, a preference loss on
- * token logits, and the optimizer step. The conventions above hold for all of
+ * factors: low-rank adapters beside a frozen projection, the norms and residuals
+ * between layers, preference and distillation losses on token logits, beam
+ * search, and the optimizer step. The conventions above hold for all of
  * them: device pointers of the caller, asynchronous on `stream`, argument
  * errors found on the host before any HIP call, no allocation, no atomics and
  * a fixed summation order.
@@ -510,6 +511,187 @@ ks_status_t ks_preference_loss(const ks_logits_t* x, const float* ref, int64_t r
                                int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream);
 ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, const float* grad, const float* upstream,
                                    void* dlogits, int64_t d_seq_stride, int64_t d_row_stride, hipStream_t stream);
+
+/*
+ * A teacher's `count` highest logits of each position: entry k of position t of
+ * sequence s is top[s * top_seq_stride + t * top_row_stride + k], for the token
+ * ids[s * id_seq_stride + t * id_row_stride + k] (strides in elements). An entry
+ * with a negative id is none, so rows may hold fewer; an entry of -inf weighs
+ * nothing. The same id may stand in a row more than once: its entries add up.
+ * An id >= vocab gives NaN.
+ */
+typedef struct ks_teacher_t {
+    const void* ids;        /* device: int32 or int64 */
+    const void* top;        /* device */
+    int64_t id_seq_stride, id_row_stride, top_seq_stride, top_row_stride;
+    int32_t count;          /* 1 .. KS_TEACHER_MAX_COUNT */
+    int32_t id_bytes;       /* 4 or 8 */
+    int32_t elem;           /* a ks_elem_t value: top's */
+    int32_t reserved;       /* must be zero */
+} ks_teacher_t;
+
+#define KS_TEACHER_MAX_COUNT 256
+
+/*
+ * ks_distil_loss: distillation from such a teacher, mixed with the labels. With
+ * q = softmax(top / temperature) over a position's entries, p = softmax(x /
+ * temperature) and p1 = softmax(x) over the vocabulary:
+ *   tokens[s][t] = weight temperature^2 sum_k q_k (log q_k - log p[id_k])
+ *                  - (1 - weight) log p1[label]        (0 where masked)
+ *   loss = sum of tokens / N,  N = the positions that are not masked
+ *   dlogits[v] = (weight temperature (p_v - q_v) + (1 - weight) (p1_v - 1[v = label])) / N
+ * A side of weight 0 is left out whatever it is; with weight 1 a label only says
+ * whether its position counts. A position without an entry has no first side.
+ *   loss    device fp32, one value (0 if every position is masked).
+ *   tokens  device fp32, sequences x tokens.
+ *   stats   device fp32, 3 x sequences x tokens + 1 values, for
+ *           ks_distil_backward: each row's maximum and its two sums of
+ *           exponentials, then 1 / N. With dlogits given only the last is
+ *           defined.
+ *   dlogits NULL: the loss alone. Else the gradient, as for ks_preference_loss;
+ *           it may be x's own memory with x's strides.
+ * 0 <= weight <= 1 and temperature > 0 (with a finite inverse square), else
+ * KS_ERR_INVALID.
+ *
+ * ks_distil_backward: that gradient from the stats of an earlier call without
+ * dlogits, times upstream[0] (device fp32; NULL means 1).
+ */
+ks_status_t ks_distil_loss(const ks_logits_t* x, const ks_teacher_t* teacher, double weight, double temperature,
+                           float* loss, float* tokens, float* stats, void* dlogits, int64_t d_seq_stride,
+                           int64_t d_row_stride, hipStream_t stream);
+ks_status_t ks_distil_backward(const ks_logits_t* x, const ks_teacher_t* teacher, double weight, double temperature,
+                               const float* stats, const float* upstream, void* dlogits, int64_t d_seq_stride,
+                               int64_t d_row_stride, hipStream_t stream);
+
+/*
+ * Beam search. Request r has `beams` beams; beam w's logits x[v] of `vocab`
+ * values lie at data[r * request_stride + w * beam_stride + v] and scores[r *
+ * beams + w] is the sum of its tokens' log probabilities. Its candidates are its
+ * continuations by every token v, with
+ *   score = scores[w] + x[v] - log sum_u exp x[u]  and  length = lengths[w] + 1,
+ * and for a beam that is done one candidate only: the token eos, with the score
+ * and the length that it has (its logits are not read and may hold anything).
+ * Candidates are ranked by score / max(length, 1)^length_penalty, those of equal
+ * rank by the lower w * vocab + v; a beam's own by their logits, which is the
+ * same order. A beam whose score is not finite, or whose logits hold NaN or +inf,
+ * has no candidate, and a logit of -inf (a banned token) is none.
+ */
+typedef struct ks_beams_t {
+    const void* data;         /* device */
+    const float* scores;      /* device, requests x beams */
+    const uint8_t* done;      /* device, requests x beams, 0 or not; NULL: none is */
+    const int32_t* lengths;   /* device, requests x beams; may be NULL if length_penalty is 0 */
+    int64_t request_stride, beam_stride;
+    int64_t requests, vocab;
+    int64_t eos;              /* the token that ends a beam; < 0: none does (done must be NULL) */
+    double length_penalty;    /* >= 0 */
+    int32_t beams;            /* 1 .. KS_BEAM_MAX */
+    int32_t elem;             /* a ks_elem_t value */
+} ks_beams_t;
+
+#define KS_BEAM_MAX 64
+
+/*
+ * ks_beam_select: the out_beams (1 .. KS_BEAM_MAX) best candidates of each
+ * request, best first, all outputs requests x out_beams:
+ *   scores   device fp32.  tokens  device int64.
+ *   parents  device int32: the beam of the candidate, 0 .. beams - 1.
+ *   done     device, 1 where the token is eos, else 0; NULL if eos < 0.
+ *   lengths  device int32; NULL exactly if x->lengths is.
+ * Where a request has fewer candidates the rest have score -inf, token eos (0
+ * without one), parent 0, length 0, and are done: nothing continues them.
+ *   ws       of ks_beam_workspace_size bytes, 16-byte aligned.
+ * beams * vocab has to stay below 2^31 (KS_ERR_INVALID).
+ *
+ * ks_beam_reorder: the beams' states follow their beams. For each of n states
+ * (host array) dst's row [r][j] of row_bytes bytes becomes src's row
+ * [r][parents[r * out_beams + j]]; src has requests x beams rows, dst requests x
+ * out_beams, one after another. A parent outside [0, beams) gives zeros.
+ */
+ks_status_t ks_beam_workspace_size(const ks_beams_t* x, int out_beams, size_t* bytes);
+ks_status_t ks_beam_select(const ks_beams_t* x, int out_beams, float* scores, int64_t* tokens, int32_t* parents,
+                           uint8_t* done, int32_t* lengths, void* ws, size_t ws_bytes, hipStream_t stream);
+
+typedef struct ks_state_t {
+    const void* src;          /* device */
+    void* dst;                /* device */
+    int64_t row_bytes;
+} ks_state_t;
+
+ks_status_t ks_beam_reorder(const ks_state_t* states, int n, const int32_t* parents, int64_t requests, int beams,
+                            int out_beams, hipStream_t stream);
+
+/*
+ * The norms around a block, with its gate and the residual. For each of `rows`
+ * rows of `width` values
+ *   u = post(y),  z = x + residual * scale . gate . u,  h = pre(z)
+ * where . multiplies value by value and a norm is, with its weight w and bias b,
+ *   KS_NORM_RMS    v / sqrt(mean v^2 + eps) w + b
+ *   KS_NORM_LAYER  (v - mean v) / sqrt(var v + eps) w + b
+ * with the mean and variance over the row. Everything between the inputs and the
+ * outputs is fp32, z before its rounding too where h is formed from it.
+ */
+typedef enum ks_norm_t {
+    KS_NORM_RMS = 0,
+    KS_NORM_LAYER = 1
+} ks_norm_t;
+
+typedef struct ks_residual_norm_t {
+    const void* pre_weight;   /* device, width values; NULL: no pre, no h */
+    const void* pre_bias;     /* NULL: none */
+    const void* post_weight;  /* NULL: no post, u = y */
+    const void* post_bias;    /* NULL: none */
+    const void* scale;        /* NULL: 1 */
+    int64_t width;            /* 1 .. KS_NORM_MAX_WIDTH (KS_ERR_UNSUPPORTED above) */
+    double eps;               /* > 0 */
+    double residual;
+    int32_t kind;             /* a ks_norm_t value */
+    int32_t elem;             /* ks_elem_t values: of the five vectors, */
+    int32_t x_elem, y_elem;   /* of x, z and their gradients, of y and its, */
+    int32_t h_elem;           /* of h and its, */
+    int32_t gate_elem;        /* of the gate and its */
+} ks_residual_norm_t;
+
+#define KS_NORM_MAX_WIDTH 8192
+
+/*
+ * ks_residual_norm: the forward pass.
+ *   y      NULL: the norm alone, h = pre(x). Then gate and z must be NULL.
+ *   gate   device, groups x width, or NULL with groups = 0: rows [i rows/groups,
+ *          (i + 1) rows/groups) have gate i. groups has to divide rows
+ *          (KS_ERR_INVALID): rows is a gate a row, 1 one for all.
+ *   z      may be x's own memory.   h  NULL exactly if pre_weight is.
+ *   stats  device fp32, 16-byte aligned, rows x 4, or NULL: mean and 1 / deviation of z, then of
+ *          y (0 and 1 where there is no norm), for the backward pass.
+ * All matrices are row-major and contiguous.
+ *
+ * ks_residual_norm_backward: the gradients of it.
+ *   dz     of z's gradient (x_elem), NULL: zero.   dh  of h's, NULL: zero.
+ *   x, y, gate, groups, stats  as the forward pass had and wrote them.
+ *   dx, dy of x and y (dy NULL exactly if y is).
+ *   g      fp32, width values each; a NULL one is not computed. NULL where the
+ *          forward pass had no such vector (KS_ERR_INVALID else).
+ *   dgate  gate's type, groups x width; NULL: not computed.
+ *   ws     of ks_residual_norm_backward_workspace_size bytes, 16-byte aligned
+ *          (may be NULL when that is 0).
+ * rows = 0 writes the zeros of g and dgate.
+ */
+typedef struct ks_residual_norm_grads_t {
+    float* pre_weight;
+    float* pre_bias;
+    float* post_weight;
+    float* post_bias;
+    float* scale;
+} ks_residual_norm_grads_t;
+
+ks_status_t ks_residual_norm(const ks_residual_norm_t* n, const void* x, const void* y, const void* gate,
+                             int64_t groups, void* z, void* h, float* stats, int64_t rows, hipStream_t stream);
+ks_status_t ks_residual_norm_backward_workspace_size(const ks_residual_norm_t* n, int64_t rows, int64_t groups,
+                                                     size_t* bytes);
+ks_status_t ks_residual_norm_backward(const ks_residual_norm_t* n, const void* dz, const void* dh, const void* x,
+                                      const void* y, const void* gate, int64_t groups, const float* stats, void* dx,
+                                      void* dy, const ks_residual_norm_grads_t* g, void* dgate, int64_t rows, void* ws,
+                                      size_t ws_bytes, hipStream_t stream);
 
 /*
  * One optimizer step over many tensors. For each element

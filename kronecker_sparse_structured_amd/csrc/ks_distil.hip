@@ -1,0 +1,383 @@
+// ks_distil.hip -- distillation from a teacher's highest logits, with the
+// gradient of the student's.
+//
+//   q = softmax(top / T) over a row's K entries, p = softmax(x / T), p1 = softmax(x)
+//   token = w T^2 sum_k q_k (log q_k - log p[id_k]) - (1 - w) log p1[label]
+//   dx_v = (w T (p_v - q_v) + (1 - w) (p1_v - 1[v = label])) / N
+//
+// A row of logits is 8 KB to 200 KB, its entries at most a few KB: one
+// workgroup a row. The maximum and both sums of exponentials are kept in one
+// pass, as in ks_preference.hip.
+
+#include <algorithm>
+#include <cmath>
+
+#include "ks_logit.h"
+#include "ks_stack.h"
+
+namespace ks {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxTop = KS_TEACHER_MAX_COUNT;
+static_assert(kMaxTop <= kThreads, "an entry a thread");
+
+// exp((x - m) / T) as exp2((x - m) hi + (x - m) lo): log2 e / T in two parts, both
+// positive, so that a difference of -inf gives 0 and not -inf + inf.
+struct Scale {
+    float hi, lo;
+};
+__device__ __forceinline__ float exp_of(float d, Scale s) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, s.hi, d * s.lo));
+}
+
+struct DistilArgs {
+    ks_logits_t x;
+    ks_teacher_t t;
+    double inverse;       // 1 / T
+    Scale scale;          // log2 e / T
+    double kl;            // w T^2
+    double ce;            // 1 - w
+    float slope;          // w T
+    int64_t row0;
+};
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+    return x;
+}
+__device__ __forceinline__ float wave_sum32(float x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+
+// A row's entry of this thread: q, its logarithm and its token (-1: none).
+struct Entry {
+    int64_t id;
+    float q, logq;
+};
+
+// buf: 2 kWaves values.
+__device__ __forceinline__ Entry teacher_entry(const DistilArgs& a, int64_t s, int64_t t, float* buf) {
+    Entry e{-1, 0.0f, 0.0f};
+    const int k = threadIdx.x, wave = k / 64;
+    float v = -INFINITY;
+    if (k < a.t.count) {
+        const int64_t at = s * a.t.id_seq_stride + t * a.t.id_row_stride + k;
+        e.id = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[at] : static_cast<const int32_t*>(a.t.ids)[at];
+        if (e.id >= 0) {
+            const int64_t from = s * a.t.top_seq_stride + t * a.t.top_row_stride + k;
+            v = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[from])
+                                         : static_cast<const float*>(a.t.top)[from];
+        }
+    }
+    float m = wave_max(v);
+    if (k % 64 == 0) buf[wave] = m;
+    __syncthreads();
+    m = buf[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, buf[w]);
+    if (m == -INFINITY) m = 0.0f;            // no entry that weighs anything
+    const float d = v - m, p = exp_of(d, a.scale);
+    const float part = wave_sum32(p);
+    if (k % 64 == 0) buf[kWaves + wave] = part;
+    __syncthreads();
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += buf[kWaves + w];
+    if (e.id >= 0 && sum != 0.0f) {
+        e.q = p / sum;
+        e.logq = static_cast<float>(static_cast<double>(d) * a.inverse - log(static_cast<double>(sum)));
+    }
+    if (e.id >= a.x.vocab) e.q = __builtin_nanf("");
+    return e;
+}
+
+// inv = 1 / (unmasked positions), at least one.
+__global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x, float* inv) {
+    __shared__ int sums[16];
+    const int64_t n = x.sequences * x.tokens;
+    int count = 0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+        const int64_t s = i / x.tokens;
+        count += x.labels[s * x.label_stride + (i - s * x.tokens)] >= 0;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
+    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = count;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int total = 0;
+        for (int w = 0; w < 16; ++w) total += sums[w];
+        *inv = static_cast<float>(1.0 / static_cast<double>(max(total, 1)));
+    }
+}
+
+// A running maximum with its two sums: exp((x - m) / T), and exp(x - m) if TWO.
+template <bool TWO>
+struct Running {
+    float m = kLowest, s = 0.0f, s1 = 0.0f;
+    __device__ __forceinline__ void raise(float top, Scale c) {
+        s *= exp_of(m - top, c);
+        if (TWO) s1 *= ks::exp_of(m - top);
+        m = top;
+    }
+    __device__ __forceinline__ void add(float x, Scale c) {
+        s += exp_of(x - m, c);
+        if (TWO) s1 += ks::exp_of(x - m);
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float s12, Scale c) {
+        const float top = fmaxf(m, m2);
+        raise(top, c);
+        s += s2 * exp_of(m2 - top, c);
+        if (TWO) s1 += s12 * ks::exp_of(m2 - top);
+    }
+};
+
+template <typename T, bool TWO>
+__global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArgs a, float* tokens, float* stats) {
+    __shared__ float buf[2 * kWaves], wave_stats[kWaves][3];
+    __shared__ double parts[kWaves];
+    constexpr int E = kVec<T>;
+    const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
+    const int64_t label = a.x.labels[s * a.x.label_stride + t];
+    const int tid = threadIdx.x;
+    if (label < 0) {
+        if (tid == 0) tokens[at] = 0.0f;
+        if (tid < 3) stats[3 * at + tid] = tid == 0 ? 0.0f : 1.0f;
+        return;
+    }
+    const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
+    const int V = static_cast<int>(a.x.vocab);
+    const int head = head_of(row, V), vecs = (V - head) / E, tail = head + vecs * E;
+    const u32x4* body = reinterpret_cast<const u32x4*>(row + head);
+    Running<TWO> run;
+    if (tid < head) {
+        const float x = to_f32(row[tid]);
+        run.raise(fmaxf(x, run.m), a.scale);
+        run.add(x, a.scale);
+    }
+    if (tid < V - tail) {
+        const float x = to_f32(row[tail + tid]);
+        run.raise(fmaxf(x, run.m), a.scale);
+        run.add(x, a.scale);
+    }
+    for (int v = tid; v < vecs; v += kThreads) {
+        float x[E], top = run.m;
+        widen<T>(body[v], x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) top = fmaxf(top, x[i]);
+        run.raise(top, a.scale);
+#pragma unroll
+        for (int i = 0; i < E; ++i) run.add(x[i], a.scale);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float m2 = __shfl_xor(run.m, d, 64), s2 = __shfl_xor(run.s, d, 64), s12 = __shfl_xor(run.s1, d, 64);
+        run.join(m2, s2, s12, a.scale);
+    }
+    if (tid % 64 == 0) {
+        wave_stats[tid / 64][0] = run.m;
+        wave_stats[tid / 64][1] = run.s;
+        wave_stats[tid / 64][2] = run.s1;
+    }
+    const Entry e = teacher_entry(a, s, t, buf);      // its barriers cover wave_stats as well
+    Running<TWO> all;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) all.join(wave_stats[w][0], wave_stats[w][1], wave_stats[w][2], a.scale);
+    if (!TWO) all.s1 = all.s;
+    // a weight of 0 leaves its side out, whatever it is
+    double part = 0.0;
+    if (a.kl > 0.0 && !(e.q == 0.0f)) {
+        const float x = e.id < a.x.vocab ? to_f32(row[e.id]) : 0.0f;
+        const double logp = (static_cast<double>(x) - all.m) * a.inverse - log(static_cast<double>(all.s));
+        part = e.q * (e.logq - logp);
+    }
+    part = wave_sum(part);
+    if (tid % 64 == 0) parts[tid / 64] = part;
+    __syncthreads();
+    if (tid == 0) {
+        double token = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) token += parts[w];
+        if (a.kl > 0.0) token *= a.kl;
+        if (a.ce > 0.0) {
+            const float x = label < a.x.vocab ? to_f32(row[label]) : __builtin_nanf("");
+            token -= a.ce * ((static_cast<double>(x) - all.m) - log(static_cast<double>(all.s1)));
+        }
+        tokens[at] = static_cast<float>(token);
+        stats[3 * at] = all.m;
+        stats[3 * at + 1] = all.s;
+        stats[3 * at + 2] = all.s1;
+    }
+}
+
+__global__ __launch_bounds__(1024) void distil_sum_kernel(const float* tokens, int64_t n, const float* inv, float* loss) {
+    __shared__ double sums[16];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(tokens[i]);
+    s = wave_sum(s);
+    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < 16; ++w) s += sums[w];
+        *loss = static_cast<float>(s * static_cast<double>(*inv));
+    }
+}
+
+// dx of one row: first as if there were no entries, then the values at the
+// entries' and the label's tokens again. Logits and gradient may be one memory,
+// so those logits are read before anything is written.
+template <typename T, bool TWO>
+__global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs a, const float* stats, const float* inv,
+                                                               const float* upstream, T* d_, int64_t d_seq,
+                                                               int64_t d_row) {
+    __shared__ float buf[2 * kWaves];
+    __shared__ int ids[kMaxTop + 1];
+    __shared__ float qs[kMaxTop + 1], xs[kMaxTop + 1];
+    constexpr int E = kVec<T>;
+    const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
+    const int64_t label = a.x.labels[s * a.x.label_stride + t];
+    const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
+    T* out = d_ + s * d_seq + t * d_row;
+    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x;
+    const int head = head_of(out, V), vecs = (V - head) / E, tail = head + vecs * E;
+    u32x4* obody = reinterpret_cast<u32x4*>(out + head);
+    if (label < 0) {
+        if (tid < head) out[tid] = narrow<T>(0.0f);
+        if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
+        const u32x4 none = {0u, 0u, 0u, 0u};
+        for (int v = tid; v < vecs; v += kThreads) obody[v] = none;
+        return;
+    }
+    const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
+    const float m = stats[3 * at];
+    float c = *inv;
+    if (upstream) c *= *upstream;
+    const Entry e = teacher_entry(a, s, t, buf);
+    // where nothing in the row weighs anything, that side is not there
+    __shared__ int any;
+    if (tid == 0) any = 0;
+    __syncthreads();
+    if (!(e.q == 0.0f)) any = 1;
+    __syncthreads();
+    const float slope = kl && any ? a.slope * c : 0.0f, hard = static_cast<float>(a.ce) * c;
+    const float sum = stats[3 * at + 1], sum1 = stats[3 * at + 2];
+    float c0 = slope / sum, c1 = hard / sum1;
+    if (!TWO) c0 = (slope + hard) / sum;       // one exponential serves both, or one side is left out
+    const int count = a.t.count + 1;
+    if (tid < a.t.count) {
+        const bool in = e.id >= 0 && e.id < V;
+        ids[tid] = in ? static_cast<int>(e.id) : !(e.q == 0.0f) ? 0 : -1;    // an id outside: the row says so at 0
+        qs[tid] = slope * e.q;
+        xs[tid] = in ? to_f32(row[e.id]) : 0.0f;
+    }
+    if (tid == 0) {
+        ids[count - 1] = !ce ? -1 : label < V ? static_cast<int>(label) : 0;
+        qs[count - 1] = label < V ? hard : __builtin_nanf("");
+        xs[count - 1] = ce ? to_f32(row[label < V ? label : 0]) : 0.0f;
+    }
+    __syncthreads();
+    auto value = [&](float x) {
+        float y = c0 * exp_of(x - m, a.scale);
+        if (TWO) y += c1 * ks::exp_of(x - m);
+        return y;
+    };
+    if (tid < head) out[tid] = narrow<T>(value(to_f32(row[tid])));
+    if (tid < V - tail) out[tail + tid] = narrow<T>(value(to_f32(row[tail + tid])));
+    if (head_of(row, V) != head) {
+        for (int v = head + tid; v < tail; v += kThreads) out[v] = narrow<T>(value(to_f32(row[v])));
+    } else {
+        const u32x4* body = reinterpret_cast<const u32x4*>(row + head);
+        for (int v = tid; v < vecs; v += kThreads) {
+            float x[E];
+            widen<T>(body[v], x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = value(x[i]);
+            obody[v] = pack<T>(x);
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < count; k += kThreads) {
+        if (ids[k] < 0) continue;
+        float q = 0.0f;
+        bool first = true;
+        for (int j = 0; j < count; ++j) {
+            if (ids[j] != ids[k]) continue;
+            first = first && j >= k;
+            q += qs[j];
+        }
+        if (first) out[ids[k]] = narrow<T>(value(xs[k]) - q);
+    }
+}
+
+DistilArgs distil_args(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o) {
+    DistilArgs a;
+    a.x = x;
+    a.t = t;
+    // a side of weight 0 may have any temperature: one exponential serves
+    const double T = o.weight > 0.0 ? o.temperature : 1.0, c = 1.44269504088896340736 / T;
+    a.inverse = 1.0 / T;
+    a.scale.hi = static_cast<float>(c);
+    if (a.scale.hi > c) a.scale.hi = std::nextafter(a.scale.hi, 0.0f);
+    a.scale.lo = static_cast<float>(std::max(c - a.scale.hi, c * 1e-12));
+    a.kl = o.weight * T * T;
+    a.ce = 1.0 - o.weight;
+    a.slope = static_cast<float>(o.weight * T);
+    a.row0 = 0;
+    return a;
+}
+
+bool two_sums(const Distil& o) { return o.weight > 0.0 && o.weight < 1.0 && o.temperature != 1.0; }
+
+}  // namespace
+
+ks_status_t launch_distil_count(const ks_logits_t& x, float* inv, hipStream_t stream) {
+    return launch_kernel(distil_count_kernel, dim3(1), dim3(1024), 0, stream, x, inv);
+}
+
+ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, const float* inv, float* loss,
+                              hipStream_t stream) {
+    return launch_kernel(distil_sum_kernel, dim3(1), dim3(1024), 0, stream, tokens, x.sequences * x.tokens, inv, loss);
+}
+
+ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens,
+                                 float* stats, hipStream_t stream) {
+    DistilArgs a = distil_args(x, t, o);
+    const bool two = two_sums(o);
+    const auto kernel = x.elem == KS_ELEM_BF16
+                            ? (two ? distil_tokens_kernel<bf16_t, true> : distil_tokens_kernel<bf16_t, false>)
+                            : (two ? distil_tokens_kernel<float, true> : distil_tokens_kernel<float, false>);
+    const int64_t rows = x.sequences * x.tokens;
+    for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid) {
+        const ks_status_t st = launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(kMaxGrid, rows - a.row0))),
+                                             dim3(kThreads), 0, stream, a, tokens, stats);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
+ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, const float* stats,
+                               const float* inv, const float* upstream, void* d, int64_t d_seq, int64_t d_row,
+                               hipStream_t stream) {
+    DistilArgs a = distil_args(x, t, o);
+    const bool two = two_sums(o);
+    const int64_t rows = x.sequences * x.tokens;
+    for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid) {
+        const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid, rows - a.row0)));
+        const ks_status_t st =
+            x.elem == KS_ELEM_BF16
+                ? launch_kernel(two ? distil_grad_kernel<bf16_t, true> : distil_grad_kernel<bf16_t, false>, grid,
+                                dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<bf16_t*>(d), d_seq, d_row)
+                : launch_kernel(two ? distil_grad_kernel<float, true> : distil_grad_kernel<float, false>, grid,
+                                dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<float*>(d), d_seq, d_row);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
+}  // namespace ks

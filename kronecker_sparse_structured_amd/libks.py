@@ -23,7 +23,7 @@ import array
 import ctypes
 import operator
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libks.so")
@@ -99,8 +99,42 @@ class ks_adamw_options_t(ctypes.Structure):
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("state_bits", ctypes.c_int32)]
 
 
+class ks_teacher_t(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("top", ctypes.c_void_p),
+                ("id_seq_stride", ctypes.c_int64), ("id_row_stride", ctypes.c_int64),
+                ("top_seq_stride", ctypes.c_int64), ("top_row_stride", ctypes.c_int64),
+                ("count", ctypes.c_int32), ("id_bytes", ctypes.c_int32), ("elem", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ks_beams_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scores", ctypes.c_void_p), ("done", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("request_stride", ctypes.c_int64), ("beam_stride", ctypes.c_int64),
+                ("requests", ctypes.c_int64), ("vocab", ctypes.c_int64), ("eos", ctypes.c_int64),
+                ("length_penalty", ctypes.c_double), ("beams", ctypes.c_int32), ("elem", ctypes.c_int32)]
+
+
+class ks_state_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
+
+
+class ks_residual_norm_t(ctypes.Structure):
+    _fields_ = [("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("width", ctypes.c_int64),
+                ("eps", ctypes.c_double), ("residual", ctypes.c_double), ("kind", ctypes.c_int32),
+                ("elem", ctypes.c_int32), ("x_elem", ctypes.c_int32), ("y_elem", ctypes.c_int32),
+                ("h_elem", ctypes.c_int32), ("gate_elem", ctypes.c_int32)]
+
+
+class ks_residual_norm_grads_t(ctypes.Structure):
+    _fields_ = [("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 # ks_elem_t
 ELEM_F32, ELEM_BF16 = 0, 1
+# ks_norm_t
+NORMS = {"rms": 0, "layer": 1}
 
 _lib = None
 
@@ -170,6 +204,8 @@ def load(path: str = LIB_PATH):
     lib.ks_matmul_dw_noalloc.restype = i32
     pp, pa, pl, pt = (ctypes.POINTER(t) for t in (ks_pattern_t, ks_adapters_t, ks_logits_t, ks_adamw_tensor_t))
     f32, size, psize = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    pk, pb, pn = (ctypes.POINTER(t) for t in (ks_teacher_t, ks_beams_t, ks_residual_norm_t))
+    f64 = ctypes.c_double
     for name, args in {
         "ks_adapter_workspace_size": [pa, i64, psize],
         "ks_adapter_matmul": [pa, vp, vp, vp, vp, i64, i32, vp, size, vp],
@@ -189,6 +225,15 @@ def load(path: str = LIB_PATH):
         "ks_grad_norm": [pt, i32, vp, vp, size, vp],
         "ks_adamw_step": [pt, i32, ctypes.POINTER(ks_adamw_options_t), vp, vp],
         "ks_adamw_state_values": [pt, i32, ctypes.POINTER(vp), ctypes.POINTER(vp), vp],
+        "ks_distil_loss": [pl, pk, f64, f64, vp, vp, vp, vp, i64, i64, vp],
+        "ks_distil_backward": [pl, pk, f64, f64, vp, vp, vp, i64, i64, vp],
+        "ks_beam_workspace_size": [pb, i32, psize],
+        "ks_beam_select": [pb, i32, vp, vp, vp, vp, vp, vp, size, vp],
+        "ks_beam_reorder": [ctypes.POINTER(ks_state_t), i32, vp, i64, i32, i32, vp],
+        "ks_residual_norm": [pn, vp, vp, vp, i64, vp, vp, vp, i64, vp],
+        "ks_residual_norm_backward_workspace_size": [pn, i64, i64, psize],
+        "ks_residual_norm_backward": [pn, vp, vp, vp, vp, vp, i64, vp, vp, vp,
+                                      ctypes.POINTER(ks_residual_norm_grads_t), vp, i64, vp, size, vp],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -856,6 +901,322 @@ def _preference_backward(logits, labels, scratch, upstream):
     _raise(load().ks_preference_backward(x, at + 4 * x.sequences, at, _ptr(upstream), dlogits.data_ptr(), d_seq, d_row,
                                          _raw_stream(logits.get_device())), "ks_preference_backward", True)
     return dlogits
+
+
+# ---------------------------------------------------------------- distillation
+
+def _teacher(ids, top, logits) -> ks_teacher_t:
+    import torch
+    if ids.dim() != 3 or ids.shape != top.shape or ids.shape[:2] != logits.shape[:2]:
+        raise ValueError("ids and top must be (sequences, tokens, count)")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    if ids.get_device() != logits.get_device() or top.get_device() != logits.get_device():
+        raise ValueError("ids and top must be on the logits' device")
+    return ks_teacher_t(ids.data_ptr(), top.data_ptr(), *_layout(ids, "ids"), *_layout(top, "top"), ids.shape[2],
+                        ids.element_size(), _elem(top.dtype, "top"), 0)
+
+
+def _distil_forward(logits, labels, ids, top, weight, temperature, dlogits=None):
+    """(loss, tokens, stats): stats as ks_distil_backward reads them."""
+    import torch
+    x = _logits(logits, labels)
+    t = _teacher(ids, top, logits)
+    d_seq = d_row = 0
+    if dlogits is not None:
+        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype \
+                or dlogits.get_device() != logits.get_device():
+            raise ValueError("dlogits must have the logits' shape, type and device")
+        d_seq, d_row = _layout(dlogits, "dlogits")
+    S, T = x.sequences, x.tokens
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    tokens, stats = loss.new_empty(S, T), loss.new_empty(3 * S * T + 1)
+    _raise(load().ks_distil_loss(x, t, weight, temperature, loss.data_ptr(), tokens.data_ptr(), stats.data_ptr(),
+                                 _ptr(dlogits), d_seq, d_row, _raw_stream(logits.get_device())), "ks_distil_loss", True)
+    return loss, tokens, stats
+
+
+def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0, dlogits=None, grad=True, stream=None):
+    """(loss, tokens, dlogits) of distillation from a teacher's highest logits
+    `top` (S, T, K), fp32 or bf16, of the tokens `ids` (S, T, K), int32 or int64
+    (negative: no entry): weight times temperature^2 times the divergence of the
+    student's probabilities from the teacher's over its K, plus 1 - weight times
+    the labels' cross entropy, the mean over the tokens that labels (S, T) int64
+    does not mask (negative). logits (S, T, V) fp32 or bf16. dlogits may be given
+    (the logits themselves too: then it replaces them); with grad=False there is
+    none."""
+    import torch
+    if stream is not None:
+        _logits(logits, labels)
+        return _on_stream(stream, logits.device, distillation_loss, logits, labels, ids, top, weight, temperature,
+                          dlogits, grad)
+    given = dlogits is not None
+    if given and not grad:
+        raise ValueError("dlogits is given, but grad is not asked for")
+    if grad and not given:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    loss, tokens, _ = _distil_forward(logits, labels, ids, top, weight, temperature, dlogits)
+    if given:
+        _wrote(dlogits)
+    return loss, tokens, dlogits
+
+
+def _distil_backward(logits, labels, ids, top, weight, temperature, stats, upstream):
+    import torch
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _raise(load().ks_distil_backward(_logits(logits, labels), _teacher(ids, top, logits), weight, temperature,
+                                     stats.data_ptr(), _ptr(upstream), dlogits.data_ptr(),
+                                     *_layout(dlogits, "dlogits"), _raw_stream(logits.get_device())),
+           "ks_distil_backward", True)
+    return dlogits
+
+
+# ---------------------------------------------------------------- beam search
+
+class Beams(NamedTuple):
+    """The best candidates of each request, best first, (requests, beams) each."""
+    scores: object     # fp32: sums of log probabilities, -inf where there is no candidate left
+    tokens: object     # int64
+    parents: object    # int32: the beam that each continues
+    done: object       # bool, or None without an eos
+    lengths: object    # int32, or None where none were given
+
+
+def beam_select(logits, scores, beams=None, done=None, lengths=None, eos=None, length_penalty=0.0, stream=None):
+    """The best `beams` (default: as many as there are) continuations of each
+    request's beams, as a Beams. logits (R, W, V) fp32 or bf16 with any row
+    strides; scores (R, W) fp32, -inf for a beam that is not there; done (R, W)
+    bool: beams that ended and go on as they are; lengths (R, W) int32. Ranked by
+    score / max(length, 1)^length_penalty, equal ones by beam and token."""
+    import torch
+    if logits.dim() != 3:
+        raise ValueError("logits must be (requests, beams, vocab)")
+    R, W, V = logits.shape
+    at = logits.get_device()
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    for t, name, kind in ((scores, "scores", torch.float32), (done, "done", torch.bool),
+                          (lengths, "lengths", torch.int32)):
+        if t is not None and (t.shape != (R, W) or t.dtype is not kind or t.get_device() != at
+                              or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous (%d, %d) %s on the logits' device" % (name, R, W, kind))
+    if done is not None and eos is None:
+        raise ValueError("done needs an eos")
+    if length_penalty != 0 and lengths is None:
+        raise ValueError("length_penalty needs lengths")
+    if eos is not None and not 0 <= eos < V:
+        raise ValueError("eos must be a token")
+    if stream is not None:
+        return Beams(*_on_stream(stream, logits.device, _beam_select, logits, scores, beams, done, lengths, eos,
+                                 length_penalty))
+    return Beams(*_beam_select(logits, scores, beams, done, lengths, eos, length_penalty))
+
+
+def _beam_select(logits, scores, beams, done, lengths, eos, length_penalty):
+    import torch
+    R, W, V = logits.shape
+    beams = W if beams is None else beams
+    x = ks_beams_t(logits.data_ptr(), scores.data_ptr(), _ptr(done), _ptr(lengths), *_layout(logits, "logits"), R, V,
+                   -1 if eos is None else eos, length_penalty, W, _elem(logits.dtype, "logits"))
+    lib, size = load(), ctypes.c_size_t(0)
+    _raise(lib.ks_beam_workspace_size(x, beams, size), "ks_beam_workspace_size", True)
+    new = scores.new_empty
+    out = (new((R, beams)), new((R, beams), dtype=torch.int64), new((R, beams), dtype=torch.int32),
+           new((R, beams), dtype=torch.bool) if eos is not None else None,
+           new((R, beams), dtype=torch.int32) if lengths is not None else None)
+    ws = new((size.value + 3) // 4)
+    _raise(lib.ks_beam_select(x, beams, *map(_ptr, out), ws.data_ptr(), size.value, _raw_stream(logits.get_device())),
+           "ks_beam_select", True)
+    return out
+
+
+def beam_reorder(states, parents, out=None, stream=None):
+    """Each state (R, W, ...) with its rows in the order of the beams that
+    parents (R, beams) int32 names, as a list of (R, beams, ...): row [r][j] is
+    the state's row [r][parents[r][j]], zeros for a parent outside [0, W). `out`
+    may give the results' tensors; a state's own memory cannot be among them."""
+    import torch
+    if parents.dim() != 2 or parents.dtype is not torch.int32 or not parents.is_cuda or not parents.is_contiguous():
+        raise ValueError("parents must be a contiguous (requests, beams) int32 device tensor")
+    (R, beams), at = parents.shape, parents.get_device()
+    if out is not None and len(out) != len(states):
+        raise ValueError("one tensor of out for each state")
+    if not states:
+        return []
+    W = states[0].shape[1] if states[0].dim() > 1 else 0
+    for t in states:
+        if t.dim() < 2 or t.shape[0] != R or t.shape[1] != W or t.get_device() != at or not t.is_contiguous():
+            raise ValueError("states must be contiguous (%d, beams, ...) on the parents' device" % R)
+    if out is not None:
+        for t, o in zip(states, out):
+            if o.shape != (R, beams, *t.shape[2:]) or o.dtype != t.dtype or o.get_device() != at \
+                    or not o.is_contiguous():
+                raise ValueError("out must hold contiguous (%d, %d, ...) tensors of the states' types" % (R, beams))
+    if stream is not None:
+        return list(_on_stream(stream, parents.device, _beam_reorder, states, parents, out))
+    return list(_beam_reorder(states, parents, out))
+
+
+def _beam_reorder(states, parents, out):
+    R, beams = parents.shape
+    W = states[0].shape[1]
+    new = out if out is not None else [t.new_empty((R, beams, *t.shape[2:])) for t in states]
+    rows = max(R * W, 1)
+    table = (ks_state_t * len(states))(*[(t.data_ptr(), o.data_ptr(), t.nbytes // rows) for t, o in zip(states, new)])
+    _raise(load().ks_beam_reorder(table, len(states), parents.data_ptr(), R, W, beams,
+                                  _raw_stream(parents.get_device())), "ks_beam_reorder", True)
+    if out is not None:
+        _wrote(list(out))
+    return tuple(new)
+
+
+# ---------------------------------------------------------------- norms between layers
+
+class NormGrads(NamedTuple):
+    """Gradients of a ResidualNorm; None for what it has not."""
+    dx: object
+    dy: object
+    gate: object
+    pre_weight: object
+    pre_bias: object
+    post_weight: object
+    post_bias: object
+    scale: object
+
+
+class ResidualNorm:
+    """The norms around a block, with its gate and the residual: for rows of
+    `width` values
+        u = post(y),  z = x + residual scale . gate . u,  h = pre(z)
+    where pre and post are norms ("rms" or "layer") with a weight and maybe a
+    bias of `width` values, left out where no weight is given.
+
+    The handle keeps the vectors, of one type (fp32 or bf16), and their
+    addresses; later in-place changes of them are seen."""
+
+    def __init__(self, width, pre_weight=None, pre_bias=None, post_weight=None, post_bias=None, scale=None, kind="rms",
+                 eps=1e-6, residual=1.0):
+        self.width = int(width)
+        self.vectors = {"pre_weight": pre_weight, "pre_bias": pre_bias, "post_weight": post_weight,
+                        "post_bias": post_bias, "scale": scale}
+        given = [t for t in self.vectors.values() if t is not None]
+        if kind not in NORMS:
+            raise ValueError("kind must be one of %s" % ", ".join(NORMS))
+        if (pre_bias is not None and pre_weight is None) or (post_bias is not None and post_weight is None):
+            raise ValueError("a norm's bias needs its weight")
+        for name, t in self.vectors.items():
+            if t is None:
+                continue
+            _check_tensor(t, name)
+            if t.shape != (self.width,):
+                raise ValueError("%s must be (%d,)" % (name, self.width))
+            if t.dtype != given[0].dtype:
+                raise TypeError("all vectors must have one type")
+            if t.device != given[0].device:
+                raise ValueError("all vectors must be on one device")
+        self._index = given[0].get_device() if given else None
+        self._n = ks_residual_norm_t(*[_ptr(t) for t in self.vectors.values()], self.width, eps, residual, NORMS[kind],
+                                     _elem(given[0].dtype, "vectors") if given else ELEM_F32)
+        self._pre = pre_weight is not None
+        self._lib = load()
+        self._sizes = {}
+
+    def _rows(self, x, y, gate):
+        """(rows, groups, the struct with the types) of a call."""
+        if x.dim() != 2 or x.shape[1] != self.width:
+            raise ValueError("x must be (rows, %d)" % self.width)
+        if not x.is_cuda or (self._index is not None and x.get_device() != self._index):
+            raise ValueError("x must be on the vectors' device")
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+        n, at, rows = ks_residual_norm_t.from_buffer_copy(self._n), x.get_device(), x.shape[0]
+        n.x_elem = _elem(x.dtype, "x")
+        if y is None:
+            if gate is not None:
+                raise ValueError("a gate needs a y")
+            return rows, 0, n
+        if y.shape != x.shape or y.get_device() != at or not y.is_contiguous():
+            raise ValueError("y must be contiguous %s on x's device" % (tuple(x.shape),))
+        n.y_elem = _elem(y.dtype, "y")
+        if gate is None:
+            return rows, 0, n
+        if gate.dim() != 2 or gate.shape[1] != self.width or gate.get_device() != at or not gate.is_contiguous():
+            raise ValueError("gate must be contiguous (groups, %d) on x's device" % self.width)
+        groups = gate.shape[0]
+        if groups == 0 and rows > 0 or groups > 0 and rows % groups:
+            raise ValueError("gate must have a row for each of equally many rows")
+        n.gate_elem = _elem(gate.dtype, "gate")
+        return rows, groups, n
+
+    def forward(self, x, y=None, gate=None, dtype=None, keep=False, stream=None):
+        """(z, h), or (z, h, stats) with keep=True, stats for backward(). x (rows,
+        width) and y fp32 or bf16 (no y: z is x itself, h the norm alone), gate
+        (groups, width), each for rows / groups rows one after another. z has x's
+        type; h (None without a pre norm) `dtype`, x's by default."""
+        if stream is not None:
+            z, h, *stats = _on_stream(stream, x.device, self._forward, x, y, gate, dtype, keep)
+            return (x if y is None else z, h, *stats)
+        return self._forward(x, y, gate, dtype, keep)
+
+    def _forward(self, x, y, gate, dtype, keep):
+        import torch
+        rows, groups, n = self._rows(x, y, gate)
+        z = h = stats = None
+        if y is not None:
+            z = x.new_empty(rows, self.width)
+        if self._pre:
+            dtype = x.dtype if dtype is None else dtype
+            n.h_elem = _elem(dtype, "h")
+            h = x.new_empty((rows, self.width), dtype=dtype)
+        if keep:
+            stats = x.new_empty((rows, 4), dtype=torch.float32)
+        if y is not None or self._pre:
+            _raise(self._lib.ks_residual_norm(n, x.data_ptr(), _ptr(y), _ptr(gate) if groups else None, groups, _ptr(z),
+                                              _ptr(h), _ptr(stats), rows, _raw_stream(x.get_device())),
+                   "ks_residual_norm", True)
+        z = x if y is None else z
+        return (z, h, stats) if keep else (z, h)
+
+    def backward(self, dz, dh, x, y, stats, gate=None, weights=True, stream=None):
+        """A NormGrads, from the gradients dz of z and dh of h (None: zero) and
+        from x, y, gate and stats as forward() had and gave them. dx and dy have
+        x's and y's type, the gate's its own, the vectors' are fp32 (None with
+        weights=False)."""
+        if stream is not None:
+            return NormGrads(*_on_stream(stream, x.device, self._backward, dz, dh, x, y, stats, gate, weights))
+        return NormGrads(*self._backward(dz, dh, x, y, stats, gate, weights))
+
+    def _backward(self, dz, dh, x, y, stats, gate, weights):
+        import torch
+        rows, groups, n = self._rows(x, y, gate)
+        if dz is not None:
+            _check_out(dz, tuple(x.shape), x.dtype, x.device, "dz")
+        if dh is not None:
+            if not self._pre:
+                raise ValueError("dh is given, but there is no pre norm")
+            n.h_elem = _elem(dh.dtype, "dh")
+            _check_out(dh, tuple(x.shape), dh.dtype, x.device, "dh")
+        _check_out(stats, (rows, 4), torch.float32, x.device, "stats")
+        dx = x.new_empty(rows, self.width)
+        dy = y.new_empty(rows, self.width) if y is not None else None
+        dgate = gate.new_empty(groups, self.width) if gate is not None else None
+        f32 = torch.float32
+        grads = [x.new_empty(self.width, dtype=f32) if weights and t is not None else None
+                 for t in self.vectors.values()]
+        size = self._sizes.get((rows, groups))
+        if size is None:
+            need = ctypes.c_size_t(0)
+            _raise(self._lib.ks_residual_norm_backward_workspace_size(n, rows, groups, need),
+                   "ks_residual_norm_backward_workspace_size", True)
+            if len(self._sizes) > 256:
+                self._sizes.clear()
+            size = self._sizes[rows, groups] = need.value
+        ws = x.new_empty(size // 4, dtype=f32) if size else None
+        _raise(self._lib.ks_residual_norm_backward(
+            n, _ptr(dz), _ptr(dh), x.data_ptr(), _ptr(y), _ptr(gate) if groups else None, groups, stats.data_ptr(),
+            dx.data_ptr(), _ptr(dy), ks_residual_norm_grads_t(*map(_ptr, grads)), _ptr(dgate) if groups else None, rows,
+            _ptr(ws), size, _raw_stream(x.get_device())), "ks_residual_norm_backward", True)
+        return (dx, dy, dgate, *grads)
 
 
 # ---------------------------------------------------------------- optimizer
