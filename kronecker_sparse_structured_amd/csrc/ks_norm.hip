@@ -17,10 +17,15 @@
 // rows with its columns' sums in registers; a second launch adds up the workers'
 // parts in a fixed order.
 //
-// A worker is 1 to 16 waves, 8 values a lane (width <= 512 a wave). Sums over a
+// A worker is 1 to 16 waves, 4 values a lane (8 above 4096 columns). Sums over a
 // row are formed in the wave and then, for more than one wave, over LDS. The
 // variance is the mean of squared differences from the mean, not a difference
-// of two large sums.
+// of two large sums. The vectors stay in registers from row to row and the next
+// row is on its way while this one's sums are formed.
+//
+// The gradients of post's vectors and of the scale need two sums, not three:
+// with t = c dx . g,  P = sum t yn  and  Q = sum t,
+//   dw2 = s P,  db2 = s Q,  ds = w2 P + b2 Q.
 
 #include <algorithm>
 
@@ -31,85 +36,147 @@
 namespace ks {
 namespace {
 
-constexpr int kLane = 8;        // values a lane holds
-constexpr int kWaveCols = 64 * kLane;
+constexpr int kNarrow = 4096;   // columns up to which a lane holds 4
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Waves of a worker: a power of two, so that workers fill a workgroup.
+int worker_waves(int64_t width) {
+    const int64_t cols = 64 * (width <= kNarrow ? 4 : 8);
+    int w = 1;
+    while (w * cols < width) w *= 2;
+    return w;
+}
 
-// Where a lane's values lie in a row. WIDE: eight neighbours, in 16-byte
-// accesses. Else (a row of any width at any address) one value of each stretch
-// of the row as long as the worker is wide.
-template <bool WIDE>
+// A lane's L values of a row as they are loaded. WIDE: neighbours, in accesses
+// of up to 16 bytes. Else (a row of any width at any address) one value of each
+// stretch of the row as long as the worker is wide.
+template <typename T, int L, bool WIDE>
+struct Raw {
+    static constexpr int kWords = L * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[WIDE ? kWords : L];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (WIDE) return i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
+        else return bf16_lo(w[i]);
+    }
+};
+
+template <int L, bool WIDE>
 struct Lanes {
     int t, threads, width;
-    __device__ __forceinline__ int at(int i) const { return WIDE ? t * kLane + i : i * threads + t; }
-    __device__ __forceinline__ bool in(int i) const { return WIDE ? t * kLane < width : at(i) < width; }
+    __device__ __forceinline__ int at(int i) const { return WIDE ? t * L + i : i * threads + t; }
+    __device__ __forceinline__ bool in(int i) const { return WIDE ? t * L < width : at(i) < width; }
 
     template <typename T>
-    __device__ __forceinline__ void load(const T* row, float (&v)[kLane]) const {
+    __device__ __forceinline__ void load(const T* row, Raw<T, L, WIDE>& r) const {
         if constexpr (WIDE) {
-            load8<true>(row + t * kLane, t * kLane < width ? kLane : 0, v);
-        } else {
+            constexpr int W = Raw<T, L, WIDE>::kWords, V = W < 4 ? W : 4;
+            typedef uint32_t vec __attribute__((ext_vector_type(V)));
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) v[i] = in(i) ? to_f32(row[at(i)]) : 0.0f;
-        }
-    }
-    __device__ __forceinline__ void load(const void* row, int elem, float (&v)[kLane]) const {
-        if (elem == KS_ELEM_BF16) load(static_cast<const bf16_t*>(row), v);
-        else load(static_cast<const float*>(row), v);
-    }
-    template <typename T>
-    __device__ __forceinline__ void store(T* row, const float (&v)[kLane]) const {
-        if constexpr (WIDE) {
-            if (t * kLane >= width) return;
-            if constexpr (sizeof(T) == 4) {
-                f32x4* p = reinterpret_cast<f32x4*>(row + t * kLane);
-                p[0] = f32x4{v[0], v[1], v[2], v[3]};
-                p[1] = f32x4{v[4], v[5], v[6], v[7]};
-            } else {
-                u32x4 w;
+            for (int k = 0; k < W; k += V) {
+                vec v = 0;
+                if (t * L < width) v = *reinterpret_cast<const vec*>(row + t * L + k * 4 / static_cast<int>(sizeof(T)));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                *reinterpret_cast<u32x4*>(row + t * kLane) = w;
+                for (int i = 0; i < V; ++i) r.w[k + i] = v[i];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) {
+            for (int i = 0; i < L; ++i) {
+                if constexpr (sizeof(T) == 4) r.w[i] = in(i) ? __float_as_uint(row[at(i)]) : 0u;
+                else r.w[i] = in(i) ? row[at(i)] : 0u;
+            }
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T* row, float (&v)[L]) const {
+        Raw<T, L, WIDE> r;
+        load(row, r);
+#pragma unroll
+        for (int i = 0; i < L; ++i) v[i] = r.get(i);
+    }
+    __device__ __forceinline__ void load(const void* row, int elem, float (&v)[L]) const {
+        if (elem == KS_ELEM_BF16) load(static_cast<const bf16_t*>(row), v);
+        else load(static_cast<const float*>(row), v);
+    }
+    // values of `size` bytes, one row after another
+    __device__ __forceinline__ void load(const void* rows, int64_t row, int elem, float (&v)[L]) const {
+        load(static_cast<const char*>(rows) + row * width * (elem == KS_ELEM_BF16 ? 2 : 4), elem, v);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, const float (&v)[L]) const {
+        if constexpr (WIDE) {
+            if (t * L >= width) return;
+            constexpr int W = Raw<T, L, WIDE>::kWords, V = W < 4 ? W : 4;
+            typedef uint32_t vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+            for (int k = 0; k < W; k += V) {
+                vec w;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[k + i]);
+                    else w[i] = pack_bf16(v[2 * (k + i)], v[2 * (k + i) + 1]);
+                }
+                *reinterpret_cast<vec*>(row + t * L + k * 4 / static_cast<int>(sizeof(T))) = w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
                 if (!in(i)) continue;
                 if constexpr (sizeof(T) == 4) row[at(i)] = v[i];
                 else row[at(i)] = to_bf16(v[i]);
             }
         }
     }
-    __device__ __forceinline__ void store(void* row, int elem, const float (&v)[kLane]) const {
-        if (elem == KS_ELEM_BF16) store(static_cast<bf16_t*>(row), v);
-        else store(static_cast<float*>(row), v);
+    __device__ __forceinline__ void store(void* rows, int64_t row, int elem, const float (&v)[L]) const {
+        if (elem == KS_ELEM_BF16) store(static_cast<bf16_t*>(rows) + row * width, v);
+        else store(static_cast<float*>(rows) + row * width, v);
     }
 };
+
+template <int L>
+__device__ __forceinline__ void fill(float (&v)[L], float x) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] = x;
+}
+
+// The wave's sums of a and b, in every lane. Exchanges within 16 lanes, then
+// lane 15 of a row of 16 to the next row, lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ void wave_sums(float& a, float& b) {
+    a += moved<0xb1, 0xf>(a);       // lane ^ 1
+    b += moved<0xb1, 0xf>(b);
+    a += moved<0x4e, 0xf>(a);       // lane ^ 2
+    b += moved<0x4e, 0xf>(b);
+    a += moved<0x141, 0xf>(a);      // mirrored in 8 lanes
+    b += moved<0x141, 0xf>(b);
+    a += moved<0x140, 0xf>(a);      // mirrored in 16
+    b += moved<0x140, 0xf>(b);
+    a += moved<0x142, 0xa>(a);      // lane 15 to rows 1 and 3
+    b += moved<0x142, 0xa>(b);
+    a += moved<0x143, 0xc>(a);      // lane 31 to rows 2 and 3
+    b += moved<0x143, 0xc>(b);
+    a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a), 63));
+    b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(b), 63));
+}
 
 // Sums over the waves of a worker. Two buffers in turn: a wave that writes one
 // for the next sum but one has passed the barrier that all waves reach after
 // they read it.
 struct RowSums {
-    float (*buf)[16][2];
+    float2 (*buf)[16];
     int wave, first, waves, turn;   // of the workgroup; of the worker; its waves
     __device__ __forceinline__ void operator()(float& a, float& b) {
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            a += __shfl_xor(a, d, 64);
-            b += __shfl_xor(b, d, 64);
-        }
+        wave_sums(a, b);
         if (waves == 1) return;
-        if (threadIdx.x % 64 == 0) {
-            buf[turn][wave][0] = a;
-            buf[turn][wave][1] = b;
-        }
+        if (threadIdx.x % 64 == 0) buf[turn][wave] = make_float2(a, b);
         lds_barrier();
         a = b = 0.0f;
         for (int w = first; w < first + waves; ++w) {
-            a += buf[turn][w][0];
-            b += buf[turn][w][1];
+            const float2 v = buf[turn][w];
+            a += v.x;
+            b += v.y;
         }
         turn ^= 1;
     }
@@ -121,26 +188,26 @@ struct NormArgs {
     const void* y;
     const void* gate;
     int64_t group_rows;     // 0: no gate
-    int64_t row0, rows;     // rows of this launch: row0 .. rows - 1
+    int64_t rows;
     int waves;              // a worker
     float eps, residual, inverse;   // inverse: 1 / width
 };
 
 // Mean (layer norm) and 1 / deviation of the row's values.
-template <bool WIDE>
-__device__ __forceinline__ void deviation(const Lanes<WIDE>& l, RowSums& sums, const NormArgs& a,
-                                          const float (&v)[kLane], float& mean, float& r) {
+template <int L, bool WIDE>
+__device__ __forceinline__ void deviation(const Lanes<L, WIDE>& l, RowSums& sums, const NormArgs& a, const float (&v)[L],
+                                          float& mean, float& r) {
     mean = 0.0f;
     float none = 0.0f;
     if (a.n.kind == KS_NORM_LAYER) {
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) mean += v[i];
+        for (int i = 0; i < L; ++i) mean += v[i];
         sums(mean, none);
         mean *= a.inverse;
     }
     float square = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) {
+    for (int i = 0; i < L; ++i) {
         const float d = l.in(i) ? v[i] - mean : 0.0f;
         square += d * d;
     }
@@ -148,76 +215,75 @@ __device__ __forceinline__ void deviation(const Lanes<WIDE>& l, RowSums& sums, c
     r = 1.0f / sqrtf(square * a.inverse + a.eps);
 }
 
-template <typename XT, typename YT, typename HT, bool WIDE>
+template <typename XT, typename YT, typename HT, int L, bool WIDE>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT* h, float* stats) {
-    __shared__ float buf[2][16][2];
+    __shared__ float2 buf[2][16];
     const int wave = threadIdx.x / 64, worker = wave / a.waves;
     const int width = static_cast<int>(a.n.width);
-    const Lanes<WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
+    const Lanes<L, WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
     RowSums sums{buf, wave, worker * a.waves, a.waves, 0};
-    const int64_t at = a.row0 + static_cast<int64_t>(blockIdx.x) * (blockDim.x / 64 / a.waves) + worker;
-    const bool on = at < a.rows;
-    const int64_t row = on ? at : a.rows - 1;       // a worker without a row goes through the barriers
-    float v[kLane], mean1 = 0.0f, r1 = 1.0f, mean2 = 0.0f, r2 = 1.0f;
-    l.load(static_cast<const XT*>(a.x) + row * width, v);
-    if (a.y) {
-        float u[kLane], w[kLane];
-        l.load(static_cast<const YT*>(a.y) + row * width, u);
-        if (a.n.post_weight) {
-            deviation(l, sums, a, u, mean2, r2);
-            l.load(a.n.post_weight, a.n.elem, w);
+    const int each = blockDim.x / 64 / a.waves;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * each;
+    const XT* X = static_cast<const XT*>(a.x);
+    const YT* Y = static_cast<const YT*>(a.y);
+    int64_t first = static_cast<int64_t>(blockIdx.x) * each;       // of the workgroup's rows
+    Raw<XT, L, WIDE> nx;
+    Raw<YT, L, WIDE> ny = {};
+    float gate[L], w1[L], b1[L], w2[L], b2[L], s[L];
+    // a worker without a row goes through the barriers with the last one
+    auto fetch = [&](int64_t row) {
+        l.load(X + row * width, nx);
+        if (Y) l.load(Y + row * width, ny);
+    };
+    fetch(min(first + worker, a.rows - 1));
+    fill(w1, 0.0f);
+    fill(b1, 0.0f);
+    fill(w2, 1.0f);
+    fill(b2, 0.0f);
+    fill(s, 1.0f);
+    fill(gate, 1.0f);
+    if (a.n.post_weight) l.load(a.n.post_weight, a.n.elem, w2);
+    if (a.n.post_bias) l.load(a.n.post_bias, a.n.elem, b2);
+    if (a.n.scale) l.load(a.n.scale, a.n.elem, s);
+    if (a.n.pre_weight) l.load(a.n.pre_weight, a.n.elem, w1);
+    if (a.n.pre_bias) l.load(a.n.pre_bias, a.n.elem, b1);
+    for (; first < a.rows; first += step) {
+        const int64_t row = min(first + worker, a.rows - 1);
+        const bool on = first + worker < a.rows;
+        float v[L], u[L], mean1 = 0.0f, r1 = 1.0f, mean2 = 0.0f, r2 = 1.0f;
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) u[i] = (u[i] - mean2) * r2 * w[i];
-            if (a.n.post_bias) {
-                l.load(a.n.post_bias, a.n.elem, w);
-#pragma unroll
-                for (int i = 0; i < kLane; ++i) u[i] += w[i];
-            }
+        for (int i = 0; i < L; ++i) {
+            v[i] = nx.get(i);
+            u[i] = ny.get(i);
         }
-        if (a.n.scale) {
-            l.load(a.n.scale, a.n.elem, w);
+        if (a.gate) l.load(a.gate, row / a.group_rows, a.n.gate_elem, gate);
+        if (first + step < a.rows) fetch(min(row + step, a.rows - 1));
+        if (Y) {
+            if (a.n.post_weight) deviation(l, sums, a, u, mean2, r2);
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) u[i] *= w[i];
+            for (int i = 0; i < L; ++i) v[i] += a.residual * (((u[i] - mean2) * r2 * w2[i] + b2[i]) * s[i] * gate[i]);
+            if (on) l.store(z + row * width, v);
         }
-        if (a.gate) {
-            const int64_t g = row / a.group_rows;
-            l.load(static_cast<const char*>(a.gate) + g * width * (a.n.gate_elem == KS_ELEM_BF16 ? 2 : 4),
-                   a.n.gate_elem, w);
+        if (a.n.pre_weight) {
+            deviation(l, sums, a, v, mean1, r1);
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) u[i] *= w[i];
+            for (int i = 0; i < L; ++i) v[i] = (v[i] - mean1) * r1 * w1[i] + b1[i];
+            if (on) l.store(h + row * width, v);
         }
-#pragma unroll
-        for (int i = 0; i < kLane; ++i) v[i] += a.residual * u[i];
-        if (on) l.store(z + row * width, v);
-    }
-    if (a.n.pre_weight) {
-        float w[kLane];
-        deviation(l, sums, a, v, mean1, r1);
-        l.load(a.n.pre_weight, a.n.elem, w);
-#pragma unroll
-        for (int i = 0; i < kLane; ++i) v[i] = (v[i] - mean1) * r1 * w[i];
-        if (a.n.pre_bias) {
-            l.load(a.n.pre_bias, a.n.elem, w);
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) v[i] += w[i];
-        }
-        if (on) l.store(h + row * width, v);
-    }
-    if (stats && on && l.t == 0) {
-        *reinterpret_cast<f32x4*>(stats + 4 * row) = f32x4{mean1, r1, mean2, r2};
+        if (stats && on && l.t == 0) *reinterpret_cast<float4*>(stats + 4 * row) = make_float4(mean1, r1, mean2, r2);
     }
 }
 
-// The workers' parts of the vectors' gradients, one vector after another, each
-// workgroups x width; then, where workers share a gate, theirs of the gate's,
-// workers x width.
+// The workgroups' parts of the vectors' sums: dw1, db1, P and Q, those that are
+// wanted, one after another, each workgroups x width; then, where workers share
+// a gate, theirs of the gate's, workers x width.
 struct NormParts {
-    float* vectors;
+    float* sums;
     float* gates;
     int64_t workgroups;
-    int want;               // bit k: the k-th vector's gradient
+    int want;               // bit k: the k-th sum
 };
-constexpr int kVectors = 5;
+constexpr int kSums = 4;
 
 struct NormGrad {
     const void* dz;
@@ -230,18 +296,17 @@ struct NormGrad {
     NormParts parts;
 };
 
-template <typename XT, typename YT, typename HT, bool WIDE>
+template <typename XT, typename YT, typename HT, int L, bool WIDE>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const NormGrad g) {
-    extern __shared__ float lds[];
-    float (*buf)[16][2] = reinterpret_cast<float (*)[16][2]>(lds);
-    float* join = lds + 2 * 16 * 2;                // a row of the worker's columns
+    extern __shared__ float join[];                // a row of the worker's columns, or its sums
+    __shared__ float2 buf[2][16];
     const int wave = threadIdx.x / 64, worker = wave / a.waves, workers = blockDim.x / 64 / a.waves;
     const int width = static_cast<int>(a.n.width);
-    const Lanes<WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
+    const Lanes<L, WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
     RowSums sums{buf, wave, worker * a.waves, a.waves, 0};
     const int64_t id = static_cast<int64_t>(blockIdx.x) * workers + worker;
     // the worker's rows, and the one at which its gate's sum is complete
-    int64_t row = id * g.split.per, end = row + g.split.per, gate_end = 0;
+    int64_t row = id * g.split.per, end = row + g.split.per;
     if (g.split.chunks > 1) {
         const int64_t group = id / g.split.chunks, chunk = id - group * g.split.chunks;
         row = group * g.split.group_rows + chunk * g.split.per;
@@ -249,54 +314,83 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     }
     if (id >= g.split.workers) row = end = 0;
     end = min(end, a.rows);
-    gate_end = g.split.chunks > 1 ? end : row + g.split.group_rows;
+    int64_t gate_end = g.split.chunks > 1 ? end : row + g.split.group_rows;
     const bool layer = a.n.kind == KS_NORM_LAYER;
-    float sum[kVectors][kLane], dg[kLane];
+    const XT* X = static_cast<const XT*>(a.x);
+    const YT* Y = static_cast<const YT*>(a.y);
+    const XT* DZ = static_cast<const XT*>(g.dz);
+    const HT* DH = static_cast<const HT*>(g.dh);
+    Raw<XT, L, WIDE> nx, nz = {};
+    Raw<YT, L, WIDE> ny = {};
+    Raw<HT, L, WIDE> nh = {};
+    float4 next = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    auto fetch = [&](int64_t at) {
+        l.load(X + at * width, nx);
+        if (Y) l.load(Y + at * width, ny);
+        if (DZ) l.load(DZ + at * width, nz);
+        if (DH) l.load(DH + at * width, nh);
+        if (g.stats) next = *reinterpret_cast<const float4*>(g.stats + 4 * at);
+    };
+    // above kNarrow columns 16 waves have no registers for the vectors, for a row
+    // ahead and for the sums: the first two are loaded where they are used, the
+    // sums are in LDS
+    constexpr bool kAhead = L == 4;
+    if (kAhead) fetch(row < end ? row : 0);
+    float held[kAhead ? kSums : 1][L], dg[L];
+    auto sum = [&](int k, int i) -> float& {
+        if constexpr (kAhead) return held[k][i];
+        else return join[(k * L + i) * blockDim.x + threadIdx.x];
+    };
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) zero(sum[k]);
-    zero(dg);
-    float w1[kLane], w2[kLane], b2[kLane], s[kLane], gate[kLane];
-    zero(w1);
-    zero(b2);
+    for (int k = 0; k < kSums; ++k)
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) w2[i] = s[i] = gate[i] = 1.0f;
-    if (a.n.pre_weight) l.load(a.n.pre_weight, a.n.elem, w1);
-    if (a.n.post_weight) l.load(a.n.post_weight, a.n.elem, w2);
-    if (a.n.post_bias) l.load(a.n.post_bias, a.n.elem, b2);
-    if (a.n.scale) l.load(a.n.scale, a.n.elem, s);
-    const int gate_size = a.n.gate_elem == KS_ELEM_BF16 ? 2 : 4;
+        for (int i = 0; i < L; ++i) sum(k, i) = 0.0f;
+    fill(dg, 0.0f);
+    float w1[L], w2[L], b2[L], s[L], gate[L];
+    auto vector = [&](const void* v, float none, float (&to)[L], bool now) {
+        if (!now) return;
+        fill(to, none);
+        if (v) l.load(v, a.n.elem, to);
+    };
+    vector(a.n.pre_weight, 0.0f, w1, kAhead);
+    vector(a.n.post_weight, 1.0f, w2, kAhead);
+    vector(a.n.post_bias, 0.0f, b2, kAhead);
+    vector(a.n.scale, 1.0f, s, kAhead);
+    fill(gate, 1.0f);
     // every worker goes through as many rounds: they meet at barriers
     for (int64_t k = 0; k < g.split.per; ++k, ++row) {
         const bool on = row < end;
-        const int64_t at = (on ? row : 0) * width;
-        float z[kLane], yn[kLane], u[kLane], d[kLane];
-        f32x4 st = {0.0f, 1.0f, 0.0f, 1.0f};
-        if (g.stats) st = *reinterpret_cast<const f32x4*>(g.stats + 4 * (on ? row : 0));
-        l.load(static_cast<const XT*>(a.x) + at, z);
-        if (a.y) {
-            l.load(static_cast<const YT*>(a.y) + at, yn);
-            if (a.gate) {
-                const int64_t group = on ? row / g.split.group_rows : 0;
-                l.load(static_cast<const char*>(a.gate) + group * width * gate_size, a.n.gate_elem, gate);
-            }
+        if (!kAhead) fetch(on ? row : 0);
+        float z[L], yn[L], d[L], dh[L];
+        const float4 st = next;
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-                if (a.n.post_weight) yn[i] = (yn[i] - st[2]) * st[3];
-                u[i] = yn[i] * w2[i] + b2[i];
-                z[i] += a.residual * u[i] * s[i] * gate[i];
+        for (int i = 0; i < L; ++i) {
+            z[i] = nx.get(i);
+            yn[i] = ny.get(i);
+            d[i] = nz.get(i);
+            dh[i] = nh.get(i);
+        }
+        if (a.gate) l.load(a.gate, on ? row / g.split.group_rows : 0, a.n.gate_elem, gate);
+        if (kAhead && row + 1 < end) fetch(row + 1);
+        if (Y) {
+            vector(a.n.post_weight, 1.0f, w2, !kAhead);
+            vector(a.n.post_bias, 0.0f, b2, !kAhead);
+            vector(a.n.scale, 1.0f, s, !kAhead);
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                if (a.n.post_weight) yn[i] = (yn[i] - st.z) * st.w;
+                z[i] += a.residual * ((yn[i] * w2[i] + b2[i]) * s[i] * gate[i]);
             }
         }
-        zero(d);
-        if (g.dz) l.load(static_cast<const XT*>(g.dz) + at, d);
-        if (g.dh) {
-            float dh[kLane], dot = 0.0f, plain = 0.0f;
-            l.load(static_cast<const HT*>(g.dh) + at, dh);
+        if (DH) {
+            float dot = 0.0f, plain = 0.0f;
+            vector(a.n.pre_weight, 0.0f, w1, !kAhead);
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-                z[i] = l.in(i) ? (z[i] - st[0]) * st[1] : 0.0f;
+            for (int i = 0; i < L; ++i) {
+                z[i] = l.in(i) ? (z[i] - st.x) * st.y : 0.0f;
                 if (on) {
-                    sum[0][i] += dh[i] * z[i];
-                    sum[1][i] += dh[i];
+                    sum(0, i) += dh[i] * z[i];
+                    if (kAhead || a.n.pre_bias) sum(1, i) += dh[i];
                 }
                 dh[i] *= w1[i];
                 dot += dh[i] * z[i];
@@ -306,22 +400,23 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             dot *= a.inverse;
             plain = layer ? plain * a.inverse : 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) d[i] += st[1] * (dh[i] - z[i] * dot - plain);
+            for (int i = 0; i < L; ++i) d[i] += st.y * (dh[i] - z[i] * dot - plain);
         }
-        if (on) l.store(static_cast<XT*>(g.dx) + at, d);
-        if (!a.y) continue;
+        if (on) l.store(static_cast<XT*>(g.dx) + row * width, d);
+        if (!Y) continue;
         float dot = 0.0f, plain = 0.0f;
+        vector(a.n.post_weight, 1.0f, w2, !kAhead);
+        vector(a.n.post_bias, 0.0f, b2, !kAhead);
+        vector(a.n.scale, 1.0f, s, !kAhead);
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-            const float t = a.residual * d[i], tu = t * u[i];
-            const float du = t * s[i] * gate[i];
+        for (int i = 0; i < L; ++i) {
+            const float t = a.residual * d[i], tg = t * gate[i];
             if (on) {
-                sum[4][i] += tu * gate[i];
-                sum[2][i] += du * yn[i];
-                sum[3][i] += du;
-                dg[i] += tu * s[i];
+                sum(2, i) += tg * yn[i];
+                if (kAhead || a.n.post_bias) sum(3, i) += tg;
+                dg[i] += t * (yn[i] * w2[i] + b2[i]) * s[i];
             }
-            d[i] = l.in(i) ? du * w2[i] : 0.0f;
+            d[i] = l.in(i) ? tg * s[i] * w2[i] : 0.0f;
             dot += d[i] * yn[i];
             plain += d[i];
         }
@@ -330,83 +425,115 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             dot *= a.inverse;
             plain = layer ? plain * a.inverse : 0.0f;
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) d[i] = st[3] * (d[i] - yn[i] * dot - plain);
+            for (int i = 0; i < L; ++i) d[i] = st.w * (d[i] - yn[i] * dot - plain);
         }
-        if (on) l.store(static_cast<YT*>(g.dy) + at, d);
+        if (on) l.store(static_cast<YT*>(g.dy) + row * width, d);
         if (g.dgate && on && row + 1 == gate_end) {
             if (g.split.chunks > 1) l.store(g.parts.gates + id * width, dg);
-            else l.store(static_cast<char*>(g.dgate) + row / g.split.group_rows * width * gate_size, a.n.gate_elem, dg);
-            zero(dg);
+            else l.store(g.dgate, row / g.split.group_rows, a.n.gate_elem, dg);
+            fill(dg, 0.0f);
             gate_end += g.split.group_rows;
         }
     }
     // the workers of a workgroup, one after another
-    for (int k = 0; k < kVectors; ++k) {
-        if (!(g.parts.want >> k & 1)) continue;
-        float mine[kLane];
+    float* to = g.parts.sums + static_cast<int64_t>(blockIdx.x) * width;
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) mine[i] = k == 0 ? sum[0][i] : k == 1 ? sum[1][i] : k == 2 ? sum[2][i] : k == 3 ? sum[3][i] : sum[4][i];
-        for (int w = 0; w < workers; ++w) {
+    for (int k = 0; k < kSums; ++k) {
+        if (!(g.parts.want >> k & 1)) continue;
+        float mine[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) mine[i] = sum(k, i);
+        for (int w = workers - 1; w > 0; --w) {
             if (w == worker) {
 #pragma unroll
-                for (int i = 0; i < kLane; ++i) {
+                for (int i = 0; i < L; ++i) {
                     float* p = join + i * l.threads + l.t;
-                    *p = w == 0 ? mine[i] : *p + mine[i];
+                    *p = w == workers - 1 ? mine[i] : *p + mine[i];
                 }
             }
-            if (workers > 1) lds_barrier();
+            lds_barrier();
         }
         if (worker == 0) {
+            if (workers > 1) {
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) mine[i] = join[i * l.threads + l.t];
-            l.store(g.parts.vectors + (__builtin_popcount(g.parts.want & ((1 << k) - 1)) * g.parts.workgroups + blockIdx.x) * width, mine);
+                for (int i = 0; i < L; ++i) mine[i] += join[i * l.threads + l.t];
+            }
+            l.store(to, mine);
         }
         if (workers > 1) lds_barrier();
+        to += g.parts.workgroups * width;
     }
 }
 
-// out[column] = sum of `count` parts `width` apart: 32 columns a workgroup, 8
-// parts at a time, added in the same order every time.
-__device__ __forceinline__ float part_sum(const float* p, int64_t count, int64_t width, int column, int row,
-                                          double (&buf)[8][32]) {
-    double s = 0.0;
-    if (column < width)
-        for (int64_t k = row; k < count; k += 8) s += static_cast<double>(p[k * width + column]);
-    buf[row][threadIdx.x % 32] = s;
-    __syncthreads();
-    s = 0.0;
-    for (int k = 0; k < 8; ++k) s += buf[k][threadIdx.x % 32];
-    return static_cast<float>(s);
-}
-
-struct VectorOut {
-    float* p[kVectors];     // those that are wanted, in order
+// Sums of parts, 32 columns a workgroup and 32 parts at a time, added in the same
+// order every time: a column of the vectors' sums, from which its thread forms
+// their gradients, or of a gate's gradient.
+struct NormJoin {
+    ks_residual_norm_t n;
+    ks_residual_norm_grads_t out;
+    NormParts parts;
+    void* dgate;
+    int64_t groups;          // workgroups of the gates' come after the vectors'
+    int chunks;
 };
 
-__global__ __launch_bounds__(256) void norm_vectors_kernel(const NormParts parts, int width, VectorOut out) {
-    __shared__ double buf[8][32];
-    const int column = blockIdx.x * 32 + threadIdx.x % 32, row = threadIdx.x / 32, k = blockIdx.y;
-    const float s = part_sum(parts.vectors + k * parts.workgroups * width, parts.workgroups, width, column, row, buf);
-    if (row == 0 && column < width) out.p[k][column] = s;
+__device__ __forceinline__ float vector_at(const void* v, int elem, int column, float none) {
+    if (!v) return none;
+    return elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(v)[column]) : static_cast<const float*>(v)[column];
 }
 
-__global__ __launch_bounds__(256) void norm_gates_kernel(const float* parts, int chunks, int width, int64_t group0,
-                                                         void* dgate, int elem) {
-    __shared__ double buf[8][32];
-    const int blocks = (width + 31) / 32;
-    const int64_t group = group0 + blockIdx.x / blocks;
-    const int column = static_cast<int>(blockIdx.x % blocks) * 32 + threadIdx.x % 32, row = threadIdx.x / 32;
-    const float s = part_sum(parts + group * chunks * width, chunks, width, column, row, buf);
-    if (row != 0 || column >= width) return;
-    if (elem == KS_ELEM_BF16) static_cast<bf16_t*>(dgate)[group * width + column] = to_bf16(s);
-    else static_cast<float*>(dgate)[group * width + column] = s;
-}
-
-// Waves of a worker: a power of two, so that workers fill a workgroup.
-int worker_waves(int64_t width) {
-    int w = 1;
-    while (static_cast<int64_t>(w) * kWaveCols < width) w *= 2;
-    return w;
+__global__ __launch_bounds__(1024) void norm_join_kernel(const NormJoin j, int64_t group0) {
+    __shared__ double buf[32][33];
+    const int width = static_cast<int>(j.n.width), blocks = (width + 31) / 32;
+    const int lane = threadIdx.x % 32, line = threadIdx.x / 32, column = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
+    const int64_t which = blockIdx.x / blocks + group0;             // 0: the vectors
+    // the sum over a column of `count` parts, in line 0's threads
+    auto total = [&](const float* p, int64_t count) {
+        double s = 0.0;
+        if (column < width) {
+            int64_t k = line;
+            for (; k + 96 < count; k += 128) {
+                const float a = p[k * width + column], b = p[(k + 32) * width + column],
+                            c = p[(k + 64) * width + column], d = p[(k + 96) * width + column];
+                s += (static_cast<double>(a) + b) + (static_cast<double>(c) + d);
+            }
+            for (; k < count; k += 32) s += static_cast<double>(p[k * width + column]);
+        }
+        __syncthreads();
+        buf[line][lane] = s;
+        __syncthreads();
+        s = 0.0;
+        if (line == 0)
+            for (int i = 0; i < 32; ++i) s += buf[i][lane];
+        return s;
+    };
+    if (which > 0) {
+        const int64_t group = which - 1;
+        const double s = total(j.parts.gates + group * j.chunks * width, j.chunks);
+        if (line != 0 || column >= width) return;
+        if (j.n.gate_elem == KS_ELEM_BF16)
+            static_cast<bf16_t*>(j.dgate)[group * width + column] = to_bf16(static_cast<float>(s));
+        else
+            static_cast<float*>(j.dgate)[group * width + column] = static_cast<float>(s);
+        return;
+    }
+    double sum[kSums];
+    const float* p = j.parts.sums;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+        sum[k] = 0.0;
+        if (!(j.parts.want >> k & 1)) continue;
+        sum[k] = total(p, j.parts.workgroups);
+        p += j.parts.workgroups * width;
+    }
+    if (line != 0 || column >= width) return;
+    const double s = vector_at(j.n.scale, j.n.elem, column, 1.0f), w2 = vector_at(j.n.post_weight, j.n.elem, column, 1.0f),
+                 b2 = vector_at(j.n.post_bias, j.n.elem, column, 0.0f);
+    if (j.out.pre_weight) j.out.pre_weight[column] = static_cast<float>(sum[0]);
+    if (j.out.pre_bias) j.out.pre_bias[column] = static_cast<float>(sum[1]);
+    if (j.out.post_weight) j.out.post_weight[column] = static_cast<float>(s * sum[2]);
+    if (j.out.post_bias) j.out.post_bias[column] = static_cast<float>(s * sum[3]);
+    if (j.out.scale) j.out.scale[column] = static_cast<float>(w2 * sum[2] + b2 * sum[3]);
 }
 
 NormArgs norm_args(const ks_residual_norm_t& n, const void* x, const void* y, const void* gate, int64_t groups,
@@ -417,7 +544,6 @@ NormArgs norm_args(const ks_residual_norm_t& n, const void* x, const void* y, co
     a.y = y;
     a.gate = gate;
     a.group_rows = groups > 0 ? rows / groups : 0;
-    a.row0 = 0;
     a.rows = rows;
     a.waves = worker_waves(n.width);
     a.eps = static_cast<float>(n.eps);
@@ -432,21 +558,21 @@ bool aligned16(std::initializer_list<const void*> ps) {
     return true;
 }
 
-template <typename XT, typename YT, typename HT>
+template <typename XT, typename YT, typename HT, int L>
 ks_status_t run_norm(const NormArgs& a, bool wide, void* z, void* h, float* stats, dim3 grid, dim3 block,
                      hipStream_t stream) {
-    return launch_kernel(wide ? norm_kernel<XT, YT, HT, true> : norm_kernel<XT, YT, HT, false>, grid, block, 0, stream,
-                         a, static_cast<XT*>(z), static_cast<HT*>(h), stats);
+    return launch_kernel(wide ? norm_kernel<XT, YT, HT, L, true> : norm_kernel<XT, YT, HT, L, false>, grid, block, 0,
+                         stream, a, static_cast<XT*>(z), static_cast<HT*>(h), stats);
 }
 
-template <typename XT, typename YT, typename HT>
+template <typename XT, typename YT, typename HT, int L>
 ks_status_t run_grad(const NormArgs& a, const NormGrad& g, bool wide, dim3 grid, dim3 block, size_t lds,
                      hipStream_t stream) {
-    return launch_kernel(wide ? norm_grad_kernel<XT, YT, HT, true> : norm_grad_kernel<XT, YT, HT, false>, grid, block,
-                         lds, stream, a, g);
+    return launch_kernel(wide ? norm_grad_kernel<XT, YT, HT, L, true> : norm_grad_kernel<XT, YT, HT, L, false>, grid,
+                         block, lds, stream, a, g);
 }
 
-// f.template operator()<XT, YT, HT>() for the types of n.
+// f(XT{}, YT{}, HT{}) for the types of n.
 template <typename XT, typename YT, typename F>
 ks_status_t with_h(const ks_residual_norm_t& n, F f) {
     return n.h_elem == KS_ELEM_BF16 ? f(XT{}, YT{}, bf16_t{}) : f(XT{}, YT{}, float{});
@@ -460,36 +586,44 @@ ks_status_t with_types(const ks_residual_norm_t& n, F f) {
     return n.x_elem == KS_ELEM_BF16 ? with_y<bf16_t>(n, f) : with_y<float>(n, f);
 }
 
+// The sums that a backward pass may need: dw1, db1, P, Q.
+int wanted(const ks_residual_norm_t& n) {
+    return (n.pre_weight ? 1 : 0) | (n.pre_bias ? 2 : 0) | (n.post_weight || n.scale ? 4 : 0) | (n.post_bias ? 8 : 0);
+}
+
+int64_t sum_parts(const ks_residual_norm_t& n, const NormSplit& s) {
+    return (__builtin_popcount(wanted(n)) * s.workgroups * n.width + 63) / 64 * 64;
+}
+
 }  // namespace
 
 ks_status_t launch_norm(const ks_residual_norm_t& n, const void* x, const void* y, const void* gate, int64_t groups,
                         void* z, void* h, float* stats, int64_t rows, hipStream_t stream) {
-    NormArgs a = norm_args(n, x, y, gate, groups, rows);
+    const NormArgs a = norm_args(n, x, y, gate, groups, rows);
     const int waves = std::max(4, a.waves);
     const int64_t each = waves / a.waves;
-    const bool wide = n.width % kLane == 0 && aligned16({x, y, gate, z, h, n.pre_weight, n.pre_bias, n.post_weight,
-                                                         n.post_bias, n.scale});
-    for (int64_t r = 0; r < rows; r += kMaxGrid / 4 * each) {
-        a.row0 = r;
-        const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid / 4, (rows - r + each - 1) / each))), block(waves * 64);
-        const ks_status_t st = with_types(n, [&](auto xt, auto yt, auto ht) {
-            return run_norm<decltype(xt), decltype(yt), decltype(ht)>(a, wide, z, h, stats, grid, block, stream);
-        });
-        if (st != KS_OK) return st;
-    }
-    return KS_OK;
+    const bool wide = n.width % (n.width <= kNarrow ? 4 : 8) == 0 && aligned16({x, y, gate, z, h, n.pre_weight, n.pre_bias, n.post_weight,
+                                                     n.post_bias, n.scale});
+    // as many workgroups as the card holds at once
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + each - 1) / each, 256 * 32 / waves)));
+    return with_types(n, [&](auto xt, auto yt, auto ht) {
+        typedef decltype(xt) XT;
+        typedef decltype(yt) YT;
+        typedef decltype(ht) HT;
+        return n.width <= kNarrow ? run_norm<XT, YT, HT, 4>(a, wide, z, h, stats, grid, dim3(waves * 64), stream)
+                                  : run_norm<XT, YT, HT, 8>(a, wide, z, h, stats, grid, dim3(waves * 64), stream);
+    });
 }
 
 NormSplit norm_split(int64_t width, int64_t rows, int64_t groups) {
     NormSplit s;
     const int waves = worker_waves(width);
-    s.groups_of_waves = std::max(1, 8 / waves);
+    s.workers_a_group = std::max(1, 8 / waves);
     // two workgroups a compute unit
-    const int64_t target = int64_t(512) * s.groups_of_waves;
+    const int64_t target = int64_t(512) * s.workers_a_group;
     const int64_t per = std::max<int64_t>(1, (rows + target - 1) / target);
     s.group_rows = groups > 0 ? rows / groups : 0;
     s.chunks = 1;
-    s.units = 1;
     if (rows == 0) {
         s.per = s.workers = 0;
     } else if (groups == 0) {
@@ -501,31 +635,17 @@ NormSplit norm_split(int64_t width, int64_t rows, int64_t groups) {
         s.chunks = static_cast<int>((s.group_rows + s.per - 1) / s.per);
         s.workers = groups * s.chunks;
     } else {
-        const int64_t units = (per + s.group_rows - 1) / s.group_rows;
-        s.units = static_cast<int>(units);
+        const int64_t units = (per + s.group_rows - 1) / s.group_rows;    // whole groups a worker
         s.per = units * s.group_rows;
         s.workers = (groups + units - 1) / units;
     }
-    s.workgroups = (s.workers + s.groups_of_waves - 1) / s.groups_of_waves;
+    s.workgroups = (s.workers + s.workers_a_group - 1) / s.workers_a_group;
     return s;
 }
 
-namespace {
-
-int wanted(const ks_residual_norm_t& n) {
-    return (n.pre_weight ? 1 : 0) | (n.pre_bias ? 2 : 0) | (n.post_weight ? 4 : 0) | (n.post_bias ? 8 : 0) |
-           (n.scale ? 16 : 0);
-}
-
-int64_t vector_parts(const ks_residual_norm_t& n, const NormSplit& s) {
-    return __builtin_popcount(wanted(n)) * s.workgroups * n.width;
-}
-
-}  // namespace
-
 size_t norm_workspace(const ks_residual_norm_t& n, const NormSplit& s, int64_t rows, int64_t groups) {
     if (rows == 0) return 0;
-    int64_t values = (vector_parts(n, s) + 63) / 64 * 64;
+    int64_t values = sum_parts(n, s);
     if (groups > 0 && s.chunks > 1) values += s.workers * n.width;
     return static_cast<size_t>(values) * 4;
 }
@@ -534,9 +654,7 @@ ks_status_t launch_norm_grad(const ks_residual_norm_t& n, const NormSplit& s, co
                              const void* x, const void* y, const void* gate, int64_t groups, const float* stats,
                              void* dx, void* dy, const ks_residual_norm_grads_t& out, void* dgate, int64_t rows, void* ws,
                              hipStream_t stream) {
-    float* const outs[kVectors] = {out.pre_weight, out.pre_bias, out.post_weight, out.post_bias, out.scale};
-    VectorOut vectors{};
-    int count = 0;
+    const bool any = out.pre_weight || out.pre_bias || out.post_weight || out.post_bias || out.scale;
     NormGrad g;
     g.dz = dz;
     g.dh = dh;
@@ -545,33 +663,32 @@ ks_status_t launch_norm_grad(const ks_residual_norm_t& n, const NormSplit& s, co
     g.dy = dy;
     g.dgate = dgate;
     g.split = s;
-    g.parts = {static_cast<float*>(ws), static_cast<float*>(ws) + (vector_parts(n, s) + 63) / 64 * 64, s.workgroups, 0};
-    for (int k = 0; k < kVectors; ++k) {
-        if (!outs[k]) continue;
-        g.parts.want |= 1 << k;
-        vectors.p[count++] = outs[k];
-    }
+    g.parts = {static_cast<float*>(ws), static_cast<float*>(ws) + sum_parts(n, s), s.workgroups, any ? wanted(n) : 0};
     const NormArgs a = norm_args(n, x, y, gate, groups, rows);
     ks_status_t st = KS_OK;
     if (rows > 0) {
-        const bool wide = n.width % kLane == 0 && aligned16({x, y, gate, dz, dh, dx, dy, dgate, ws, n.pre_weight,
-                                                             n.post_weight, n.post_bias, n.scale});
-        const size_t lds = (2 * 16 * 2 + static_cast<size_t>(a.waves) * kWaveCols) * 4;
+        const bool wide = n.width % (n.width <= kNarrow ? 4 : 8) == 0 && aligned16({x, y, gate, dz, dh, dx, dy, dgate, ws, n.pre_weight,
+                                                         n.post_weight, n.post_bias, n.scale});
+        const dim3 grid(static_cast<unsigned>(s.workgroups)), block(s.workers_a_group * a.waves * 64);
+        const bool narrow = n.width <= kNarrow;
+        const size_t row = static_cast<size_t>(a.waves) * 64 * (narrow ? 4 : 8) * 4;
+        const size_t lds = !narrow ? kSums * row : s.workers_a_group > 1 ? row : 0;
         st = with_types(n, [&](auto xt, auto yt, auto ht) {
-            return run_grad<decltype(xt), decltype(yt), decltype(ht)>(
-                a, g, wide, dim3(static_cast<unsigned>(s.workgroups)), dim3(s.groups_of_waves * a.waves * 64), lds,
-                stream);
+            typedef decltype(xt) XT;
+            typedef decltype(yt) YT;
+            typedef decltype(ht) HT;
+            return narrow ? run_grad<XT, YT, HT, 4>(a, g, wide, grid, block, lds, stream)
+                          : run_grad<XT, YT, HT, 8>(a, g, wide, grid, block, lds, stream);
         });
     }
-    if (st == KS_OK && count > 0)
-        st = launch_kernel(norm_vectors_kernel, dim3(static_cast<unsigned>((n.width + 31) / 32), count), dim3(256), 0,
-                           stream, g.parts, static_cast<int>(n.width), vectors);
-    if (!dgate || groups == 0 || (rows > 0 && s.chunks == 1)) return st;
-    const int64_t blocks = (n.width + 31) / 32, most = kMaxGrid / blocks;
-    for (int64_t first = 0; st == KS_OK && first < groups; first += most)
-        st = launch_kernel(norm_gates_kernel, dim3(static_cast<unsigned>(std::min(most, groups - first) * blocks)),
-                           dim3(256), 0, stream, g.parts.gates, rows > 0 ? s.chunks : 0, static_cast<int>(n.width), first,
-                           dgate, n.gate_elem);
+    // the vectors and the gates that workers share (of no rows: zeros), in one launch
+    const bool shared = dgate && groups > 0 && (rows == 0 || s.chunks > 1);
+    const int64_t blocks = (n.width + 31) / 32, from = any ? 0 : 1, to = shared ? groups + 1 : 1;
+    const NormJoin j{n, out, g.parts, dgate, groups, rows > 0 ? s.chunks : 0};
+    const int64_t most = kMaxGrid / 4 / blocks;
+    for (int64_t at = from; st == KS_OK && at < to; at += most)
+        st = launch_kernel(norm_join_kernel, dim3(static_cast<unsigned>(std::min(most, to - at) * blocks)), dim3(1024), 0,
+                           stream, j, at);
     return st;
 }
 

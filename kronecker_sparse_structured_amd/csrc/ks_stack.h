@@ -11,14 +11,14 @@ constexpr int64_t kMaxGrid = int64_t(1) << 23;   // workgroups a launch: a grid 
 
 // ---- residual norms (ks_norm.hip)
 
-// How a backward pass cuts its rows: `workers` contiguous ranges. With a gate of
-// several rows a group either `chunks` workers share a group (and add up their
-// parts of its gradient later) or a worker has `units` whole groups.
+// How a backward pass cuts its rows: `workers` contiguous ranges of `per`. With a
+// gate of several rows a group either `chunks` workers share a group (and their
+// parts of its gradient are added up later) or a worker has whole groups.
 struct NormSplit {
-    int64_t workers, per;     // rows a worker
+    int64_t workers, per;
     int64_t group_rows;       // rows that share a gate (0: no gate)
-    int chunks, units;
-    int groups_of_waves;      // workers a workgroup
+    int chunks;
+    int workers_a_group;      // workers a workgroup
     int64_t workgroups;
 };
 NormSplit norm_split(int64_t width, int64_t rows, int64_t groups);
