@@ -17,7 +17,7 @@
 // rows with its columns' sums in registers; a second launch adds up the workers'
 // parts in a fixed order.
 //
-// A worker is 1 to 16 waves, 4 values a lane (8 above 4096 columns). Sums over a
+// A worker is 1 to 16 waves with 4 or 8 values a lane. Sums over a
 // row are formed in the wave and then, for more than one wave, over LDS. The
 // variance is the mean of squared differences from the mean, not a difference
 // of two large sums. The vectors stay in registers from row to row and the next
@@ -36,59 +36,69 @@
 namespace ks {
 namespace {
 
-constexpr int kNarrow = 4096;   // columns up to which a lane holds 4
-
-// Waves of a worker: a power of two, so that workers fill a workgroup.
-int worker_waves(int64_t width) {
-    const int64_t cols = 64 * (width <= kNarrow ? 4 : 8);
+// Waves of a worker of which a lane holds `lane` values: a power of two, so that
+// workers fill a workgroup.
+int worker_waves(int64_t width, int lane) {
     int w = 1;
-    while (w * cols < width) w *= 2;
+    while (w * 64 * lane < width) w *= 2;
     return w;
 }
 
-// A lane's L values of a row as they are loaded. WIDE: neighbours, in accesses
-// of up to 16 bytes. Else (a row of any width at any address) one value of each
-// stretch of the row as long as the worker is wide.
-template <typename T, int L, bool WIDE>
+// The values that a lane holds. Forward: 8 keep more bytes on their way (4096 x
+// 4096 in bf16 30 us, 54 with 4), unless one wave of 4 would do. Backward: 4, as
+// long as 16 waves reach (8192 x 2048 53 us, 91 with 8).
+int forward_lane(int64_t width) { return width <= 256 ? 4 : 8; }
+int backward_lane(int64_t width) { return width <= 4096 ? 4 : 8; }
+
+// A lane's L values of a row as they are loaded: neighbours, in accesses of up to
+// 16 bytes that may start at any element (a row of an odd width does), the last
+// lane's one by one if the row ends among them.
+template <typename T, int L>
 struct Raw {
     static constexpr int kWords = L * static_cast<int>(sizeof(T)) / 4;
-    uint32_t w[WIDE ? kWords : L];
+    uint32_t w[kWords];
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        else if constexpr (WIDE) return i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
-        else return bf16_lo(w[i]);
+        else return i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
     }
 };
 
-template <int L, bool WIDE>
+template <typename T, int V>
+struct Access {
+    typedef uint32_t vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+};
+
+template <int L>
 struct Lanes {
-    int t, threads, width;
-    __device__ __forceinline__ int at(int i) const { return WIDE ? t * L + i : i * threads + t; }
-    __device__ __forceinline__ bool in(int i) const { return WIDE ? t * L < width : at(i) < width; }
+    int t, left;            // the lane in its worker; columns from its first on, none below 0
+    __device__ __forceinline__ bool in(int i) const { return i < left; }
 
     template <typename T>
-    __device__ __forceinline__ void load(const T* row, Raw<T, L, WIDE>& r) const {
-        if constexpr (WIDE) {
-            constexpr int W = Raw<T, L, WIDE>::kWords, V = W < 4 ? W : 4;
-            typedef uint32_t vec __attribute__((ext_vector_type(V)));
+    __device__ __forceinline__ void load(const T* row, Raw<T, L>& r) const {
+        constexpr int W = Raw<T, L>::kWords, V = W < 4 ? W : 4;
+        typedef typename Access<T, V>::vec vec;
+        const T* p = row + t * L;
+#pragma unroll
+        for (int k = 0; k < W; ++k) r.w[k] = 0u;
+        if (left >= L) {
 #pragma unroll
             for (int k = 0; k < W; k += V) {
-                vec v = 0;
-                if (t * L < width) v = *reinterpret_cast<const vec*>(row + t * L + k * 4 / static_cast<int>(sizeof(T)));
+                const vec v = *reinterpret_cast<const vec*>(p + k * 4 / static_cast<int>(sizeof(T)));
 #pragma unroll
                 for (int i = 0; i < V; ++i) r.w[k + i] = v[i];
             }
-        } else {
+        } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if constexpr (sizeof(T) == 4) r.w[i] = in(i) ? __float_as_uint(row[at(i)]) : 0u;
-                else r.w[i] = in(i) ? row[at(i)] : 0u;
+                if (!in(i)) continue;
+                if constexpr (sizeof(T) == 4) r.w[i] = __float_as_uint(p[i]);
+                else r.w[i / 2] |= static_cast<uint32_t>(p[i]) << (i % 2 * 16);
             }
         }
     }
     template <typename T>
     __device__ __forceinline__ void load(const T* row, float (&v)[L]) const {
-        Raw<T, L, WIDE> r;
+        Raw<T, L> r;
         load(row, r);
 #pragma unroll
         for (int i = 0; i < L; ++i) v[i] = r.get(i);
@@ -97,16 +107,12 @@ struct Lanes {
         if (elem == KS_ELEM_BF16) load(static_cast<const bf16_t*>(row), v);
         else load(static_cast<const float*>(row), v);
     }
-    // values of `size` bytes, one row after another
-    __device__ __forceinline__ void load(const void* rows, int64_t row, int elem, float (&v)[L]) const {
-        load(static_cast<const char*>(rows) + row * width * (elem == KS_ELEM_BF16 ? 2 : 4), elem, v);
-    }
     template <typename T>
     __device__ __forceinline__ void store(T* row, const float (&v)[L]) const {
-        if constexpr (WIDE) {
-            if (t * L >= width) return;
-            constexpr int W = Raw<T, L, WIDE>::kWords, V = W < 4 ? W : 4;
-            typedef uint32_t vec __attribute__((ext_vector_type(V)));
+        constexpr int W = Raw<T, L>::kWords, V = W < 4 ? W : 4;
+        typedef typename Access<T, V>::vec vec;
+        T* p = row + t * L;
+        if (left >= L) {
 #pragma unroll
             for (int k = 0; k < W; k += V) {
                 vec w;
@@ -115,22 +121,23 @@ struct Lanes {
                     if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[k + i]);
                     else w[i] = pack_bf16(v[2 * (k + i)], v[2 * (k + i) + 1]);
                 }
-                *reinterpret_cast<vec*>(row + t * L + k * 4 / static_cast<int>(sizeof(T))) = w;
+                *reinterpret_cast<vec*>(p + k * 4 / static_cast<int>(sizeof(T))) = w;
             }
-        } else {
+        } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (!in(i)) continue;
-                if constexpr (sizeof(T) == 4) row[at(i)] = v[i];
-                else row[at(i)] = to_bf16(v[i]);
+                if constexpr (sizeof(T) == 4) p[i] = v[i];
+                else p[i] = to_bf16(v[i]);
             }
         }
     }
-    __device__ __forceinline__ void store(void* rows, int64_t row, int elem, const float (&v)[L]) const {
-        if (elem == KS_ELEM_BF16) store(static_cast<bf16_t*>(rows) + row * width, v);
-        else store(static_cast<float*>(rows) + row * width, v);
-    }
 };
+
+// Row `row` of a matrix whose type is known at run time.
+__device__ __forceinline__ const void* row_of(const void* rows, int64_t row, int width, int elem) {
+    return static_cast<const char*>(rows) + row * width * (elem == KS_ELEM_BF16 ? 2 : 4);
+}
 
 template <int L>
 __device__ __forceinline__ void fill(float (&v)[L], float x) {
@@ -172,11 +179,20 @@ struct RowSums {
         if (waves == 1) return;
         if (threadIdx.x % 64 == 0) buf[turn][wave] = make_float2(a, b);
         lds_barrier();
-        a = b = 0.0f;
-        for (int w = first; w < first + waves; ++w) {
-            const float2 v = buf[turn][w];
-            a += v.x;
-            b += v.y;
+        const float2 v = buf[turn][first + (threadIdx.x & (waves - 1))];
+        a = v.x + moved<0xb1, 0xf>(v.x);
+        b = v.y + moved<0xb1, 0xf>(v.y);
+        if (waves > 2) {
+            a += moved<0x4e, 0xf>(a);
+            b += moved<0x4e, 0xf>(b);
+        }
+        if (waves > 4) {
+            a += moved<0x141, 0xf>(a);
+            b += moved<0x141, 0xf>(b);
+        }
+        if (waves > 8) {
+            a += moved<0x140, 0xf>(a);
+            b += moved<0x140, 0xf>(b);
         }
         turn ^= 1;
     }
@@ -194,8 +210,8 @@ struct NormArgs {
 };
 
 // Mean (layer norm) and 1 / deviation of the row's values.
-template <int L, bool WIDE>
-__device__ __forceinline__ void deviation(const Lanes<L, WIDE>& l, RowSums& sums, const NormArgs& a, const float (&v)[L],
+template <int L>
+__device__ __forceinline__ void deviation(const Lanes<L>& l, RowSums& sums, const NormArgs& a, const float (&v)[L],
                                           float& mean, float& r) {
     mean = 0.0f;
     float none = 0.0f;
@@ -215,20 +231,21 @@ __device__ __forceinline__ void deviation(const Lanes<L, WIDE>& l, RowSums& sums
     r = 1.0f / sqrtf(square * a.inverse + a.eps);
 }
 
-template <typename XT, typename YT, typename HT, int L, bool WIDE>
+template <typename XT, typename YT, typename HT, int L>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT* h, float* stats) {
     __shared__ float2 buf[2][16];
     const int wave = threadIdx.x / 64, worker = wave / a.waves;
     const int width = static_cast<int>(a.n.width);
-    const Lanes<L, WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
+    const int t = static_cast<int>(threadIdx.x) - worker * a.waves * 64;
+    const Lanes<L> l{t, width - t * L};
     RowSums sums{buf, wave, worker * a.waves, a.waves, 0};
     const int each = blockDim.x / 64 / a.waves;
     const int64_t step = static_cast<int64_t>(gridDim.x) * each;
     const XT* X = static_cast<const XT*>(a.x);
     const YT* Y = static_cast<const YT*>(a.y);
     int64_t first = static_cast<int64_t>(blockIdx.x) * each;       // of the workgroup's rows
-    Raw<XT, L, WIDE> nx;
-    Raw<YT, L, WIDE> ny = {};
+    Raw<XT, L> nx;
+    Raw<YT, L> ny = {};
     float gate[L], w1[L], b1[L], w2[L], b2[L], s[L];
     // a worker without a row goes through the barriers with the last one
     auto fetch = [&](int64_t row) {
@@ -256,7 +273,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT*
             v[i] = nx.get(i);
             u[i] = ny.get(i);
         }
-        if (a.gate) l.load(a.gate, row / a.group_rows, a.n.gate_elem, gate);
+        if (a.gate) l.load(row_of(a.gate, row / a.group_rows, width, a.n.gate_elem), a.n.gate_elem, gate);
         if (first + step < a.rows) fetch(min(row + step, a.rows - 1));
         if (Y) {
             if (a.n.post_weight) deviation(l, sums, a, u, mean2, r2);
@@ -270,7 +287,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT*
             for (int i = 0; i < L; ++i) v[i] = (v[i] - mean1) * r1 * w1[i] + b1[i];
             if (on) l.store(h + row * width, v);
         }
-        if (stats && on && l.t == 0) *reinterpret_cast<float4*>(stats + 4 * row) = make_float4(mean1, r1, mean2, r2);
+        if (stats && on && t == 0) *reinterpret_cast<float4*>(stats + 4 * row) = make_float4(mean1, r1, mean2, r2);
     }
 }
 
@@ -296,13 +313,14 @@ struct NormGrad {
     NormParts parts;
 };
 
-template <typename XT, typename YT, typename HT, int L, bool WIDE>
+template <typename XT, typename YT, typename HT, int L>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const NormGrad g) {
     extern __shared__ float join[];                // a row of the worker's columns, or its sums
     __shared__ float2 buf[2][16];
     const int wave = threadIdx.x / 64, worker = wave / a.waves, workers = blockDim.x / 64 / a.waves;
     const int width = static_cast<int>(a.n.width);
-    const Lanes<L, WIDE> l{static_cast<int>(threadIdx.x) - worker * a.waves * 64, a.waves * 64, width};
+    const int t = static_cast<int>(threadIdx.x) - worker * a.waves * 64;
+    const Lanes<L> l{t, width - t * L};
     RowSums sums{buf, wave, worker * a.waves, a.waves, 0};
     const int64_t id = static_cast<int64_t>(blockIdx.x) * workers + worker;
     // the worker's rows, and the one at which its gate's sum is complete
@@ -320,18 +338,24 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     const YT* Y = static_cast<const YT*>(a.y);
     const XT* DZ = static_cast<const XT*>(g.dz);
     const HT* DH = static_cast<const HT*>(g.dh);
-    Raw<XT, L, WIDE> nx, nz = {};
-    Raw<YT, L, WIDE> ny = {};
-    Raw<HT, L, WIDE> nh = {};
+    Raw<XT, L> nx, nz = {};
+    Raw<YT, L> ny = {};
+    Raw<HT, L> nh = {};
     float4 next = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-    auto fetch = [&](int64_t at) {
+    auto fetch_block = [&](int64_t at) {
         l.load(X + at * width, nx);
         if (Y) l.load(Y + at * width, ny);
-        if (DZ) l.load(DZ + at * width, nz);
-        if (DH) l.load(DH + at * width, nh);
         if (g.stats) next = *reinterpret_cast<const float4*>(g.stats + 4 * at);
     };
-    // above kNarrow columns 16 waves have no registers for the vectors, for a row
+    auto fetch_grads = [&](int64_t at) {
+        if (DZ) l.load(DZ + at * width, nz);
+        if (DH) l.load(DH + at * width, nh);
+    };
+    auto fetch = [&](int64_t at) {
+        fetch_block(at);
+        fetch_grads(at);
+    };
+    // with 8 values a lane 16 waves have no registers for the vectors, for a row
     // ahead and for the sums: the first two are loaded where they are used, the
     // sums are in LDS
     constexpr bool kAhead = L == 4;
@@ -360,17 +384,23 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     // every worker goes through as many rounds: they meet at barriers
     for (int64_t k = 0; k < g.split.per; ++k, ++row) {
         const bool on = row < end;
-        if (!kAhead) fetch(on ? row : 0);
+        const int64_t here = on ? row : 0;
+        if (!kAhead) fetch_block(here);
         float z[L], yn[L], d[L], dh[L];
         const float4 st = next;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             z[i] = nx.get(i);
             yn[i] = ny.get(i);
-            d[i] = nz.get(i);
-            dh[i] = nh.get(i);
         }
-        if (a.gate) l.load(a.gate, on ? row / g.split.group_rows : 0, a.n.gate_elem, gate);
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                d[i] = nz.get(i);
+                dh[i] = nh.get(i);
+            }
+        }
+        if (a.gate) l.load(row_of(a.gate, here / g.split.group_rows, width, a.n.gate_elem), a.n.gate_elem, gate);
         if (kAhead && row + 1 < end) fetch(row + 1);
         if (Y) {
             vector(a.n.post_weight, 1.0f, w2, !kAhead);
@@ -380,6 +410,15 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             for (int i = 0; i < L; ++i) {
                 if (a.n.post_weight) yn[i] = (yn[i] - st.z) * st.w;
                 z[i] += a.residual * ((yn[i] * w2[i] + b2[i]) * s[i] * gate[i]);
+            }
+        }
+        if (!kAhead) {
+            asm volatile("" ::: "memory");          // these loads not before that arithmetic
+            fetch_grads(here);
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                d[i] = nz.get(i);
+                dh[i] = nh.get(i);
             }
         }
         if (DH) {
@@ -430,7 +469,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         if (on) l.store(static_cast<YT*>(g.dy) + row * width, d);
         if (g.dgate && on && row + 1 == gate_end) {
             if (g.split.chunks > 1) l.store(g.parts.gates + id * width, dg);
-            else l.store(g.dgate, row / g.split.group_rows, a.n.gate_elem, dg);
+            else if (a.n.gate_elem == KS_ELEM_BF16) l.store(static_cast<bf16_t*>(g.dgate) + row / g.split.group_rows * width, dg);
+            else l.store(static_cast<float*>(g.dgate) + row / g.split.group_rows * width, dg);
             fill(dg, 0.0f);
             gate_end += g.split.group_rows;
         }
@@ -447,7 +487,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             if (w == worker) {
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
-                    float* p = join + i * l.threads + l.t;
+                    float* p = join + i * a.waves * 64 + t;
                     *p = w == workers - 1 ? mine[i] : *p + mine[i];
                 }
             }
@@ -456,7 +496,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         if (worker == 0) {
             if (workers > 1) {
 #pragma unroll
-                for (int i = 0; i < L; ++i) mine[i] += join[i * l.threads + l.t];
+                for (int i = 0; i < L; ++i) mine[i] += join[i * a.waves * 64 + t];
             }
             l.store(to, mine);
         }
@@ -466,78 +506,84 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
 }
 
 // Sums of parts, 32 columns a workgroup and 32 parts at a time, added in the same
-// order every time: a column of the vectors' sums, from which its thread forms
-// their gradients, or of a gate's gradient.
+// order every time. Of the vectors' sums workgroups 0, 1 and 2 of a range of
+// columns take dw1, db1, and P with Q, from which they form the gradients; the
+// others take a gate's gradient each.
 struct NormJoin {
     ks_residual_norm_t n;
     ks_residual_norm_grads_t out;
     NormParts parts;
     void* dgate;
-    int64_t groups;          // workgroups of the gates' come after the vectors'
-    int chunks;
+    int chunks;              // parts of a gate
 };
+constexpr int kVectorJobs = 3;
 
-__device__ __forceinline__ float vector_at(const void* v, int elem, int column, float none) {
+__device__ __forceinline__ double vector_at(const void* v, int elem, int column, double none) {
     if (!v) return none;
     return elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(v)[column]) : static_cast<const float*>(v)[column];
 }
 
-__global__ __launch_bounds__(1024) void norm_join_kernel(const NormJoin j, int64_t group0) {
+__global__ __launch_bounds__(1024) void norm_join_kernel(const NormJoin j, int64_t job0) {
     __shared__ double buf[32][33];
     const int width = static_cast<int>(j.n.width), blocks = (width + 31) / 32;
-    const int lane = threadIdx.x % 32, line = threadIdx.x / 32, column = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
-    const int64_t which = blockIdx.x / blocks + group0;             // 0: the vectors
-    // the sum over a column of `count` parts, in line 0's threads
+    const int64_t job = blockIdx.x / blocks + job0;
+    const int first = static_cast<int>(blockIdx.x % blocks) * 32, low = threadIdx.x % 32, high = threadIdx.x / 32;
+    // the sum of `count` parts, for column first + high in that column's 32 threads
     auto total = [&](const float* p, int64_t count) {
         double s = 0.0;
-        if (column < width) {
-            int64_t k = line;
-            for (; k + 96 < count; k += 128) {
-                const float a = p[k * width + column], b = p[(k + 32) * width + column],
-                            c = p[(k + 64) * width + column], d = p[(k + 96) * width + column];
-                s += (static_cast<double>(a) + b) + (static_cast<double>(c) + d);
+        if (first + low < width) {
+            p += first + low;
+            int64_t k = high;
+            for (; k + 224 < count; k += 256) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = p[(k + 32 * u) * width];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) s += static_cast<double>(v[u]);
             }
-            for (; k < count; k += 32) s += static_cast<double>(p[k * width + column]);
+            for (; k < count; k += 32) s += static_cast<double>(p[k * width]);
         }
         __syncthreads();
-        buf[line][lane] = s;
+        buf[high][low] = s;
         __syncthreads();
-        s = 0.0;
-        if (line == 0)
-            for (int i = 0; i < 32; ++i) s += buf[i][lane];
+        s = buf[low][high];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) s += __shfl_xor(s, d, 64);
         return s;
     };
-    if (which > 0) {
-        const int64_t group = which - 1;
-        const double s = total(j.parts.gates + group * j.chunks * width, j.chunks);
-        if (line != 0 || column >= width) return;
-        if (j.n.gate_elem == KS_ELEM_BF16)
-            static_cast<bf16_t*>(j.dgate)[group * width + column] = to_bf16(static_cast<float>(s));
-        else
-            static_cast<float*>(j.dgate)[group * width + column] = static_cast<float>(s);
-        return;
+    // where sum k's parts are; none: not formed
+    auto parts = [&](int k) {
+        return j.parts.sums + __builtin_popcount(j.parts.want & ((1 << k) - 1)) * j.parts.workgroups * width;
+    };
+    const int column = first + high;
+    const bool writes = low == 0 && column < width;
+    if (job >= kVectorJobs) {
+        const int64_t group = job - kVectorJobs;
+        const float s = static_cast<float>(total(j.parts.gates + group * j.chunks * width, j.chunks));
+        if (!writes) return;
+        if (j.n.gate_elem == KS_ELEM_BF16) static_cast<bf16_t*>(j.dgate)[group * width + column] = to_bf16(s);
+        else static_cast<float*>(j.dgate)[group * width + column] = s;
+    } else if (job < 2) {
+        float* out = job == 0 ? j.out.pre_weight : j.out.pre_bias;
+        if (!out) return;
+        const double s = total(parts(static_cast<int>(job)), j.parts.workgroups);
+        if (writes) out[column] = static_cast<float>(s);
+    } else {
+        if (!j.out.post_weight && !j.out.post_bias && !j.out.scale) return;
+        const double P = j.parts.want & 4 ? total(parts(2), j.parts.workgroups) : 0.0;
+        const double Q = j.parts.want & 8 ? total(parts(3), j.parts.workgroups) : 0.0;
+        if (!writes) return;
+        const double s = vector_at(j.n.scale, j.n.elem, column, 1.0),
+                     w2 = vector_at(j.n.post_weight, j.n.elem, column, 1.0),
+                     b2 = vector_at(j.n.post_bias, j.n.elem, column, 0.0);
+        if (j.out.post_weight) j.out.post_weight[column] = static_cast<float>(s * P);
+        if (j.out.post_bias) j.out.post_bias[column] = static_cast<float>(s * Q);
+        if (j.out.scale) j.out.scale[column] = static_cast<float>(w2 * P + b2 * Q);
     }
-    double sum[kSums];
-    const float* p = j.parts.sums;
-#pragma unroll
-    for (int k = 0; k < kSums; ++k) {
-        sum[k] = 0.0;
-        if (!(j.parts.want >> k & 1)) continue;
-        sum[k] = total(p, j.parts.workgroups);
-        p += j.parts.workgroups * width;
-    }
-    if (line != 0 || column >= width) return;
-    const double s = vector_at(j.n.scale, j.n.elem, column, 1.0f), w2 = vector_at(j.n.post_weight, j.n.elem, column, 1.0f),
-                 b2 = vector_at(j.n.post_bias, j.n.elem, column, 0.0f);
-    if (j.out.pre_weight) j.out.pre_weight[column] = static_cast<float>(sum[0]);
-    if (j.out.pre_bias) j.out.pre_bias[column] = static_cast<float>(sum[1]);
-    if (j.out.post_weight) j.out.post_weight[column] = static_cast<float>(s * sum[2]);
-    if (j.out.post_bias) j.out.post_bias[column] = static_cast<float>(s * sum[3]);
-    if (j.out.scale) j.out.scale[column] = static_cast<float>(w2 * sum[2] + b2 * sum[3]);
 }
 
 NormArgs norm_args(const ks_residual_norm_t& n, const void* x, const void* y, const void* gate, int64_t groups,
-                   int64_t rows) {
+                   int64_t rows, int lane) {
     NormArgs a;
     a.n = n;
     a.x = x;
@@ -545,31 +591,23 @@ NormArgs norm_args(const ks_residual_norm_t& n, const void* x, const void* y, co
     a.gate = gate;
     a.group_rows = groups > 0 ? rows / groups : 0;
     a.rows = rows;
-    a.waves = worker_waves(n.width);
+    a.waves = worker_waves(n.width, lane);
     a.eps = static_cast<float>(n.eps);
     a.residual = static_cast<float>(n.residual);
     a.inverse = static_cast<float>(1.0 / static_cast<double>(n.width));
     return a;
 }
 
-bool aligned16(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
-    return true;
+template <typename XT, typename YT, typename HT, int L>
+ks_status_t run_norm(const NormArgs& a, void* z, void* h, float* stats, dim3 grid, dim3 block,
+                     hipStream_t stream) {
+    return launch_kernel(norm_kernel<XT, YT, HT, L>, grid, block, 0, stream, a, static_cast<XT*>(z), static_cast<HT*>(h),
+                         stats);
 }
 
 template <typename XT, typename YT, typename HT, int L>
-ks_status_t run_norm(const NormArgs& a, bool wide, void* z, void* h, float* stats, dim3 grid, dim3 block,
-                     hipStream_t stream) {
-    return launch_kernel(wide ? norm_kernel<XT, YT, HT, L, true> : norm_kernel<XT, YT, HT, L, false>, grid, block, 0,
-                         stream, a, static_cast<XT*>(z), static_cast<HT*>(h), stats);
-}
-
-template <typename XT, typename YT, typename HT, int L>
-ks_status_t run_grad(const NormArgs& a, const NormGrad& g, bool wide, dim3 grid, dim3 block, size_t lds,
-                     hipStream_t stream) {
-    return launch_kernel(wide ? norm_grad_kernel<XT, YT, HT, L, true> : norm_grad_kernel<XT, YT, HT, L, false>, grid,
-                         block, lds, stream, a, g);
+ks_status_t run_grad(const NormArgs& a, const NormGrad& g, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
+    return launch_kernel(norm_grad_kernel<XT, YT, HT, L>, grid, block, lds, stream, a, g);
 }
 
 // f(XT{}, YT{}, HT{}) for the types of n.
@@ -599,28 +637,27 @@ int64_t sum_parts(const ks_residual_norm_t& n, const NormSplit& s) {
 
 ks_status_t launch_norm(const ks_residual_norm_t& n, const void* x, const void* y, const void* gate, int64_t groups,
                         void* z, void* h, float* stats, int64_t rows, hipStream_t stream) {
-    const NormArgs a = norm_args(n, x, y, gate, groups, rows);
+    const int lane = forward_lane(n.width);
+    const NormArgs a = norm_args(n, x, y, gate, groups, rows, lane);
     const int waves = std::max(4, a.waves);
     const int64_t each = waves / a.waves;
-    const bool wide = n.width % (n.width <= kNarrow ? 4 : 8) == 0 && aligned16({x, y, gate, z, h, n.pre_weight, n.pre_bias, n.post_weight,
-                                                     n.post_bias, n.scale});
-    // as many workgroups as the card holds at once
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + each - 1) / each, 256 * 32 / waves)));
+    // 16 waves a compute unit: what it holds at once with 8 values a lane
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + each - 1) / each, 256 * 16 / waves)));
     return with_types(n, [&](auto xt, auto yt, auto ht) {
         typedef decltype(xt) XT;
         typedef decltype(yt) YT;
         typedef decltype(ht) HT;
-        return n.width <= kNarrow ? run_norm<XT, YT, HT, 4>(a, wide, z, h, stats, grid, dim3(waves * 64), stream)
-                                  : run_norm<XT, YT, HT, 8>(a, wide, z, h, stats, grid, dim3(waves * 64), stream);
+        return lane == 4 ? run_norm<XT, YT, HT, 4>(a, z, h, stats, grid, dim3(waves * 64), stream)
+                         : run_norm<XT, YT, HT, 8>(a, z, h, stats, grid, dim3(waves * 64), stream);
     });
 }
 
 NormSplit norm_split(int64_t width, int64_t rows, int64_t groups) {
     NormSplit s;
-    const int waves = worker_waves(width);
+    const int waves = worker_waves(width, backward_lane(width));
     s.workers_a_group = std::max(1, 8 / waves);
-    // two workgroups a compute unit
-    const int64_t target = int64_t(512) * s.workers_a_group;
+    // 16 waves a compute unit
+    const int64_t target = int64_t(256 * 16 / waves);
     const int64_t per = std::max<int64_t>(1, (rows + target - 1) / target);
     s.group_rows = groups > 0 ? rows / groups : 0;
     s.chunks = 1;
@@ -664,27 +701,25 @@ ks_status_t launch_norm_grad(const ks_residual_norm_t& n, const NormSplit& s, co
     g.dgate = dgate;
     g.split = s;
     g.parts = {static_cast<float*>(ws), static_cast<float*>(ws) + sum_parts(n, s), s.workgroups, any ? wanted(n) : 0};
-    const NormArgs a = norm_args(n, x, y, gate, groups, rows);
+    const int lane = backward_lane(n.width);
+    const NormArgs a = norm_args(n, x, y, gate, groups, rows, lane);
     ks_status_t st = KS_OK;
     if (rows > 0) {
-        const bool wide = n.width % (n.width <= kNarrow ? 4 : 8) == 0 && aligned16({x, y, gate, dz, dh, dx, dy, dgate, ws, n.pre_weight,
-                                                         n.post_weight, n.post_bias, n.scale});
         const dim3 grid(static_cast<unsigned>(s.workgroups)), block(s.workers_a_group * a.waves * 64);
-        const bool narrow = n.width <= kNarrow;
-        const size_t row = static_cast<size_t>(a.waves) * 64 * (narrow ? 4 : 8) * 4;
-        const size_t lds = !narrow ? kSums * row : s.workers_a_group > 1 ? row : 0;
+        const size_t row = static_cast<size_t>(a.waves) * 64 * lane * 4;
+        const size_t lds = lane == 8 ? kSums * row : s.workers_a_group > 1 ? row : 0;
         st = with_types(n, [&](auto xt, auto yt, auto ht) {
             typedef decltype(xt) XT;
             typedef decltype(yt) YT;
             typedef decltype(ht) HT;
-            return narrow ? run_grad<XT, YT, HT, 4>(a, g, wide, grid, block, lds, stream)
-                          : run_grad<XT, YT, HT, 8>(a, g, wide, grid, block, lds, stream);
+            return lane == 4 ? run_grad<XT, YT, HT, 4>(a, g, grid, block, lds, stream)
+                             : run_grad<XT, YT, HT, 8>(a, g, grid, block, lds, stream);
         });
     }
     // the vectors and the gates that workers share (of no rows: zeros), in one launch
     const bool shared = dgate && groups > 0 && (rows == 0 || s.chunks > 1);
-    const int64_t blocks = (n.width + 31) / 32, from = any ? 0 : 1, to = shared ? groups + 1 : 1;
-    const NormJoin j{n, out, g.parts, dgate, groups, rows > 0 ? s.chunks : 0};
+    const int64_t blocks = (n.width + 31) / 32, from = any ? 0 : kVectorJobs, to = kVectorJobs + (shared ? groups : 0);
+    const NormJoin j{n, out, g.parts, dgate, rows > 0 ? s.chunks : 0};
     const int64_t most = kMaxGrid / 4 / blocks;
     for (int64_t at = from; st == KS_OK && at < to; at += most)
         st = launch_kernel(norm_join_kernel, dim3(static_cast<unsigned>(std::min(most, to - at) * blocks)), dim3(1024), 0,
