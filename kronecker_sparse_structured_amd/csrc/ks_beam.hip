@@ -9,11 +9,13 @@
 // and finds its best `keep` values (keep = min(out_beams, vocab)) without a
 // barrier:
 //   1. the keep-th largest of the 64 lanes' own maxima is a bound: at least keep
-//      values of the slice reach it, and only keep lanes hold any,
-//   2. the values that reach it go to a list in LDS (at most keep times what a
-//      lane holds; keep or a few more of random values),
+//      values of the slice reach it,
+//   2. those that do go to a list in LDS: keep or a few more of random values. Only
+//      keep lanes have any, so the list has room for all, unless lanes' maxima are
+//      (nearly) equal: then the bound is taken again over values with their
+//      tokens, of which no two are,
 //   3. each of them counts how many of the list are before it: its place.
-// Values are compared as 64-bit keys, their order's 32 bits and then the lower
+// Values are ordered as 64-bit keys, their order's 32 bits and then the lower
 // token, so that no two are equal and every choice is the same each time.
 //
 // Then one workgroup a request joins the slices of each beam (its lists in the
@@ -29,10 +31,10 @@ namespace ks {
 namespace {
 
 constexpr int kMaxBeams = KS_BEAM_MAX;
-constexpr int kHold = 4;                 // 16-byte vectors a lane holds of a slice
-constexpr int kSliceBytes = 64 * 16 * kHold;
+constexpr int kHeld = 32;                // values a lane holds of a slice
+constexpr int kSlice = 64 * kHeld;
 constexpr int kSelectWaves = 4;          // a workgroup of the first launch
-constexpr int kJoinWaves = 8;            // of the second, at most
+constexpr int kJoinWaves = 16;           // of the second, at most
 constexpr int kJoinHold = 8;             // keys a lane holds there
 
 // The order of fp32 values as unsigned numbers; -0 is 0.
@@ -48,27 +50,48 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
     return static_cast<uint64_t>(ordered(x)) << 32 | (0xffffffffu - token);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int d) {
-    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(x), d, 64), hi = __shfl_xor(static_cast<uint32_t>(x >> 32), d, 64);
-    return static_cast<uint64_t>(hi) << 32 | lo;
+// The wave's largest x, in every lane: exchanges within 16 lanes, then lane 15 of a
+// row of 16 to the next row, lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_with(uint32_t x) {
+    return max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xf, false)));
 }
-__device__ __forceinline__ uint64_t wave_max64(uint64_t x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t y = shfl_xor64(x, d);
-        x = y > x ? y : x;
-    }
-    return x;
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = max_with<0xb1, 0xf>(x);
+    x = max_with<0x4e, 0xf>(x);
+    x = max_with<0x141, 0xf>(x);
+    x = max_with<0x140, 0xf>(x);
+    x = max_with<0x142, 0xa>(x);
+    x = max_with<0x143, 0xc>(x);
+    return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
+    const uint32_t hi = wave_max(static_cast<uint32_t>(x >> 32));
+    return static_cast<uint64_t>(hi) << 32 | wave_max(static_cast<uint32_t>(x >> 32) == hi ? static_cast<uint32_t>(x) : 0u);
 }
 
-// The keep-th largest of the lanes' keys (0 if fewer lanes have one).
-__device__ __forceinline__ uint64_t bound_of(uint64_t mine, int keep) {
-    uint64_t top = 0;
-    for (int k = 0; k < keep; ++k) {
-        top = wave_max64(mine);
-        if (mine == top) mine = 0;
+// The upper BITS bits of the keep-th largest of the lanes' x, the others 0: bit by
+// bit, by how many lanes reach it (keep rounds of a maximum take longer from 6 on).
+template <int BITS, typename K>
+__device__ __forceinline__ K bound_of(K x, int keep) {
+    constexpr int kAll = 8 * sizeof(K);
+    K t = 0;
+#pragma unroll
+    for (int b = kAll - 1; b >= kAll - BITS; --b) {
+        const K higher = t | K(1) << b;
+        if (__popcll(__ballot(x >= higher)) >= keep) t = higher;
     }
-    return top;
+    return t;
+}
+
+// Appends the lanes' keys that are `in` to a list of n with room for `most`; n
+// counts those without room too.
+__device__ __forceinline__ void append(uint64_t* list, int& n, int most, bool in, uint64_t key) {
+    const uint64_t mask = __ballot(in);
+    if (mask == 0) return;
+    const int at = n + __popcll(mask & ((1ull << (threadIdx.x % 64)) - 1));
+    if (in && at < most) list[at] = key;
+    n += __popcll(mask);
 }
 
 // What the wave's lanes wrote to LDS is there for all of them.
@@ -83,6 +106,7 @@ __device__ __forceinline__ void sort_best(const uint64_t* list, int n, int keep,
     for (int i = lane; i < n; i += 64) {
         const uint64_t mine = list[i];
         int place = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j) place += list[j] > mine;
         if (place < keep) out[place] = mine;
     }
@@ -98,9 +122,9 @@ struct Slices {
 
 template <typename T>
 __global__ __launch_bounds__(kSelectWaves * 64) void beam_slices_kernel(const ks_beams_t x, Slices s, int64_t unit0) {
-    constexpr int E = kVec<T>, kHeld = E * kHold, kSlice = 64 * kHeld;
+    constexpr int E = kVec<T>, kHold = kHeld / E;
     extern __shared__ uint64_t lists[];                    // kSelectWaves x keep x kHeld
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int64_t unit = unit0 + static_cast<int64_t>(blockIdx.x) * kSelectWaves + wave;
     const int64_t row = unit / s.slices;
     if (row >= x.requests * x.beams) return;
@@ -109,119 +133,156 @@ __global__ __launch_bounds__(kSelectWaves * 64) void beam_slices_kernel(const ks
     const int64_t r = row / x.beams;
     const T* data = static_cast<const T*>(x.data) + r * x.request_stride + (row - r * x.beams) * x.beam_stride;
     const uint32_t first = slice * kSlice, V = static_cast<uint32_t>(x.vocab);   // below 2^31 + kSlice
+    // 16-byte accesses that may start at any element: rows of an odd vocabulary do
+    typedef typename Access<T, 4>::vec access;
     float v[kHold][E];
-    const bool wide = reinterpret_cast<uintptr_t>(data) % 16 == 0;
+    if (first + kSlice <= V) {
+        u32x4 w[kHold];
 #pragma unroll
-    for (int u = 0; u < kHold; ++u) {
-        const uint32_t at = first + (u * 64 + lane) * E;
-        if (wide && at + E <= V) {
-            widen<T>(*reinterpret_cast<const u32x4*>(data + at), v[u]);
-        } else {
+        for (int u = 0; u < kHold; ++u) w[u] = *reinterpret_cast<const access*>(data + first + (u * 64 + lane) * E);
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[u][i] = at + i < V ? to_f32(data[at + i]) : -INFINITY;
+        for (int u = 0; u < kHold; ++u) widen<T>(w[u], v[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+            const uint32_t at = first + (u * 64 + lane) * E;
+            if (at + E <= V) {
+                widen<T>(*reinterpret_cast<const access*>(data + at), v[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[u][i] = at + i < V ? to_f32(data[at + i]) : -INFINITY;
+            }
         }
     }
-    float top = kLowest;
-    uint64_t best = 0;
+    float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kHold; ++u)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const uint32_t at = first + (u * 64 + lane) * E + i;
-            top = fmaxf(top, v[u][i]);
-            const uint64_t k = key_of(v[u][i], at);
-            if (at < V && k > best) best = k;
-        }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        for (int i = 0; i < E; ++i) top = fmaxf(top, v[u][i]);
+    const uint32_t mine = ordered(top);
+    top = fmaxf(value_of(wave_max(mine)), kLowest);
     float sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kHold; ++u)
+    for (int u = 0; u < kHold; ++u) {
+        float part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum += exp_of(v[u][i] - top);
+        for (int i = 0; i < E; ++i) part += exp_of(v[u][i] - top);
+        sum += part;
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
     if (lane == 0) s.stats[unit] = make_float2(top, sum);
-    const uint64_t bound = bound_of(best, s.keep);
-    uint64_t* list = lists + static_cast<size_t>(wave) * s.keep * kHeld;
-    int n = 0;
+    // 16 bits of the bound will do: a few more values reach it
+    const float bound = value_of(max(bound_of<16>(mine, s.keep), ordered(-INFINITY)));
+    const int most = s.keep * kHeld;
+    uint64_t* list = lists + static_cast<size_t>(wave) * most;
+    auto key = [&](int u, int i) {
+        const uint32_t at = first + (u * 64 + lane) * E + i;
+        return at < V ? key_of(v[u][i], at) : 0;
+    };
+    auto collect = [&](uint64_t least) {
+        int n = 0;
 #pragma unroll
-    for (int u = 0; u < kHold; ++u)
+        for (int u = 0; u < kHold; ++u)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const uint32_t at = first + (u * 64 + lane) * E + i;
-            const uint64_t k = key_of(v[u][i], at);
-            const bool in = at < V && k >= bound;
-            const uint64_t mask = __ballot(in);
-            if (in) list[n + __popcll(mask & ((1ull << lane) - 1))] = k;
-            n += __popcll(mask);
-        }
+            for (int i = 0; i < E; ++i)
+                if (__ballot(v[u][i] >= bound)) append(list, n, most, v[u][i] >= bound && key(u, i) >= least, key(u, i));
+        return n;
+    };
+    int n = collect(1);
+    if (n > most) {
+        uint64_t best = 0;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) best = max(best, key(u, i));
+        n = collect(max(bound_of<64>(best, s.keep), uint64_t(1)));
+    }
     wave_lds_fence();
     sort_best(list, n, s.keep, s.keys + unit * s.keep);
 }
 
-// x is better than y: a higher rank, or an equal one earlier.
-__device__ __forceinline__ bool better(double x, int at, double y, int other) {
-    return x > y || (x == y && at < other);
+// The order of doubles as unsigned numbers above 0; -0 is 0.
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
+    return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// The best candidates of one request.
+// The best candidates of one request: a wave joins a beam's slices, all rank the
+// beams' candidates, and the first picks.
 __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_beams_t x, Slices s, BeamOut out,
                                                                     int64_t request0) {
     extern __shared__ uint64_t lds[];
-    const int waves = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64, W = x.beams, keep = s.keep;
+    const int waves = blockDim.x / 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int W = x.beams, keep = s.keep;
     uint64_t* best = lds;                                             // W x keep
-    uint64_t* list = best + W * keep + wave * keep * kJoinHold;
+    uint64_t* ranks = best + W * keep;                                // W x keep
+    uint64_t* list = ranks + W * keep + wave * keep * kJoinHold;
     __shared__ double base[kMaxBeams], divisor[kMaxBeams];            // score = base + x, rank = score / divisor
-    __shared__ int length[kMaxBeams];
+    __shared__ int length[kMaxBeams], chosen[kMaxBeams];
     const int64_t request = request0 + blockIdx.x;
     for (int w = wave; w < W; w += waves) {
         const int64_t row = request * W + w;
+        // everything that may be needed is asked for at once (what a beam that is
+        // done left in the workspace is not used)
+        const uint64_t* keys = s.keys + row * s.slices * keep;
+        const int n = s.slices * keep;
+        uint64_t mine[kJoinHold];
+#pragma unroll
+        for (int u = 1; u < kJoinHold; ++u) {
+            const int i = (u - 1) * 64 + lane;
+            mine[u] = i < n ? keys[i] : 0;
+        }
+        const float2* st = s.stats + row * s.slices;
+        const float2 own = lane < s.slices ? st[lane] : make_float2(kLowest, 0.0f);
         const double score = x.scores[row];
         const bool done = x.done && x.done[row];
         const int len = x.lengths ? x.lengths[row] + (done ? 0 : 1) : 0;
         double shift = 0.0;
         bool live = score - score == 0.0;                             // finite
-        if (!done) {
-            const float2* st = s.stats + row * s.slices;
-            double top = kLowest, sum = 0.0;
-            for (int i = lane; i < s.slices; i += 64) top = fmax(top, static_cast<double>(st[i].x));
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) top = fmax(top, __shfl_xor(top, d, 64));
-            for (int i = lane; i < s.slices; i += 64)
+        if (done) {
+            for (int i = lane; i < keep; i += 64)
+                best[w * keep + i] = i == 0 ? key_of(0.0f, static_cast<uint32_t>(x.eos)) : 0;
+        } else {
+            float top = own.x;
+            for (int i = 64 + lane; i < s.slices; i += 64) top = fmaxf(top, st[i].x);
+            top = value_of(wave_max(ordered(top)));
+            double sum = static_cast<double>(own.y) * exp(static_cast<double>(own.x) - top);
+            for (int i = 64 + lane; i < s.slices; i += 64)
                 sum += static_cast<double>(st[i].y) * exp(static_cast<double>(st[i].x) - top);
             sum = wave_sum(sum);
             shift = -top - log(sum);
             live = live && sum > 0.0 && sum - sum == 0.0;
             // the slices' keys, as many at a time as the list has room for beside
             // the best of those before
-            const uint64_t* keys = s.keys + row * s.slices * keep;
-            const int n = s.slices * keep;
-            uint64_t mine[kJoinHold];
             for (int first = 0; first < n; first += 64 * (kJoinHold - 1)) {
-                uint64_t high = mine[0] = first > 0 && lane < keep ? best[w * keep + lane] : 0;
+                mine[0] = first > 0 && lane < keep ? best[w * keep + lane] : 0;
+                uint64_t high = mine[0];
 #pragma unroll
                 for (int u = 1; u < kJoinHold; ++u) {
                     const int i = first + (u - 1) * 64 + lane;
-                    mine[u] = i < n ? keys[i] : 0;
-                    high = mine[u] > high ? mine[u] : high;
+                    if (first > 0) mine[u] = i < n ? keys[i] : 0;
+                    high = max(high, mine[u]);
                 }
-                const uint64_t bound = bound_of(high, keep);
-                int count = 0;
+                // as in a slice: by the values alone, and with the tokens if too many reach it
+                uint64_t least = static_cast<uint64_t>(bound_of<32>(static_cast<uint32_t>(high >> 32), keep)) << 32;
+                const int most = keep * kJoinHold;
+                auto collect = [&]() {
+                    int count = 0;
+                    least = max(least, uint64_t(1));
 #pragma unroll
-                for (int u = 0; u < kJoinHold; ++u) {
-                    const bool in = mine[u] != 0 && mine[u] >= bound;
-                    const uint64_t mask = __ballot(in);
-                    if (in) list[count + __popcll(mask & ((1ull << lane) - 1))] = mine[u];
-                    count += __popcll(mask);
+                    for (int u = 0; u < kJoinHold; ++u) append(list, count, most, mine[u] >= least, mine[u]);
+                    return count;
+                };
+                int count = collect();
+                if (count > most) {
+                    least = bound_of<64>(high, keep);
+                    count = collect();
                 }
                 wave_lds_fence();
                 sort_best(list, count, keep, best + w * keep);
                 wave_lds_fence();
             }
-        } else {
-            for (int i = lane; i < keep; i += 64)
-                best[w * keep + i] = i == 0 ? key_of(0.0f, static_cast<uint32_t>(x.eos)) : 0;
         }
         if (lane == 0) {
             base[w] = live ? score + shift : -INFINITY;
@@ -230,53 +291,40 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         }
     }
     __syncthreads();
+    for (int i = threadIdx.x; i < W * keep; i += blockDim.x) {
+        const uint64_t k = best[i];
+        const double score = base[i / keep] + static_cast<double>(value_of(static_cast<uint32_t>(k >> 32)));
+        // no candidate: below every rank
+        ranks[i] = k != 0 && base[i / keep] > -INFINITY && score > -INFINITY ? ordered(score / divisor[i / keep]) : 0;
+    }
+    __syncthreads();
     if (wave != 0) return;
-    // lane w goes down beam w's list
-    int next = 0, token = 0;
-    double score = -INFINITY, rank = -INFINITY;
-    auto take = [&]() {
-        score = rank = -INFINITY;
-        if (lane >= W || next >= keep) return;
-        const uint64_t k = best[lane * keep + next];
-        ++next;
-        if (k == 0 || !(base[lane] > -INFINITY)) return;
-        token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
-        score = base[lane] + static_cast<double>(value_of(static_cast<uint32_t>(k >> 32)));
-        rank = score > -INFINITY ? score / divisor[lane] : score;
-    };
-    take();
-    const int64_t to = request * out.beams;
-    for (int j = 0; j < out.beams; ++j) {
-        double high = rank;
-        int at = lane < W ? lane : 64;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double other = __shfl_xor(high, d, 64);
-            const int from = __shfl_xor(at, d, 64);
-            if (better(other, from, high, at)) {
-                high = other;
-                at = from;
-            }
-        }
-        if (!(high > -INFINITY)) {                                    // none is left
-            if (lane == 0) {
-                out.scores[to + j] = -INFINITY;
-                out.tokens[to + j] = x.eos >= 0 ? x.eos : 0;
-                out.parents[to + j] = 0;
-                if (out.done) out.done[to + j] = 1;
-                if (out.lengths) out.lengths[to + j] = 0;
-            }
-            continue;
-        }
-        if (lane == at) {
-            out.scores[to + j] = static_cast<float>(score);
-            out.tokens[to + j] = token;
-            out.parents[to + j] = lane;
-            if (out.done) out.done[to + j] = token == x.eos;
-            if (out.lengths) out.lengths[to + j] = length[lane];
-            take();
+    // lane w goes down beam w's list, the rank after the next at hand
+    const uint64_t* mine = ranks + lane * keep;
+    int at = 0, found = 0;
+    uint64_t rank = lane < W ? mine[0] : 0, after = lane < W && keep > 1 ? mine[1] : 0;
+    for (; found < out.beams; ++found) {
+        const uint64_t high = wave_max(rank);
+        if (high == 0) break;                                         // none is left
+        if (lane == __ffsll(__ballot(rank == high)) - 1) {            // the lowest beam of equal rank
+            chosen[found] = lane * keep + at;
+            ++at;
+            rank = after;
+            after = at + 1 < keep ? mine[at + 1] : 0;
         }
     }
+    wave_lds_fence();
+    if (lane >= out.beams) return;
+    const int64_t to = request * out.beams + lane;
+    const bool is = lane < found;
+    const int pick = is ? chosen[lane] : 0, w = pick / keep;
+    const uint64_t k = best[pick];
+    const int64_t token = is ? static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(k)) : x.eos >= 0 ? x.eos : 0;
+    out.scores[to] = is ? static_cast<float>(base[w] + static_cast<double>(value_of(static_cast<uint32_t>(k >> 32)))) : -INFINITY;
+    out.tokens[to] = token;
+    out.parents[to] = is ? w : 0;
+    if (out.done) out.done[to] = !is || token == x.eos;
+    if (out.lengths) out.lengths[to] = is ? length[w] : 0;
 }
 
 // ---------------------------------------------------------------- states
@@ -300,18 +348,28 @@ struct StateTable {
 template <typename V>
 __device__ __forceinline__ void copy_piece(const StateEntry& e, int64_t row, int64_t from, int64_t piece, bool valid) {
     const int lane = threadIdx.x % 64;
-    const int64_t n = e.row_bytes / static_cast<int64_t>(sizeof(V));
-    V* dst = reinterpret_cast<V*>(e.dst + row * e.row_bytes);
-    const V* src = reinterpret_cast<const V*>(e.src + (valid ? from : 0) * e.row_bytes);
-    for (int k = 0; k < kPiece; ++k) {
-        const int64_t i = (piece * kPiece + k) * 64 + lane;
-        if (i < n) dst[i] = valid ? src[i] : V{};
+    const int64_t n = e.row_bytes / static_cast<int64_t>(sizeof(V)), at = piece * kPiece * 64 + lane;
+    V* dst = reinterpret_cast<V*>(e.dst + row * e.row_bytes) + at;
+    const V* src = reinterpret_cast<const V*>(e.src + (valid ? from : 0) * e.row_bytes) + at;
+    const int left = static_cast<int>(min(n - at, int64_t(kPiece) * 64));
+    constexpr int U = 4;         // on their way at once
+#pragma unroll 1
+    for (int k0 = 0; k0 < kPiece; k0 += U) {
+        V v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            v[k] = V{};
+            if (valid && (k0 + k) * 64 < left) v[k] = src[(k0 + k) * 64];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if ((k0 + k) * 64 < left) dst[(k0 + k) * 64] = v[k];
     }
 }
 
 __global__ __launch_bounds__(256) void beam_reorder_kernel(const StateTable t, const int32_t* parents, int beams,
                                                            int out_beams, int64_t wave0, int64_t waves) {
-    const int64_t unit = wave0 + static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+    const int64_t unit = wave0 + static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (unit >= waves) return;
     int k = 0;
     for (int i = 1; i < t.count; ++i)
@@ -327,8 +385,7 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(const StateTable t, c
 }
 
 int slice_count(const ks_beams_t& x) {
-    const int64_t slice = kSliceBytes / (x.elem == KS_ELEM_BF16 ? 2 : 4);
-    return static_cast<int>((x.vocab + slice - 1) / slice);
+    return static_cast<int>((x.vocab + kSlice - 1) / kSlice);
 }
 
 Slices slices_of(const ks_beams_t& x, int out_beams, void* ws) {
@@ -352,7 +409,7 @@ ks_status_t launch_beam_select(const ks_beams_t& x, const BeamOut& out, void* ws
     const Slices s = slices_of(x, out.beams, ws);
     const int64_t units = x.requests * x.beams * s.slices;
     const bool bf16 = x.elem == KS_ELEM_BF16;
-    const size_t lds = static_cast<size_t>(kSelectWaves) * s.keep * kHold * (bf16 ? 8 : 4) * 8;
+    const size_t lds = static_cast<size_t>(kSelectWaves) * s.keep * kHeld * 8;
     const int64_t groups = (units + kSelectWaves - 1) / kSelectWaves;
     for (int64_t g = 0; g < groups; g += kMaxGrid) {
         const ks_status_t st = launch_kernel(bf16 ? beam_slices_kernel<bf16_t> : beam_slices_kernel<float>,
@@ -361,7 +418,7 @@ ks_status_t launch_beam_select(const ks_beams_t& x, const BeamOut& out, void* ws
         if (st != KS_OK) return st;
     }
     const int waves = std::min(kJoinWaves, x.beams);
-    const size_t join = static_cast<size_t>(x.beams * s.keep + waves * s.keep * kJoinHold) * 8;
+    const size_t join = static_cast<size_t>(2 * x.beams * s.keep + waves * s.keep * kJoinHold) * 8;
     for (int64_t r = 0; r < x.requests; r += kMaxGrid) {
         const ks_status_t st = launch_kernel(beam_join_kernel,
                                              dim3(static_cast<unsigned>(std::min(kMaxGrid, x.requests - r))),

@@ -17,6 +17,12 @@ __device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float(stati
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// V words in one access that may start at any element of type T.
+template <typename T, int V>
+struct Access {
+    typedef uint32_t vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+};
+
 // Four consecutive elements (16-byte aligned for fp32, 8-byte for bf16),
 // widened to fp32, in one load.
 __device__ __forceinline__ void load4_f32(const float* p, float (&v)[4]) {

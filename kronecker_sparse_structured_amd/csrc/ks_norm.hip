@@ -63,11 +63,6 @@ struct Raw {
     }
 };
 
-template <typename T, int V>
-struct Access {
-    typedef uint32_t vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-};
-
 template <int L>
 struct Lanes {
     int t, left;            // the lane in its worker; columns from its first on, none below 0
