@@ -6,8 +6,12 @@
 //   dx_v = (w T (p_v - q_v) + (1 - w) (p1_v - 1[v = label])) / N
 //
 // A row of logits is 8 KB to 200 KB, its entries at most a few KB: one
-// workgroup a row. The maximum and both sums of exponentials are kept in one
-// pass, as in ks_preference.hip.
+// workgroup a row. The factor of a row's gradient is known before any row is, so
+// where loss and gradient are asked for together a row is read once and written
+// once: a workgroup holds it in registers (up to 256 KB) while its maximum, its
+// sums and its entries' part are formed. Longer rows, and a gradient that is
+// asked for later, go through the row again; there the maximum and both sums of
+// exponentials are kept in one pass, as in ks_preference.hip.
 
 #include <algorithm>
 #include <cmath>
@@ -22,6 +26,21 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxTop = KS_TEACHER_MAX_COUNT;
 static_assert(kMaxTop <= kThreads, "an entry a thread");
+
+// 16 bytes of values that no maximum and no sum sees.
+template <typename T>
+__device__ __forceinline__ u32x4 lowest() {
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;      // -inf
+    return u32x4{w, w, w, w};
+}
+
+// Keeps a row's values as they were loaded: without it the compiler widens them
+// once for all phases, which takes twice their registers.
+template <int U>
+__device__ __forceinline__ void keep_narrow(u32x4 (&w)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" : "+v"(w[u]));
+}
 
 // exp((x - m) / T) as exp2((x - m) hi + (x - m) lo): log2 e / T in two parts, both
 // positive, so that a difference of -inf gives 0 and not -inf + inf.
@@ -52,6 +71,25 @@ __device__ __forceinline__ float wave_sum32(float x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
     return x;
+}
+
+__device__ __forceinline__ float uniform(float x) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+// Of the W waves' values: a lane reads one, W lanes exchange them.
+template <int W>
+__device__ __forceinline__ float waves_max(const float (&v)[W]) {
+    float x = v[threadIdx.x % W];
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+    return uniform(x);
+}
+template <int W>
+__device__ __forceinline__ float waves_sum(const float (&v)[W]) {
+    float x = v[threadIdx.x % W];
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) x += __shfl_xor(x, d, 64);
+    return uniform(x);
 }
 
 // A row's entry of this thread: q, its logarithm and its token (-1: none).
@@ -96,14 +134,24 @@ __device__ __forceinline__ Entry teacher_entry(const DistilArgs& a, int64_t s, i
     return e;
 }
 
+// The label of row `at`, of rows below 2^31.
+__device__ __forceinline__ int64_t label_at(const ks_logits_t& x, int64_t at) {
+    const uint32_t s = static_cast<uint32_t>(at) / static_cast<uint32_t>(x.tokens);
+    return x.labels[s * x.label_stride + (at - static_cast<int64_t>(s) * x.tokens)];
+}
+
 // inv = 1 / (unmasked positions), at least one.
 __global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x, float* inv) {
     __shared__ int sums[16];
     const int64_t n = x.sequences * x.tokens;
     int count = 0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        const int64_t s = i / x.tokens;
-        count += x.labels[s * x.label_stride + (i - s * x.tokens)] >= 0;
+    constexpr int U = 8;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
+        int64_t label[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) label[u] = i0 + 1024 * u < n ? label_at(x, i0 + 1024 * u) : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) count += label[u] >= 0;
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
@@ -218,7 +266,14 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
 __global__ __launch_bounds__(1024) void distil_sum_kernel(const float* tokens, int64_t n, const float* inv, float* loss) {
     __shared__ double sums[16];
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(tokens[i]);
+    constexpr int U = 8;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = i0 + 1024 * u < n ? tokens[i0 + 1024 * u] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += static_cast<double>(v[u]);
+    }
     s = wave_sum(s);
     if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
     __syncthreads();
@@ -315,6 +370,209 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
     }
 }
 
+// Loss and gradient of a row that the workgroup holds, U 16-byte vectors a lane.
+// Rows of logits and of their gradient may start at any element: the vectors
+// start where the gradient's lines do, so that stores fill them; what lies before
+// the first and behind the last goes element-wise. COUNT: the workgroup counts
+// the unmasked positions itself.
+template <typename T, bool TWO, int NT, int U, bool COUNT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 : U == 8 ? 6 : 4))) void distil_row_kernel(
+    const DistilArgs a, float* tokens, float* inv, T* d_, int64_t d_seq, int64_t d_row) {
+    constexpr int E = kVec<T>, W = NT / 64;
+    __shared__ float maxima[2][W], sums[3][W];
+    __shared__ double parts[W];
+    __shared__ int counts[W];
+    __shared__ int ids[kMaxTop + 1];
+    __shared__ float qs[kMaxTop + 1], xs[kMaxTop + 1];
+    const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
+    const int64_t label = a.x.labels[s * a.x.label_stride + t];
+    const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
+    T* out = d_ + s * d_seq + t * d_row;
+    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x, wave = tid / 64;
+    const int head = head_of(out, V), vecs = (V - head) / E, tail = head + vecs * E;
+    typedef typename Access<T, 4>::vec access;
+    u32x4* obody = reinterpret_cast<u32x4*>(out + head);
+    if (label < 0 && !(COUNT && at == 0)) {
+        if (tid == 0) tokens[at] = 0.0f;
+        if (tid < head) out[tid] = narrow<T>(0.0f);
+        if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
+        const u32x4 none = {0u, 0u, 0u, 0u};
+        for (int v = tid; v < vecs; v += NT) __builtin_nontemporal_store(none, &obody[v]);
+        return;
+    }
+    // the row
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = u * NT + tid;
+        w[u] = lowest<T>();
+        if (v < vecs) w[u] = *reinterpret_cast<const access*>(row + head + v * E);
+    }
+    const float xh = tid < head ? to_f32(row[tid]) : -INFINITY, xt = tid < V - tail ? to_f32(row[tail + tid]) : -INFINITY;
+    // its entries: one a thread
+    const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
+    int64_t id = -1;
+    float top = -INFINITY, xe = 0.0f;
+    if (kl && tid < a.t.count) {
+        const int64_t from = s * a.t.id_seq_stride + t * a.t.id_row_stride + tid;
+        id = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[from] : static_cast<const int32_t*>(a.t.ids)[from];
+        if (id >= 0) {
+            const int64_t k = s * a.t.top_seq_stride + t * a.t.top_row_stride + tid;
+            top = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[k])
+                                           : static_cast<const float*>(a.t.top)[k];
+            if (id < V) xe = to_f32(row[id]);
+        }
+    }
+    const float xl = tid == 0 && ce && label >= 0 ? to_f32(row[label < V ? label : 0]) : 0.0f;
+    int count = 0;
+    if (COUNT) {
+        const int n = static_cast<int>(a.x.sequences * a.x.tokens);
+        for (int i = tid; i < n; i += NT) count += label_at(a.x, i) >= 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
+    }
+    // maxima
+    float m = fmaxf(fmaxf(xh, xt), kLowest);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float x[E];
+        widen<T>(w[u], x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) m = fmaxf(m, x[i]);
+    }
+    m = wave_max(m);
+    float tm = wave_max(top);
+    if (tid % 64 == 0) {
+        maxima[0][wave] = m;
+        maxima[1][wave] = tm;
+        if (COUNT) counts[wave] = count;
+    }
+    __syncthreads();
+    m = waves_max(maxima[0]);
+    tm = waves_max(maxima[1]);
+    float scale;
+    if (COUNT) {
+        count = 0;
+        for (int k = 0; k < W; ++k) count += counts[k];
+        scale = static_cast<float>(1.0 / static_cast<double>(max(count, 1)));
+        if (at == 0 && tid == 0) *inv = scale;
+        if (label < 0) {                     // row 0, which stayed to count
+            if (tid == 0) tokens[at] = 0.0f;
+            for (int v = tid; v < V; v += NT) out[v] = narrow<T>(0.0f);
+            return;
+        }
+    } else {
+        scale = *inv;
+    }
+    // sums
+    keep_narrow(w);
+    if (tm == -INFINITY) tm = 0.0f;          // no entry that weighs anything
+    const float p = exp_of(top - tm, a.scale);
+    float sum = exp_of(xh - m, a.scale) + exp_of(xt - m, a.scale), sum1 = 0.0f;
+    if (TWO) sum1 = ks::exp_of(xh - m) + ks::exp_of(xt - m);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u * NT >= vecs) continue;        // the same for all threads
+        float x[E], part = 0.0f, part1 = 0.0f;
+        widen<T>(w[u], x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            part += exp_of(x[i] - m, a.scale);
+            if (TWO) part1 += ks::exp_of(x[i] - m);
+        }
+        sum += part;
+        if (TWO) sum1 += part1;
+    }
+    sum = wave_sum32(sum);
+    if (TWO) sum1 = wave_sum32(sum1);
+    float tsum = wave_sum32(p);
+    if (tid % 64 == 0) {
+        sums[0][wave] = sum;
+        sums[1][wave] = sum1;
+        sums[2][wave] = tsum;
+    }
+    __syncthreads();
+    sum = sum1 = tsum = 0.0f;
+    for (int k = 0; k < W; ++k) {
+        sum += sums[0][k];
+        if (TWO) sum1 += sums[1][k];
+        tsum += sums[2][k];
+    }
+    if (!TWO) sum1 = sum;
+    keep_narrow(w);
+    // what the gradient needs of the entries
+    const bool any = kl && tsum != 0.0f;     // else that side is not there
+    const float slope = any ? a.slope * scale : 0.0f, hard = static_cast<float>(a.ce) * scale;
+    float q = id >= 0 && any ? p / tsum : 0.0f;
+    if (id >= V) q = __builtin_nanf("");
+    const int entries = a.t.count + 1;
+    if (tid < a.t.count) {
+        const bool in = id >= 0 && id < V;
+        ids[tid] = in ? static_cast<int>(id) : !(q == 0.0f) ? 0 : -1;      // an id outside: the row says so at 0
+        qs[tid] = slope * q;
+        xs[tid] = in ? xe : 0.0f;
+    }
+    if (tid == 0) {
+        ids[entries - 1] = !ce ? -1 : label < V ? static_cast<int>(label) : 0;
+        qs[entries - 1] = label < V ? hard : __builtin_nanf("");
+        xs[entries - 1] = xl;
+    }
+    // the gradient as if there were no entries
+    const float c0 = uniform(TWO ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
+    auto value = [&](float x) {
+        // (x - m) log2 e / T is off by 1e-7 of itself without the second part: far
+        // below a rounding of the value's type, or of the sums before it
+        float y = c0 * __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
+        if (TWO) y += c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
+        return y;
+    };
+    if (tid < head) out[tid] = narrow<T>(value(xh));
+    if (tid < V - tail) out[tail + tid] = narrow<T>(value(xt));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = u * NT + tid;
+        if (v >= vecs) continue;
+        float x[E];
+        widen<T>(w[u], x);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = value(x[i]);
+        __builtin_nontemporal_store(pack<T>(x), &obody[v]);
+    }
+    // the entries' part of the loss
+    double part = 0.0;
+    if (!(q == 0.0f)) {
+        const double logq = static_cast<double>(top - tm) * a.inverse - log(static_cast<double>(tsum));
+        const double logp = (static_cast<double>(xe) - m) * a.inverse - log(static_cast<double>(sum));
+        part = q * (logq - logp);
+    }
+    if (wave * 64 < a.t.count) part = wave_sum(part);
+    if (tid % 64 == 0) parts[wave] = part;
+    __syncthreads();
+    // the values at the entries' and the label's tokens again
+    for (int k = tid; k < entries; k += NT) {
+        const int mine = ids[k];
+        if (mine < 0) continue;
+        float taken = 0.0f;
+        bool first = true;
+        for (int j = 0; j < entries; ++j) {
+            if (ids[j] != mine) continue;
+            first = first && j >= k;
+            taken += qs[j];
+        }
+        if (first) out[mine] = narrow<T>(value(xs[k]) - taken);
+    }
+    if (tid == 0) {
+        double token = 0.0;
+        for (int k = 0; k * 64 < a.t.count; ++k) token += parts[k];
+        token = kl ? token * a.kl : 0.0;
+        if (ce) {
+            const double x = label < V ? xl : __builtin_nanf("");
+            token -= a.ce * ((x - m) - log(static_cast<double>(sum1)));
+        }
+        tokens[at] = static_cast<float>(token);
+    }
+}
+
 DistilArgs distil_args(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o) {
     DistilArgs a;
     a.x = x;
@@ -375,6 +633,52 @@ ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, cons
                                 dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<bf16_t*>(d), d_seq, d_row)
                 : launch_kernel(two ? distil_grad_kernel<float, true> : distil_grad_kernel<float, false>, grid,
                                 dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<float*>(d), d_seq, d_row);
+        if (st != KS_OK) return st;
+    }
+    return KS_OK;
+}
+
+namespace {
+
+// Positions up to which each workgroup counts the unmasked ones itself (a launch
+// less): 8 to 32 labels a thread.
+constexpr int64_t kCountRows = 2048;
+
+template <typename T, bool TWO, int NT, int U>
+ks_status_t run_rows(const DistilArgs& a, bool count, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq,
+                     int64_t d_row, hipStream_t stream) {
+    return launch_kernel(count ? distil_row_kernel<T, TWO, NT, U, true> : distil_row_kernel<T, TWO, NT, U, false>,
+                         dim3(static_cast<unsigned>(n)), dim3(NT), 0, stream, a, tokens, inv, static_cast<T*>(d), d_seq,
+                         d_row);
+}
+
+// The smallest workgroup that holds the row's vectors.
+template <typename T, bool TWO>
+ks_status_t pick_rows(const DistilArgs& a, bool count, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq,
+                      int64_t d_row, hipStream_t stream) {
+    const int64_t vecs = a.x.vocab / kVec<T>;
+    const auto run = vecs <= 256 ? run_rows<T, TWO, 256, 1> : vecs <= 512 ? run_rows<T, TWO, 256, 2>
+                   : vecs <= 1024 ? run_rows<T, TWO, 256, 4> : vecs <= 2048 ? run_rows<T, TWO, 256, 8>
+                   : vecs <= 4096 ? run_rows<T, TWO, 256, 16> : vecs <= 8192 ? run_rows<T, TWO, 512, 16>
+                   : run_rows<T, TWO, 1024, 16>;
+    return run(a, count, n, tokens, inv, d, d_seq, d_row, stream);
+}
+
+}  // namespace
+
+bool distil_holds(const ks_logits_t& x) { return x.vocab / (x.elem == KS_ELEM_BF16 ? 8 : 4) <= 16384; }
+
+bool distil_counts(const ks_logits_t& x) { return distil_holds(x) && x.sequences * x.tokens <= kCountRows; }
+
+ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
+                               void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
+    DistilArgs a = distil_args(x, t, o);
+    const bool two = two_sums(o), count = distil_counts(x);
+    const auto pick = x.elem == KS_ELEM_BF16 ? (two ? pick_rows<bf16_t, true> : pick_rows<bf16_t, false>)
+                                             : (two ? pick_rows<float, true> : pick_rows<float, false>);
+    const int64_t rows = x.sequences * x.tokens;
+    for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid / 4) {
+        const ks_status_t st = pick(a, count, std::min(kMaxGrid / 4, rows - a.row0), tokens, inv, d, d_seq, d_row, stream);
         if (st != KS_OK) return st;
     }
     return KS_OK;

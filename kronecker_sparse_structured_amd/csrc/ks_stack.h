@@ -41,6 +41,12 @@ ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, co
                                  float* stats, hipStream_t stream);
 ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, const float* inv, float* loss,
                               hipStream_t stream);
+// Loss and gradient at once, of rows that a workgroup holds; `counts`: inv is
+// formed by this launch too (there must be a row).
+bool distil_holds(const ks_logits_t& x);
+bool distil_counts(const ks_logits_t& x);
+ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
+                               void* d, int64_t d_seq, int64_t d_row, hipStream_t stream);
 ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, const float* stats,
                                const float* inv, const float* upstream, void* d, int64_t d_seq, int64_t d_row,
                                hipStream_t stream);

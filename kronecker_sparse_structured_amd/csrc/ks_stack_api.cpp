@@ -126,12 +126,17 @@ ks_status_t ks_distil_loss(const ks_logits_t* x, const ks_teacher_t* teacher, do
         return KS_ERR_OVERLAP;
     const Distil o{weight, temperature};
     float* inv = stats + 3 * rows;
-    st = launch_distil_count(*x, inv, stream);
-    if (st == KS_OK) st = launch_distil_tokens(*x, *teacher, o, tokens, stats, stream);
-    if (st == KS_OK) st = launch_distil_sum(*x, tokens, inv, loss, stream);
-    if (st == KS_OK && dlogits)
-        st = launch_distil_grad(*x, *teacher, o, stats, inv, nullptr, dlogits, d_seq_stride, d_row_stride, stream);
-    return st;
+    const bool held = dlogits && rows > 0 && distil_holds(*x);
+    if (!held || !distil_counts(*x)) st = launch_distil_count(*x, inv, stream);
+    if (st != KS_OK) return st;
+    if (held) {
+        st = launch_distil_rows(*x, *teacher, o, tokens, inv, dlogits, d_seq_stride, d_row_stride, stream);
+    } else {
+        st = launch_distil_tokens(*x, *teacher, o, tokens, stats, stream);
+        if (st == KS_OK && dlogits)
+            st = launch_distil_grad(*x, *teacher, o, stats, inv, nullptr, dlogits, d_seq_stride, d_row_stride, stream);
+    }
+    return st != KS_OK ? st : launch_distil_sum(*x, tokens, inv, loss, stream);
 }
 
 ks_status_t ks_distil_backward(const ks_logits_t* x, const ks_teacher_t* teacher, double weight, double temperature,
