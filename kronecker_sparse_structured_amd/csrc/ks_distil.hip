@@ -370,35 +370,60 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
     }
 }
 
+// The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
+// not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
+// as the square of the first (8192 rows of 50257 in bf16 313 us, 366 so).
+enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
+
 // Loss and gradient of a row that the workgroup holds, U 16-byte vectors a lane.
 // Rows of logits and of their gradient may start at any element: the vectors
 // start where the gradient's lines do, so that stores fill them; what lies before
 // the first and behind the last goes element-wise. COUNT: the workgroup counts
 // the unmasked positions itself.
-template <typename T, bool TWO, int NT, int U, bool COUNT>
+template <typename T, int MODE, int NT, int U, bool COUNT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 : U == 8 ? 6 : 4))) void distil_row_kernel(
     const DistilArgs a, float* tokens, float* inv, T* d_, int64_t d_seq, int64_t d_row) {
-    constexpr int E = kVec<T>, W = NT / 64;
+    constexpr int E = kVec<T>, W = NT / 64, EN = NT < kMaxTop ? kMaxTop / NT : 1;    // entries a thread
+    constexpr bool TWO = MODE != kOne;
+    extern __shared__ uint32_t seen[];        // a bit a token: whether an entry has it
     __shared__ float maxima[2][W], sums[3][W];
     __shared__ double parts[W];
-    __shared__ int counts[W];
-    __shared__ int ids[kMaxTop + 1];
-    __shared__ float qs[kMaxTop + 1], xs[kMaxTop + 1];
+    __shared__ int counts[W], twice, label_in;
+    __shared__ int ids[kMaxTop];
+    __shared__ float qs[kMaxTop];
     const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
     const int64_t label = a.x.labels[s * a.x.label_stride + t];
     const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
     T* out = d_ + s * d_seq + t * d_row;
-    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x, wave = tid / 64;
+    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x, wave = tid / 64, entries = a.t.count;
     const int head = head_of(out, V), vecs = (V - head) / E, tail = head + vecs * E;
     typedef typename Access<T, 4>::vec access;
     u32x4* obody = reinterpret_cast<u32x4*>(out + head);
     if (label < 0 && !(COUNT && at == 0)) {
         if (tid == 0) tokens[at] = 0.0f;
-        if (tid < head) out[tid] = narrow<T>(0.0f);
+        for (int v = tid; v < head; v += NT) out[v] = narrow<T>(0.0f);
         if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
         const u32x4 none = {0u, 0u, 0u, 0u};
         for (int v = tid; v < vecs; v += NT) __builtin_nontemporal_store(none, &obody[v]);
         return;
+    }
+    // the entries' ids first: what follows from them is asked for behind the row
+    const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
+    int64_t id[EN];
+    float top[EN], xe[EN];
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        const int k = n * NT + tid;
+        id[n] = -1;
+        top[n] = -INFINITY;
+        xe[n] = 0.0f;
+        if (kl && k < entries) {
+            const int64_t from = s * a.t.id_seq_stride + t * a.t.id_row_stride + k;
+            id[n] = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[from] : static_cast<const int32_t*>(a.t.ids)[from];
+            const int64_t where = s * a.t.top_seq_stride + t * a.t.top_row_stride + k;
+            top[n] = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[where])
+                                              : static_cast<const float*>(a.t.top)[where];
+        }
     }
     // the row
     u32x4 w[U];
@@ -409,21 +434,14 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         if (v < vecs) w[u] = *reinterpret_cast<const access*>(row + head + v * E);
     }
     const float xh = tid < head ? to_f32(row[tid]) : -INFINITY, xt = tid < V - tail ? to_f32(row[tail + tid]) : -INFINITY;
-    // its entries: one a thread
-    const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
-    int64_t id = -1;
-    float top = -INFINITY, xe = 0.0f;
-    if (kl && tid < a.t.count) {
-        const int64_t from = s * a.t.id_seq_stride + t * a.t.id_row_stride + tid;
-        id = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[from] : static_cast<const int32_t*>(a.t.ids)[from];
-        if (id >= 0) {
-            const int64_t k = s * a.t.top_seq_stride + t * a.t.top_row_stride + tid;
-            top = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[k])
-                                           : static_cast<const float*>(a.t.top)[k];
-            if (id < V) xe = to_f32(row[id]);
-        }
-    }
     const float xl = tid == 0 && ce && label >= 0 ? to_f32(row[label < V ? label : 0]) : 0.0f;
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        if (id[n] < 0) top[n] = -INFINITY;
+        else if (id[n] < V) xe[n] = to_f32(row[id[n]]);
+    }
+    for (int i = tid; i < (V + 31) / 32; i += NT) seen[i] = 0;
+    if (tid == 0) twice = label_in = 0;
     int count = 0;
     if (COUNT) {
         const int n = static_cast<int>(a.x.sequences * a.x.tokens);
@@ -432,7 +450,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
     }
     // maxima
-    float m = fmaxf(fmaxf(xh, xt), kLowest);
+    float m = fmaxf(fmaxf(xh, xt), kLowest), tm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float x[E];
@@ -440,8 +458,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
 #pragma unroll
         for (int i = 0; i < E; ++i) m = fmaxf(m, x[i]);
     }
+#pragma unroll
+    for (int n = 0; n < EN; ++n) tm = fmaxf(tm, top[n]);
     m = wave_max(m);
-    float tm = wave_max(top);
+    tm = wave_max(tm);
     if (tid % 64 == 0) {
         maxima[0][wave] = m;
         maxima[1][wave] = tm;
@@ -467,64 +487,72 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     // sums
     keep_narrow(w);
     if (tm == -INFINITY) tm = 0.0f;          // no entry that weighs anything
-    const float p = exp_of(top - tm, a.scale);
-    float sum = exp_of(xh - m, a.scale) + exp_of(xt - m, a.scale), sum1 = 0.0f;
-    if (TWO) sum1 = ks::exp_of(xh - m) + ks::exp_of(xt - m);
+    float p[EN], tsum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        p[n] = exp_of(top[n] - tm, a.scale);
+        tsum += p[n];
+        if (id[n] < 0 || id[n] >= V) continue;
+        // duplicates are rare: looked for here, added up below if there is one
+        const int k = static_cast<int>(id[n]);
+        if (atomicOr(&seen[k / 32], 1u << k % 32) >> k % 32 & 1) twice = 1;
+        if (id[n] == label) label_in = 1;
+    }
+    float sum = 0.0f, sum1 = 0.0f;
+    auto add = [&](float x, float& s0, float& s1) {
+        const float e = exp_of(x - m, a.scale);
+        s0 += e;
+        if (MODE == kBoth) s1 += ks::exp_of(x - m);
+        if (MODE == kSquare) s1 += e * e;
+    };
+    add(xh, sum, sum1);
+    add(xt, sum, sum1);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (u * NT >= vecs) continue;        // the same for all threads
         float x[E], part = 0.0f, part1 = 0.0f;
         widen<T>(w[u], x);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            part += exp_of(x[i] - m, a.scale);
-            if (TWO) part1 += ks::exp_of(x[i] - m);
-        }
+        for (int i = 0; i < E; ++i) add(x[i], part, part1);
         sum += part;
-        if (TWO) sum1 += part1;
+        sum1 += part1;
     }
     sum = wave_sum32(sum);
     if (TWO) sum1 = wave_sum32(sum1);
-    float tsum = wave_sum32(p);
+    tsum = wave_sum32(tsum);
     if (tid % 64 == 0) {
         sums[0][wave] = sum;
         sums[1][wave] = sum1;
         sums[2][wave] = tsum;
     }
     __syncthreads();
-    sum = sum1 = tsum = 0.0f;
-    for (int k = 0; k < W; ++k) {
-        sum += sums[0][k];
-        if (TWO) sum1 += sums[1][k];
-        tsum += sums[2][k];
-    }
-    if (!TWO) sum1 = sum;
-    keep_narrow(w);
+    sum = waves_sum(sums[0]);
+    sum1 = TWO ? waves_sum(sums[1]) : sum;
+    tsum = waves_sum(sums[2]);
     // what the gradient needs of the entries
     const bool any = kl && tsum != 0.0f;     // else that side is not there
     const float slope = any ? a.slope * scale : 0.0f, hard = static_cast<float>(a.ce) * scale;
-    float q = id >= 0 && any ? p / tsum : 0.0f;
-    if (id >= V) q = __builtin_nanf("");
-    const int entries = a.t.count + 1;
-    if (tid < a.t.count) {
-        const bool in = id >= 0 && id < V;
-        ids[tid] = in ? static_cast<int>(id) : !(q == 0.0f) ? 0 : -1;      // an id outside: the row says so at 0
-        qs[tid] = slope * q;
-        xs[tid] = in ? xe : 0.0f;
+    float q[EN];
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        const int k = n * NT + tid;
+        q[n] = id[n] >= 0 && any ? p[n] / tsum : 0.0f;
+        if (id[n] >= V) q[n] = __builtin_nanf("");
+        if (k < entries) {
+            ids[k] = id[n] < V ? static_cast<int>(id[n]) : -1;
+            qs[k] = slope * q[n];
+        }
     }
-    if (tid == 0) {
-        ids[entries - 1] = !ce ? -1 : label < V ? static_cast<int>(label) : 0;
-        qs[entries - 1] = label < V ? hard : __builtin_nanf("");
-        xs[entries - 1] = xl;
-    }
+    keep_narrow(w);
     // the gradient as if there were no entries
     const float c0 = uniform(TWO ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
     auto value = [&](float x) {
         // (x - m) log2 e / T is off by 1e-7 of itself without the second part: far
         // below a rounding of the value's type, or of the sums before it
-        float y = c0 * __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
-        if (TWO) y += c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
-        return y;
+        const float e = __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
+        if (MODE == kBoth) return c0 * e + c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
+        if (MODE == kSquare) return e * (c0 + c1 * e);
+        return c0 * e;
     };
     if (tid < head) out[tid] = narrow<T>(value(xh));
     if (tid < V - tail) out[tail + tid] = narrow<T>(value(xt));
@@ -540,37 +568,49 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     }
     // the entries' part of the loss
     double part = 0.0;
-    if (!(q == 0.0f)) {
-        const double logq = static_cast<double>(top - tm) * a.inverse - log(static_cast<double>(tsum));
-        const double logp = (static_cast<double>(xe) - m) * a.inverse - log(static_cast<double>(sum));
-        part = q * (logq - logp);
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        if (q[n] == 0.0f) continue;
+        const double logq = static_cast<double>(top[n] - tm) * a.inverse - log(static_cast<double>(tsum));
+        const double logp = (static_cast<double>(xe[n]) - m) * a.inverse - log(static_cast<double>(sum));
+        part += q[n] * (logq - logp);
     }
-    if (wave * 64 < a.t.count) part = wave_sum(part);
+    if (wave * 64 < entries) part = wave_sum(part);
     if (tid % 64 == 0) parts[wave] = part;
     __syncthreads();
-    // the values at the entries' and the label's tokens again
-    for (int k = tid; k < entries; k += NT) {
-        const int mine = ids[k];
-        if (mine < 0) continue;
-        float taken = 0.0f;
+    // the values at the entries' tokens again, and at the label's if it is none of them
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        const int k = n * NT + tid;
+        if (k >= entries || id[n] < 0) continue;
+        if (id[n] >= V) {                    // a token outside: the row says so at its first
+            out[0] = narrow<T>(__builtin_nanf(""));
+            continue;
+        }
+        float taken = qs[k];
         bool first = true;
-        for (int j = 0; j < entries; ++j) {
-            if (ids[j] != mine) continue;
-            first = first && j >= k;
-            taken += qs[j];
+        if (twice) {
+            taken = 0.0f;
+            for (int j = 0; j < entries; ++j) {
+                if (ids[j] != ids[k]) continue;
+                first = first && j >= k;
+                taken += qs[j];
+            }
         }
-        if (first) out[mine] = narrow<T>(value(xs[k]) - taken);
+        if (ce && id[n] == label) taken += hard;
+        if (first) out[id[n]] = narrow<T>(value(xe[n]) - taken);
     }
-    if (tid == 0) {
-        double token = 0.0;
-        for (int k = 0; k * 64 < a.t.count; ++k) token += parts[k];
-        token = kl ? token * a.kl : 0.0;
-        if (ce) {
-            const double x = label < V ? xl : __builtin_nanf("");
-            token -= a.ce * ((x - m) - log(static_cast<double>(sum1)));
-        }
-        tokens[at] = static_cast<float>(token);
+    if (tid != 0) return;
+    if (ce && label >= V) out[0] = narrow<T>(__builtin_nanf(""));
+    else if (ce && !label_in) out[label] = narrow<T>(value(xl) - hard);
+    double token = 0.0;
+    for (int k = 0; k < W && k * 64 < entries; ++k) token += parts[k];
+    token = kl ? token * a.kl : 0.0;
+    if (ce) {
+        const double x = label < V ? xl : __builtin_nanf("");
+        token -= a.ce * ((x - m) - log(static_cast<double>(sum1)));
     }
+    tokens[at] = static_cast<float>(token);
 }
 
 DistilArgs distil_args(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o) {
@@ -641,27 +681,34 @@ ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, cons
 namespace {
 
 // Positions up to which each workgroup counts the unmasked ones itself (a launch
-// less): 8 to 32 labels a thread.
+// less): 2 to 8 labels a thread.
 constexpr int64_t kCountRows = 2048;
 
-template <typename T, bool TWO, int NT, int U>
-ks_status_t run_rows(const DistilArgs& a, bool count, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq,
-                     int64_t d_row, hipStream_t stream) {
-    return launch_kernel(count ? distil_row_kernel<T, TWO, NT, U, true> : distil_row_kernel<T, TWO, NT, U, false>,
-                         dim3(static_cast<unsigned>(n)), dim3(NT), 0, stream, a, tokens, inv, static_cast<T*>(d), d_seq,
-                         d_row);
+template <typename T, int MODE, int NT, int U, bool COUNT>
+ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq, int64_t d_row,
+                     hipStream_t stream) {
+    return launch_kernel(distil_row_kernel<T, MODE, NT, U, COUNT>, dim3(static_cast<unsigned>(n)), dim3(NT),
+                         static_cast<size_t>((a.x.vocab + 31) / 32 * 4), stream, a, tokens, inv, static_cast<T*>(d),
+                         d_seq, d_row);
 }
 
-// The smallest workgroup that holds the row's vectors.
-template <typename T, bool TWO>
-ks_status_t pick_rows(const DistilArgs& a, bool count, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq,
-                      int64_t d_row, hipStream_t stream) {
+// The workgroup that holds a row's vectors: of few rows as many threads as it
+// takes, for the time of one row; of many rows 8 or 16 vectors a lane, so that the
+// card has more rows on their way (16384 rows of 4096 in bf16 PLACE us, 71 with 2).
+template <typename T, int MODE>
+ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq, int64_t d_row,
+                      hipStream_t stream) {
     const int64_t vecs = a.x.vocab / kVec<T>;
-    const auto run = vecs <= 256 ? run_rows<T, TWO, 256, 1> : vecs <= 512 ? run_rows<T, TWO, 256, 2>
-                   : vecs <= 1024 ? run_rows<T, TWO, 256, 4> : vecs <= 2048 ? run_rows<T, TWO, 256, 8>
-                   : vecs <= 4096 ? run_rows<T, TWO, 256, 16> : vecs <= 8192 ? run_rows<T, TWO, 512, 16>
-                   : run_rows<T, TWO, 1024, 16>;
-    return run(a, count, n, tokens, inv, d, d_seq, d_row, stream);
+    const auto run =
+        distil_counts(a.x)
+            ? (vecs <= 256 ? run_rows<T, MODE, 256, 1, true> : vecs <= 512 ? run_rows<T, MODE, 256, 2, true>
+               : vecs <= 1024 ? run_rows<T, MODE, 256, 4, true> : vecs <= 2048 ? run_rows<T, MODE, 256, 8, true>
+               : vecs <= 4096 ? run_rows<T, MODE, 256, 16, true> : vecs <= 8192 ? run_rows<T, MODE, 512, 16, true>
+               : run_rows<T, MODE, 1024, 16, true>)
+            : (vecs <= 512 ? run_rows<T, MODE, 64, 8, false> : vecs <= 1024 ? run_rows<T, MODE, 128, 8, false>
+               : vecs <= 2048 ? run_rows<T, MODE, 256, 8, false> : vecs <= 4096 ? run_rows<T, MODE, 256, 16, false>
+               : vecs <= 8192 ? run_rows<T, MODE, 512, 16, false> : run_rows<T, MODE, 1024, 16, false>);
+    return run(a, n, tokens, inv, d, d_seq, d_row, stream);
 }
 
 }  // namespace
@@ -673,12 +720,14 @@ bool distil_counts(const ks_logits_t& x) { return distil_holds(x) && x.sequences
 ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
                                void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
     DistilArgs a = distil_args(x, t, o);
-    const bool two = two_sums(o), count = distil_counts(x);
-    const auto pick = x.elem == KS_ELEM_BF16 ? (two ? pick_rows<bf16_t, true> : pick_rows<bf16_t, false>)
-                                             : (two ? pick_rows<float, true> : pick_rows<float, false>);
+    const int mode = !two_sums(o) ? kOne : o.temperature == 2.0 ? kSquare : kBoth;
+    const auto pick = x.elem == KS_ELEM_BF16 ? (mode == kOne ? pick_rows<bf16_t, kOne> : mode == kBoth ? pick_rows<bf16_t, kBoth>
+                                                : pick_rows<bf16_t, kSquare>)
+                                             : (mode == kOne ? pick_rows<float, kOne> : mode == kBoth ? pick_rows<float, kBoth>
+                                                : pick_rows<float, kSquare>);
     const int64_t rows = x.sequences * x.tokens;
     for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid / 4) {
-        const ks_status_t st = pick(a, count, std::min(kMaxGrid / 4, rows - a.row0), tokens, inv, d, d_seq, d_row, stream);
+        const ks_status_t st = pick(a, std::min(kMaxGrid / 4, rows - a.row0), tokens, inv, d, d_seq, d_row, stream);
         if (st != KS_OK) return st;
     }
     return KS_OK;
