@@ -140,9 +140,21 @@ __device__ __forceinline__ int64_t label_at(const ks_logits_t& x, int64_t at) {
     return x.labels[s * x.label_stride + (at - static_cast<int64_t>(s) * x.tokens)];
 }
 
-// inv = 1 / (unmasked positions), at least one.
-__global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x, float* inv) {
-    __shared__ int sums[16];
+// The workgroup's sum of x, in thread 0.
+__device__ __forceinline__ double group_sum(double x) {
+    __shared__ double sums[16];
+    x = wave_sum(x);
+    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = x;
+    __syncthreads();
+    double total = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < 16; ++w) total += sums[w];
+    __syncthreads();
+    return total;
+}
+
+// The unmasked positions, in thread 0.
+__device__ __forceinline__ double count_rows(const ks_logits_t& x) {
     const int64_t n = x.sequences * x.tokens;
     int count = 0;
     constexpr int U = 8;
@@ -153,15 +165,36 @@ __global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x,
 #pragma unroll
         for (int u = 0; u < U; ++u) count += label[u] >= 0;
     }
+    return group_sum(static_cast<double>(count));
+}
+
+__device__ __forceinline__ float inverse_of(double count) { return static_cast<float>(1.0 / fmax(count, 1.0)); }
+
+// inv = 1 / (unmasked positions), at least one.
+__global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x, float* inv) {
+    const double count = count_rows(x);
+    if (threadIdx.x == 0) *inv = inverse_of(count);
+}
+
+// loss = the tokens' sum times inv, which is formed here where COUNT.
+template <bool COUNT>
+__global__ __launch_bounds__(1024) void distil_sum_kernel(const ks_logits_t x, const float* tokens, float* inv,
+                                                          float* loss) {
+    const int64_t n = x.sequences * x.tokens;
+    double s = 0.0;
+    constexpr int U = 8;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
+        float v[U];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
-    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = count;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int total = 0;
-        for (int w = 0; w < 16; ++w) total += sums[w];
-        *inv = static_cast<float>(1.0 / static_cast<double>(max(total, 1)));
+        for (int u = 0; u < U; ++u) v[u] = i0 + 1024 * u < n ? tokens[i0 + 1024 * u] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += static_cast<double>(v[u]);
     }
+    const double count = COUNT ? count_rows(x) : 0.0;
+    s = group_sum(s);
+    if (threadIdx.x != 0) return;
+    if (COUNT) *inv = inverse_of(count);
+    *loss = static_cast<float>(s * static_cast<double>(*inv));
 }
 
 // A running maximum with its two sums: exp((x - m) / T), and exp(x - m) if TWO.
@@ -263,27 +296,6 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
     }
 }
 
-__global__ __launch_bounds__(1024) void distil_sum_kernel(const float* tokens, int64_t n, const float* inv, float* loss) {
-    __shared__ double sums[16];
-    double s = 0.0;
-    constexpr int U = 8;
-    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
-        float v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = i0 + 1024 * u < n ? tokens[i0 + 1024 * u] : 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) s += static_cast<double>(v[u]);
-    }
-    s = wave_sum(s);
-    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        s = 0.0;
-        for (int w = 0; w < 16; ++w) s += sums[w];
-        *loss = static_cast<float>(s * static_cast<double>(*inv));
-    }
-}
-
 // dx of one row: first as if there were no entries, then the values at the
 // entries' and the label's tokens again. Logits and gradient may be one memory,
 // so those logits are read before anything is written.
@@ -375,14 +387,15 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
 // as the square of the first (8192 rows of 50257 in bf16 313 us, 366 so).
 enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
 
-// Loss and gradient of a row that the workgroup holds, U 16-byte vectors a lane.
+// Loss and gradient (d_ null: the loss alone, and stats for a later gradient) of a
+// row that the workgroup holds, U 16-byte vectors a lane.
 // Rows of logits and of their gradient may start at any element: the vectors
 // start where the gradient's lines do, so that stores fill them; what lies before
 // the first and behind the last goes element-wise. COUNT: the workgroup counts
 // the unmasked positions itself.
 template <typename T, int MODE, int NT, int U, bool COUNT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 : U == 8 ? 6 : 4))) void distil_row_kernel(
-    const DistilArgs a, float* tokens, float* inv, T* d_, int64_t d_seq, int64_t d_row) {
+    const DistilArgs a, float* tokens, float* inv, float* stats, T* d_, int64_t d_seq, int64_t d_row) {
     constexpr int E = kVec<T>, W = NT / 64, EN = NT < kMaxTop ? kMaxTop / NT : 1;    // entries a thread
     constexpr bool TWO = MODE != kOne;
     extern __shared__ uint32_t seen[];        // a bit a token: whether an entry has it
@@ -396,12 +409,14 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
     T* out = d_ + s * d_seq + t * d_row;
     const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x, wave = tid / 64, entries = a.t.count;
-    const int head = head_of(out, V), vecs = (V - head) / E, tail = head + vecs * E;
+    const int head = head_of(d_ ? out : row, V), vecs = (V - head) / E, tail = head + vecs * E;
     typedef typename Access<T, 4>::vec access;
     u32x4* obody = reinterpret_cast<u32x4*>(out + head);
     if (label < 0 && !(COUNT && at == 0)) {
         if (tid == 0) tokens[at] = 0.0f;
-        for (int v = tid; v < head; v += NT) out[v] = narrow<T>(0.0f);
+        if (stats && tid < 3) stats[3 * at + tid] = tid == 0 ? 0.0f : 1.0f;
+        if (!d_) return;
+        if (tid < head) out[tid] = narrow<T>(0.0f);
         if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
         const u32x4 none = {0u, 0u, 0u, 0u};
         for (int v = tid; v < vecs; v += NT) __builtin_nontemporal_store(none, &obody[v]);
@@ -478,11 +493,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         if (at == 0 && tid == 0) *inv = scale;
         if (label < 0) {                     // row 0, which stayed to count
             if (tid == 0) tokens[at] = 0.0f;
-            for (int v = tid; v < V; v += NT) out[v] = narrow<T>(0.0f);
+            if (stats && tid < 3) stats[3 * at + tid] = tid == 0 ? 0.0f : 1.0f;
+            for (int v = tid; d_ && v < V; v += NT) out[v] = narrow<T>(0.0f);
             return;
         }
     } else {
-        scale = *inv;
+        scale = d_ ? *inv : 0.0f;
     }
     // sums
     keep_narrow(w);
@@ -554,12 +570,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         if (MODE == kSquare) return e * (c0 + c1 * e);
         return c0 * e;
     };
-    if (tid < head) out[tid] = narrow<T>(value(xh));
-    if (tid < V - tail) out[tail + tid] = narrow<T>(value(xt));
+    if (d_ && tid < head) out[tid] = narrow<T>(value(xh));
+    if (d_ && tid < V - tail) out[tail + tid] = narrow<T>(value(xt));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int v = u * NT + tid;
-        if (v >= vecs) continue;
+        if (!d_ || v >= vecs) continue;
         float x[E];
         widen<T>(w[u], x);
 #pragma unroll
@@ -582,7 +598,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
 #pragma unroll
     for (int n = 0; n < EN; ++n) {
         const int k = n * NT + tid;
-        if (k >= entries || id[n] < 0) continue;
+        if (!d_ || k >= entries || id[n] < 0) continue;
         if (id[n] >= V) {                    // a token outside: the row says so at its first
             out[0] = narrow<T>(__builtin_nanf(""));
             continue;
@@ -601,8 +617,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         if (first) out[id[n]] = narrow<T>(value(xe[n]) - taken);
     }
     if (tid != 0) return;
-    if (ce && label >= V) out[0] = narrow<T>(__builtin_nanf(""));
-    else if (ce && !label_in) out[label] = narrow<T>(value(xl) - hard);
+    if (d_ && ce && label >= V) out[0] = narrow<T>(__builtin_nanf(""));
+    else if (d_ && ce && !label_in) out[label] = narrow<T>(value(xl) - hard);
     double token = 0.0;
     for (int k = 0; k < W && k * 64 < entries; ++k) token += parts[k];
     token = kl ? token * a.kl : 0.0;
@@ -611,6 +627,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         token -= a.ce * ((x - m) - log(static_cast<double>(sum1)));
     }
     tokens[at] = static_cast<float>(token);
+    if (!stats) return;
+    stats[3 * at] = m;
+    stats[3 * at + 1] = sum;
+    stats[3 * at + 2] = sum1;
 }
 
 DistilArgs distil_args(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o) {
@@ -638,9 +658,10 @@ ks_status_t launch_distil_count(const ks_logits_t& x, float* inv, hipStream_t st
     return launch_kernel(distil_count_kernel, dim3(1), dim3(1024), 0, stream, x, inv);
 }
 
-ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, const float* inv, float* loss,
+ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, float* inv, bool count, float* loss,
                               hipStream_t stream) {
-    return launch_kernel(distil_sum_kernel, dim3(1), dim3(1024), 0, stream, tokens, x.sequences * x.tokens, inv, loss);
+    return launch_kernel(count ? distil_sum_kernel<true> : distil_sum_kernel<false>, dim3(1), dim3(1024), 0, stream, x,
+                         tokens, inv, loss);
 }
 
 ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens,
@@ -685,10 +706,10 @@ namespace {
 constexpr int64_t kCountRows = 2048;
 
 template <typename T, int MODE, int NT, int U, bool COUNT>
-ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq, int64_t d_row,
+ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, float* stats, void* d, int64_t d_seq, int64_t d_row,
                      hipStream_t stream) {
     return launch_kernel(distil_row_kernel<T, MODE, NT, U, COUNT>, dim3(static_cast<unsigned>(n)), dim3(NT),
-                         static_cast<size_t>((a.x.vocab + 31) / 32 * 4), stream, a, tokens, inv, static_cast<T*>(d),
+                         static_cast<size_t>((a.x.vocab + 31) / 32 * 4), stream, a, tokens, inv, stats, static_cast<T*>(d),
                          d_seq, d_row);
 }
 
@@ -696,7 +717,7 @@ ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, 
 // takes, for the time of one row; of many rows 8 or 16 vectors a lane, so that the
 // card has more rows on their way (16384 rows of 4096 in bf16 PLACE us, 71 with 2).
 template <typename T, int MODE>
-ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, void* d, int64_t d_seq, int64_t d_row,
+ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, float* stats, void* d, int64_t d_seq, int64_t d_row,
                       hipStream_t stream) {
     const int64_t vecs = a.x.vocab / kVec<T>;
     const auto run =
@@ -708,17 +729,22 @@ ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv,
             : (vecs <= 512 ? run_rows<T, MODE, 64, 8, false> : vecs <= 1024 ? run_rows<T, MODE, 128, 8, false>
                : vecs <= 2048 ? run_rows<T, MODE, 256, 8, false> : vecs <= 4096 ? run_rows<T, MODE, 256, 16, false>
                : vecs <= 8192 ? run_rows<T, MODE, 512, 16, false> : run_rows<T, MODE, 1024, 16, false>);
-    return run(a, n, tokens, inv, d, d_seq, d_row, stream);
+    return run(a, n, tokens, inv, stats, d, d_seq, d_row, stream);
 }
 
 }  // namespace
 
-bool distil_holds(const ks_logits_t& x) { return x.vocab / (x.elem == KS_ELEM_BF16 ? 8 : 4) <= 16384; }
+// With a gradient as long as registers reach. The loss alone up to 32768 values:
+// of longer rows a workgroup that goes through the row keeps more bytes on their way
+// (8192 rows of 50257 in bf16 150 us, 173 held; 4096 rows of 32000 in fp32 75 us, 69 held).
+bool distil_holds(const ks_logits_t& x, bool gradient) {
+    return gradient ? x.vocab / (x.elem == KS_ELEM_BF16 ? 8 : 4) <= 16384 : x.vocab <= 32768;
+}
 
-bool distil_counts(const ks_logits_t& x) { return distil_holds(x) && x.sequences * x.tokens <= kCountRows; }
+bool distil_counts(const ks_logits_t& x) { return x.sequences * x.tokens <= kCountRows; }
 
 ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
-                               void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
+                               float* stats, void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
     DistilArgs a = distil_args(x, t, o);
     const int mode = !two_sums(o) ? kOne : o.temperature == 2.0 ? kSquare : kBoth;
     const auto pick = x.elem == KS_ELEM_BF16 ? (mode == kOne ? pick_rows<bf16_t, kOne> : mode == kBoth ? pick_rows<bf16_t, kBoth>
@@ -727,7 +753,7 @@ ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, cons
                                                 : pick_rows<float, kSquare>);
     const int64_t rows = x.sequences * x.tokens;
     for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid / 4) {
-        const ks_status_t st = pick(a, std::min(kMaxGrid / 4, rows - a.row0), tokens, inv, d, d_seq, d_row, stream);
+        const ks_status_t st = pick(a, std::min(kMaxGrid / 4, rows - a.row0), tokens, inv, stats, d, d_seq, d_row, stream);
         if (st != KS_OK) return st;
     }
     return KS_OK;

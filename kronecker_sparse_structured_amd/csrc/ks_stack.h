@@ -35,18 +35,20 @@ ks_status_t launch_norm_grad(const ks_residual_norm_t& n, const NormSplit& s, co
 struct Distil {
     double weight, temperature;
 };
-// inv = 1 / (unmasked rows), then tokens and stats of every row, then the loss.
+// inv: 1 / (unmasked rows).
 ks_status_t launch_distil_count(const ks_logits_t& x, float* inv, hipStream_t stream);
-ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens,
-                                 float* stats, hipStream_t stream);
-ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, const float* inv, float* loss,
-                              hipStream_t stream);
-// Loss and gradient at once, of rows that a workgroup holds; `counts`: inv is
-// formed by this launch too (there must be a row).
-bool distil_holds(const ks_logits_t& x);
+// Loss and gradient at once (d null: tokens and stats), of rows that a workgroup
+// holds; of few rows the launch counts them as well.
+bool distil_holds(const ks_logits_t& x, bool gradient);
 bool distil_counts(const ks_logits_t& x);
 ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
-                               void* d, int64_t d_seq, int64_t d_row, hipStream_t stream);
+                               float* stats, void* d, int64_t d_seq, int64_t d_row, hipStream_t stream);
+// Of longer rows, in two launches.
+ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens,
+                                 float* stats, hipStream_t stream);
+// The loss; count: and inv.
+ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, float* inv, bool count, float* loss,
+                              hipStream_t stream);
 ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, const float* stats,
                                const float* inv, const float* upstream, void* d, int64_t d_seq, int64_t d_row,
                                hipStream_t stream);

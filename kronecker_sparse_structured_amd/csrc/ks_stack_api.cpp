@@ -126,17 +126,19 @@ ks_status_t ks_distil_loss(const ks_logits_t* x, const ks_teacher_t* teacher, do
         return KS_ERR_OVERLAP;
     const Distil o{weight, temperature};
     float* inv = stats + 3 * rows;
-    const bool held = dlogits && rows > 0 && distil_holds(*x);
-    if (!held || !distil_counts(*x)) st = launch_distil_count(*x, inv, stream);
+    // the gradient's factor is 1 / N, so that comes first; without one it can come last
+    const bool held = rows > 0 && distil_holds(*x, dlogits != nullptr), counted = held && distil_counts(*x);
+    if (dlogits && !counted) st = launch_distil_count(*x, inv, stream);
     if (st != KS_OK) return st;
     if (held) {
-        st = launch_distil_rows(*x, *teacher, o, tokens, inv, dlogits, d_seq_stride, d_row_stride, stream);
+        st = launch_distil_rows(*x, *teacher, o, tokens, inv, dlogits ? nullptr : stats, dlogits, d_seq_stride,
+                                d_row_stride, stream);
     } else {
         st = launch_distil_tokens(*x, *teacher, o, tokens, stats, stream);
         if (st == KS_OK && dlogits)
             st = launch_distil_grad(*x, *teacher, o, stats, inv, nullptr, dlogits, d_seq_stride, d_row_stride, stream);
     }
-    return st != KS_OK ? st : launch_distil_sum(*x, tokens, inv, loss, stream);
+    return st != KS_OK ? st : launch_distil_sum(*x, tokens, inv, !dlogits && !counted, loss, stream);
 }
 
 ks_status_t ks_distil_backward(const ks_logits_t* x, const ks_teacher_t* teacher, double weight, double temperature,
