@@ -339,8 +339,9 @@ struct StateEntry {
     int64_t pieces;                      // waves a row
     int64_t size;                        // bytes of an access: 16, 4 or 1
 };
+template <int N>
 struct StateTable {
-    StateEntry e[kStates];
+    StateEntry e[N];
     int32_t count;
 };
 
@@ -367,7 +368,8 @@ __device__ __forceinline__ void copy_piece(const StateEntry& e, int64_t row, int
     }
 }
 
-__global__ __launch_bounds__(256) void beam_reorder_kernel(const StateTable t, const int32_t* parents, int beams,
+template <int N>
+__global__ __launch_bounds__(256) void beam_reorder_kernel(const StateTable<N> t, const int32_t* parents, int beams,
                                                            int out_beams, int64_t wave0, int64_t waves) {
     const int64_t unit = wave0 + static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (unit >= waves) return;
@@ -428,34 +430,46 @@ ks_status_t launch_beam_select(const ks_beams_t& x, const BeamOut& out, void* ws
     return KS_OK;
 }
 
-ks_status_t launch_beam_reorder(const ks_state_t* states, int n, const int32_t* parents, int64_t requests, int beams,
-                                int out_beams, hipStream_t stream) {
-    for (int i = 0; i < n;) {
-        StateTable t;
-        t.count = 0;
-        int64_t waves = 0;
-        for (; i < n && t.count < kStates; ++i) {
-            if (states[i].row_bytes == 0) continue;
-            StateEntry& e = t.e[t.count++];
-            e.src = static_cast<const char*>(states[i].src);
-            e.dst = static_cast<char*>(states[i].dst);
-            e.row_bytes = states[i].row_bytes;
-            const uint64_t bits = reinterpret_cast<uintptr_t>(e.src) | reinterpret_cast<uintptr_t>(e.dst) |
-                                  static_cast<uint64_t>(e.row_bytes);
-            e.size = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
-            e.pieces = (e.row_bytes / e.size + 64 * kPiece - 1) / (64 * kPiece);
-            e.first = waves;
-            waves += requests * out_beams * e.pieces;
-        }
-        if (waves == 0) continue;
-        const int64_t groups = (waves + 3) / 4;
-        for (int64_t g = 0; g < groups; g += kMaxGrid) {
-            const ks_status_t st = launch_kernel(beam_reorder_kernel, dim3(static_cast<unsigned>(std::min(kMaxGrid, groups - g))),
-                                                 dim3(256), 0, stream, t, parents, beams, out_beams, g * 4, waves);
-            if (st != KS_OK) return st;
-        }
+namespace {
+
+// Up to N states a launch, from states[i] on.
+template <int N>
+ks_status_t reorder_some(const ks_state_t* states, int n, int& i, const int32_t* parents, int64_t requests, int beams,
+                         int out_beams, hipStream_t stream) {
+    StateTable<N> t;
+    t.count = 0;
+    int64_t waves = 0;
+    for (; i < n && t.count < N; ++i) {
+        if (states[i].row_bytes == 0) continue;
+        StateEntry& e = t.e[t.count++];
+        e.src = static_cast<const char*>(states[i].src);
+        e.dst = static_cast<char*>(states[i].dst);
+        e.row_bytes = states[i].row_bytes;
+        const uint64_t bits = reinterpret_cast<uintptr_t>(e.src) | reinterpret_cast<uintptr_t>(e.dst) |
+                              static_cast<uint64_t>(e.row_bytes);
+        e.size = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+        e.pieces = (e.row_bytes / e.size + 64 * kPiece - 1) / (64 * kPiece);
+        e.first = waves;
+        waves += requests * out_beams * e.pieces;
+    }
+    const int64_t groups = (waves + 3) / 4;
+    for (int64_t g = 0; g < groups; g += kMaxGrid) {
+        const ks_status_t st = launch_kernel(beam_reorder_kernel<N>, dim3(static_cast<unsigned>(std::min(kMaxGrid, groups - g))),
+                                             dim3(256), 0, stream, t, parents, beams, out_beams, g * 4, waves);
+        if (st != KS_OK) return st;
     }
     return KS_OK;
+}
+
+}  // namespace
+
+ks_status_t launch_beam_reorder(const ks_state_t* states, int n, const int32_t* parents, int64_t requests, int beams,
+                                int out_beams, hipStream_t stream) {
+    ks_status_t st = KS_OK;
+    for (int i = 0; i < n && st == KS_OK;)
+        st = n <= 8 ? reorder_some<8>(states, n, i, parents, requests, beams, out_beams, stream)
+                    : reorder_some<kStates>(states, n, i, parents, requests, beams, out_beams, stream);
+    return st;
 }
 
 }  // namespace ks

@@ -1012,22 +1012,38 @@ def beam_select(logits, scores, beams=None, done=None, lengths=None, eos=None, l
     return Beams(*_beam_select(logits, scores, beams, done, lengths, eos, length_penalty))
 
 
+_BEAM_WORKSPACE = {}     # bytes by sizes, asked for once each
+
+
 def _beam_select(logits, scores, beams, done, lengths, eos, length_penalty):
     import torch
     R, W, V = logits.shape
-    beams = W if beams is None else beams
+    if beams is None:
+        beams = W
+    elem = _elem(logits.dtype, "logits")
     x = ks_beams_t(logits.data_ptr(), scores.data_ptr(), _ptr(done), _ptr(lengths), *_layout(logits, "logits"), R, V,
-                   -1 if eos is None else eos, length_penalty, W, _elem(logits.dtype, "logits"))
-    lib, size = load(), ctypes.c_size_t(0)
-    _raise(lib.ks_beam_workspace_size(x, beams, size), "ks_beam_workspace_size", True)
-    new = scores.new_empty
-    out = (new((R, beams)), new((R, beams), dtype=torch.int64), new((R, beams), dtype=torch.int32),
-           new((R, beams), dtype=torch.bool) if eos is not None else None,
-           new((R, beams), dtype=torch.int32) if lengths is not None else None)
-    ws = new((size.value + 3) // 4)
-    _raise(lib.ks_beam_select(x, beams, *map(_ptr, out), ws.data_ptr(), size.value, _raw_stream(logits.get_device())),
+                   -1 if eos is None else eos, length_penalty, W, elem)
+    lib, key = load(), (R, W, V, beams, elem)
+    size = _BEAM_WORKSPACE.get(key)
+    if size is None:
+        need = ctypes.c_size_t(0)
+        _raise(lib.ks_beam_workspace_size(x, beams, need), "ks_beam_workspace_size", True)
+        if len(_BEAM_WORKSPACE) > 256:
+            _BEAM_WORKSPACE.clear()
+        size = _BEAM_WORKSPACE[key] = need.value
+    new, i32 = scores.new_empty, lengths
+    # of a tensor that has the type, where there is one: a type by keyword costs as much again
+    tokens = new((R, beams), dtype=torch.int64)
+    parents = new((R, beams), dtype=torch.int32) if i32 is None else i32.new_empty((R, beams))
+    out_done = None
+    if eos is not None:
+        out_done = new((R, beams), dtype=torch.bool) if done is None else done.new_empty((R, beams))
+    out_lengths = None if i32 is None else i32.new_empty((R, beams))
+    best, ws = new((R, beams)), new((size + 3) // 4)
+    _raise(lib.ks_beam_select(x, beams, best.data_ptr(), tokens.data_ptr(), parents.data_ptr(), _ptr(out_done),
+                              _ptr(out_lengths), ws.data_ptr(), size, _raw_stream(logits.get_device())),
            "ks_beam_select", True)
-    return out
+    return best, tokens, parents, out_done, out_lengths
 
 
 def beam_reorder(states, parents, out=None, stream=None):
@@ -1045,11 +1061,13 @@ def beam_reorder(states, parents, out=None, stream=None):
         return []
     W = states[0].shape[1] if states[0].dim() > 1 else 0
     for t in states:
-        if t.dim() < 2 or t.shape[0] != R or t.shape[1] != W or t.get_device() != at or not t.is_contiguous():
+        shape = t.shape
+        if len(shape) < 2 or shape[0] != R or shape[1] != W or t.get_device() != at or not t.is_contiguous():
             raise ValueError("states must be contiguous (%d, beams, ...) on the parents' device" % R)
     if out is not None:
         for t, o in zip(states, out):
-            if o.shape != (R, beams, *t.shape[2:]) or o.dtype != t.dtype or o.get_device() != at \
+            shape = o.shape
+            if shape[:2] != (R, beams) or shape[2:] != t.shape[2:] or o.dtype is not t.dtype or o.get_device() != at \
                     or not o.is_contiguous():
                 raise ValueError("out must hold contiguous (%d, %d, ...) tensors of the states' types" % (R, beams))
     if stream is not None:
