@@ -500,73 +500,86 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     }
 }
 
-// Sums of parts, 32 columns a workgroup and 32 parts at a time, added in the same
-// order every time. Of the vectors' sums workgroups 0, 1 and 2 of a range of
-// columns take dw1, db1, and P with Q, from which they form the gradients; the
-// others take a gate's gradient each.
+// Sums of parts, added in the same order every time. Of the vectors' sums, 32
+// columns a workgroup and 32 parts at a time: job 0 takes dw1, job 1 db1, job 2 P
+// and Q, from which it forms the gradients. Of the gates', which have few parts
+// each, 128 columns of one gate a workgroup and 8 parts at a time.
 struct NormJoin {
     ks_residual_norm_t n;
     ks_residual_norm_grads_t out;
     NormParts parts;
     void* dgate;
     int chunks;              // parts of a gate
+    int64_t vector_groups;   // workgroups of the vectors, before those of the gates
 };
-constexpr int kVectorJobs = 3;
+constexpr int kVectorJobs = 3, kVectorCols = 32, kGateCols = 128;
 
 __device__ __forceinline__ double vector_at(const void* v, int elem, int column, double none) {
     if (!v) return none;
     return elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(v)[column]) : static_cast<const float*>(v)[column];
 }
 
-__global__ __launch_bounds__(1024) void norm_join_kernel(const NormJoin j, int64_t job0) {
-    __shared__ double buf[32][33];
-    const int width = static_cast<int>(j.n.width), blocks = (width + 31) / 32;
-    const int64_t job = blockIdx.x / blocks + job0;
-    const int first = static_cast<int>(blockIdx.x % blocks) * 32, low = threadIdx.x % 32, high = threadIdx.x / 32;
-    // the sum of `count` parts, for column first + high in that column's 32 threads
-    auto total = [&](const float* p, int64_t count) {
+// A thread's share of a column's parts: `from`, from + STEP, ... of `count`.
+template <int STEP>
+__device__ __forceinline__ double some_parts(const float* p, int64_t from, int64_t count, int width) {
+    double s = 0.0;
+    int64_t k = from;
+    for (; k + 7 * STEP < count; k += 8 * STEP) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = p[(k + STEP * u) * width];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += static_cast<double>(v[u]);
+    }
+    for (; k < count; k += STEP) s += static_cast<double>(p[k * width]);
+    return s;
+}
+
+__global__ __launch_bounds__(1024) void norm_join_kernel(const NormJoin j, int64_t group0) {
+    __shared__ double buf[1056];
+    const int width = static_cast<int>(j.n.width), tid = threadIdx.x;
+    const int64_t group = blockIdx.x + group0;
+    if (group >= j.vector_groups) {
+        const int blocks = (width + kGateCols - 1) / kGateCols;
+        const int64_t gate = (group - j.vector_groups) / blocks;
+        const int column = static_cast<int>((group - j.vector_groups) % blocks) * kGateCols + tid % kGateCols;
         double s = 0.0;
-        if (first + low < width) {
-            p += first + low;
-            int64_t k = high;
-            for (; k + 224 < count; k += 256) {
-                float v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = p[(k + 32 * u) * width];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) s += static_cast<double>(v[u]);
-            }
-            for (; k < count; k += 32) s += static_cast<double>(p[k * width]);
-        }
+        if (column < width) s = some_parts<8>(j.parts.gates + gate * j.chunks * width + column, tid / kGateCols, j.chunks, width);
+        buf[tid] = s;
         __syncthreads();
-        buf[high][low] = s;
+        if (tid >= kGateCols || column >= width) return;
+        for (int i = 1; i < 8; ++i) s += buf[i * kGateCols + tid];
+        if (j.n.gate_elem == KS_ELEM_BF16)
+            static_cast<bf16_t*>(j.dgate)[gate * width + column] = to_bf16(static_cast<float>(s));
+        else
+            static_cast<float*>(j.dgate)[gate * width + column] = static_cast<float>(s);
+        return;
+    }
+    const int blocks = (width + kVectorCols - 1) / kVectorCols, job = static_cast<int>(group / blocks);
+    const int first = static_cast<int>(group % blocks) * kVectorCols, low = tid % 32, high = tid / 32;
+    // the sum k for column first + high, in that column's 32 threads
+    auto total = [&](int k) {
+        const float* p = j.parts.sums + __builtin_popcount(j.parts.want & ((1 << k) - 1)) * j.parts.workgroups * width;
+        double s = 0.0;
+        if (first + low < width) s = some_parts<32>(p + first + low, high, j.parts.workgroups, width);
         __syncthreads();
-        s = buf[low][high];
+        buf[high * 33 + low] = s;
+        __syncthreads();
+        s = buf[low * 33 + high];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) s += __shfl_xor(s, d, 64);
         return s;
     };
-    // where sum k's parts are; none: not formed
-    auto parts = [&](int k) {
-        return j.parts.sums + __builtin_popcount(j.parts.want & ((1 << k) - 1)) * j.parts.workgroups * width;
-    };
     const int column = first + high;
     const bool writes = low == 0 && column < width;
-    if (job >= kVectorJobs) {
-        const int64_t group = job - kVectorJobs;
-        const float s = static_cast<float>(total(j.parts.gates + group * j.chunks * width, j.chunks));
-        if (!writes) return;
-        if (j.n.gate_elem == KS_ELEM_BF16) static_cast<bf16_t*>(j.dgate)[group * width + column] = to_bf16(s);
-        else static_cast<float*>(j.dgate)[group * width + column] = s;
-    } else if (job < 2) {
+    if (job < 2) {
         float* out = job == 0 ? j.out.pre_weight : j.out.pre_bias;
         if (!out) return;
-        const double s = total(parts(static_cast<int>(job)), j.parts.workgroups);
+        const double s = total(job);
         if (writes) out[column] = static_cast<float>(s);
     } else {
         if (!j.out.post_weight && !j.out.post_bias && !j.out.scale) return;
-        const double P = j.parts.want & 4 ? total(parts(2), j.parts.workgroups) : 0.0;
-        const double Q = j.parts.want & 8 ? total(parts(3), j.parts.workgroups) : 0.0;
+        const double P = j.parts.want & 4 ? total(2) : 0.0, Q = j.parts.want & 8 ? total(3) : 0.0;
         if (!writes) return;
         const double s = vector_at(j.n.scale, j.n.elem, column, 1.0),
                      w2 = vector_at(j.n.post_weight, j.n.elem, column, 1.0),
@@ -713,11 +726,11 @@ ks_status_t launch_norm_grad(const ks_residual_norm_t& n, const NormSplit& s, co
     }
     // the vectors and the gates that workers share (of no rows: zeros), in one launch
     const bool shared = dgate && groups > 0 && (rows == 0 || s.chunks > 1);
-    const int64_t blocks = (n.width + 31) / 32, from = any ? 0 : kVectorJobs, to = kVectorJobs + (shared ? groups : 0);
-    const NormJoin j{n, out, g.parts, dgate, rows > 0 ? s.chunks : 0};
-    const int64_t most = kMaxGrid / 4 / blocks;
-    for (int64_t at = from; st == KS_OK && at < to; at += most)
-        st = launch_kernel(norm_join_kernel, dim3(static_cast<unsigned>(std::min(most, to - at) * blocks)), dim3(1024), 0,
+    const int64_t vectors = any ? kVectorJobs * ((n.width + kVectorCols - 1) / kVectorCols) : 0;
+    const int64_t total = vectors + (shared ? groups * ((n.width + kGateCols - 1) / kGateCols) : 0);
+    const NormJoin j{n, out, g.parts, dgate, rows > 0 ? s.chunks : 0, vectors};
+    for (int64_t at = 0; st == KS_OK && at < total; at += kMaxGrid / 4)
+        st = launch_kernel(norm_join_kernel, dim3(static_cast<unsigned>(std::min(kMaxGrid / 4, total - at))), dim3(1024), 0,
                            stream, j, at);
     return st;
 }
