@@ -2,8 +2,10 @@
 through libks (KS abstract page, taxoreview.com "dblp:303/4794", first
 paragraph: the layer built from KS factors; the gradients are the chain rule
 on Y = X W^T, see include/ks.h). AdapterLinear: such a layer, frozen, with
-low-rank adapters of many requests beside it. preference_loss: the paired
-preference loss on token logits.
+low-rank adapters of many requests beside it. ResidualNorm and ResidualStack:
+the norms, gates and residuals around such layers. preference_loss and
+distillation_loss: the paired preference loss on token logits, and the loss
+against a teacher's highest logits.
 
 Argument marshalling only: every product runs in the HIP library. The gradients
 are not differentiable themselves: a second derivative raises. With
@@ -236,14 +238,168 @@ def preference_loss(logits, labels, ref, beta=0.1, smoothing=0.0):
     return _PREFERENCE.apply(logits, labels, ref, beta, smoothing)
 
 
+def make_distillation_function():
+    import torch
+
+    class DistillationFunction(torch.autograd.Function):
+        """The distillation loss; its gradient goes to the student's logits."""
+
+        @staticmethod
+        def forward(ctx, logits, labels, ids, top, weight, temperature):
+            loss, tokens, stats = libks._distil_forward(logits, labels, ids, top, weight, temperature)
+            ctx.save_for_backward(logits, labels, ids, top, stats)
+            ctx.options = weight, temperature
+            ctx.mark_non_differentiable(tokens)
+            return loss, tokens
+
+        @staticmethod
+        @_first_only
+        def backward(ctx, upstream, _tokens):
+            logits, labels, ids, top, stats = ctx.saved_tensors
+            return libks._distil_backward(logits, labels, ids, top, *ctx.options, stats,
+                                          upstream.float().contiguous()), None, None, None, None, None
+
+    return DistillationFunction
+
+
+_DISTILLATION = None
+
+
+def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0):
+    """(loss, tokens) as libks.distillation_loss gives them, with the loss
+    differentiable in the logits (the teacher is a constant). The gradient is
+    computed in backward(), from the logits: they must not be changed in place
+    before it. libks.distillation_loss forms both at once, in one pass over the
+    logits."""
+    global _DISTILLATION
+    if _DISTILLATION is None:
+        _DISTILLATION = make_distillation_function()
+    return _DISTILLATION.apply(logits, labels, ids, top, weight, temperature)
+
+
+def make_norm_classes():
+    import torch
+
+    class NormFunction(torch.autograd.Function):
+        """(z, h) of a libks.ResidualNorm, h alone without a y; gradients of x, y,
+        the gate and the vectors."""
+
+        @staticmethod
+        def forward(ctx, norm, dtype, x, y, gate, *vectors):
+            z, h, stats = norm.forward(x, y, gate, dtype=dtype, keep=True)
+            ctx.norm = norm
+            ctx.has = y is not None, gate is not None
+            # the vectors too, for autograd's check of in-place changes
+            ctx.save_for_backward(x, y, gate, stats, *vectors)
+            ctx.set_materialize_grads(False)
+            return h if y is None else z if h is None else (z, h)
+
+        @staticmethod
+        @_first_only
+        def backward(ctx, *grads):
+            x, y, gate, stats, *vectors = ctx.saved_tensors
+            if y is None:
+                dz, dh = None, grads[0]
+            else:
+                dz, dh = grads if len(grads) == 2 else (grads[0], None)
+            dz, dh = (None if g is None else g.contiguous() for g in (dz, dh))
+            wanted = ctx.needs_input_grad
+            g = ctx.norm.backward(dz, dh, x, y, stats, gate, weights=any(wanted[5:]))
+            mine = [None if v is None or d is None else d.to(v.dtype) for v, d in zip(vectors, g[3:])]
+            return (None, None, g.dx, g.dy, g.gate, *mine)
+
+    class ResidualNorm(torch.nn.Module):
+        """What stands between two blocks: (z, h) = (x + residual scale . gate .
+        post(y), pre(z)), with z the residual and h the next block's input. pre and
+        post are norms of `kind` "rms" or "layer" (the latter with biases) over the
+        last dimension, `scale` a vector that starts at that value; each is left out
+        if it is false or None. forward(x, y=None, gate=None): x and y (..., width);
+        without a y, z is x. The gate has x's shape, or that of its first dimensions
+        (1 for the others, or none) and width: one for all rows that share them. h is
+        of `dtype`, x's by default."""
+
+        def __init__(self, width, kind="rms", pre=True, post=False, scale=None, residual=1.0, eps=1e-6, dtype=None,
+                     params=None, device=None):
+            super().__init__()
+            self.width, self.kind, self.residual, self.eps, self.dtype = int(width), kind, residual, eps, dtype
+
+            def vector(value):
+                return torch.nn.Parameter(torch.full((self.width,), float(value), device=device,
+                                                     dtype=params or torch.float32))
+
+            bias = kind == "layer"
+            self.pre_weight = vector(1) if pre else None
+            self.pre_bias = vector(0) if pre and bias else None
+            self.post_weight = vector(1) if post else None
+            self.post_bias = vector(0) if post and bias else None
+            self.scale = vector(scale) if scale is not None else None
+
+        def forward(self, x, y=None, gate=None):
+            lead = x.shape[:-1]
+
+            def rows(t):
+                return None if t is None else t.reshape(-1, self.width).contiguous()
+
+            if gate is not None:
+                own = list(gate.shape[:-1])
+                while own and own[-1] == 1:
+                    own.pop()
+                if own != list(lead[:len(own)]):
+                    raise ValueError("the gate's leading dimensions must be the first of x's")
+            vectors = (self.pre_weight, self.pre_bias, self.post_weight, self.post_bias, self.scale)
+            x2, y2, gate2 = rows(x), rows(y), rows(gate)
+            if y is None and self.pre_weight is None:
+                return x, None
+            # the handle holds addresses, so it is made for the tensors of this call
+            norm = libks.ResidualNorm(self.width, *[None if v is None else v.detach() for v in vectors], kind=self.kind,
+                                      eps=self.eps, residual=self.residual)
+            grad = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, y, gate, *vectors))
+            if not grad:
+                z, h = norm.forward(x2, y2, gate2, dtype=self.dtype)
+            else:
+                out = NormFunction.apply(norm, self.dtype, x2, y2, gate2, *vectors)
+                z, h = (x2, out) if y is None else (out, None) if self.pre_weight is None else out
+            z = x if y is None else z.reshape(*lead, self.width)
+            return z, None if h is None else h.reshape(*lead, self.width)
+
+    class ResidualStack(torch.nn.Module):
+        """Blocks (KSLinear, or any modules width -> width) with a residual around
+        each: h = pre(x), then z = x + residual scale . gate . post(block(h)) for
+        each block in turn, each followed by the norm before the next one in the
+        same launch, the last by one more norm. Options as ResidualNorm's. forward(x,
+        gates=None): x (..., width), gates one for each block; returns the last
+        norm's output."""
+
+        def __init__(self, blocks, width, kind="rms", post=False, scale=None, residual=1.0, eps=1e-6, dtype=None,
+                     params=None, device=None):
+            super().__init__()
+            self.blocks = torch.nn.ModuleList(blocks)
+            options = dict(kind=kind, eps=eps, dtype=dtype, params=params, device=device)
+            self.first = ResidualNorm(width, **options)
+            self.norms = torch.nn.ModuleList(ResidualNorm(width, post=post, scale=scale, residual=residual, **options)
+                                             for _ in self.blocks)
+
+        def forward(self, x, gates=None):
+            if gates is not None and len(gates) != len(self.blocks):
+                raise ValueError("one gate for each block")
+            z, h = self.first(x)
+            for k, (block, norm) in enumerate(zip(self.blocks, self.norms)):
+                z, h = norm(z, block(h), None if gates is None else gates[k])
+            return h
+
+    return ResidualNorm, ResidualStack
+
+
 _LAYER = None
 _ADAPTER = None
+_NORMS = None
 
 
 def __getattr__(name):
-    """``layer.KSLinear`` and ``layer.AdapterLinear`` build their class on
-    first use (torch is imported lazily, as everywhere in this package)."""
-    global _LAYER, _ADAPTER
+    """``layer.KSLinear``, ``layer.AdapterLinear``, ``layer.ResidualNorm`` and
+    ``layer.ResidualStack`` build their class on first use (torch is imported
+    lazily, as everywhere in this package)."""
+    global _LAYER, _ADAPTER, _NORMS
     if name == "KSLinear":
         if _LAYER is None:
             _LAYER = make_layer_class()
@@ -252,4 +408,8 @@ def __getattr__(name):
         if _ADAPTER is None:
             _ADAPTER = make_adapter_class()
         return _ADAPTER
+    if name in ("ResidualNorm", "ResidualStack"):
+        if _NORMS is None:
+            _NORMS = make_norm_classes()
+        return _NORMS[name == "ResidualStack"]
     raise AttributeError(name)
