@@ -339,8 +339,8 @@ ks_status_t ks_chain_describe(const ks_pattern_t* p, int n, int64_t batch, ks_dt
  * between layers, preference and distillation losses on token logits, beam
  * search, and the optimizer step. The conventions above hold for all of
  * them: device pointers of the caller, asynchronous on `stream`, argument
- * errors found on the host before any HIP call, no allocation, no atomics and
- * a fixed summation order.
+ * errors found on the host before any HIP call, no allocation, and a fixed
+ * summation order (no sum is formed by atomics).
  */
 
 /* Element types of single tensors (the types that ks_dtype_t combines). */

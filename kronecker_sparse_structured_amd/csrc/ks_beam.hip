@@ -421,9 +421,9 @@ ks_status_t launch_beam_select(const ks_beams_t& x, const BeamOut& out, void* ws
     }
     const int waves = std::min(kJoinWaves, x.beams);
     const size_t join = static_cast<size_t>(2 * x.beams * s.keep + waves * s.keep * kJoinHold) * 8;
-    for (int64_t r = 0; r < x.requests; r += kMaxGrid) {
+    for (int64_t r = 0; r < x.requests; r += kMaxGrid / 4) {
         const ks_status_t st = launch_kernel(beam_join_kernel,
-                                             dim3(static_cast<unsigned>(std::min(kMaxGrid, x.requests - r))),
+                                             dim3(static_cast<unsigned>(std::min(kMaxGrid / 4, x.requests - r))),
                                              dim3(waves * 64), join, stream, x, s, out, r);
         if (st != KS_OK) return st;
     }

@@ -296,96 +296,113 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
     }
 }
 
+// The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
+// not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
+// as the square of the first (8192 rows of 50257 in bf16 313 us, 366 so).
+enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
+
 // dx of one row: first as if there were no entries, then the values at the
 // entries' and the label's tokens again. Logits and gradient may be one memory,
-// so those logits are read before anything is written.
-template <typename T, bool TWO>
+// so those logits are read before anything is written. Two entries of one token
+// are looked for in a bit a token (`bits`: there is room for one), and added up
+// where there are any; over wider vocabularies that is done for every row.
+constexpr int kSeenVocab = 1 << 17;
+template <typename T, int MODE>
 __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs a, const float* stats, const float* inv,
                                                                const float* upstream, T* d_, int64_t d_seq,
-                                                               int64_t d_row) {
+                                                               int64_t d_row, bool bits) {
+    extern __shared__ uint32_t seen[];
     __shared__ float buf[2 * kWaves];
-    __shared__ int ids[kMaxTop + 1];
-    __shared__ float qs[kMaxTop + 1], xs[kMaxTop + 1];
+    __shared__ int ids[kMaxTop], any, twice, label_in;
+    __shared__ float qs[kMaxTop];
     constexpr int E = kVec<T>;
     const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
     const int64_t label = a.x.labels[s * a.x.label_stride + t];
     const T* row = static_cast<const T*>(a.x.data) + s * a.x.seq_stride + t * a.x.row_stride;
     T* out = d_ + s * d_seq + t * d_row;
-    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x;
+    const int V = static_cast<int>(a.x.vocab), tid = threadIdx.x, entries = a.t.count;
     const int head = head_of(out, V), vecs = (V - head) / E, tail = head + vecs * E;
+    typedef typename Access<T, 4>::vec access;
     u32x4* obody = reinterpret_cast<u32x4*>(out + head);
     if (label < 0) {
         if (tid < head) out[tid] = narrow<T>(0.0f);
         if (tid < V - tail) out[tail + tid] = narrow<T>(0.0f);
         const u32x4 none = {0u, 0u, 0u, 0u};
-        for (int v = tid; v < vecs; v += kThreads) obody[v] = none;
+        for (int v = tid; v < vecs; v += kThreads) __builtin_nontemporal_store(none, &obody[v]);
         return;
     }
     const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
-    const float m = stats[3 * at];
+    const float m = uniform(stats[3 * at]), sum = stats[3 * at + 1], sum1 = stats[3 * at + 2];
     float c = *inv;
     if (upstream) c *= *upstream;
-    const Entry e = teacher_entry(a, s, t, buf);
-    // where nothing in the row weighs anything, that side is not there
-    __shared__ int any;
-    if (tid == 0) any = 0;
-    __syncthreads();
-    if (!(e.q == 0.0f)) any = 1;
-    __syncthreads();
-    const float slope = kl && any ? a.slope * c : 0.0f, hard = static_cast<float>(a.ce) * c;
-    const float sum = stats[3 * at + 1], sum1 = stats[3 * at + 2];
-    float c0 = slope / sum, c1 = hard / sum1;
-    if (!TWO) c0 = (slope + hard) / sum;       // one exponential serves both, or one side is left out
-    const int count = a.t.count + 1;
-    if (tid < a.t.count) {
-        const bool in = e.id >= 0 && e.id < V;
-        ids[tid] = in ? static_cast<int>(e.id) : !(e.q == 0.0f) ? 0 : -1;    // an id outside: the row says so at 0
-        qs[tid] = slope * e.q;
-        xs[tid] = in ? to_f32(row[e.id]) : 0.0f;
-    }
     if (tid == 0) {
-        ids[count - 1] = !ce ? -1 : label < V ? static_cast<int>(label) : 0;
-        qs[count - 1] = label < V ? hard : __builtin_nanf("");
-        xs[count - 1] = ce ? to_f32(row[label < V ? label : 0]) : 0.0f;
+        any = label_in = 0;
+        twice = !bits;
     }
+    for (int i = tid; bits && i < (V + 31) / 32; i += kThreads) seen[i] = 0;
+    Entry e{-1, 0.0f, 0.0f};
+    if (kl) e = teacher_entry(a, s, t, buf);       // its barriers cover what was cleared
+    const bool in = e.id >= 0 && e.id < V;
+    const float xe = in ? to_f32(row[e.id]) : 0.0f;
+    const float xl = ce && tid == 0 ? to_f32(row[label < V ? label : 0]) : 0.0f;
+    if (in) {
+        const int k = static_cast<int>(e.id);
+        if (bits && atomicOr(&seen[k / 32], 1u << k % 32) >> k % 32 & 1) twice = 1;
+        if (e.id == label) label_in = 1;
+    }
+    if (!(e.q == 0.0f)) any = 1;
+    if (tid < entries) ids[tid] = in ? static_cast<int>(e.id) : -1;
     __syncthreads();
+    // where nothing in the row weighs anything, that side is not there
+    const float slope = any ? a.slope * c : 0.0f, hard = static_cast<float>(a.ce) * c;
+    const float c0 = uniform(MODE != kOne ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
+    if (tid < entries) qs[tid] = slope * e.q;
     auto value = [&](float x) {
-        float y = c0 * exp_of(x - m, a.scale);
-        if (TWO) y += c1 * ks::exp_of(x - m);
-        return y;
+        // without the second part of log2 e / T, as in distil_row_kernel
+        const float y = __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
+        if (MODE == kBoth) return c0 * y + c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
+        if (MODE == kSquare) return y * (c0 + c1 * y);
+        return c0 * y;
     };
     if (tid < head) out[tid] = narrow<T>(value(to_f32(row[tid])));
     if (tid < V - tail) out[tail + tid] = narrow<T>(value(to_f32(row[tail + tid])));
-    if (head_of(row, V) != head) {
-        for (int v = head + tid; v < tail; v += kThreads) out[v] = narrow<T>(value(to_f32(row[v])));
-    } else {
-        const u32x4* body = reinterpret_cast<const u32x4*>(row + head);
-        for (int v = tid; v < vecs; v += kThreads) {
-            float x[E];
-            widen<T>(body[v], x);
+    auto put = [&](int v, u32x4 w) {
+        float x[E];
+        widen<T>(w, x);
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = value(x[i]);
-            obody[v] = pack<T>(x);
-        }
+        for (int i = 0; i < E; ++i) x[i] = value(x[i]);
+        __builtin_nontemporal_store(pack<T>(x), &obody[v]);
+    };
+    constexpr int U = 4;
+    int v = tid;
+    for (; v + (U - 1) * kThreads < vecs; v += U * kThreads) {
+        u32x4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const access*>(row + head + (v + u * kThreads) * E);
+#pragma unroll
+        for (int u = 0; u < U; ++u) put(v + u * kThreads, w[u]);
     }
+    for (; v < vecs; v += kThreads) put(v, *reinterpret_cast<const access*>(row + head + v * E));
     __syncthreads();
-    for (int k = tid; k < count; k += kThreads) {
-        if (ids[k] < 0) continue;
-        float q = 0.0f;
+    if (tid < entries && e.id >= V) out[0] = narrow<T>(__builtin_nanf(""));     // a token outside: the row says so at its first
+    if (tid < entries && in) {
+        float taken = qs[tid];
         bool first = true;
-        for (int j = 0; j < count; ++j) {
-            if (ids[j] != ids[k]) continue;
-            first = first && j >= k;
-            q += qs[j];
+        if (twice) {
+            taken = 0.0f;
+            for (int j = 0; j < entries; ++j) {
+                if (ids[j] != ids[tid]) continue;
+                first = first && j >= tid;
+                taken += qs[j];
+            }
         }
-        if (first) out[ids[k]] = narrow<T>(value(xs[k]) - q);
+        if (ce && e.id == label) taken += hard;
+        if (first) out[e.id] = narrow<T>(value(xe) - taken);
     }
+    if (tid != 0 || !ce) return;
+    if (label >= V) out[0] = narrow<T>(__builtin_nanf(""));
+    else if (!label_in) out[label] = narrow<T>(value(xl) - hard);
 }
-
-// The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
-// not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
-// as the square of the first (8192 rows of 50257 in bf16 313 us, 366 so).
-enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
 
 // Loss and gradient (d_ null: the loss alone, and stats for a later gradient) of a
 // row that the workgroup holds, U 16-byte vectors a lane.
@@ -650,7 +667,10 @@ DistilArgs distil_args(const ks_logits_t& x, const ks_teacher_t& t, const Distil
     return a;
 }
 
-bool two_sums(const Distil& o) { return o.weight > 0.0 && o.weight < 1.0 && o.temperature != 1.0; }
+int exps_of(const Distil& o) {
+    if (!(o.weight > 0.0 && o.weight < 1.0 && o.temperature != 1.0)) return kOne;
+    return o.temperature == 2.0 ? kSquare : kBoth;
+}
 
 }  // namespace
 
@@ -667,7 +687,7 @@ ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, float* 
 ks_status_t launch_distil_tokens(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens,
                                  float* stats, hipStream_t stream) {
     DistilArgs a = distil_args(x, t, o);
-    const bool two = two_sums(o);
+    const bool two = exps_of(o) != kOne;
     const auto kernel = x.elem == KS_ELEM_BF16
                             ? (two ? distil_tokens_kernel<bf16_t, true> : distil_tokens_kernel<bf16_t, false>)
                             : (two ? distil_tokens_kernel<float, true> : distil_tokens_kernel<float, false>);
@@ -684,16 +704,23 @@ ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, cons
                                const float* inv, const float* upstream, void* d, int64_t d_seq, int64_t d_row,
                                hipStream_t stream) {
     DistilArgs a = distil_args(x, t, o);
-    const bool two = two_sums(o);
+    const bool bits = x.vocab <= kSeenVocab;
+    const size_t lds = bits ? static_cast<size_t>((x.vocab + 31) / 32 * 4) : 0;
+    const int mode = exps_of(o);
     const int64_t rows = x.sequences * x.tokens;
     for (a.row0 = 0; a.row0 < rows; a.row0 += kMaxGrid) {
         const dim3 grid(static_cast<unsigned>(std::min(kMaxGrid, rows - a.row0)));
+        const auto run = [&](auto type, auto kernel) {
+            typedef decltype(type) T;
+            return launch_kernel(kernel, grid, dim3(kThreads), lds, stream, a, stats, inv, upstream, static_cast<T*>(d), d_seq,
+                                 d_row, bits);
+        };
         const ks_status_t st =
             x.elem == KS_ELEM_BF16
-                ? launch_kernel(two ? distil_grad_kernel<bf16_t, true> : distil_grad_kernel<bf16_t, false>, grid,
-                                dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<bf16_t*>(d), d_seq, d_row)
-                : launch_kernel(two ? distil_grad_kernel<float, true> : distil_grad_kernel<float, false>, grid,
-                                dim3(kThreads), 0, stream, a, stats, inv, upstream, static_cast<float*>(d), d_seq, d_row);
+                ? run(bf16_t{}, mode == kOne ? distil_grad_kernel<bf16_t, kOne> : mode == kBoth
+                                ? distil_grad_kernel<bf16_t, kBoth> : distil_grad_kernel<bf16_t, kSquare>)
+                : run(float{}, mode == kOne ? distil_grad_kernel<float, kOne> : mode == kBoth
+                               ? distil_grad_kernel<float, kBoth> : distil_grad_kernel<float, kSquare>);
         if (st != KS_OK) return st;
     }
     return KS_OK;
@@ -746,7 +773,7 @@ bool distil_counts(const ks_logits_t& x) { return x.sequences * x.tokens <= kCou
 ks_status_t launch_distil_rows(const ks_logits_t& x, const ks_teacher_t& t, const Distil& o, float* tokens, float* inv,
                                float* stats, void* d, int64_t d_seq, int64_t d_row, hipStream_t stream) {
     DistilArgs a = distil_args(x, t, o);
-    const int mode = !two_sums(o) ? kOne : o.temperature == 2.0 ? kSquare : kBoth;
+    const int mode = exps_of(o);
     const auto pick = x.elem == KS_ELEM_BF16 ? (mode == kOne ? pick_rows<bf16_t, kOne> : mode == kBoth ? pick_rows<bf16_t, kBoth>
                                                 : pick_rows<bf16_t, kSquare>)
                                              : (mode == kOne ? pick_rows<float, kOne> : mode == kBoth ? pick_rows<float, kBoth>

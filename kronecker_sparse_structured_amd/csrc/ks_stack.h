@@ -7,7 +7,9 @@
 
 namespace ks {
 
-constexpr int64_t kMaxGrid = int64_t(1) << 23;   // workgroups a launch: a grid counts its threads in 32 bits
+// Workgroups of 256 threads a launch (a quarter of 1024): a grid counts its threads
+// in 32 bits.
+constexpr int64_t kMaxGrid = int64_t(1) << 23;
 
 // ---- residual norms (ks_norm.hip)
 

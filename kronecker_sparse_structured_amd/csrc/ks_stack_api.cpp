@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <vector>
 
 #include "ks_check.h"
@@ -85,17 +86,6 @@ ks_status_t check_norm(const ks_residual_norm_t* n, int64_t rows, int64_t groups
     for (const void* v : {n->pre_weight, n->pre_bias, n->post_weight, n->post_bias, n->scale})
         if (!aligned(v, size_of(n->elem))) return KS_ERR_ALIGN;
     return KS_OK;
-}
-
-// What a call writes (`out`) meets something else that it writes or reads.
-bool meets(const std::vector<Range>& out, const std::vector<Range>& in) {
-    for (size_t i = 0; i < out.size(); ++i) {
-        for (size_t k = i + 1; k < out.size(); ++k)
-            if (overlap(out[i].p, out[i].bytes, out[k].p, out[k].bytes)) return true;
-        for (const Range& r : in)
-            if (overlap(out[i].p, out[i].bytes, r.p, r.bytes)) return true;
-    }
-    return false;
 }
 
 }  // namespace
@@ -205,6 +195,11 @@ ks_status_t ks_beam_reorder(const ks_state_t* states, int n, const int32_t* pare
         bool written;
     };
     std::vector<Span> spans;
+    try {
+        spans.reserve(2 * static_cast<size_t>(n) + 1);
+    } catch (const std::exception&) {      // no exception passes a C entry
+        return KS_ERR_INVALID;
+    }
     for (int i = 0; i < n; ++i) {
         const ks_state_t& s = states[i];
         if (s.row_bytes < 0 || s.row_bytes >= (int64_t(1) << 40)) return KS_ERR_INVALID;
@@ -289,7 +284,7 @@ ks_status_t ks_residual_norm_backward(const ks_residual_norm_t* n, const void* d
         if (!aligned(p, 4)) return KS_ERR_ALIGN;
     const uint64_t values = static_cast<uint64_t>(rows) * n->width, w = static_cast<uint64_t>(n->width) * size_of(n->elem);
     const uint64_t f = static_cast<uint64_t>(n->width) * 4, gates = static_cast<uint64_t>(groups) * n->width * gs;
-    if (meets({{dx, values * xs}, {dy, values * ys}, {dgate, gates}, {g->pre_weight, f}, {g->pre_bias, f},
+    if (any_overlap({{dx, values * xs}, {dy, values * ys}, {dgate, gates}, {g->pre_weight, f}, {g->pre_bias, f},
                {g->post_weight, f}, {g->post_bias, f}, {g->scale, f}, {need > 0 ? ws : nullptr, need}},
               {{dz, values * xs}, {dh, values * hs}, {x, values * xs}, {y, values * ys}, {gate, gates},
                {stats, static_cast<uint64_t>(rows) * 16}, {n->pre_weight, w}, {n->pre_bias, w}, {n->post_weight, w},

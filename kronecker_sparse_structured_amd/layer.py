@@ -246,7 +246,8 @@ def make_distillation_function():
 
         @staticmethod
         def forward(ctx, logits, labels, ids, top, weight, temperature):
-            loss, tokens, stats = libks._distil_forward(logits, labels, ids, top, weight, temperature)
+            loss, tokens, stats = libks._on_device(logits.get_device(), libks._distil_forward, logits, labels, ids, top,
+                                                   weight, temperature)
             ctx.save_for_backward(logits, labels, ids, top, stats)
             ctx.options = weight, temperature
             ctx.mark_non_differentiable(tokens)
@@ -256,8 +257,8 @@ def make_distillation_function():
         @_first_only
         def backward(ctx, upstream, _tokens):
             logits, labels, ids, top, stats = ctx.saved_tensors
-            return libks._distil_backward(logits, labels, ids, top, *ctx.options, stats,
-                                          upstream.float().contiguous()), None, None, None, None, None
+            return libks._on_device(logits.get_device(), libks._distil_backward, logits, labels, ids, top, *ctx.options,
+                                    stats, upstream.float().contiguous()), None, None, None, None, None
 
     return DistillationFunction
 

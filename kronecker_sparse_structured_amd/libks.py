@@ -300,6 +300,23 @@ def _on_stream(stream, device, call, *args):
     return out
 
 
+def _current_device() -> int:
+    """Torch's current device (without the checks of its public function where
+    torch has the number at hand)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get is not None else torch.cuda.current_device()
+
+
+def _on_device(index: int, call, *args):
+    """call(*args) with this device as the current one, which launches need."""
+    import torch
+    if _current_device() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
+
+
 def _raise(status: int, where: str, check: bool) -> int:
     if check and status != 0:
         raise KSError(status, where)
@@ -955,7 +972,8 @@ def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0, dlo
         raise ValueError("dlogits is given, but grad is not asked for")
     if grad and not given:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
-    loss, tokens, _ = _distil_forward(logits, labels, ids, top, weight, temperature, dlogits)
+    loss, tokens, _ = _on_device(logits.get_device(), _distil_forward, logits, labels, ids, top, weight, temperature,
+                                 dlogits)
     if given:
         _wrote(dlogits)
     return loss, tokens, dlogits
@@ -1009,7 +1027,7 @@ def beam_select(logits, scores, beams=None, done=None, lengths=None, eos=None, l
     if stream is not None:
         return Beams(*_on_stream(stream, logits.device, _beam_select, logits, scores, beams, done, lengths, eos,
                                  length_penalty))
-    return Beams(*_beam_select(logits, scores, beams, done, lengths, eos, length_penalty))
+    return Beams(*_on_device(at, _beam_select, logits, scores, beams, done, lengths, eos, length_penalty))
 
 
 _BEAM_WORKSPACE = {}     # bytes by sizes, asked for once each
@@ -1072,7 +1090,7 @@ def beam_reorder(states, parents, out=None, stream=None):
                 raise ValueError("out must hold contiguous (%d, %d, ...) tensors of the states' types" % (R, beams))
     if stream is not None:
         return list(_on_stream(stream, parents.device, _beam_reorder, states, parents, out))
-    return list(_beam_reorder(states, parents, out))
+    return list(_on_device(at, _beam_reorder, states, parents, out))
 
 
 def _beam_reorder(states, parents, out):
@@ -1174,7 +1192,7 @@ class ResidualNorm:
         if stream is not None:
             z, h, *stats = _on_stream(stream, x.device, self._forward, x, y, gate, dtype, keep)
             return (x if y is None else z, h, *stats)
-        return self._forward(x, y, gate, dtype, keep)
+        return _on_device(x.get_device(), self._forward, x, y, gate, dtype, keep)
 
     def _forward(self, x, y, gate, dtype, keep):
         import torch
@@ -1202,7 +1220,7 @@ class ResidualNorm:
         weights=False)."""
         if stream is not None:
             return NormGrads(*_on_stream(stream, x.device, self._backward, dz, dh, x, y, stats, gate, weights))
-        return NormGrads(*self._backward(dz, dh, x, y, stats, gate, weights))
+        return NormGrads(*_on_device(x.get_device(), self._backward, dz, dh, x, y, stats, gate, weights))
 
     def _backward(self, dz, dh, x, y, stats, gate, weights):
         import torch

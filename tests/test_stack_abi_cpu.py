@@ -227,3 +227,20 @@ def test_host_tensors_are_refused(call):
             libks.beam_reorder([x], ids[:, :, 0].contiguous())
         else:
             libks.ResidualNorm(10, torch.ones(10))
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    import contextlib
+
+    import torch
+    entered = []
+
+    @contextlib.contextmanager
+    def device(index):
+        entered.append(index)
+        yield
+
+    monkeypatch.setattr(libks, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    assert libks._on_device(0, lambda a: a + 1, 4) == 5 and entered == []
+    assert libks._on_device(3, lambda a: a + 1, 4) == 5 and entered == [3]
