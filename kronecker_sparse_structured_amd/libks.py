@@ -309,9 +309,10 @@ def _current_device() -> int:
 
 
 def _on_device(index: int, call, *args):
-    """call(*args) with this device as the current one, which launches need."""
+    """call(*args) with this device as the current one, which launches need (a host
+    tensor's -1 is for the call to refuse)."""
     import torch
-    if _current_device() == index:
+    if index < 0 or _current_device() == index:
         return call(*args)
     with torch.cuda.device(index):
         return call(*args)
