@@ -1050,15 +1050,19 @@ def _beam_select(logits, scores, beams, done, lengths, eos, length_penalty):
         if len(_BEAM_WORKSPACE) > 256:
             _BEAM_WORKSPACE.clear()
         size = _BEAM_WORKSPACE[key] = need.value
-    new, i32 = scores.new_empty, lengths
-    # of a tensor that has the type, where there is one: a type by keyword costs as much again
-    tokens = new((R, beams), dtype=torch.int64)
-    parents = new((R, beams), dtype=torch.int32) if i32 is None else i32.new_empty((R, beams))
-    out_done = None
-    if eos is not None:
-        out_done = new((R, beams), dtype=torch.bool) if done is None else done.new_empty((R, beams))
-    out_lengths = None if i32 is None else i32.new_empty((R, beams))
-    best, ws = new((R, beams)), new((size + 3) // 4)
+    # of a tensor of that type, where there is one, and of its shape: cheaper than to say both
+    like = torch.empty_like
+    if beams == W:
+        best = like(scores)
+        parents = like(scores, dtype=torch.int32) if lengths is None else like(lengths)
+        out_lengths = None if lengths is None else like(lengths)
+        out_done = None if eos is None else like(scores, dtype=torch.bool) if done is None else like(done)
+    else:
+        new, shape = scores.new_empty, (R, beams)
+        best, parents = new(shape), new(shape, dtype=torch.int32)
+        out_lengths = None if lengths is None else lengths.new_empty(shape)
+        out_done = None if eos is None else new(shape, dtype=torch.bool)
+    tokens, ws = scores.new_empty((R, beams), dtype=torch.int64), scores.new_empty((size + 3) // 4)
     _raise(lib.ks_beam_select(x, beams, best.data_ptr(), tokens.data_ptr(), parents.data_ptr(), _ptr(out_done),
                               _ptr(out_lengths), ws.data_ptr(), size, _raw_stream(logits.get_device())),
            "ks_beam_select", True)
@@ -1198,13 +1202,15 @@ class ResidualNorm:
     def _forward(self, x, y, gate, dtype, keep):
         import torch
         rows, groups, n = self._rows(x, y, gate)
+        like = torch.empty_like
         z = h = stats = None
         if y is not None:
-            z = x.new_empty(rows, self.width)
+            z = like(x)
         if self._pre:
-            dtype = x.dtype if dtype is None else dtype
-            n.h_elem = _elem(dtype, "h")
-            h = x.new_empty((rows, self.width), dtype=dtype)
+            if dtype is None or dtype is x.dtype:
+                n.h_elem, h = n.x_elem, like(x)
+            else:
+                n.h_elem, h = _elem(dtype, "h"), like(x, dtype=dtype)
         if keep:
             stats = x.new_empty((rows, 4), dtype=torch.float32)
         if y is not None or self._pre:
@@ -1234,11 +1240,11 @@ class ResidualNorm:
             n.h_elem = _elem(dh.dtype, "dh")
             _check_out(dh, tuple(x.shape), dh.dtype, x.device, "dh")
         _check_out(stats, (rows, 4), torch.float32, x.device, "stats")
-        dx = x.new_empty(rows, self.width)
-        dy = y.new_empty(rows, self.width) if y is not None else None
-        dgate = gate.new_empty(groups, self.width) if gate is not None else None
-        f32 = torch.float32
-        grads = [x.new_empty(self.width, dtype=f32) if weights and t is not None else None
+        like, f32 = torch.empty_like, torch.float32
+        dx = like(x)
+        dy = like(y) if y is not None else None
+        dgate = like(gate) if gate is not None else None
+        grads = [None if t is None or not weights else like(t) if t.dtype is f32 else like(t, dtype=f32)
                  for t in self.vectors.values()]
         size = self._sizes.get((rows, groups))
         if size is None:
