@@ -12,6 +12,16 @@
 // sums and its entries' part are formed. Longer rows, and a gradient that is
 // asked for later, go through the row again; there the maximum and both sums of
 // exponentials are kept in one pass, as in ks_preference.hip.
+//
+// The gradient goes out in two steps: the whole row as if there were no entries, in
+// 16-byte nontemporal stores (8192 rows of 50257 in bf16 338 us, 352 with ordinary
+// ones), and behind a barrier the few values at the entries' and the label's tokens
+// again.
+//
+// What bounds it: the row's read and write. 8192 rows of 50257 in bf16 (1.65 GB)
+// with one exponential a value 320 us, 5.1 TB/s, a device copy of as much 320;
+// with two, 338 to 373: there the exponentials' arithmetic shows. In fp32, 8192 rows
+// of 32000 (2.1 GB), 398 us either way.
 
 #include <algorithm>
 #include <cmath>
@@ -50,6 +60,15 @@ struct Scale {
 __device__ __forceinline__ float exp_of(float d, Scale s) {
     return __builtin_amdgcn_exp2f(__builtin_fmaf(d, s.hi, d * s.lo));
 }
+
+// The same for a value that is rounded to T: for bf16 without the second part, which
+// is 1e-6 of it at most.
+template <typename T>
+__device__ __forceinline__ float short_exp(float d, Scale s) {
+    if constexpr (sizeof(T) == 4) return exp_of(d, s);
+    else return __builtin_amdgcn_exp2f(d * s.hi);
+}
+constexpr Scale kNatural{kLog2e, kLog2eLow};
 
 struct DistilArgs {
     ks_logits_t x;
@@ -298,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
 
 // The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
 // not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
-// as the square of the first (8192 rows of 50257 in bf16 313 us, 366 so).
+// as the square of the first (8192 rows of 50257 in bf16 338 us, 373 otherwise).
 enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
 
 // dx of one row: first as if there were no entries, then the values at the
@@ -358,9 +377,8 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
     const float c0 = uniform(MODE != kOne ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
     if (tid < entries) qs[tid] = slope * e.q;
     auto value = [&](float x) {
-        // without the second part of log2 e / T, as in distil_row_kernel
-        const float y = __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
-        if (MODE == kBoth) return c0 * y + c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
+        const float y = short_exp<T>(x - m, a.scale);
+        if (MODE == kBoth) return c0 * y + c1 * short_exp<T>(x - m, kNatural);
         if (MODE == kSquare) return y * (c0 + c1 * y);
         return c0 * y;
     };
@@ -580,10 +598,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     // the gradient as if there were no entries
     const float c0 = uniform(TWO ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
     auto value = [&](float x) {
-        // (x - m) log2 e / T is off by 1e-7 of itself without the second part: far
-        // below a rounding of the value's type, or of the sums before it
-        const float e = __builtin_amdgcn_exp2f((x - m) * a.scale.hi);
-        if (MODE == kBoth) return c0 * e + c1 * __builtin_amdgcn_exp2f((x - m) * kLog2e);
+        const float e = short_exp<T>(x - m, a.scale);
+        if (MODE == kBoth) return c0 * e + c1 * short_exp<T>(x - m, kNatural);
         if (MODE == kSquare) return e * (c0 + c1 * e);
         return c0 * e;
     };
@@ -742,7 +758,7 @@ ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, 
 
 // The workgroup that holds a row's vectors: of few rows as many threads as it
 // takes, for the time of one row; of many rows 8 or 16 vectors a lane, so that the
-// card has more rows on their way (16384 rows of 4096 in bf16 PLACE us, 71 with 2).
+// card has more rows on their way (16384 rows of 4096 in bf16 63 us, 71 with 2).
 template <typename T, int MODE>
 ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, float* stats, void* d, int64_t d_seq, int64_t d_row,
                       hipStream_t stream) {
