@@ -6,8 +6,8 @@ taxoreview.com "dblp:303/4794", first paragraph). The compute path is the
 HIP library libks.so (C ABI in include/ks.h); ``libks`` is its ctypes
 binding. Importing this package loads nothing; the first call does.
 ``layer`` and ``optim`` hold what a model trains with: KS layers, low-rank
-adapters beside them, a preference loss and AdamW (``finetune`` runs them
-together).
+adapters beside them, the norms and residuals between them, preference and
+distillation losses and AdamW (``finetune`` runs them together).
 """
 from . import datagen  # noqa: F401  (seeded inputs; no KS arithmetic)
 

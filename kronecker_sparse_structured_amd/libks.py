@@ -11,7 +11,7 @@ loading fails loudly.
 
 ``matmul`` and ``chain_matmul`` are conveniences over the same calls that
 allocate the output (and the chain workspace) with torch. They, the adapters,
-the preference loss and the optimizer count what they write into a caller's
+the losses, beam search and the optimizer count what they write into a caller's
 tensor as an in-place change (torch's version counter), so that autograd sees
 it; the ``ks_`` calls write through addresses and do not. Their ``stream``
 (default: torch's current one) is the one that the call launches on and
