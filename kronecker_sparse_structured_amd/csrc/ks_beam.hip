@@ -233,6 +233,9 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         const int64_t row = request * W + w;
         // everything that may be needed is asked for at once (a beam that is done, or
         // whose score is not finite, has written nothing, and it is not used)
+        const float score = x.scores[row];
+        const bool done = x.done && x.done[row];
+        const int len = x.lengths ? x.lengths[row] + (done ? 0 : 1) : 0;
         const uint64_t* keys = s.keys + row * s.slices * keep;
         const int n = s.slices * keep;
         uint64_t mine[kJoinHold];
@@ -243,9 +246,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         }
         const float2* st = s.stats + row * s.slices;
         const float2 own = lane < s.slices ? st[lane] : make_float2(kLowest, 0.0f);
-        const float score = x.scores[row];
-        const bool done = x.done && x.done[row];
-        const int len = x.lengths ? x.lengths[row] + (done ? 0 : 1) : 0;
+        // while the keys are on their way
+        const double power = x.length_penalty == 0.0 ? 1.0 : pow(static_cast<double>(max(len, 1)), x.length_penalty);
         double shift = 0.0;
         bool live = finite(score);
         if (done || !live) {
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         if (lane == 0) {
             base[w] = live ? static_cast<double>(score) + shift : -INFINITY;
             length[w] = len;
-            divisor[w] = x.length_penalty == 0.0 ? 1.0 : pow(static_cast<double>(max(len, 1)), x.length_penalty);
+            divisor[w] = power;
         }
     }
     __syncthreads();
