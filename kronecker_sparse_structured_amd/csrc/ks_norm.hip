@@ -24,7 +24,7 @@
 // this one's sums are formed.
 //
 // What bounds it: memory. Forward 16384 x 1024 (fp32 in, bf16 h, 235 MB) 37 us, 6.3
-// TB/s with the last cache's help; 4096 x 4096 in bf16 (101 MB) 27 us, 3.7 TB/s: two
+// TB/s with the last cache's help; 4096 x 4096 in bf16 (101 MB) 26 us, 3.9 TB/s: two
 // bytes a value keep too few on their way (a second row ahead 26 us there, but 43 for
 // 39 in fp32). Backward 25216 x 384 in fp32 with a gate of 197 rows (232 MB) 47 us,
 // 4.9 TB/s; 4096 x 4096 in bf16 (201 MB) 43 us, 4.7 TB/s. The parts' launch takes 5
@@ -53,7 +53,8 @@ int worker_waves(int64_t width, int lane) {
 
 // The values that a lane holds. Forward: 8 keep more bytes on their way (4096 x
 // 4096 in bf16 27 us, 54 with 4), unless one wave of 4 would do. Backward: 4, as
-// long as 16 waves reach (8192 x 2048 47 us, 91 with 8).
+// long as 16 waves reach (8192 x 2048 47 us; as many values as 2048 x 8192, with 8,
+// 94 us: its vectors and sums do not fit the registers).
 int forward_lane(int64_t width) { return width <= 256 ? 4 : 8; }
 int backward_lane(int64_t width) { return width <= 4096 ? 4 : 8; }
 
@@ -233,6 +234,28 @@ __device__ __forceinline__ void deviation(const Lanes<L>& l, RowSums& sums, cons
     r = 1.0f / sqrtf(square * a.inverse + a.eps);
 }
 
+template <int L>
+__device__ __forceinline__ void vector(const Lanes<L>& l, const void* v, int elem, float none, float (&to)[L]) {
+    fill(to, none);
+    if (v) l.load(v, elem, to);
+}
+
+// s u = w yn + b with the scale in post's vectors: two products and 8 registers a
+// lane less in every row (4096 x 4096 in bf16 26.0 us for 26.7; backward the same
+// costs 3 to 10 us: its sums need s by itself too).
+template <int L>
+__device__ __forceinline__ void scaled_post(const Lanes<L>& l, const ks_residual_norm_t& n, float (&w)[L], float (&b)[L]) {
+    float s[L];
+    vector(l, n.scale, n.elem, 1.0f, s);
+    vector(l, n.post_weight, n.elem, 1.0f, w);
+    vector(l, n.post_bias, n.elem, 0.0f, b);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        w[i] *= s[i];
+        b[i] *= s[i];
+    }
+}
+
 template <typename XT, typename YT, typename HT, int L>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT* h, float* stats) {
     __shared__ float2 buf[2][16];
@@ -248,24 +271,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT*
     int64_t first = static_cast<int64_t>(blockIdx.x) * each;       // of the workgroup's rows
     Raw<XT, L> nx;
     Raw<YT, L> ny = {};
-    float gate[L], w1[L], b1[L], w2[L], b2[L], s[L];
+    float gate[L], w1[L], b1[L], w2[L], b2[L];
     // a worker without a row goes through the barriers with the last one
     auto fetch = [&](int64_t row) {
         l.load(X + row * width, nx);
         if (Y) l.load(Y + row * width, ny);
     };
     fetch(min(first + worker, a.rows - 1));
-    fill(w1, 0.0f);
-    fill(b1, 0.0f);
-    fill(w2, 1.0f);
-    fill(b2, 0.0f);
-    fill(s, 1.0f);
     fill(gate, 1.0f);
-    if (a.n.post_weight) l.load(a.n.post_weight, a.n.elem, w2);
-    if (a.n.post_bias) l.load(a.n.post_bias, a.n.elem, b2);
-    if (a.n.scale) l.load(a.n.scale, a.n.elem, s);
-    if (a.n.pre_weight) l.load(a.n.pre_weight, a.n.elem, w1);
-    if (a.n.pre_bias) l.load(a.n.pre_bias, a.n.elem, b1);
+    scaled_post(l, a.n, w2, b2);
+    vector(l, a.n.pre_weight, a.n.elem, 0.0f, w1);
+    vector(l, a.n.pre_bias, a.n.elem, 0.0f, b1);
     for (; first < a.rows; first += step) {
         const int64_t row = min(first + worker, a.rows - 1);
         const bool on = first + worker < a.rows;
@@ -280,7 +296,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, XT* z, HT*
         if (Y) {
             if (a.n.post_weight) deviation(l, sums, a, u, mean2, r2);
 #pragma unroll
-            for (int i = 0; i < L; ++i) v[i] += a.residual * (((u[i] - mean2) * r2 * w2[i] + b2[i]) * s[i] * gate[i]);
+            for (int i = 0; i < L; ++i) v[i] += a.residual * (((u[i] - mean2) * r2 * w2[i] + b2[i]) * gate[i]);
             if (on) l.store(z + row * width, v);
         }
         if (a.n.pre_weight) {
@@ -365,7 +381,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     float held[kAhead ? kSums : 1][L], dg[L];
     auto sum = [&](int k, int i) -> float& {
         if constexpr (kAhead) return held[k][i];
-        else return join[(k * L + i) * blockDim.x + threadIdx.x];
+        else return join[(k * L + i) * 1024 + threadIdx.x];      // 16 waves: a constant stride takes no registers
     };
 #pragma unroll
     for (int k = 0; k < kSums; ++k)
@@ -373,15 +389,15 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         for (int i = 0; i < L; ++i) sum(k, i) = 0.0f;
     fill(dg, 0.0f);
     float w1[L], w2[L], b2[L], s[L], gate[L];
-    auto vector = [&](const void* v, float none, float (&to)[L], bool now) {
+    auto hold = [&](const void* v, float none, float (&to)[L], bool now) {
         if (!now) return;
         fill(to, none);
         if (v) l.load(v, a.n.elem, to);
     };
-    vector(a.n.pre_weight, 0.0f, w1, kAhead);
-    vector(a.n.post_weight, 1.0f, w2, kAhead);
-    vector(a.n.post_bias, 0.0f, b2, kAhead);
-    vector(a.n.scale, 1.0f, s, kAhead);
+    hold(a.n.pre_weight, 0.0f, w1, kAhead);
+    hold(a.n.post_weight, 1.0f, w2, kAhead);
+    hold(a.n.post_bias, 0.0f, b2, kAhead);
+    hold(a.n.scale, 1.0f, s, kAhead);
     fill(gate, 1.0f);
     // every worker goes through as many rounds: they meet at barriers
     for (int64_t k = 0; k < g.split.per; ++k, ++row) {
@@ -405,9 +421,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         if (a.gate) l.load(row_of(a.gate, here / g.split.group_rows, width, a.n.gate_elem), a.n.gate_elem, gate);
         if (kAhead && row + 1 < end) fetch(row + 1);
         if (Y) {
-            vector(a.n.post_weight, 1.0f, w2, !kAhead);
-            vector(a.n.post_bias, 0.0f, b2, !kAhead);
-            vector(a.n.scale, 1.0f, s, !kAhead);
+            hold(a.n.post_weight, 1.0f, w2, !kAhead);
+            hold(a.n.post_bias, 0.0f, b2, !kAhead);
+            hold(a.n.scale, 1.0f, s, !kAhead);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (a.n.post_weight) yn[i] = (yn[i] - st.z) * st.w;
@@ -425,7 +441,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         }
         if (DH) {
             float dot = 0.0f, plain = 0.0f;
-            vector(a.n.pre_weight, 0.0f, w1, !kAhead);
+            hold(a.n.pre_weight, 0.0f, w1, !kAhead);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 z[i] = l.in(i) ? (z[i] - st.x) * st.y : 0.0f;
@@ -446,9 +462,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
         if (on) l.store(static_cast<XT*>(g.dx) + row * width, d);
         if (!Y) continue;
         float dot = 0.0f, plain = 0.0f;
-        vector(a.n.post_weight, 1.0f, w2, !kAhead);
-        vector(a.n.post_bias, 0.0f, b2, !kAhead);
-        vector(a.n.scale, 1.0f, s, !kAhead);
+        hold(a.n.post_weight, 1.0f, w2, !kAhead);
+        hold(a.n.post_bias, 0.0f, b2, !kAhead);
+        hold(a.n.scale, 1.0f, s, !kAhead);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const float t = a.residual * d[i], tg = t * gate[i];
