@@ -54,7 +54,7 @@ int worker_waves(int64_t width, int lane) {
 // The values that a lane holds. Forward: 8 keep more bytes on their way (4096 x
 // 4096 in bf16 27 us, 54 with 4), unless one wave of 4 would do. Backward: 4, as
 // long as 16 waves reach (8192 x 2048 47 us; as many values as 2048 x 8192, with 8,
-// 94 us: its vectors and sums do not fit the registers).
+// 63 us: its vectors and sums do not fit the registers).
 int forward_lane(int64_t width) { return width <= 256 ? 4 : 8; }
 int backward_lane(int64_t width) { return width <= 4096 ? 4 : 8; }
 
@@ -331,7 +331,7 @@ struct NormGrad {
     NormParts parts;
 };
 
-template <typename XT, typename YT, typename HT, int L>
+template <typename XT, typename YT, typename HT, int L, bool GATE>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const NormGrad g) {
     extern __shared__ float join[];                // a row of the worker's columns, or its sums
     __shared__ float2 buf[2][16];
@@ -360,22 +360,16 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     Raw<YT, L> ny = {};
     Raw<HT, L> nh = {};
     float4 next = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-    auto fetch_block = [&](int64_t at) {
+    auto fetch = [&](int64_t at) {
         l.load(X + at * width, nx);
         if (Y) l.load(Y + at * width, ny);
         if (g.stats) next = *reinterpret_cast<const float4*>(g.stats + 4 * at);
-    };
-    auto fetch_grads = [&](int64_t at) {
         if (DZ) l.load(DZ + at * width, nz);
         if (DH) l.load(DH + at * width, nh);
     };
-    auto fetch = [&](int64_t at) {
-        fetch_block(at);
-        fetch_grads(at);
-    };
     // with 8 values a lane 16 waves have no registers for the vectors, for a row
-    // ahead and for the sums: the first two are loaded where they are used, the
-    // sums are in LDS
+    // ahead and for the sums: the vectors are loaded where they are used, a row when
+    // it begins, the sums are in LDS
     constexpr bool kAhead = L == 4;
     if (kAhead) fetch(row < end ? row : 0);
     float held[kAhead ? kSums : 1][L], dg[L];
@@ -403,22 +397,17 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
     for (int64_t k = 0; k < g.split.per; ++k, ++row) {
         const bool on = row < end;
         const int64_t here = on ? row : 0;
-        if (!kAhead) fetch_block(here);
+        if (!kAhead) fetch(here);
         float z[L], yn[L], d[L], dh[L];
         const float4 st = next;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             z[i] = nx.get(i);
             yn[i] = ny.get(i);
+            d[i] = nz.get(i);
+            dh[i] = nh.get(i);
         }
-        if (kAhead) {
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                d[i] = nz.get(i);
-                dh[i] = nh.get(i);
-            }
-        }
-        if (a.gate) l.load(row_of(a.gate, here / g.split.group_rows, width, a.n.gate_elem), a.n.gate_elem, gate);
+        if (GATE && a.gate) l.load(row_of(a.gate, here / g.split.group_rows, width, a.n.gate_elem), a.n.gate_elem, gate);
         if (kAhead && row + 1 < end) fetch(row + 1);
         if (Y) {
             hold(a.n.post_weight, 1.0f, w2, !kAhead);
@@ -428,15 +417,6 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             for (int i = 0; i < L; ++i) {
                 if (a.n.post_weight) yn[i] = (yn[i] - st.z) * st.w;
                 z[i] += a.residual * ((yn[i] * w2[i] + b2[i]) * s[i] * gate[i]);
-            }
-        }
-        if (!kAhead) {
-            asm volatile("" ::: "memory");          // these loads not before that arithmetic
-            fetch_grads(here);
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                d[i] = nz.get(i);
-                dh[i] = nh.get(i);
             }
         }
         if (DH) {
@@ -471,7 +451,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             if (on) {
                 sum(2, i) += tg * yn[i];
                 if (kAhead || a.n.post_bias) sum(3, i) += tg;
-                dg[i] += t * (yn[i] * w2[i] + b2[i]) * s[i];
+                if (GATE) dg[i] += t * (yn[i] * w2[i] + b2[i]) * s[i];
             }
             d[i] = l.in(i) ? tg * s[i] * w2[i] : 0.0f;
             dot += d[i] * yn[i];
@@ -485,7 +465,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormArgs a, const
             for (int i = 0; i < L; ++i) d[i] = st.w * (d[i] - yn[i] * dot - plain);
         }
         if (on) l.store(static_cast<YT*>(g.dy) + row * width, d);
-        if (g.dgate && on && row + 1 == gate_end) {
+        if (GATE && g.dgate && on && row + 1 == gate_end) {
             if (g.split.chunks > 1) l.store(g.parts.gates + id * width, dg);
             else if (a.n.gate_elem == KS_ELEM_BF16) l.store(static_cast<bf16_t*>(g.dgate) + row / g.split.group_rows * width, dg);
             else l.store(static_cast<float*>(g.dgate) + row / g.split.group_rows * width, dg);
@@ -638,7 +618,12 @@ ks_status_t run_norm(const NormArgs& a, void* z, void* h, float* stats, dim3 gri
 
 template <typename XT, typename YT, typename HT, int L>
 ks_status_t run_grad(const NormArgs& a, const NormGrad& g, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
-    return launch_kernel(norm_grad_kernel<XT, YT, HT, L>, grid, block, lds, stream, a, g);
+    // with 8 values a lane the gate and its sum spill registers (2048 x 8192 in bf16
+    // 104 us with a gate, 63 without one; 72 if the kernel had both): a kernel without
+    // them. With 4 values they fit and the same split gains nothing.
+    if constexpr (L == 8)
+        if (!a.gate) return launch_kernel(norm_grad_kernel<XT, YT, HT, L, false>, grid, block, lds, stream, a, g);
+    return launch_kernel(norm_grad_kernel<XT, YT, HT, L, true>, grid, block, lds, stream, a, g);
 }
 
 // f(XT{}, YT{}, HT{}) for the types of n.

@@ -226,6 +226,16 @@ def test_many_rows_a_worker():
         check(p, run(p))
 
 
+@pytest.mark.parametrize("groups", [0, 2, 300, 600])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_widest_rows(kind, groups):
+    """More rows than workers where a row takes 16 waves of 8 values a lane."""
+    require_gpu()
+    for width, y in ((5001, F32), (8192, BF16)):
+        p = make(600, width, kind, groups=groups, y=y, seed=groups + width)
+        check(p, run(p))
+
+
 PARTS = [dict(post=False), dict(scale=False), dict(bias=False), dict(pre=False), dict(pre=False, post=False),
          dict(post=False, scale=False, groups=0), dict(y=None, post=False, scale=False), dict(y=None)]
 
