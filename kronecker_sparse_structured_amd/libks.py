@@ -1003,10 +1003,11 @@ class Beams(NamedTuple):
 
 def beam_select(logits, scores, beams=None, done=None, lengths=None, eos=None, length_penalty=0.0, stream=None):
     """The best `beams` (default: as many as there are) continuations of each
-    request's beams, as a Beams. logits (R, W, V) fp32 or bf16 with any row
-    strides; scores (R, W) fp32, -inf for a beam that is not there; done (R, W)
-    bool: beams that ended and go on as they are; lengths (R, W) int32. Ranked by
-    score / max(length, 1)^length_penalty, equal ones by beam and token."""
+    request's beams, as a Beams. logits (R, W, V) fp32 or bf16, rows any distance
+    apart that do not overlap; scores (R, W) fp32, -inf for a beam that is not
+    there; done (R, W) bool: beams that ended and go on as they are; lengths (R, W)
+    int32. Ranked by score / max(length, 1)^length_penalty, equal ones by beam and
+    token."""
     import torch
     if logits.dim() != 3:
         raise ValueError("logits must be (requests, beams, vocab)")
