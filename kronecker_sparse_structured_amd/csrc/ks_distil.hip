@@ -14,14 +14,17 @@
 // exponentials are kept in one pass, as in ks_preference.hip.
 //
 // The gradient goes out in two steps: the whole row as if there were no entries, in
-// 16-byte nontemporal stores (8192 rows of 50257 in bf16 338 us, 352 with ordinary
+// 16-byte nontemporal stores (8192 rows of 50257 in bf16 329 us, 333 with ordinary
 // ones), and behind a barrier the few values at the entries' and the label's tokens
 // again.
 //
 // What bounds it: the row's read and write. 8192 rows of 50257 in bf16 (1.65 GB)
-// with one exponential a value 320 us, 5.1 TB/s, a device copy of as much 320;
-// with two, 338 to 373: there the exponentials' arithmetic shows. In fp32, 8192 rows
-// of 32000 (2.1 GB), 398 us either way.
+// with one exponential a value 312 us, 5.3 TB/s, a device copy of as much 320;
+// with two, 329 to 360: there the exponentials' arithmetic shows. In fp32, 8192 rows
+// of 32000 (2.1 GB), 393 us either way. What a row needs beside its vectors (its
+// entries, what lies before and behind them) is on its way with them: a load whose
+// value is converted in a branch is waited for in that branch (8192 rows of 16000 in
+// bf16 109 us, 124 with such loads).
 
 #include <algorithm>
 #include <cmath>
@@ -35,6 +38,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxTop = KS_TEACHER_MAX_COUNT;
+// Positions up to which each workgroup counts the unmasked ones itself (a launch
+// less): 2 to 8 labels a thread.
+constexpr int kCountRows = 2048;
 static_assert(kMaxTop <= kThreads, "an entry a thread");
 
 // 16 bytes of values that no maximum and no sum sees.
@@ -117,19 +123,45 @@ struct Entry {
     float q, logq;
 };
 
+__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t bits_of(bf16_t x) { return x; }
+template <typename T>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+    return __uint_as_float(sizeof(T) == 4 ? bits : bits << 16);
+}
+
+// Entry k of a row as it is loaded, with nothing that depends on the values: the
+// loads stay on their way (what is converted in a branch is waited for there).
+// Both words of an id and both halves of a value, of the short types the same twice.
+struct RawEntry {
+    uint32_t lo, hi, first, second;
+};
+__device__ __forceinline__ RawEntry ask_entry(const DistilArgs& a, int64_t s, int64_t t, int k) {
+    k = min(k, a.t.count - 1);
+    const int64_t i = s * a.t.id_seq_stride + t * a.t.id_row_stride + k;
+    const int64_t v = s * a.t.top_seq_stride + t * a.t.top_row_stride + k;
+    const int iw = a.t.id_bytes / 4, vw = a.t.elem == KS_ELEM_BF16 ? 1 : 2;
+    const uint32_t* ids = static_cast<const uint32_t*>(a.t.ids) + i * iw;
+    const uint16_t* top = static_cast<const uint16_t*>(a.t.top) + v * vw;
+    return {ids[0], ids[iw - 1], top[0], top[vw - 1]};
+}
+__device__ __forceinline__ int64_t id_of(const DistilArgs& a, const RawEntry& e) {
+    return a.t.id_bytes == 8 ? static_cast<int64_t>(static_cast<uint64_t>(e.hi) << 32 | e.lo) : static_cast<int32_t>(e.lo);
+}
+__device__ __forceinline__ float top_of(const DistilArgs& a, const RawEntry& e) {
+    const uint32_t high = e.second << 16;
+    return __uint_as_float(a.t.elem == KS_ELEM_BF16 ? high : high | e.first);
+}
+
 // buf: 2 kWaves values.
 __device__ __forceinline__ Entry teacher_entry(const DistilArgs& a, int64_t s, int64_t t, float* buf) {
     Entry e{-1, 0.0f, 0.0f};
     const int k = threadIdx.x, wave = k / 64;
     float v = -INFINITY;
     if (k < a.t.count) {
-        const int64_t at = s * a.t.id_seq_stride + t * a.t.id_row_stride + k;
-        e.id = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[at] : static_cast<const int32_t*>(a.t.ids)[at];
-        if (e.id >= 0) {
-            const int64_t from = s * a.t.top_seq_stride + t * a.t.top_row_stride + k;
-            v = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[from])
-                                         : static_cast<const float*>(a.t.top)[from];
-        }
+        const RawEntry raw = ask_entry(a, s, t, k);
+        e.id = id_of(a, raw);
+        if (e.id >= 0) v = top_of(a, raw);
     }
     float m = wave_max(v);
     if (k % 64 == 0) buf[wave] = m;
@@ -180,9 +212,9 @@ __device__ __forceinline__ double count_rows(const ks_logits_t& x) {
     for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
         int64_t label[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) label[u] = i0 + 1024 * u < n ? label_at(x, i0 + 1024 * u) : -1;
+        for (int u = 0; u < U; ++u) label[u] = label_at(x, min(i0 + 1024 * u, n - 1));
 #pragma unroll
-        for (int u = 0; u < U; ++u) count += label[u] >= 0;
+        for (int u = 0; u < U; ++u) count += i0 + 1024 * u < n && label[u] >= 0;
     }
     return group_sum(static_cast<double>(count));
 }
@@ -200,20 +232,22 @@ template <bool COUNT>
 __global__ __launch_bounds__(1024) void distil_sum_kernel(const ks_logits_t x, const float* tokens, float* inv,
                                                           float* loss) {
     const int64_t n = x.sequences * x.tokens;
+    const float given = COUNT ? 0.0f : *inv;       // on its way beside the tokens
     double s = 0.0;
     constexpr int U = 8;
     for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
         float v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = i0 + 1024 * u < n ? tokens[i0 + 1024 * u] : 0.0f;
+        for (int u = 0; u < U; ++u) v[u] = tokens[min(i0 + 1024 * u, n - 1)];
 #pragma unroll
-        for (int u = 0; u < U; ++u) s += static_cast<double>(v[u]);
+        for (int u = 0; u < U; ++u) s += i0 + 1024 * u < n ? static_cast<double>(v[u]) : 0.0;
     }
     const double count = COUNT ? count_rows(x) : 0.0;
     s = group_sum(s);
     if (threadIdx.x != 0) return;
-    if (COUNT) *inv = inverse_of(count);
-    *loss = static_cast<float>(s * static_cast<double>(*inv));
+    const float scale = COUNT ? inverse_of(count) : given;
+    if (COUNT) *inv = scale;
+    *loss = static_cast<float>(s * static_cast<double>(scale));
 }
 
 // A running maximum with its two sums: exp((x - m) / T), and exp(x - m) if TWO.
@@ -317,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
 
 // The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
 // not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
-// as the square of the first (8192 rows of 50257 in bf16 338 us, 373 otherwise).
+// as the square of the first (8192 rows of 50257 in bf16 329 us, 360 otherwise).
 enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
 
 // dx of one row: first as if there were no entries, then the values at the
@@ -457,23 +491,19 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         for (int v = tid; v < vecs; v += NT) __builtin_nontemporal_store(none, &obody[v]);
         return;
     }
-    // the entries' ids first: what follows from them is asked for behind the row
+    // the entries first: what follows from them is asked for behind the row
     const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
     int64_t id[EN];
     float top[EN], xe[EN];
+    RawEntry raw[EN] = {};
 #pragma unroll
-    for (int n = 0; n < EN; ++n) {
-        const int k = n * NT + tid;
-        id[n] = -1;
-        top[n] = -INFINITY;
-        xe[n] = 0.0f;
-        if (kl && k < entries) {
-            const int64_t from = s * a.t.id_seq_stride + t * a.t.id_row_stride + k;
-            id[n] = a.t.id_bytes == 8 ? static_cast<const int64_t*>(a.t.ids)[from] : static_cast<const int32_t*>(a.t.ids)[from];
-            const int64_t where = s * a.t.top_seq_stride + t * a.t.top_row_stride + k;
-            top[n] = a.t.elem == KS_ELEM_BF16 ? to_f32(static_cast<const bf16_t*>(a.t.top)[where])
-                                              : static_cast<const float*>(a.t.top)[where];
-        }
+    for (int n = 0; n < EN; ++n)
+        if (n * NT + wave * 64 < entries) raw[n] = ask_entry(a, s, t, n * NT + tid);
+    uint32_t rh = 0, rt = 0, rl = 0;
+    if (wave == 0) {
+        rh = bits_of(row[min(tid, V - 1)]);
+        rt = bits_of(row[min(tail + tid, V - 1)]);
+        rl = bits_of(row[label >= 0 && label < V ? label : 0]);
     }
     // the row
     u32x4 w[U];
@@ -483,24 +513,21 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         w[u] = lowest<T>();
         if (v < vecs) w[u] = *reinterpret_cast<const access*>(row + head + v * E);
     }
-    const float xh = tid < head ? to_f32(row[tid]) : -INFINITY, xt = tid < V - tail ? to_f32(row[tail + tid]) : -INFINITY;
-    const float xl = tid == 0 && ce && label >= 0 ? to_f32(row[label < V ? label : 0]) : 0.0f;
-#pragma unroll
-    for (int n = 0; n < EN; ++n) {
-        if (id[n] < 0) top[n] = -INFINITY;
-        else if (id[n] < V) xe[n] = to_f32(row[id[n]]);
-    }
     for (int i = tid; i < (V + 31) / 32; i += NT) seen[i] = 0;
     if (tid == 0) twice = label_in = 0;
     int count = 0;
     if (COUNT) {
         const int n = static_cast<int>(a.x.sequences * a.x.tokens);
-        for (int i = tid; i < n; i += NT) count += label_at(a.x, i) >= 0;
+        int64_t labels[kCountRows / NT];
+#pragma unroll
+        for (int k = 0; k < kCountRows / NT; ++k) labels[k] = label_at(a.x, min(k * NT + tid, n - 1));
+#pragma unroll
+        for (int k = 0; k < kCountRows / NT; ++k) count += k * NT + tid < n && labels[k] >= 0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) count += __shfl_xor(count, d, 64);
     }
     // maxima
-    float m = fmaxf(fmaxf(xh, xt), kLowest), tm = -INFINITY;
+    float m = kLowest, tm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float x[E];
@@ -508,8 +535,21 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
 #pragma unroll
         for (int i = 0; i < E; ++i) m = fmaxf(m, x[i]);
     }
+    // what came beside the row: not looked at before, in whatever order it is built
+    asm volatile("" : "+v"(rh), "+v"(rt), "+v"(rl));
+    const float xh = tid < head ? value_of<T>(rh) : -INFINITY, xt = tid < V - tail ? value_of<T>(rt) : -INFINITY;
+    float xl = value_of<T>(rl);
+    m = fmaxf(m, fmaxf(xh, xt));
+    // the logits at the entries are on their way through the sums
+    uint32_t re[EN] = {};
 #pragma unroll
-    for (int n = 0; n < EN; ++n) tm = fmaxf(tm, top[n]);
+    for (int n = 0; n < EN; ++n) {
+        asm volatile("" : "+v"(raw[n].lo), "+v"(raw[n].hi), "+v"(raw[n].first), "+v"(raw[n].second));
+        id[n] = kl && n * NT + tid < entries ? id_of(a, raw[n]) : -1;
+        top[n] = id[n] < 0 ? -INFINITY : top_of(a, raw[n]);
+        tm = fmaxf(tm, top[n]);
+        if (n * NT + wave * 64 < entries) re[n] = bits_of(row[id[n] >= 0 && id[n] < V ? id[n] : 0]);
+    }
     m = wave_max(m);
     tm = wave_max(tm);
     if (tid % 64 == 0) {
@@ -567,6 +607,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         for (int i = 0; i < E; ++i) add(x[i], part, part1);
         sum += part;
         sum1 += part1;
+    }
+    // here at the latest: behind the barrier the gradient may take the logits' place
+#pragma unroll
+    for (int n = 0; n < EN; ++n) {
+        asm volatile("" : "+v"(re[n]));
+        xe[n] = value_of<T>(re[n]);
     }
     sum = wave_sum32(sum);
     if (TWO) sum1 = wave_sum32(sum1);
@@ -744,10 +790,6 @@ ks_status_t launch_distil_grad(const ks_logits_t& x, const ks_teacher_t& t, cons
 
 namespace {
 
-// Positions up to which each workgroup counts the unmasked ones itself (a launch
-// less): 2 to 8 labels a thread.
-constexpr int64_t kCountRows = 2048;
-
 template <typename T, int MODE, int NT, int U, bool COUNT>
 ks_status_t run_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv, float* stats, void* d, int64_t d_seq, int64_t d_row,
                      hipStream_t stream) {
@@ -779,7 +821,7 @@ ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv,
 
 // With a gradient as long as registers reach. The loss alone up to 32768 values:
 // of longer rows a workgroup that goes through the row keeps more bytes on their way
-// (8192 rows of 50257 in bf16 150 us, 173 held; 4096 rows of 32000 in fp32 75 us, 69 held).
+// (8192 rows of 50257 in bf16 156 us, 187 held; 4096 rows of 32000 in fp32 100 us, 95 held).
 bool distil_holds(const ks_logits_t& x, bool gradient) {
     return gradient ? x.vocab / (x.elem == KS_ELEM_BF16 ? 8 : 4) <= 16384 : x.vocab <= 32768;
 }
