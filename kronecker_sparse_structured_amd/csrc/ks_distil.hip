@@ -204,50 +204,39 @@ __device__ __forceinline__ double group_sum(double x) {
     return total;
 }
 
-// The unmasked positions, in thread 0.
-__device__ __forceinline__ double count_rows(const ks_logits_t& x) {
-    const int64_t n = x.sequences * x.tokens;
-    int count = 0;
-    constexpr int U = 8;
-    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
-        int64_t label[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) label[u] = label_at(x, min(i0 + 1024 * u, n - 1));
-#pragma unroll
-        for (int u = 0; u < U; ++u) count += i0 + 1024 * u < n && label[u] >= 0;
-    }
-    return group_sum(static_cast<double>(count));
-}
-
 __device__ __forceinline__ float inverse_of(double count) { return static_cast<float>(1.0 / fmax(count, 1.0)); }
 
-// inv = 1 / (unmasked positions), at least one.
-__global__ __launch_bounds__(1024) void distil_count_kernel(const ks_logits_t x, float* inv) {
-    const double count = count_rows(x);
-    if (threadIdx.x == 0) *inv = inverse_of(count);
-}
-
-// loss = the tokens' sum times inv, which is formed here where COUNT.
-template <bool COUNT>
+// SUM: loss = the tokens' sum times inv. COUNT: inv = 1 / (unmasked positions), at
+// least one, before that. Of one workgroup: what it reads is asked for 8 at a time.
+template <bool SUM, bool COUNT>
 __global__ __launch_bounds__(1024) void distil_sum_kernel(const ks_logits_t x, const float* tokens, float* inv,
                                                           float* loss) {
     const int64_t n = x.sequences * x.tokens;
-    const float given = COUNT ? 0.0f : *inv;       // on its way beside the tokens
+    const float given = COUNT ? 0.0f : *inv;
     double s = 0.0;
+    int count = 0;
     constexpr int U = 8;
     for (int64_t i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
         float v[U];
+        int64_t label[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = tokens[min(i0 + 1024 * u, n - 1)];
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = min(i0 + 1024 * u, n - 1);
+            v[u] = SUM ? tokens[i] : 0.0f;
+            label[u] = COUNT ? label_at(x, i) : 0;
+        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) s += i0 + 1024 * u < n ? static_cast<double>(v[u]) : 0.0;
+        for (int u = 0; u < U; ++u) {
+            const bool in = i0 + 1024 * u < n;
+            s += in ? static_cast<double>(v[u]) : 0.0;
+            count += in && label[u] >= 0;
+        }
     }
-    const double count = COUNT ? count_rows(x) : 0.0;
-    s = group_sum(s);
+    const float scale = COUNT ? inverse_of(group_sum(static_cast<double>(count))) : given;
+    if (SUM) s = group_sum(s);
     if (threadIdx.x != 0) return;
-    const float scale = COUNT ? inverse_of(count) : given;
     if (COUNT) *inv = scale;
-    *loss = static_cast<float>(s * static_cast<double>(scale));
+    if (SUM) *loss = static_cast<float>(s * static_cast<double>(scale));
 }
 
 // A running maximum with its two sums: exp((x - m) / T), and exp(x - m) if TWO.
@@ -491,11 +480,19 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         for (int v = tid; v < vecs; v += NT) __builtin_nontemporal_store(none, &obody[v]);
         return;
     }
-    // the entries first: what follows from them is asked for behind the row
     const bool kl = a.kl > 0.0, ce = a.ce > 0.0;
     int64_t id[EN];
     float top[EN], xe[EN];
     RawEntry raw[EN] = {};
+    // the row, then what else it needs (before it: 4096 rows of 32000 in fp32, the loss
+    // alone, 96 us for 94)
+    u32x4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = u * NT + tid;
+        w[u] = lowest<T>();
+        if (v < vecs) w[u] = *reinterpret_cast<const access*>(row + head + v * E);
+    }
 #pragma unroll
     for (int n = 0; n < EN; ++n)
         if (n * NT + wave * 64 < entries) raw[n] = ask_entry(a, s, t, n * NT + tid);
@@ -504,14 +501,6 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         rh = bits_of(row[min(tid, V - 1)]);
         rt = bits_of(row[min(tail + tid, V - 1)]);
         rl = bits_of(row[label >= 0 && label < V ? label : 0]);
-    }
-    // the row
-    u32x4 w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int v = u * NT + tid;
-        w[u] = lowest<T>();
-        if (v < vecs) w[u] = *reinterpret_cast<const access*>(row + head + v * E);
     }
     for (int i = tid; i < (V + 31) / 32; i += NT) seen[i] = 0;
     if (tid == 0) twice = label_in = 0;
@@ -737,12 +726,12 @@ int exps_of(const Distil& o) {
 }  // namespace
 
 ks_status_t launch_distil_count(const ks_logits_t& x, float* inv, hipStream_t stream) {
-    return launch_kernel(distil_count_kernel, dim3(1), dim3(1024), 0, stream, x, inv);
+    return launch_kernel(distil_sum_kernel<false, true>, dim3(1), dim3(1024), 0, stream, x, nullptr, inv, nullptr);
 }
 
 ks_status_t launch_distil_sum(const ks_logits_t& x, const float* tokens, float* inv, bool count, float* loss,
                               hipStream_t stream) {
-    return launch_kernel(count ? distil_sum_kernel<true> : distil_sum_kernel<false>, dim3(1), dim3(1024), 0, stream, x,
+    return launch_kernel(count ? distil_sum_kernel<true, true> : distil_sum_kernel<true, false>, dim3(1), dim3(1024), 0, stream, x,
                          tokens, inv, loss);
 }
 
