@@ -246,8 +246,8 @@ def make_distillation_function():
 
         @staticmethod
         def forward(ctx, logits, labels, ids, top, weight, temperature):
-            loss, tokens, stats = libks._on_device(logits.get_device(), libks._distil_forward, logits, labels, ids, top,
-                                                   weight, temperature)
+            loss, tokens, stats, _ = libks._on_device(logits.get_device(), libks._distil_forward, logits, labels, ids,
+                                                      top, weight, temperature)
             ctx.save_for_backward(logits, labels, ids, top, stats)
             ctx.options = weight, temperature
             ctx.mark_non_differentiable(tokens)

@@ -925,33 +925,37 @@ def _preference_backward(logits, labels, scratch, upstream):
 
 def _teacher(ids, top, logits) -> ks_teacher_t:
     import torch
-    if ids.dim() != 3 or ids.shape != top.shape or ids.shape[:2] != logits.shape[:2]:
+    shape, (S, T, _), at = ids.shape, logits.shape, logits.get_device()
+    if len(shape) != 3 or shape != top.shape or shape[0] != S or shape[1] != T:
         raise ValueError("ids and top must be (sequences, tokens, count)")
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
-    if ids.get_device() != logits.get_device() or top.get_device() != logits.get_device():
+    if ids.get_device() != at or top.get_device() != at:
         raise ValueError("ids and top must be on the logits' device")
-    return ks_teacher_t(ids.data_ptr(), top.data_ptr(), *_layout(ids, "ids"), *_layout(top, "top"), ids.shape[2],
+    return ks_teacher_t(ids.data_ptr(), top.data_ptr(), *_layout(ids, "ids"), *_layout(top, "top"), shape[2],
                         ids.element_size(), _elem(top.dtype, "top"), 0)
 
 
-def _distil_forward(logits, labels, ids, top, weight, temperature, dlogits=None):
-    """(loss, tokens, stats): stats as ks_distil_backward reads them."""
+def _distil_forward(logits, labels, ids, top, weight, temperature, grad=False, dlogits=None):
+    """(loss, tokens, stats, dlogits): without a gradient stats as
+    ks_distil_backward reads them."""
     import torch
     x = _logits(logits, labels)
     t = _teacher(ids, top, logits)
-    d_seq = d_row = 0
+    S, T, d_row = logits.shape
+    d_seq = T * d_row
     if dlogits is not None:
         if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype \
                 or dlogits.get_device() != logits.get_device():
             raise ValueError("dlogits must have the logits' shape, type and device")
         d_seq, d_row = _layout(dlogits, "dlogits")
-    S, T = x.sequences, x.tokens
+    elif grad:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
     tokens, stats = loss.new_empty(S, T), loss.new_empty(3 * S * T + 1)
     _raise(load().ks_distil_loss(x, t, weight, temperature, loss.data_ptr(), tokens.data_ptr(), stats.data_ptr(),
                                  _ptr(dlogits), d_seq, d_row, _raw_stream(logits.get_device())), "ks_distil_loss", True)
-    return loss, tokens, stats
+    return loss, tokens, stats, dlogits
 
 
 def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0, dlogits=None, grad=True, stream=None):
@@ -963,7 +967,6 @@ def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0, dlo
     does not mask (negative). logits (S, T, V) fp32 or bf16. dlogits may be given
     (the logits themselves too: then it replaces them); with grad=False there is
     none."""
-    import torch
     if stream is not None:
         _logits(logits, labels)
         return _on_stream(stream, logits.device, distillation_loss, logits, labels, ids, top, weight, temperature,
@@ -971,10 +974,8 @@ def distillation_loss(logits, labels, ids, top, weight=1.0, temperature=1.0, dlo
     given = dlogits is not None
     if given and not grad:
         raise ValueError("dlogits is given, but grad is not asked for")
-    if grad and not given:
-        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
-    loss, tokens, _ = _on_device(logits.get_device(), _distil_forward, logits, labels, ids, top, weight, temperature,
-                                 dlogits)
+    loss, tokens, _, dlogits = _on_device(logits.get_device(), _distil_forward, logits, labels, ids, top, weight,
+                                          temperature, grad, dlogits)
     if given:
         _wrote(dlogits)
     return loss, tokens, dlogits
