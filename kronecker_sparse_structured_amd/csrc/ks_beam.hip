@@ -25,7 +25,7 @@
 // What bounds it: many rows the arithmetic of the first launch beside its reads
 // (32 x 16 beams of 32000 in fp32, 66 MB, 17 us, and 64 x 4 of 50257 in bf16, 26 MB,
 // 10 us: 3.9 and 2.6 TB/s), few rows the two launches' latency, 6 us each. The second
-// launch is a chain of dependent steps, 6 us for 4 beams and 13 for 16.
+// launch is a chain of dependent steps, 6 us for 4 beams and 11 for 16.
 
 #include <algorithm>
 
@@ -71,10 +71,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
     x = max_with<0x142, 0xa>(x);
     x = max_with<0x143, 0xc>(x);
     return __builtin_amdgcn_readlane(x, 63);
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
-    const uint32_t hi = wave_max(static_cast<uint32_t>(x >> 32));
-    return static_cast<uint64_t>(hi) << 32 | wave_max(static_cast<uint32_t>(x >> 32) == hi ? static_cast<uint32_t>(x) : 0u);
 }
 
 // The upper BITS bits of the keep-th largest of the lanes' x, the others 0: bit by
@@ -216,6 +212,10 @@ __device__ __forceinline__ uint64_t ordered(double x) {
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
+__device__ __forceinline__ double beam_score(double base, double total, uint64_t key) {
+    return base - log(total) + static_cast<double>(value_of(static_cast<uint32_t>(key >> 32)));
+}
+
 // The best candidates of one request: a wave joins a beam's slices, all rank the
 // beams' candidates, and the first picks.
 __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_beams_t x, Slices s, BeamOut out,
@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
     uint64_t* best = lds;                                             // W x keep
     uint64_t* ranks = best + W * keep;                                // W x keep
     uint64_t* list = ranks + W * keep + wave * keep * kJoinHold;
-    __shared__ double base[kMaxBeams], divisor[kMaxBeams];            // score = base + x, rank = score / divisor
+    // score = base + x - log total, rank = score / divisor
+    __shared__ double base[kMaxBeams], total[kMaxBeams], divisor[kMaxBeams];
     __shared__ int length[kMaxBeams], chosen[kMaxBeams];
     const int64_t request = request0 + blockIdx.x;
     for (int w = wave; w < W; w += waves) {
@@ -235,7 +236,6 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         // whose score is not finite, has written nothing, and it is not used)
         const float score = x.scores[row];
         const bool done = x.done && x.done[row];
-        const int len = x.lengths ? x.lengths[row] + (done ? 0 : 1) : 0;
         const uint64_t* keys = s.keys + row * s.slices * keep;
         const int n = s.slices * keep;
         uint64_t mine[kJoinHold];
@@ -246,9 +246,16 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         }
         const float2* st = s.stats + row * s.slices;
         const float2 own = lane < s.slices ? st[lane] : make_float2(kLowest, 0.0f);
-        // while the keys are on their way
-        const double power = x.length_penalty == 0.0 ? 1.0 : pow(static_cast<double>(max(len, 1)), x.length_penalty);
-        double shift = 0.0;
+        // while the keys are on their way: one wave for all beams, since 16 waves that take
+        // a power (or a logarithm: below) each are in each other's way (32 x 16 beams 26 us
+        // for 27.6)
+        if (w == waves - 1 && lane < W) {
+            const int64_t beam = request * W + lane;
+            const int len = x.lengths ? x.lengths[beam] + (x.done && x.done[beam] ? 0 : 1) : 0;
+            length[lane] = len;
+            divisor[lane] = x.length_penalty == 0.0 ? 1.0 : pow(static_cast<double>(max(len, 1)), x.length_penalty);
+        }
+        double shift = 0.0, all = 1.0;
         bool live = finite(score);
         if (done || !live) {
             for (int i = lane; i < keep; i += 64)
@@ -261,7 +268,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
             for (int i = 64 + lane; i < s.slices; i += 64)
                 sum += static_cast<double>(st[i].y) * exp(static_cast<double>(st[i].x) - top);
             sum = wave_sum(sum);
-            shift = -top - log(sum);
+            shift = -top;
+            all = sum;
             live = live && sum > 0.0 && sum - sum == 0.0;
             // the slices' keys, as many at a time as the list has room for beside
             // the best of those before
@@ -274,8 +282,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
                     if (first > 0) mine[u] = i < n ? keys[i] : 0;
                     high = max(high, mine[u]);
                 }
-                // as in a slice: by the values alone, and with the tokens if too many reach it
-                uint64_t least = static_cast<uint64_t>(bound_of<32>(static_cast<uint32_t>(high >> 32), keep)) << 32;
+                // as in a slice: by 16 bits of the values, and with the tokens if too many reach it
+                uint64_t least = static_cast<uint64_t>(bound_of<16>(static_cast<uint32_t>(high >> 32), keep)) << 32;
                 const int most = keep * kJoinHold;
                 auto collect = [&]() {
                     int count = 0;
@@ -296,16 +304,16 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
         }
         if (lane == 0) {
             base[w] = live ? static_cast<double>(score) + shift : -INFINITY;
-            length[w] = len;
-            divisor[w] = power;
+            total[w] = all;
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < W * keep; i += blockDim.x) {
         const uint64_t k = best[i];
-        const double score = base[i / keep] + static_cast<double>(value_of(static_cast<uint32_t>(k >> 32)));
+        const int w = i / keep;
+        const double score = beam_score(base[w], total[w], k);
         // no candidate: below every rank
-        ranks[i] = k != 0 && base[i / keep] > -INFINITY && score > -INFINITY ? ordered(score / divisor[i / keep]) : 0;
+        ranks[i] = k != 0 && base[w] > -INFINITY && score > -INFINITY ? ordered(score / divisor[w]) : 0;
     }
     __syncthreads();
     if (wave != 0) return;
@@ -314,9 +322,15 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
     int at = 0, found = 0;
     uint64_t rank = lane < W ? mine[0] : 0, after = lane < W && keep > 1 ? mine[1] : 0;
     for (; found < out.beams; ++found) {
-        const uint64_t high = wave_max(rank);
+        // by their upper halves, and by the lower ones where those are equal
+        const uint32_t upper = static_cast<uint32_t>(rank >> 32), high = wave_max(upper);
         if (high == 0) break;                                         // none is left
-        if (lane == __ffsll(__ballot(rank == high)) - 1) {            // the lowest beam of equal rank
+        unsigned long long best_lanes = __ballot(upper == high);
+        if (best_lanes & (best_lanes - 1)) {
+            const uint32_t lower = upper == high ? static_cast<uint32_t>(rank) : 0, most = wave_max(lower);
+            best_lanes &= __ballot(lower == most);
+        }
+        if (lane == __ffsll(best_lanes) - 1) {                        // the lowest beam of equal rank
             chosen[found] = lane * keep + at;
             ++at;
             rank = after;
@@ -330,7 +344,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
     const int pick = is ? chosen[lane] : 0, w = pick / keep;
     const uint64_t k = best[pick];
     const int64_t token = is ? static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(k)) : x.eos >= 0 ? x.eos : 0;
-    out.scores[to] = is ? static_cast<float>(base[w] + static_cast<double>(value_of(static_cast<uint32_t>(k >> 32)))) : -INFINITY;
+    out.scores[to] = is ? static_cast<float>(beam_score(base[w], total[w], k)) : -INFINITY;
     out.tokens[to] = token;
     out.parents[to] = is ? w : 0;
     if (out.done) out.done[to] = !is || token == x.eos;

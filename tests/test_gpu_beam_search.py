@@ -162,6 +162,22 @@ def test_sorted_and_constant_rows_fill_the_lists():
               gaps(x, scores, None, None, None, 0.0, K))
 
 
+def test_scores_a_step_apart():
+    """Ranks that differ in the last bits of an fp32 score alone; two are equal."""
+    require_gpu()
+    V = 3000
+    x = (-torch.arange(V, dtype=torch.float32)).expand(1, 4, V).contiguous().to(DEV)
+    s = torch.tensor([-1.0])
+    up, down = torch.nextafter(s, s + 1), torch.nextafter(s, s - 1)
+    for order in ([s, down, up, s], [down, s, s, up], [up, up, down, s], [down, down, down, down]):
+        scores = torch.cat(order)[None].to(DEV)
+        want = sorted(range(4), key=lambda w: (-float(order[w]), w))
+        got = libks.beam_select(x, scores, 8)
+        assert got.parents[0].tolist() == want + want
+        assert got.tokens[0].tolist() == [0] * 4 + [1] * 4
+        assert bool((got.scores[0, :-1] >= got.scores[0, 1:]).all())
+
+
 def test_beams_that_ended():
     require_gpu()
     x, scores, done, lengths = draw(6, 5, 700, BF16, seed=5)
