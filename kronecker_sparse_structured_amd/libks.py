@@ -1216,9 +1216,11 @@ class ResidualNorm:
         if keep:
             stats = x.new_empty((rows, 4), dtype=torch.float32)
         if y is not None or self._pre:
-            _raise(self._lib.ks_residual_norm(n, x.data_ptr(), _ptr(y), _ptr(gate) if groups else None, groups, _ptr(z),
-                                              _ptr(h), _ptr(stats), rows, _raw_stream(x.get_device())),
-                   "ks_residual_norm", True)
+            _raise(self._lib.ks_residual_norm(n, x.data_ptr(), None if y is None else y.data_ptr(),
+                                              gate.data_ptr() if groups else None, groups,
+                                              None if z is None else z.data_ptr(), None if h is None else h.data_ptr(),
+                                              None if stats is None else stats.data_ptr(), rows,
+                                              _raw_stream(x.get_device())), "ks_residual_norm", True)
         z = x if y is None else z
         return (z, h, stats) if keep else (z, h)
 
@@ -1234,15 +1236,18 @@ class ResidualNorm:
     def _backward(self, dz, dh, x, y, stats, gate, weights):
         import torch
         rows, groups, n = self._rows(x, y, gate)
-        if dz is not None:
-            _check_out(dz, tuple(x.shape), x.dtype, x.device, "dz")
+        like, f32, at, shape = torch.empty_like, torch.float32, x.get_device(), x.shape
+        if dz is not None and (dz.shape != shape or dz.dtype is not x.dtype or dz.get_device() != at
+                               or not dz.is_contiguous()):
+            raise ValueError("dz must be contiguous, with x's shape, type and device")
         if dh is not None:
             if not self._pre:
                 raise ValueError("dh is given, but there is no pre norm")
             n.h_elem = _elem(dh.dtype, "dh")
-            _check_out(dh, tuple(x.shape), dh.dtype, x.device, "dh")
-        _check_out(stats, (rows, 4), torch.float32, x.device, "stats")
-        like, f32 = torch.empty_like, torch.float32
+            if dh.shape != shape or dh.get_device() != at or not dh.is_contiguous():
+                raise ValueError("dh must be contiguous, with x's shape and device")
+        if stats.shape != (rows, 4) or stats.dtype is not f32 or stats.get_device() != at or not stats.is_contiguous():
+            raise ValueError("stats must be contiguous (%d, 4) fp32 on x's device" % rows)
         dx = like(x)
         dy = like(y) if y is not None else None
         dgate = like(gate) if gate is not None else None
@@ -1257,10 +1262,14 @@ class ResidualNorm:
                 self._sizes.clear()
             size = self._sizes[rows, groups] = need.value
         ws = x.new_empty(size // 4, dtype=f32) if size else None
+        # addresses in place: a call of _ptr for each costs as much as an allocation
         _raise(self._lib.ks_residual_norm_backward(
-            n, _ptr(dz), _ptr(dh), x.data_ptr(), _ptr(y), _ptr(gate) if groups else None, groups, stats.data_ptr(),
-            dx.data_ptr(), _ptr(dy), ks_residual_norm_grads_t(*map(_ptr, grads)), _ptr(dgate) if groups else None, rows,
-            _ptr(ws), size, _raw_stream(x.get_device())), "ks_residual_norm_backward", True)
+            n, None if dz is None else dz.data_ptr(), None if dh is None else dh.data_ptr(), x.data_ptr(),
+            None if y is None else y.data_ptr(), gate.data_ptr() if groups else None, groups, stats.data_ptr(),
+            dx.data_ptr(), None if dy is None else dy.data_ptr(),
+            ks_residual_norm_grads_t(*[None if t is None else t.data_ptr() for t in grads]),
+            dgate.data_ptr() if groups else None, rows, None if ws is None else ws.data_ptr(), size, _raw_stream(at)),
+            "ks_residual_norm_backward", True)
         return (dx, dy, dgate, *grads)
 
 
