@@ -23,12 +23,12 @@
 // vectors stay in registers from row to row and the next row is on its way while
 // this one's sums are formed.
 //
-// What bounds it: memory. Forward 16384 x 1024 (fp32 in, bf16 h, 235 MB) 37 us, 6.3
-// TB/s with the last cache's help; 4096 x 4096 in bf16 (101 MB) 26 us, 3.9 TB/s: two
-// bytes a value keep too few on their way (a second row ahead 26 us there, but 43 for
-// 39 in fp32). Backward 25216 x 384 in fp32 with a gate of 197 rows (232 MB) 47 us,
-// 4.9 TB/s; 4096 x 4096 in bf16 (201 MB) 43 us, 4.7 TB/s. The parts' launch takes 5
-// to 6 us.
+// What bounds it: memory, at the rate of a large copy (4.9 TB/s) or, with the last
+// cache's help, above it. Forward 16384 x 1024 (fp32 in, bf16 h, 235 MB) 36 us, 6.5
+// TB/s; 4096 x 4096 in bf16 (134 MB) 26 us, 5.2 TB/s (a second row ahead 26 us too,
+// and 43 for 39 in fp32). Backward 25216 x 384 in fp32 with a gate of 197 rows (232
+// MB) 50 us, 4.6 TB/s; 4096 x 4096 in bf16 (201 MB) 45 us, 4.5 TB/s. The parts'
+// launch takes 5 to 7 us.
 //
 // The gradients of post's vectors and of the scale need two sums, not three:
 // with t = c dx . g,  P = sum t yn  and  Q = sum t,
