@@ -625,7 +625,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         q[n] = id[n] >= 0 && any ? p[n] / tsum : 0.0f;
         if (id[n] >= V) q[n] = __builtin_nanf("");
         if (k < entries) {
-            ids[k] = id[n] < V ? static_cast<int>(id[n]) : -1;
+            ids[k] = id[n] >= 0 && id[n] < V ? static_cast<int>(id[n]) : -1;      // an id of 64 bits is no token by its lower 32
             qs[k] = slope * q[n];
         }
     }
