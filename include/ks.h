@@ -518,7 +518,8 @@ ks_status_t ks_preference_backward(const ks_logits_t* x, const float* stats, con
  * ids[s * id_seq_stride + t * id_row_stride + k] (strides in elements). An entry
  * with a negative id is none, so rows may hold fewer; an entry of -inf weighs
  * nothing. The same id may stand in a row more than once: its entries add up.
- * An id >= vocab gives NaN.
+ * A position with an id >= vocab gives NaN, in its loss and its whole gradient (a
+ * label >= vocab too, where labels weigh anything).
  */
 typedef struct ks_teacher_t {
     const void* ids;        /* device: int32 or int64 */

@@ -355,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
                                                                int64_t d_row, bool bits) {
     extern __shared__ uint32_t seen[];
     __shared__ float buf[2 * kWaves];
-    __shared__ int ids[kMaxTop], any, twice, label_in;
+    __shared__ int ids[kMaxTop], any, twice, label_in, outside;
     __shared__ float qs[kMaxTop];
     constexpr int E = kVec<T>;
     const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
@@ -380,6 +380,7 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
     if (tid == 0) {
         any = label_in = 0;
         twice = !bits;
+        outside = ce && label >= V;
     }
     for (int i = tid; bits && i < (V + 31) / 32; i += kThreads) seen[i] = 0;
     Entry e{-1, 0.0f, 0.0f};
@@ -392,12 +393,15 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
         if (bits && atomicOr(&seen[k / 32], 1u << k % 32) >> k % 32 & 1) twice = 1;
         if (e.id == label) label_in = 1;
     }
+    if (e.id >= V) outside = 1;
     if (!(e.q == 0.0f)) any = 1;
     if (tid < entries) ids[tid] = in ? static_cast<int>(e.id) : -1;
     __syncthreads();
     // where nothing in the row weighs anything, that side is not there
     const float slope = any ? a.slope * c : 0.0f, hard = static_cast<float>(a.ce) * c;
-    const float c0 = uniform(MODE != kOne ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
+    // a token outside the vocabulary makes its whole row NaN
+    const float c0 = uniform(outside ? __builtin_nanf("") : MODE != kOne ? slope / sum : (slope + hard) / sum);
+    const float c1 = uniform(hard / sum1);
     if (tid < entries) qs[tid] = slope * e.q;
     auto value = [&](float x) {
         const float y = short_exp<T>(x - m, a.scale);
@@ -425,7 +429,6 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
     }
     for (; v < vecs; v += kThreads) put(v, *reinterpret_cast<const access*>(row + head + v * E));
     __syncthreads();
-    if (tid < entries && e.id >= V) out[0] = narrow<T>(__builtin_nanf(""));     // a token outside: the row says so at its first
     if (tid < entries && in) {
         float taken = qs[tid];
         bool first = true;
@@ -440,9 +443,7 @@ __global__ __launch_bounds__(kThreads) void distil_grad_kernel(const DistilArgs 
         if (ce && e.id == label) taken += hard;
         if (first) out[e.id] = narrow<T>(value(xe) - taken);
     }
-    if (tid != 0 || !ce) return;
-    if (label >= V) out[0] = narrow<T>(__builtin_nanf(""));
-    else if (!label_in) out[label] = narrow<T>(value(xl) - hard);
+    if (tid == 0 && ce && label < V && !label_in) out[label] = narrow<T>(value(xl) - hard);
 }
 
 // Loss and gradient (d_ null: the loss alone, and stats for a later gradient) of a
@@ -459,7 +460,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     extern __shared__ uint32_t seen[];        // a bit a token: whether an entry has it
     __shared__ float maxima[2][W], sums[3][W];
     __shared__ double parts[W];
-    __shared__ int counts[W], twice, label_in;
+    __shared__ int counts[W], twice, label_in, outside;
     __shared__ int ids[kMaxTop];
     __shared__ float qs[kMaxTop];
     const int64_t at = a.row0 + blockIdx.x, s = at / a.x.tokens, t = at - s * a.x.tokens;
@@ -503,7 +504,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         rl = bits_of(row[label >= 0 && label < V ? label : 0]);
     }
     for (int i = tid; i < (V + 31) / 32; i += NT) seen[i] = 0;
-    if (tid == 0) twice = label_in = 0;
+    if (tid == 0) {
+        twice = label_in = 0;
+        outside = ce && label >= V;
+    }
     int count = 0;
     if (COUNT) {
         const int n = static_cast<int>(a.x.sequences * a.x.tokens);
@@ -572,6 +576,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     for (int n = 0; n < EN; ++n) {
         p[n] = exp_of(top[n] - tm, a.scale);
         tsum += p[n];
+        if (id[n] >= V) outside = 1;
         if (id[n] < 0 || id[n] >= V) continue;
         // duplicates are rare: looked for here, added up below if there is one
         const int k = static_cast<int>(id[n]);
@@ -631,7 +636,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
     }
     keep_narrow(w);
     // the gradient as if there were no entries
-    const float c0 = uniform(TWO ? slope / sum : (slope + hard) / sum), c1 = uniform(hard / sum1);
+    // a token outside the vocabulary makes its whole row NaN
+    const float c0 = uniform(outside ? __builtin_nanf("") : TWO ? slope / sum : (slope + hard) / sum);
+    const float c1 = uniform(hard / sum1);
     auto value = [&](float x) {
         const float e = short_exp<T>(x - m, a.scale);
         if (MODE == kBoth) return c0 * e + c1 * short_exp<T>(x - m, kNatural);
@@ -666,11 +673,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
 #pragma unroll
     for (int n = 0; n < EN; ++n) {
         const int k = n * NT + tid;
-        if (!d_ || k >= entries || id[n] < 0) continue;
-        if (id[n] >= V) {                    // a token outside: the row says so at its first
-            out[0] = narrow<T>(__builtin_nanf(""));
-            continue;
-        }
+        if (!d_ || k >= entries || id[n] < 0 || id[n] >= V) continue;
         float taken = qs[k];
         bool first = true;
         if (twice) {
@@ -685,8 +688,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(U <= 4 ? 8 :
         if (first) out[id[n]] = narrow<T>(value(xe[n]) - taken);
     }
     if (tid != 0) return;
-    if (d_ && ce && label >= V) out[0] = narrow<T>(__builtin_nanf(""));
-    else if (d_ && ce && !label_in) out[label] = narrow<T>(value(xl) - hard);
+    if (d_ && ce && label < V && !label_in) out[label] = narrow<T>(value(xl) - hard);
     double token = 0.0;
     for (int k = 0; k < W && k * 64 < entries; ++k) token += parts[k];
     token = kl ? token * a.kl : 0.0;
