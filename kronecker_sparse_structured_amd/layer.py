@@ -314,10 +314,10 @@ def make_norm_classes():
         post(y), pre(z)), with z the residual and h the next block's input. pre and
         post are norms of `kind` "rms" or "layer" (the latter with biases) over the
         last dimension, `scale` a vector that starts at that value; each is left out
-        if it is false or None. forward(x, y=None, gate=None): x and y (..., width);
-        without a y, z is x. The gate has x's shape, or that of its first dimensions
-        (1 for the others, or none) and width: one for all rows that share them. h is
-        of `dtype`, x's by default."""
+        if it is false or None. forward(x, y=None, gate=None): x and y of one shape
+        (..., width); without a y, z is x. The gate has x's shape, or that of its first
+        dimensions (1 for the others, or none) and width: one for all rows that share
+        them. h is of `dtype`, x's by default."""
 
         def __init__(self, width, kind="rms", pre=True, post=False, scale=None, residual=1.0, eps=1e-6, dtype=None,
                      params=None, device=None):
@@ -336,12 +336,21 @@ def make_norm_classes():
             self.scale = vector(scale) if scale is not None else None
 
         def forward(self, x, y=None, gate=None):
+            # of these shapes only are the rows below what they are meant to be: as many
+            # values of another shape would be cut into rows as well
             lead = x.shape[:-1]
+            if x.shape[-1:] != (self.width,):
+                raise ValueError("x must be (..., %d), not %s" % (self.width, tuple(x.shape)))
+            if y is not None and y.shape != x.shape:
+                raise ValueError("y must have x's shape %s, not %s" % (tuple(x.shape), tuple(y.shape)))
 
             def rows(t):
                 return None if t is None else t.reshape(-1, self.width).contiguous()
 
             if gate is not None:
+                if gate.shape[-1:] != (self.width,) or gate.dim() > x.dim():
+                    raise ValueError("the gate must be (..., %d) with at most x's dimensions, not %s"
+                                     % (self.width, tuple(gate.shape)))
                 own = list(gate.shape[:-1])
                 while own and own[-1] == 1:
                     own.pop()
