@@ -348,6 +348,8 @@ def make_norm_classes():
                 return None if t is None else t.reshape(-1, self.width).contiguous()
 
             if gate is not None:
+                if y is None:
+                    raise ValueError("a gate needs a y")
                 if gate.shape[-1:] != (self.width,) or gate.dim() > x.dim():
                     raise ValueError("the gate must be (..., %d) with at most x's dimensions, not %s"
                                      % (self.width, tuple(gate.shape)))

@@ -18,7 +18,8 @@ class Handle:
     def forward(self, x, y=None, gate=None, dtype=None, keep=False):
         assert x.dim() == 2 and x.shape[1] == self.width
         if y is None:
-            assert gate is None
+            if gate is not None:
+                raise ValueError("a gate needs a y")
             return x, x.clone()
         assert y.shape == x.shape
         rows = len(x)
@@ -82,3 +83,10 @@ def test_one_row_and_none(norm):
     for shape, gate in (((0, 8), (0, 8)), ((0, 5, 8), (0, 8)), ((4, 0, 8), (4, 8)), ((4, 0, 8), (8,))):
         z, h = norm(torch.ones(shape), torch.ones(shape), torch.ones(gate))
         assert z.shape == shape and h.shape == shape
+
+
+def test_a_gate_without_a_block_is_refused(norm):
+    x = torch.randn(4, 6, 8)
+    for m in (norm, layer.ResidualNorm(8, pre=False)):       # with nothing to compute too
+        with pytest.raises(ValueError):
+            m(x, gate=torch.ones(4, 8))
