@@ -8,10 +8,10 @@ distillation_loss: the paired preference loss on token logits, and the loss
 against a teacher's highest logits.
 
 Argument marshalling only: every product runs in the HIP library. The gradients
-are not differentiable themselves: a second derivative raises. With
-gradients enabled each factor is its own launch, so that the intermediates
-the backward pass needs are kept; without, the chain goes through
-``chain_matmul`` and may run fused pairs.
+are not differentiable themselves: a second derivative raises, and so does a
+forward-mode one. With gradients enabled each factor is its own launch, so that
+the intermediates the backward pass needs are kept; without, the chain goes
+through ``chain_matmul`` and may run fused pairs.
 """
 from __future__ import annotations
 
@@ -47,6 +47,19 @@ def _first_only(backward):
         return tuple(g if g is None else Refuse.apply(g.requires_grad_()) for g in out)
 
     return call
+
+
+def _no_tangents(tensors):
+    """Raises if one of a call's tensors(), asked for inside a dual level alone,
+    carries a forward-mode tangent, which the library's calls would drop: the
+    derivative would read as zero. (An autograd function raises by itself, but a call
+    that needs no gradient goes past it.)"""
+    import torch
+    forward_ad = torch.autograd.forward_ad
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors()):
+        raise NotImplementedError("forward-mode derivatives through libks are not formed")
 
 
 def _autograd():
@@ -124,6 +137,7 @@ def make_layer_class():
 
         def forward(self, x):
             lead = x.shape[:-1]
+            _no_tangents(lambda: (x, *self.weights))
             x2 = x.reshape(-1, self.n_in).contiguous()
             grad = torch.is_grad_enabled() and (x.requires_grad or any(w.requires_grad for w in self.weights))
             same = all(w.dtype == x2.dtype for w in self.weights) and x2.dtype in (torch.float32, torch.bfloat16)
@@ -188,6 +202,7 @@ def make_adapter_class():
 
         def forward(self, x, ids):
             lead = x.shape[:-1]
+            _no_tangents(lambda: (x, self.A, self.B, self.scale, *self.layer.weights))
             x2 = x.reshape(-1, self.layer.n_in).contiguous()
             ids2 = ids.reshape(-1).contiguous()
             # the handle holds addresses, so it is made for the tensors of this call
@@ -362,6 +377,7 @@ def make_norm_classes():
             x2, y2, gate2 = rows(x), rows(y), rows(gate)
             if y is None and self.pre_weight is None:
                 return x, None
+            _no_tangents(lambda: (x, y, gate, *vectors))
             # the handle holds addresses, so it is made for the tensors of this call
             norm = libks.ResidualNorm(self.width, *[None if v is None else v.detach() for v in vectors], kind=self.kind,
                                       eps=self.eps, residual=self.residual)
