@@ -22,6 +22,19 @@ from typing import Sequence
 from . import libks
 
 
+def _no_tangents(tensors):
+    """Raises if one of a call's tensors(), asked for inside a dual level alone,
+    carries a forward-mode tangent, which the library's calls would drop: the
+    derivative would read as zero. (An autograd function raises by itself, but a call
+    that needs no gradient goes past it.)"""
+    import torch
+    forward_ad = torch.autograd.forward_ad
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors()):
+        raise NotImplementedError("forward-mode derivatives through libks are not formed")
+
+
 def _first_only(backward):
     """A backward() whose gradients are constants to autograd: a derivative of one
     raises, where it would silently be zero. (torch's once_differentiable raises
@@ -40,6 +53,7 @@ def _first_only(backward):
 
     @functools.wraps(backward)
     def call(ctx, *grads):
+        _no_tangents(lambda: grads)
         with torch.no_grad():
             out = backward(ctx, *grads)
         if not torch.is_grad_enabled():                # without create_graph
@@ -47,19 +61,6 @@ def _first_only(backward):
         return tuple(g if g is None else Refuse.apply(g.requires_grad_()) for g in out)
 
     return call
-
-
-def _no_tangents(tensors):
-    """Raises if one of a call's tensors(), asked for inside a dual level alone,
-    carries a forward-mode tangent, which the library's calls would drop: the
-    derivative would read as zero. (An autograd function raises by itself, but a call
-    that needs no gradient goes past it.)"""
-    import torch
-    forward_ad = torch.autograd.forward_ad
-    if getattr(forward_ad, "_current_level", 0) < 0:
-        return
-    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors()):
-        raise NotImplementedError("forward-mode derivatives through libks are not formed")
 
 
 def _autograd():

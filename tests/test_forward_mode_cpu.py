@@ -87,3 +87,16 @@ def test_a_tangent_of_the_block_or_its_gate_raises():
     with forward_ad.dual_level():                    # x itself, tangent and all: nothing is computed
         dual = forward_ad.make_dual(x, torch.ones_like(x))
         assert forward_ad.unpack_dual(plain(dual)[0]).tangent is not None
+
+
+def test_a_tangent_of_the_gradient_raises(monkeypatch):
+    """The derivative of a backward pass by what it is given."""
+    monkeypatch.setattr(libks, "matmul_dx", lambda dY, W, p: torch.zeros(len(dY), 8))
+    x = torch.randn(5, 8, requires_grad=True)
+    y = layer.ks_matmul_autograd(x, torch.randn(1, 4, 4, 2), PATTERNS[0])
+    torch.autograd.grad(y, x, torch.ones_like(y), retain_graph=True)
+    with forward_ad.dual_level():
+        upstream = forward_ad.make_dual(torch.ones_like(y), torch.ones_like(y))
+        for create_graph in (False, True):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(y, x, upstream, retain_graph=True, create_graph=create_graph)
