@@ -644,8 +644,8 @@ typedef struct ks_residual_norm_t {
     const void* post_bias;    /* NULL: none */
     const void* scale;        /* NULL: 1 */
     int64_t width;            /* 1 .. KS_NORM_MAX_WIDTH (KS_ERR_UNSUPPORTED above) */
-    double eps;               /* > 0 */
-    double residual;
+    double eps;               /* > 0, and finite, as fp32 too */
+    double residual;          /* finite, as fp32 too */
     int32_t kind;             /* a ks_norm_t value */
     int32_t elem;             /* ks_elem_t values: of the five vectors, */
     int32_t x_elem, y_elem;   /* of x, z and their gradients, of y and its, */

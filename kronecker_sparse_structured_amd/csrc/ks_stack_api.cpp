@@ -79,7 +79,7 @@ ks_status_t check_norm(const ks_residual_norm_t* n, int64_t rows, int64_t groups
     if (n->width < 1) return KS_ERR_INVALID;
     if (n->width > KS_NORM_MAX_WIDTH) return KS_ERR_UNSUPPORTED;
     if (!(n->eps > 0.0) || !std::isfinite(n->eps) || !(static_cast<float>(n->eps) > 0.0f) ||
-        !std::isfinite(static_cast<float>(n->eps)) || !std::isfinite(n->residual))
+        !std::isfinite(static_cast<float>(n->eps)) || !std::isfinite(static_cast<float>(n->residual)))
         return KS_ERR_INVALID;
     if (groups < 0 || groups >= kLimit || (groups > 0 && rows % groups != 0)) return KS_ERR_INVALID;
     if ((n->pre_bias && !n->pre_weight) || (n->post_bias && !n->post_weight)) return KS_ERR_INVALID;
