@@ -23,9 +23,9 @@
 // which are sorted, the best head out_beams times.
 //
 // What bounds it: many rows the arithmetic of the first launch beside its reads
-// (32 x 16 beams of 32000 in fp32, 66 MB, 17 us, and 64 x 4 of 50257 in bf16, 26 MB,
-// 10 us: 3.9 and 2.6 TB/s), few rows the two launches' latency, 6 us each. The second
-// launch is a chain of dependent steps, 6 us for 4 beams and 11 for 16.
+// (32 x 16 beams of 32000 in fp32, 66 MB, 15 us, and 64 x 4 of 50257 in bf16, 26 MB,
+// 10 us: 4.4 and 2.6 TB/s), few rows the two launches' latency, 6 us each. The second
+// launch is a chain of dependent steps, 6 to 7 us for 4 beams and 11 for 16.
 
 #include <algorithm>
 
@@ -353,8 +353,10 @@ __global__ __launch_bounds__(kJoinWaves * 64) void beam_join_kernel(const ks_bea
 
 // ---------------------------------------------------------------- states
 //
-// A copy of rows, bound by memory: 64 beams of 2 MB, 268 MB in and out, 35 us
-// (7.6 TB/s: a part of it is still in the last cache).
+// A copy of rows, bound by memory: 64 beams of 2 MB, 268 MB in and out, 36 us
+// (7.4 TB/s: a part of it is still in the last cache). Where addresses or rows are no
+// multiple of 4 bytes a lane copies one byte at a time and the accesses bound it: rows
+// 2 bytes longer take 105 us.
 
 constexpr int kStates = 60;              // a launch: their table is a kernel argument
 constexpr int kPiece = 16;               // accesses of a wave

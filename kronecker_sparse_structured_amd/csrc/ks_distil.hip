@@ -14,17 +14,19 @@
 // exponentials are kept in one pass, as in ks_preference.hip.
 //
 // The gradient goes out in two steps: the whole row as if there were no entries, in
-// 16-byte nontemporal stores (8192 rows of 50257 in bf16 329 us, 333 with ordinary
+// 16-byte nontemporal stores (8192 rows of 50257 in bf16 329 us a call, 333 with ordinary
 // ones), and behind a barrier the few values at the entries' and the label's tokens
 // again.
 //
 // What bounds it: the row's read and write. 8192 rows of 50257 in bf16 (1.65 GB)
-// with one exponential a value 312 us, 5.3 TB/s, a device copy of as much 320;
-// with two, 329 to 360: there the exponentials' arithmetic shows. In fp32, 8192 rows
-// of 32000 (2.1 GB), 393 us either way. What a row needs beside its vectors (its
+// with one exponential a value 313 us a call, 5.3 TB/s, a device copy of as much 320;
+// with two, 332 (temperature 2) and 367: there the exponentials' arithmetic shows. In
+// fp32, 8192 rows of 32000 (2.1 GB), 393 us either way. With the gradient in a call of
+// its own 170 and 338 us, 4096 rows of 70000 in fp32 (1.15 GB a pass), which no
+// workgroup holds, 205 and 452. What a row needs beside its vectors (its
 // entries, what lies before and behind them) is on its way with them: a load whose
 // value is converted in a branch is waited for in that branch (8192 rows of 16000 in
-// bf16 109 us, 124 with such loads).
+// bf16 110 us, 124 with such loads).
 
 #include <algorithm>
 #include <cmath>
@@ -340,7 +342,8 @@ __global__ __launch_bounds__(kThreads) void distil_tokens_kernel(const DistilArg
 
 // The exponentials of a row: exp((x - m) / T) and, where both sides weigh and T is
 // not 1, exp(x - m): by an exponential of its own, or for T = 2 (the usual choice)
-// as the square of the first (8192 rows of 50257 in bf16 329 us, 360 otherwise).
+// as the square of the first (8192 rows of 50257 in bf16 332 us a call; 367 at
+// temperature 3, with an exponential of its own).
 enum Exps : int { kOne = 0, kBoth = 1, kSquare = 2 };
 
 // dx of one row: first as if there were no entries, then the values at the
@@ -812,7 +815,8 @@ ks_status_t pick_rows(const DistilArgs& a, int64_t n, float* tokens, float* inv,
 
 // With a gradient as long as registers reach. The loss alone up to 32768 values:
 // of longer rows a workgroup that goes through the row keeps more bytes on their way
-// (8192 rows of 50257 in bf16 156 us, 187 held; 4096 rows of 32000 in fp32 100 us, 95 held).
+// (8192 rows of 50257 in bf16 161 us, 191 held; 4096 of them in fp32 150, 205 held;
+// 4096 rows of 32000 in fp32 100, 95 held).
 bool distil_holds(const ks_logits_t& x, bool gradient) {
     return gradient ? x.vocab / (x.elem == KS_ELEM_BF16 ? 8 : 4) <= 16384 : x.vocab <= 32768;
 }

@@ -24,10 +24,11 @@
 // this one's sums are formed.
 //
 // What bounds it: memory, at the rate of a large copy (4.9 TB/s) or, with the last
-// cache's help, above it. Forward 16384 x 1024 (fp32 in, bf16 h, 235 MB) 36 us, 6.5
-// TB/s; 4096 x 4096 in bf16 (134 MB) 26 us, 5.2 TB/s (a second row ahead 26 us too,
+// cache's help, above it. Forward 16384 x 1024 (fp32 in, bf16 h, 235 MB) 37 us, 6.4
+// TB/s; 4096 x 4096 in bf16 (134 MB) 28 us, 4.8 TB/s (a second row ahead the same,
 // and 43 for 39 in fp32). Backward 25216 x 384 in fp32 with a gate of 197 rows (232
-// MB) 50 us, 4.6 TB/s; 4096 x 4096 in bf16 (201 MB) 45 us, 4.5 TB/s. The parts'
+// MB) 51 us, 4.5 TB/s; 4096 x 4096 in bf16 (201 MB) 47 us, 4.3 TB/s; 2048 x 8192 in
+// bf16 (201 MB) 60 us, 3.3 TB/s: one row a compute unit, and none ahead. The parts'
 // launch takes 5 to 7 us.
 //
 // The gradients of post's vectors and of the scale need two sums, not three:
@@ -53,8 +54,8 @@ int worker_waves(int64_t width, int lane) {
 
 // The values that a lane holds. Forward: 8 keep more bytes on their way (4096 x
 // 4096 in bf16 27 us, 54 with 4), unless one wave of 4 would do. Backward: 4, as
-// long as 16 waves reach (8192 x 2048 47 us; as many values as 2048 x 8192, with 8,
-// 63 us: its vectors and sums do not fit the registers).
+// long as 16 waves reach (8192 x 2048 46 us; as many values as 2048 x 8192, with 8,
+// 60 us: its vectors and sums do not fit the registers).
 int forward_lane(int64_t width) { return width <= 256 ? 4 : 8; }
 int backward_lane(int64_t width) { return width <= 4096 ? 4 : 8; }
 
@@ -619,8 +620,8 @@ ks_status_t run_norm(const NormArgs& a, void* z, void* h, float* stats, dim3 gri
 template <typename XT, typename YT, typename HT, int L>
 ks_status_t run_grad(const NormArgs& a, const NormGrad& g, dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
     // with 8 values a lane the gate and its sum spill registers (2048 x 8192 in bf16
-    // 104 us with a gate, 63 without one; 72 if the kernel had both): a kernel without
-    // them. With 4 values they fit and the same split gains nothing.
+    // 81 us with a gate a row; without one 60, 67 if one kernel had both): a kernel
+    // without them. With 4 values they fit and the same split gains nothing.
     if constexpr (L == 8)
         if (!a.gate) return launch_kernel(norm_grad_kernel<XT, YT, HT, L, false>, grid, block, lds, stream, a, g);
     return launch_kernel(norm_grad_kernel<XT, YT, HT, L, true>, grid, block, lds, stream, a, g);
