@@ -102,3 +102,23 @@ def test_few_positions_at_temperature_2(case):
         loss, tokens = layer.distillation_loss(x, *data[1:], w, T)
         (2.5 * loss).backward()
         dist.check((loss.detach(), tokens, x.grad), want, upstream=2.5)
+
+
+@pytest.mark.parametrize("case", [(70001, 256, F32), (140001, 128, BF16), (32001, 200, BF16)], ids=lambda c: "%d-%d-%s" % (*c[:2], str(c[2])[6:]))
+def test_the_gradient_in_the_logits_place(case):
+    """Also of rows that are read twice, in one call and with the gradient in a call of its own."""
+    require_gpu()
+    V, K, dtype = case
+    data, rows = draw(3, 701, V, K, dtype, seed=V)
+    for w, T in MODES:
+        x = data[0].clone()
+        loss, tokens, d = libks.distillation_loss(x, *data[1:], w, T, dlogits=x)
+        assert d is x
+        check((loss, tokens, d), data, rows, w, T)
+        x = data[0].clone()
+        loss, tokens, stats, _ = libks._distil_forward(x, *data[1:], w, T)
+        want = libks._distil_backward(x, *data[1:], w, T, stats, None)
+        lib, logits = libks.load(), libks._logits(x, data[1])
+        status = lib.ks_distil_backward(logits, libks._teacher(*data[2:], x), w, T, stats.data_ptr(), None, x.data_ptr(),
+                                        *libks._layout(x, "x"), libks._raw_stream(x.get_device()))
+        assert status == libks.KS_OK and torch.equal(x, want)
